@@ -6,9 +6,10 @@ cache), tree_attention (the step's tokens against cache and tree), tree_verify (
 drafted tree against the logits) and kv_commit (accepted rows moved together).
 
 The cache holds 16-token tiles in matrix-operand order.  A page of one head is block/16 tiles; for
-2-byte elements a K tile is [D/32][4 g][16 m][8 e] with token m, d = 32 c + 8 g + e and a V tile is
-[D/32][4 g][16 m][2 u][4 i] with token 4 g + i, d = 32 c + 16 u + m; for e4m3 a K tile is
-[D/64][4][16][16] with d = 64 c + 16 g + e and a V tile [D/64][4][16][4][4] with d = 64 c + 16 u + m.
+2-byte elements a K tile is [D/32][4 g][16 p][8 e] with d = 32 c + 8 g + e and a V tile is
+[D/16][2 o][16 m][8 i] with token 8 o + i, d = 16 c + m; for e4m3 a K tile is [D/64][4 g][16 p][16 e]
+with d = 64 c + 16 g + e and a V tile [D/32][2 o][16 m][2 u][8 i] with d = 32 c + 16 u + m.  Place p of
+a K tile holds the token with bits (p2, p3, p1, p0).
 """
 import math
 
@@ -262,15 +263,19 @@ def prepare(case, seed):
 
 # --------------------------------------------------------------------------- plain forms
 def _k_tiles(cache):
-    """The K cache [..., heads, block, D] as [..., heads, block/16, D/w, 4, 16, w/4]: token at dim -2."""
-    w = 32 if cache.dtype == torch.bfloat16 else 64
-    return _bits(cache).unflatten(-2, (-1, 16)).flatten(-2).unflatten(-1, (cache.shape[-1] // w, 4, 16, w // 4))
+    """The K cache [..., heads, block, D] as [..., heads, block/16, D/w, 4, 16, e]: place at dim -2."""
+    e = 8 if cache.dtype == torch.bfloat16 else 16
+    return _bits(cache).unflatten(-2, (-1, 16)).flatten(-2).unflatten(-1, (cache.shape[-1] // (4 * e), 4, 16, e))
 
 
 def _v_tiles(cache):
-    """The V cache as [..., heads, block/16, D/w, 4, 16, w/16, 4]: token 4 g + i at dims -4 and -1."""
-    w = 32 if cache.dtype == torch.bfloat16 else 64
-    return _bits(cache).unflatten(-2, (-1, 16)).flatten(-2).unflatten(-1, (cache.shape[-1] // w, 4, 16, w // 16, 4))
+    """The V cache as [..., heads, block/16, D/w, 2, 16, u, 8]: token 8 o + i at dims -4 and -1."""
+    u = 1 if cache.dtype == torch.bfloat16 else 2
+    return _bits(cache).unflatten(-2, (-1, 16)).flatten(-2).unflatten(-1, (cache.shape[-1] // (16 * u), 2, 16, u, 8))
+
+
+def _place(token):
+    return token % 4 + token // 8 % 2 * 4 + token // 4 % 2 * 8
 
 
 def _bits(cache):
@@ -284,7 +289,7 @@ def _values(bits):
 def _k_rows(cache, slots, block, rows=None):
     """Raw rows [n, ..., heads, D] of the K cache at `slots` [n], or with `rows` writes them."""
     t, b, i = _k_tiles(cache), slots // block, slots % block
-    at = (b, slice(None), i // 16, slice(None), slice(None), i % 16)
+    at = (b, slice(None), i // 16, slice(None), slice(None), _place(i % 16))
     at = at if t.dim() == 7 else (slice(None),) + at
     if rows is None:
         return t[at].flatten(-3)
@@ -293,7 +298,7 @@ def _k_rows(cache, slots, block, rows=None):
 
 def _v_rows(cache, slots, block, rows=None):
     t, b, i = _v_tiles(cache), slots // block, slots % block
-    at = (b, slice(None), i // 16, slice(None), i % 16 // 4, slice(None), slice(None), i % 4)
+    at = (b, slice(None), i // 16, slice(None), i % 16 // 8, slice(None), slice(None), i % 8)
     at = at if t.dim() == 8 else (slice(None),) + at
     if rows is None:
         return t[at].transpose(-1, -2).flatten(-3)
@@ -356,7 +361,8 @@ def _rotated(x, cos_sin, positions):
 
 
 def _e4m3(x):
-    scale = x.float().abs().amax(-1) / E4M3_MAX
+    top = x.float().abs().amax(-1)
+    scale = top / torch.full_like(top, E4M3_MAX)  # a tensor: torch multiplies by a number's reciprocal instead
     code = torch.where(scale[..., None] > 0, x.float() / scale[..., None], 0.0)
     return code.to(torch.float8_e4m3fn), scale
 
@@ -380,8 +386,11 @@ def _attend_plain(s):
     H, D = s["k_cache"].shape[1], s["k_cache"].shape[3]
     R, T, G = table.shape[0], q.shape[0], q.shape[1] // H
     # pages [R, pages, heads, tiles, ...] laid out as rows [R, heads, tokens, D]
-    k = _values(_k_tiles(s["k_cache"])[table].permute(0, 2, 1, 3, 6, 4, 5, 7).contiguous()).reshape(R, H, -1, D)
-    v = _values(_v_tiles(s["v_cache"])[table].permute(0, 2, 1, 3, 5, 8, 4, 7, 6).contiguous()).reshape(R, H, -1, D)
+    place = _place(torch.arange(16, device=q.device))
+    k = _k_tiles(s["k_cache"])[table].index_select(6, place).permute(0, 2, 1, 3, 6, 4, 5, 7)
+    v = _v_tiles(s["v_cache"])[table].permute(0, 2, 1, 3, 5, 8, 4, 7, 6)
+    k = _values(k.contiguous()).reshape(R, H, -1, D)
+    v = _values(v.contiguous()).reshape(R, H, -1, D)
     if s["k_scale"] is not None:
         k = k * s["k_scale"][table].transpose(1, 2).reshape(R, H, -1, 1)
         v = v * s["v_scale"][table].transpose(1, 2).reshape(R, H, -1, 1)
@@ -512,12 +521,13 @@ def work(case):
 def _untile(cache, scale, pages):
     """(a page list's) tokens [len(pages) * block, heads, D] in 64 bits, element by element from the layout."""
     H, bs, D = cache.shape[-3:]
-    w, is_k = (32, 8) if cache.dtype == torch.bfloat16 else (64, 16)
+    e, u = (8, 1) if cache.dtype == torch.bfloat16 else (16, 2)
     flat = cache.reshape(-1, H, bs * D)[pages]
     tok, d = torch.meshgrid(torch.arange(bs, device=DEV), torch.arange(D, device=DEV), indexing="ij")
-    tile, m, c = tok // 16 * (16 * D), tok % 16, d // w * (16 * w)
-    k_at = tile + c + d % w // is_k * (16 * is_k) + m * is_k + d % is_k
-    v_at = tile + c + m // 4 * (4 * w) + d % 16 * (w // 4) + d % w // 16 * 4 + m % 4
+    tile, t = tok // 16 * (16 * D), tok % 16
+    p = (t & 3) | (t & 8) >> 1 | (t & 4) << 1
+    k_at = tile + d // (4 * e) * (64 * e) + d % (4 * e) // e * (16 * e) + p * e + d % e
+    v_at = tile + d // (16 * u) * (256 * u) + t // 8 * (128 * u) + d % 16 * (8 * u) + d // 16 % u * 8 + t % 8
     return flat, k_at.reshape(-1), v_at.reshape(-1)
 
 
