@@ -239,7 +239,7 @@ def prepare(case, seed):
     R, H, D, bs = len(ctx), case["kv_heads"], case["head_dim"], case["block"]
     lens = [c + n for c, n in zip(ctx, new)]
     s["table"], pages = _pool(g, lens, bs, 2)
-    s["kv_lens"], s["q_start"] = _ints(lens), _ints([0] + list(np.cumsum(new)))
+    s["ctx"], s["kv_lens"], s["q_start"] = _ints(ctx), _ints(lens), _ints([0] + np.cumsum(new).tolist())
     s["widest"], s["longest"] = max(new), max(lens)
     lead = (case["layers"],) if op == "commit" else ()
     for n in "kv":
@@ -449,7 +449,7 @@ def _verify_plain(s):
 
 def _commit_plain(s):
     bs, table, path = s["block"], s["table"].long(), s["path"].long()
-    ctx = s["kv_lens"].long() - (s["q_start"][1:] - s["q_start"][:-1]).long()
+    ctx = s["ctx"].long()
     i = torch.arange(MAX_NODES, device=path.device)
     go = i < s["accepted"][:, None]
     src = (ctx[:, None] + torch.where(go, path, 0))                     # the others rewrite the root's row onto itself
@@ -485,7 +485,7 @@ def run(s):
                                  max_nodes=s["widest"], out=s["out"], lse=s["lse"])
     if op == "verify":
         return tl.tree_verify(s["logits"], s["draft"], s["parents"], s["q_start"])
-    tl.kv_commit(s["accepted"], s["path"], s["q_start"], s["kv_lens"], s["table"], s["k_cache"], s["v_cache"],
+    tl.kv_commit(s["accepted"], s["path"], s["ctx"], s["kv_lens"], s["table"], s["k_cache"], s["v_cache"],
                  k_scale=s["k_scale"], v_scale=s["v_scale"], ctx_out=s["ctx_out"])
     return s["ctx_out"], s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"]
 
