@@ -78,6 +78,8 @@ extern "C" {
 /* output element types */
 #define TL_BF16 0 /* bfloat16, round to nearest even from fp32 */
 #define TL_F32 1  /* IEEE binary32 */
+/* element type of an 8-bit K/V cache (not an output type) */
+#define TL_E4M3 2 /* 8-bit float: 4 exponent, 3 mantissa bits, largest 448, no infinities */
 
 /* Version of the packed layout and of the signatures below (TL_ABI_VERSION). */
 int tl_abi_version(void);
@@ -386,6 +388,159 @@ size_t tl_noalloc_scratch_bytes(void);
 int tl_linear_apply_noalloc(const uint16_t *x, int64_t T, int64_t K, int64_t N, const int8_t *signs,
                             const uint32_t *packed, const uint16_t *scales, const int8_t *q,
                             const float *row_scale, void *y, int y_dtype, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * One step of speculative decoding over a paged K/V cache.  A step brings R
+ * requests new tokens: the nodes of a drafted tree, one token, or a chunk of a
+ * prompt.  Its calls, in order:
+ *   tl_step_plan       block tables, slots, positions and tree masks from the lengths
+ *   (per layer)        the qkv layer, tl_kv_write, tl_tree_attention, the o layer, ...
+ *   tl_tree_verify     accepted path and next token of every request from the logits
+ *   tl_kv_commit       the accepted rows moved together, for all layers at once
+ * Lengths live on the device: no call waits for them on the host, and a step can be
+ * captured in a graph with T and R as capacities.
+ *
+ * The cache.  `pages` pages of `block` tokens (a power of two, 16..4096) for each of
+ * H heads of D = 64, 128 or 256 elements, bf16 or e4m3 with one f32 scale per token
+ * and head ([pages, H, block]).  The block * D elements of a (page, head) are block/16
+ * tiles of 16 tokens, in matrix-operand order:
+ *   bf16  K [D/32][4 g][16 p][8 e]       d = 32 c + 8 g + e
+ *         V [D/16][2 o][16 m][8 i]       token 8 o + i, d = 16 c + m
+ *   e4m3  K [D/64][4 g][16 p][16 e]      d = 64 c + 16 g + e
+ *         V [D/32][2 o][16 m][2 u][8 i]  token 8 o + i, d = 32 c + 16 u + m
+ * Place p of a K tile holds the token whose bits are (p2, p3, p1, p0).
+ * tl_kv_offset gives an element's place.  A slot is page * block + place in the page;
+ * request r's token at position pos lies in page table[r, pos / block].  A table entry
+ * outside [0, pages) is a page whose tokens are not there; a slot outside
+ * [0, pages * block) is not written.
+ *
+ * Metadata arrays (lengths, tables, slots, masks, paths) need natural alignment only.
+ */
+#define TL_MAX_REQUESTS 4096
+#define TL_TREE_NODES 64 /* nodes of a drafted tree */
+
+/* Element offset of (page, head, token in the page, d) in a cache; which = 0 for K,
+ * 1 for V; -1 for arguments out of range. */
+int64_t tl_kv_offset(int which, int cache_dtype, int64_t H, int64_t D, int64_t block, int64_t page, int64_t head,
+                     int64_t token, int64_t d);
+
+/*
+ * tl_step_plan
+ * in  ctx_lens   int32 [R]  tokens in the cache (negative values count as 0 here and below)
+ * in  new_lens   int32 [R]  tokens of this step
+ * in  owned      int32 [R]  pages of the table that are the request's
+ * io  table      int32 [R, table_width]: entries owned[r] .. are filled with new pages
+ * in  free_list  int32 [free_count], free_head int32 [1]: pages free_list[free_head..] are
+ *                free, and are taken in this order, request by request
+ * in  parents    int32 [T] or NULL: a tree node's parent, as its number inside the request;
+ *                a value that is not an earlier node makes a root
+ * out q_start    int32 [R + 1]  first token of each request (exclusive sums of new_lens, at most T)
+ * out kv_lens    int32 [R]      ctx + new, or 0 for a request that is not served
+ * out slots      int64 [T]      where each token's rows go; -1: nowhere
+ * out positions  int32 [T]      ctx + depth in the tree, or ctx + number of the token
+ * out tree_mask  uint64 [T]     (with parents) the node and its ancestors, a bit each
+ * out owned_out  int32 [R], free_head_out int32 [1]: both after this step
+ * A request is served if its tokens fit table_width pages and the pages it needs beyond
+ * `owned` are free after those of the requests before it; one that is not served gets
+ * slots of -1 and takes no page.  With parents, requests of more than 64 new tokens are
+ * chains (mask 0).  Tokens from q_start[R] on get slot -1, position 0 and mask 0.
+ * No output may be an input; table is the only in-out argument.
+ * Requires 0 <= R <= 4096, T and free_count < 2^31, table_width * block < 2^31.
+ */
+int tl_step_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *owned, int64_t R, int32_t *table,
+                 int64_t table_width, int64_t block, const int32_t *free_list, int64_t free_count,
+                 const int32_t *free_head, const int32_t *parents, int64_t T, int32_t *q_start, int32_t *kv_lens,
+                 int64_t *slots, int32_t *positions, uint64_t *tree_mask, int32_t *owned_out,
+                 int32_t *free_head_out, void *stream);
+
+/*
+ * tl_kv_write
+ * in  k, v       bf16 [T, H, D], tokens ldk / ldv elements apart (column ranges of the qkv
+ *                layer's output, for instance); multiples of 8
+ * in  slots      int64 [T]; two tokens of a call must not share a slot
+ * in  q          bf16 [T, Hq, D], tokens ldq apart, or NULL (then q_out is not written)
+ * in  positions  int32 [T], cos_sin f32 [max_pos, rot]: rot/2 cosines, then rot/2 sines, of
+ *                each position; or cos_sin NULL: no rotation.  The first rot elements of
+ *                every q and k row are rotated in pairs (d, d + rot/2), in f32, and rounded
+ *                to bf16.  Positions are clamped to the table.
+ * out q_out      bf16 [T, Hq, D]
+ * io  k_cache, v_cache and, for e4m3, k_scale, v_scale: the tokens' rows.  e4m3: scale =
+ *                fl32(amax / 448) of the (rotated, rounded) row, code = RNE(fl32(x / scale)),
+ *                both 0 for a row of zeros.
+ * Requires rot a multiple of 16, at most D; finite inputs.
+ */
+int tl_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t T,
+                int64_t H, int64_t D, const uint16_t *q, int64_t ldq, int64_t Hq, const int32_t *positions,
+                const float *cos_sin, int64_t max_pos, int64_t rot, uint16_t *q_out, void *k_cache, void *v_cache,
+                float *k_scale, float *v_scale, int cache_dtype, int64_t pages, int64_t block, void *stream);
+
+/*
+ * tl_tree_attention
+ * in  q          bf16 [T, H * G, D], tokens ldq elements apart (a multiple of 8); query heads
+ *                h G .. h G + G - 1 read cache head h
+ * in  caches and scales as tl_kv_write leaves them; the step's own rows are in them
+ * in  table      int32 [R, table_width]
+ * in  q_start    int32 [R + 1], kv_lens int32 [R]: request r's tokens are q_start[r] ..
+ *                q_start[r + 1] - 1 (n of them), its keys the positions 0 .. kv_lens[r] - 1,
+ *                of which the last n are its own tokens
+ * in  tree_mask  uint64 [T] or NULL.  A token sees every key before its request's own
+ *                tokens and, with a mask in a request of up to 64 tokens, the own token j
+ *                where bit j is set; else the own tokens up to itself.
+ * out out        bf16 [T, H * G, D]: softmax(scale q K^T) V over the keys it sees, 0 if none
+ * out lse        f32 [T, H * G] or NULL: log of the sum of exponentials, -inf if none
+ * max_nodes      the most tokens a request has, as far as the caller knows: it chooses the
+ *                kernel and sizes the workspace; lengths above it are still right
+ * workspace      tl_tree_attention_workspace_size(max_nodes, G, D, cache_dtype) bytes, 16-byte
+ *                aligned, contents free; calls that overlap in time must not share it
+ * What lies in keys a token does not see (infinities and NaN among it) does not reach it.
+ * Rows of out and lse of tokens that belong to no request are left as they are.
+ * Requires scale > 0 and finite, 1 <= G <= 64, max_nodes >= 1, 0 <= R <= 4096.
+ */
+size_t tl_tree_attention_workspace_size(int64_t max_nodes, int64_t G, int64_t D, int cache_dtype);
+int tl_tree_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H, int64_t G, int64_t D, const void *k_cache,
+                      const void *v_cache, const float *k_scale, const float *v_scale, int cache_dtype,
+                      int64_t pages, int64_t block, const int32_t *table, int64_t table_width, int64_t R,
+                      const int32_t *q_start, const int32_t *kv_lens, const uint64_t *tree_mask, float scale,
+                      int64_t max_nodes, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/*
+ * tl_tree_verify -- greedy check of drafted trees.
+ * in  logits     [T, V] of logits_dtype (TL_BF16 or TL_F32), rows ld elements apart
+ * in  draft      int32 [T]  the nodes' tokens; parents int32 [T] as for tl_step_plan
+ * in  q_start    int32 [R + 1]
+ * out target     int32 [T]  index of the row's largest logit, the lowest of equals (-0 equals
+ *                +0; a NaN counts as larger than every number)
+ * out accepted   int32 [R]  nodes on the accepted path: node 0, then from node c the lowest
+ *                node whose parent is c and whose token is target(c), as long as there is one
+ * out path       int32 [R, path_width] their numbers, then -1
+ * out next       int32 [R]  target of the last accepted node (-1 for a request of no tokens)
+ * A request of more than 64 tokens is a prompt: all its tokens count as accepted, path is
+ * -1, next its last token's target.
+ * workspace      tl_tree_verify_workspace_size(T, V) bytes, 16-byte aligned, contents free
+ * Requires 1 <= path_width <= 64, 1 <= V < 2^31, 0 <= R <= 4096.
+ */
+size_t tl_tree_verify_workspace_size(int64_t T, int64_t V);
+int tl_tree_verify(const void *logits, int logits_dtype, int64_t ld, int64_t T, int64_t V, const int32_t *draft,
+                   const int32_t *parents, const int32_t *q_start, int64_t R, int32_t *accepted, int32_t *path,
+                   int64_t path_width, int32_t *next, int32_t *target, void *workspace, size_t workspace_bytes,
+                   void *stream);
+
+/*
+ * tl_kv_commit -- the accepted nodes' rows to the positions after the context.
+ * in  accepted   int32 [R], path int32 [R, path_width] from tl_tree_verify
+ * in  ctx_lens   int32 [R] (before the step), kv_lens int32 [R] from tl_step_plan
+ * in  table      int32 [R, table_width]
+ * io  k_cache, v_cache [L, pages, H, block, D] and, for e4m3, the scales: for each layer and
+ *                head the row of position ctx + path[i] goes to ctx + i, for i < accepted;
+ *                every source is read before it is overwritten
+ * out ctx_out    int32 [R]: ctx + accepted; ctx for a request that was not served
+ * Entries of path that do not move a row forward inside the request are skipped.
+ */
+int tl_kv_commit(const int32_t *accepted, const int32_t *path, int64_t path_width, const int32_t *ctx_lens,
+                 const int32_t *kv_lens, const int32_t *table, int64_t table_width, int64_t R, void *k_cache,
+                 void *v_cache, float *k_scale, float *v_scale, int cache_dtype, int64_t L, int64_t pages, int64_t H,
+                 int64_t block, int64_t D, int32_t *ctx_out, void *stream);
 
 #ifdef __cplusplus
 }

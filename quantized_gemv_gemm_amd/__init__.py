@@ -17,7 +17,7 @@ import os
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtl.so")
 
-TL_BF16, TL_F32 = 0, 1
+TL_BF16, TL_F32, TL_E4M3 = 0, 1, 2
 GROUP, HBLOCK = 128, 1024
 
 _lib = None
@@ -60,6 +60,21 @@ _SIGS = {
     "tl_noalloc_scratch_bytes": (_c_sz, []),
     "tl_read_probe": (ctypes.c_int, [_c_p, _c_sz, _c_p, _c_p]),
     "tl_mfma_probe": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _c_p, _c_p]),
+    "tl_kv_offset": (_c_i64, [ctypes.c_int, ctypes.c_int] + [_c_i64] * 7),
+    "tl_step_plan": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_i64,
+                                    _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "tl_kv_write": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64,
+                                   _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, ctypes.c_int, _c_i64,
+                                   _c_i64, _c_p]),
+    "tl_tree_attention_workspace_size": (_c_sz, [_c_i64, _c_i64, _c_i64, ctypes.c_int]),
+    "tl_tree_attention": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p,
+                                         ctypes.c_int, _c_i64, _c_i64, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p,
+                                         ctypes.c_float, _c_i64, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "tl_tree_verify_workspace_size": (_c_sz, [_c_i64, _c_i64]),
+    "tl_tree_verify": (ctypes.c_int, [_c_p, ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p,
+                                      _c_i64, _c_p, _c_p, _c_p, _c_sz, _c_p]),
+    "tl_kv_commit": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p,
+                                    ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p]),
     "tl_linear_apply_noalloc": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p,
                                                _c_p, ctypes.c_int, _c_p]),
 }
@@ -557,3 +572,263 @@ def hadamard_join(u_lo, u_hi, half, out=None):
     _check("tl_hadamard_join", lib().tl_hadamard_join(_ptr(u_lo), _ptr(u_hi), T, int(half), _ptr(out),
                                                       out.stride(0) if T > 1 else 512, _stream(u_lo.device)))
     return out
+
+
+# ---------------------------------------------------------------------------
+# one step of speculative decoding over a paged cache
+# ---------------------------------------------------------------------------
+TREE_NODES = 64
+
+
+def _given(t, name, dtype, shape, index):
+    """A contiguous GPU tensor of this dtype and shape, on device number ``index``; its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
+        _need(t, name, dtype, len(shape))
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, name, index):
+    """A bf16 [tokens, heads, D] tensor with whole rows next to each other, tokens any distance
+    apart: its address and that distance."""
+    import torch
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.get_device() != index:
+        _need(t.contiguous(), name, torch.bfloat16, 3)
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    T, H, D = t.shape
+    ld, sh, sd = t.stride()
+    if sd != 1 and D > 1 or sh != D and H > 1:
+        raise ValueError(f"{name}'s heads must lie next to each other (strides {t.stride()})")
+    return t.data_ptr(), max(ld, H * D) if T > 1 else H * D
+
+
+def _index_of(t, name):
+    """The number of the GPU that ``t`` is on."""
+    i = t.get_device() if hasattr(t, "get_device") else None
+    if i is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if i < 0:
+        raise ValueError(f"{name} must be on a GPU, got {t.device}")
+    return i
+
+
+def _cache_code(k_cache, k_scale, v_scale):
+    import torch
+    if k_cache.dtype is torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("a bfloat16 cache has no scales")
+        return TL_BF16
+    if k_cache.dtype is torch.float8_e4m3fn:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an e4m3 cache needs k_scale and v_scale")
+        return TL_E4M3
+    raise TypeError("the cache must be torch.bfloat16 or torch.float8_e4m3fn")
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, index, layers=False):
+    """Checks a cache; its dtype code and addresses."""
+    import torch
+    code = _cache_code(k_cache, k_scale, v_scale)
+    if k_cache.dim() != (5 if layers else 4):
+        raise ValueError(f"k_cache must be [{'layers, ' if layers else ''}pages, heads, block, D]")
+    shape = k_cache.shape
+    k = _given(k_cache, "k_cache", k_cache.dtype, shape, index)
+    v = _given(v_cache, "v_cache", k_cache.dtype, shape, index)
+    if code == TL_BF16:
+        return code, k, v, None, None
+    ks = _given(k_scale, "k_scale", torch.float32, shape[:-1], index)
+    return code, k, v, ks, _given(v_scale, "v_scale", torch.float32, shape[:-1], index)
+
+
+def kv_cache(pages, heads, block, D, dtype=None, layers=None, device="cuda"):
+    """A zeroed cache: (k_cache, v_cache, k_scale, v_scale), the caches [pages, heads, block, D]
+    of bfloat16 (the default; scales None) or float8_e4m3fn (scales f32 [pages, heads, block]),
+    each with a leading dimension if ``layers`` is given."""
+    import torch
+    dtype = dtype or torch.bfloat16
+    shape = ((layers,) if layers is not None else ()) + (pages, heads, block, D)
+    bits = {torch.bfloat16: torch.int16, torch.float8_e4m3fn: torch.uint8}.get(dtype)
+    if bits is None:
+        raise TypeError("the cache must be torch.bfloat16 or torch.float8_e4m3fn")
+    k, v = (torch.zeros(shape, dtype=bits, device=device).view(dtype) for _ in "kv")
+    if bits is torch.int16:
+        return k, v, None, None
+    return (k, v, *(torch.zeros(shape[:-1], dtype=torch.float32, device=device) for _ in "kv"))
+
+
+def kv_offset(which, dtype, heads, D, block, page, head, token, d) -> int:
+    """Element offset of (page, head, token in the page, d) in a cache layer; which is "k" or "v"."""
+    import torch
+    code = {torch.bfloat16: TL_BF16, torch.float8_e4m3fn: TL_E4M3}.get(dtype, -1)
+    at = int(lib().tl_kv_offset({"k": 0, "v": 1}.get(which, -1), code, heads, D, block, page, head, token, d))
+    if at < 0:
+        raise ValueError("kv_offset: argument out of range")
+    return at
+
+
+def step_plan(ctx_lens, new_lens, owned, block_table, free_list, free_head, tokens, block, parents=None):
+    """Metadata of a step from the request lengths (int32 [R] each), on the GPU: takes pages from
+    ``free_list`` into ``block_table`` int32 [R, width] (in place) and returns (q_start [R+1],
+    kv_lens [R], slots int64 [tokens], positions [tokens], tree_mask int64 [tokens] or None,
+    owned [R], free_head [1]).  ``tokens`` is the step's token count or more (a graph's capacity)."""
+    import torch
+    i32 = torch.int32
+    i = _index_of(ctx_lens, "ctx_lens")
+    if ctx_lens.dim() != 1 or block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("step_plan needs ctx_lens [R], block_table [R, width] and free_list [F]")
+    R, width, T = ctx_lens.shape[0], block_table.shape[1], int(tokens)
+    if T < 0:
+        raise ValueError("tokens must not be negative")
+    p = [_given(ctx_lens, "ctx_lens", i32, (R,), i), _given(new_lens, "new_lens", i32, (R,), i),
+         _given(owned, "owned", i32, (R,), i), _given(block_table, "block_table", i32, (R, width), i),
+         _given(free_list, "free_list", i32, free_list.shape, i), _given(free_head, "free_head", i32, (1,), i),
+         None if parents is None else _given(parents, "parents", i32, (T,), i)]
+    dev = ctx_lens.device
+    q_start = torch.empty(R + 1, dtype=i32, device=dev)
+    kv_lens = torch.empty(R, dtype=i32, device=dev)
+    slots = torch.empty(T, dtype=torch.int64, device=dev)
+    positions = torch.empty(T, dtype=i32, device=dev)
+    mask = None if parents is None else torch.empty(T, dtype=torch.int64, device=dev)
+    owned_out = torch.empty(R, dtype=i32, device=dev)
+    head_out = torch.empty(1, dtype=i32, device=dev)
+    _check("tl_step_plan", lib().tl_step_plan(
+        p[0], p[1], p[2], R, p[3], width, int(block), p[4], free_list.shape[0], p[5], p[6], T, q_start.data_ptr(),
+        kv_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), None if mask is None else mask.data_ptr(),
+        owned_out.data_ptr(), head_out.data_ptr(), _stream(dev)))
+    return q_start, kv_lens, slots, positions, mask, owned_out, head_out
+
+
+def kv_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, q=None, positions=None, cos_sin=None,
+             q_out=None):
+    """Writes rows k, v bf16 [T, H, D] (any token distance) to the cache at slots int64 [T] and
+    returns q_out bf16 [T, Hq, D] if q is given.  With positions int32 [T] and cos_sin f32
+    [max_pos, rot] (cosines, then sines) the first rot elements of q and k are rotated first.
+    An e4m3 cache gets codes and scales."""
+    import torch
+    i = _index_of(k, "k")
+    code, kc, vc, ks, vs = _cache_args(k_cache, v_cache, k_scale, v_scale, i)
+    pages, H, block, D = k_cache.shape
+    kp, ldk = _rows(k, "k", i)
+    vp, ldv = _rows(v, "v", i)
+    T = k.shape[0]
+    if k.shape != (T, H, D) or v.shape != (T, H, D):
+        raise ValueError(f"k and v must be [T, {H}, {D}]")
+    sp = _given(slots, "slots", torch.int64, (T,), i)
+    qp, ldq, Hq, qo = None, 0, 0, None
+    if q is not None:
+        qp, ldq = _rows(q, "q", i)
+        Hq = q.shape[1]
+        if q.shape != (T, Hq, D):
+            raise ValueError(f"q must be [{T}, heads, {D}]")
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
+        qo = _given(q_out, "q_out", torch.bfloat16, (T, Hq, D), i)
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    pp, cp, most, rot = None, None, 0, 0
+    if cos_sin is not None:
+        if positions is None or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_pos, rot] and needs positions")
+        most, rot = cos_sin.shape
+        cp = _given(cos_sin, "cos_sin", torch.float32, (most, rot), i)
+        pp = _given(positions, "positions", torch.int32, (T,), i)
+    _check("tl_kv_write", lib().tl_kv_write(kp, ldk, vp, ldv, sp, T, H, D, qp, ldq, Hq, pp, cp, most, rot, qo, kc, vc,
+                                            ks, vs, code, pages, block, _stream(k.device)))
+    return q_out
+
+
+def tree_attention_workspace_size(max_nodes: int, group: int, D: int, dtype=None) -> int:
+    """Bytes of workspace tree_attention needs; dtype is the cache's (bfloat16 by default)."""
+    import torch
+    code = TL_E4M3 if dtype is torch.float8_e4m3fn else TL_BF16
+    return int(lib().tl_tree_attention_workspace_size(max_nodes, group, D, code))
+
+
+def tree_attention(q, k_cache, v_cache, block_table, q_start, kv_lens, tree_mask=None, k_scale=None, v_scale=None,
+                   scale=None, max_nodes=None, out=None, lse=None, workspace=None):
+    """Attention of q bf16 [T, Hq, D] (any token distance) over the paged cache: request r's tokens
+    q_start[r] .. q_start[r+1]-1 see its first kv_lens[r] - n keys and, of its own n, those that
+    tree_mask int64 [T] names (or, without a mask or above 64 tokens, those up to themselves).
+    Returns out bf16 [T, Hq, D], or (out, lse) if ``lse`` f32 [T, Hq] is given (True: made here).
+    ``max_nodes``: the most tokens of a request, as far as known (chooses the kernel)."""
+    import torch
+    i = _index_of(q, "q")
+    code, kc, vc, ks, vs = _cache_args(k_cache, v_cache, k_scale, v_scale, i)
+    pages, H, block, D = k_cache.shape
+    qp, ldq = _rows(q, "q", i)
+    T, Hq, width = q.shape[0], q.shape[1], block_table.shape[-1]
+    R = block_table.shape[0]
+    if q.shape[2] != D or Hq % H or Hq == 0:
+        raise ValueError(f"q must be [T, a multiple of {H}, {D}]")
+    G = Hq // H
+    tp = _given(block_table, "block_table", torch.int32, (R, width), i)
+    sp = _given(q_start, "q_start", torch.int32, (R + 1,), i)
+    lp = _given(kv_lens, "kv_lens", torch.int32, (R,), i)
+    mp = None if tree_mask is None else _given(tree_mask, "tree_mask", torch.int64, (T,), i)
+    out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if out is None else out
+    op = _given(out, "out", torch.bfloat16, (T, Hq, D), i)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is True else lse
+    ep = None if lse is None else _given(lse, "lse", torch.float32, (T, Hq), i)
+    if max_nodes is None:
+        max_nodes = max(1, -(-T // max(R, 1)))
+    if workspace is None:
+        need = lib().tl_tree_attention_workspace_size(max_nodes, G, D, code)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    wp = _given(workspace, "workspace", torch.uint8, (workspace.numel(),), i)
+    _check("tl_tree_attention", lib().tl_tree_attention(
+        qp, ldq, T, H, G, D, kc, vc, ks, vs, code, pages, block, tp, width, R, sp, lp, mp,
+        D ** -0.5 if scale is None else scale, max_nodes, op, ep, wp, workspace.numel(), _stream(q.device)))
+    return out if lse is None else (out, lse)
+
+
+def tree_verify(logits, draft, parents, q_start, path_width=TREE_NODES, workspace=None):
+    """Greedy check of drafted trees: logits bf16 or f32 [T, V] (any row distance), draft and parents
+    int32 [T], q_start int32 [R+1] -> (accepted [R], path [R, path_width], next [R], target [T])."""
+    import torch
+    i = _index_of(logits, "logits")
+    code = _out_code(logits.dtype)
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits must be [T, V] with unit column stride")
+    T, V = logits.shape
+    R = q_start.shape[0] - 1
+    i32 = torch.int32
+    dp = _given(draft, "draft", i32, (T,), i)
+    pp = _given(parents, "parents", i32, (T,), i)
+    sp = _given(q_start, "q_start", i32, (R + 1,), i)
+    dev = logits.device
+    accepted = torch.empty(R, dtype=i32, device=dev)
+    path = torch.empty((R, path_width), dtype=i32, device=dev)
+    nxt = torch.empty(R, dtype=i32, device=dev)
+    target = torch.empty(T, dtype=i32, device=dev)
+    if workspace is None:
+        need = lib().tl_tree_verify_workspace_size(T, V)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    wp = _given(workspace, "workspace", torch.uint8, (workspace.numel(),), i)
+    _check("tl_tree_verify", lib().tl_tree_verify(
+        logits.data_ptr(), code, logits.stride(0) if T > 1 else V, T, V, dp, pp, sp, R, accepted.data_ptr(),
+        path.data_ptr(), path_width, nxt.data_ptr(), target.data_ptr(), wp, workspace.numel(), _stream(dev)))
+    return accepted, path, nxt, target
+
+
+def kv_commit(accepted, path, ctx_lens, kv_lens, block_table, k_cache, v_cache, k_scale=None, v_scale=None,
+              ctx_out=None):
+    """Moves the rows of the accepted nodes (tree_verify's accepted [R] and path [R, width]) to the
+    positions after the context, in a cache layer [pages, H, block, D] or all of them
+    [L, pages, H, block, D]; returns the new context lengths int32 [R]."""
+    import torch
+    i = _index_of(accepted, "accepted")
+    layers = k_cache.dim() == 5
+    code, kc, vc, ks, vs = _cache_args(k_cache, v_cache, k_scale, v_scale, i, layers)
+    pages, H, block, D = k_cache.shape[-4:]
+    R, i32 = accepted.shape[0], torch.int32
+    if path.dim() != 2 or block_table.dim() != 2:
+        raise ValueError("path must be [R, width] and block_table [R, pages]")
+    ctx_out = torch.empty(R, dtype=i32, device=accepted.device) if ctx_out is None else ctx_out
+    _check("tl_kv_commit", lib().tl_kv_commit(
+        _given(accepted, "accepted", i32, (R,), i), _given(path, "path", i32, (R, path.shape[1]), i), path.shape[1],
+        _given(ctx_lens, "ctx_lens", i32, (R,), i), _given(kv_lens, "kv_lens", i32, (R,), i),
+        _given(block_table, "block_table", i32, (R, block_table.shape[1]), i), block_table.shape[1], R, kc, vc, ks, vs,
+        code, k_cache.shape[0] if layers else 1, pages, H, block, D, _given(ctx_out, "ctx_out", i32, (R,), i),
+        _stream(accepted.device)))
+    return ctx_out

@@ -4,6 +4,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include "kv_layout.h"
 #include "tl_internal.h"
 
 namespace tl {
@@ -45,6 +46,31 @@ int from_hip(hipError_t e) {
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;  // rows, tokens and K stay below 2^31
+
+// one step of speculative decoding over a paged cache
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+template <typename... P>
+bool aligned_to(size_t n, P... p) {
+  return (aligned(p, n) && ...);
+}
+template <typename... P>
+bool any_null(P... p) {
+  return (!p || ...);
+}
+
+bool count_ok(int64_t n) { return n >= 0 && n < kMaxDim; }
+bool block_ok(int64_t block) { return block >= tl::kKvTile && block <= 4096 && (block & (block - 1)) == 0; }
+int log2_of(int64_t n) { return __builtin_ctzll(uint64_t(n)); }
+bool width_ok(int64_t D) { return D == 64 || D == 128 || D == 256; }
+
+// sizes of a cache: 0 or a status
+int check_cache(int cache_dtype, int64_t pages, int64_t H, int64_t block, int64_t D) {
+  if (cache_dtype != TL_BF16 && cache_dtype != TL_E4M3) return TL_ERR_DTYPE;
+  if (!width_ok(D) || !block_ok(block) || H < 1 || H > 65536 || pages < 1 || pages >= kMaxDim) return TL_ERR_SHAPE;
+  if (pages > (int64_t(1) << 50) / (H * block * D)) return TL_ERR_SHAPE;
+  return TL_OK;
+}
+size_t cache_bytes(int cache_dtype, int64_t tokens, int64_t D) { return size_t(tokens) * D * (cache_dtype == TL_BF16 ? 2 : 1); }
 
 }  // namespace
 
@@ -457,6 +483,187 @@ int tl_linear_apply(const uint16_t *x, int64_t T, int64_t K, int64_t N, const in
   if (T == 0 || N == 0) return TL_OK;
   return tl::linear_run(x, T, K, N, signs, packed, scales, q, row_scale, y, y_dtype, workspace,
                         workspace_bytes, static_cast<hipStream_t>(stream));
+}
+
+// ---------------------------------------------------------------------------
+// one step of speculative decoding over a paged cache
+int64_t tl_kv_offset(int which, int cache_dtype, int64_t H, int64_t D, int64_t block, int64_t page, int64_t head,
+                     int64_t token, int64_t d) {
+  if (check_cache(cache_dtype, 1, H, block, D) || (which != 0 && which != 1)) return -1;
+  if (page < 0 || page >= kMaxDim || head < 0 || head >= H || token < 0 || token >= block || d < 0 || d >= D) return -1;
+  const int es = cache_dtype == TL_BF16 ? 2 : 1, t = int(token & (tl::kKvTile - 1));
+  const int in_tile = which ? tl::kv_tile_v(t, int(d), es) : tl::kv_tile_k(t, int(d), es);
+  return ((page * H + head) * block + token - t) * D + in_tile;
+}
+
+int tl_step_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t *owned, int64_t R, int32_t *table,
+                 int64_t table_width, int64_t block, const int32_t *free_list, int64_t free_count,
+                 const int32_t *free_head, const int32_t *parents, int64_t T, int32_t *q_start, int32_t *kv_lens,
+                 int64_t *slots, int32_t *positions, uint64_t *tree_mask, int32_t *owned_out,
+                 int32_t *free_head_out, void *stream) {
+  if (R < 0 || R > TL_MAX_REQUESTS || !count_ok(T) || !count_ok(free_count) || !block_ok(block)) return TL_ERR_SHAPE;
+  if (table_width < 0 || table_width > (kMaxDim - 1) / block) return TL_ERR_SHAPE;
+  if (any_null(free_head, q_start, free_head_out)) return TL_ERR_NULLPTR;
+  if (R && (any_null(ctx_lens, new_lens, owned, kv_lens, owned_out) || (table_width && !table))) return TL_ERR_NULLPTR;
+  if (T && (any_null(slots, positions) || (parents && !tree_mask))) return TL_ERR_NULLPTR;
+  if (free_count && !free_list) return TL_ERR_NULLPTR;
+  if (!aligned_to(4, ctx_lens, new_lens, owned, table, free_list, free_head, parents, q_start, kv_lens, positions,
+                  owned_out, free_head_out) ||
+      !aligned_to(8, slots, tree_mask))
+    return TL_ERR_ALIGN;
+  const size_t r4 = size_t(R) * 4, t4 = size_t(T) * 4;
+  const bool tree = parents && T;
+  Span in[] = {{ctx_lens, r4}, {new_lens, r4}, {owned, r4}, {free_list, size_t(free_count) * 4}, {free_head, 4},
+               {parents, t4}};
+  Span out[] = {{table, r4 * table_width}, {q_start, r4 + 4}, {kv_lens, r4}, {slots, 2 * t4}, {positions, t4},
+                {tree ? tree_mask : nullptr, 2 * t4}, {owned_out, r4}, {free_head_out, 4}};
+  if (any_alias(in, 6, out, 8)) return TL_ERR_ALIAS;
+  tl::StepArgs a = {ctx_lens, new_lens, owned, table, free_list, free_head, parents, q_start, kv_lens, slots, positions,
+                    tree ? tree_mask : nullptr, owned_out, free_head_out, free_count, int(T), int(R),
+                    int(table_width), int(block)};
+  return from_hip(tl::launch_step_plan(a, static_cast<hipStream_t>(stream)));
+}
+
+int tl_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t T,
+                int64_t H, int64_t D, const uint16_t *q, int64_t ldq, int64_t Hq, const int32_t *positions,
+                const float *cos_sin, int64_t max_pos, int64_t rot, uint16_t *q_out, void *k_cache, void *v_cache,
+                float *k_scale, float *v_scale, int cache_dtype, int64_t pages, int64_t block, void *stream) {
+  if (int s = check_cache(cache_dtype, pages, H, block, D)) return s;
+  if (!count_ok(T) || ldk < H * D || ldv < H * D || ldk >= kMaxDim || ldv >= kMaxDim) return TL_ERR_SHAPE;
+  if (q && (Hq < 1 || Hq > 65536 || ldq < Hq * D || ldq >= kMaxDim)) return TL_ERR_SHAPE;
+  if (cos_sin && (rot < 16 || rot % 16 || rot > D || max_pos < 1 || max_pos >= kMaxDim)) return TL_ERR_SHAPE;
+  if (T == 0) return TL_OK;
+  const bool e4m3 = cache_dtype == TL_E4M3;
+  if (any_null(k, v, slots, k_cache, v_cache) || (q && !q_out) || (cos_sin && !positions)) return TL_ERR_NULLPTR;
+  if (e4m3 && any_null(k_scale, v_scale)) return TL_ERR_NULLPTR;
+  if (!aligned_to(16, k, v, q, q_out, cos_sin, k_cache, v_cache) || ldk % 8 || ldv % 8 || (q && ldq % 8) ||
+      !aligned_to(8, slots) || !aligned_to(4, positions, k_scale, v_scale))
+    return TL_ERR_ALIGN;
+  const size_t kv = cache_bytes(cache_dtype, pages * H * block, D), sc = e4m3 ? size_t(pages) * H * block * 4 : 0;
+  Span in[] = {{k, (size_t(T - 1) * ldk + H * D) * 2}, {v, (size_t(T - 1) * ldv + H * D) * 2}, {slots, size_t(T) * 8},
+               {q, q ? (size_t(T - 1) * ldq + Hq * D) * 2 : 0}, {positions, cos_sin ? size_t(T) * 4 : 0},
+               {cos_sin, cos_sin ? size_t(max_pos) * rot * 4 : 0}};
+  Span out[] = {{k_cache, kv}, {v_cache, kv}, {k_scale, sc}, {v_scale, sc}, {q_out, q ? size_t(T) * Hq * D * 2 : 0}};
+  if (any_alias(in, 6, out, 5)) return TL_ERR_ALIAS;
+  tl::WriteArgs a = {q, k, v, slots, positions, cos_sin, q_out, k_cache, v_cache, k_scale, v_scale, ldq, ldk, ldv,
+                     pages * block, int(T), int(Hq), int(H), cos_sin ? int(rot) : 0, int(max_pos), log2_of(block)};
+  return from_hip(tl::launch_kv_write(a, D, e4m3, static_cast<hipStream_t>(stream)));
+}
+
+size_t tl_tree_attention_workspace_size(int64_t max_nodes, int64_t G, int64_t D, int cache_dtype) {
+  if (max_nodes < 1 || max_nodes >= kMaxDim || G < 1 || G > 64 || !width_ok(D)) return 0;
+  if (cache_dtype != TL_BF16 && cache_dtype != TL_E4M3) return 0;
+  return tl::tree_workspace_bytes(max_nodes, G, D, cache_dtype == TL_E4M3);
+}
+
+int tl_tree_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H, int64_t G, int64_t D, const void *k_cache,
+                      const void *v_cache, const float *k_scale, const float *v_scale, int cache_dtype,
+                      int64_t pages, int64_t block, const int32_t *table, int64_t table_width, int64_t R,
+                      const int32_t *q_start, const int32_t *kv_lens, const uint64_t *tree_mask, float scale,
+                      int64_t max_nodes, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
+                      void *stream) {
+  if (int s = check_cache(cache_dtype, pages, H, block, D)) return s;
+  if (!count_ok(T) || R < 0 || R > TL_MAX_REQUESTS || G < 1 || G > 64 || max_nodes < 1 || max_nodes >= kMaxDim)
+    return TL_ERR_SHAPE;
+  if (ldq < H * G * D || ldq >= kMaxDim || T * G >= kMaxDim) return TL_ERR_SHAPE;
+  if (table_width < 0 || table_width > (kMaxDim - 1) / block) return TL_ERR_SHAPE;
+  if (!(scale > 0.0f && scale < __builtin_inff())) return TL_ERR_SHAPE;
+  if (T == 0 || R == 0) return TL_OK;
+  // the units of work the kernel counts stay below 2^31
+  if (double(H) * (double(T) * G / 16 + R) * (double(table_width) * block / 128 + 1) >= 2147483648.0) return TL_ERR_SHAPE;
+  const bool e4m3 = cache_dtype == TL_E4M3;
+  if (any_null(q, k_cache, v_cache, q_start, kv_lens, out) || (table_width && !table)) return TL_ERR_NULLPTR;
+  if (e4m3 && any_null(k_scale, v_scale)) return TL_ERR_NULLPTR;
+  const size_t need = tl::tree_workspace_bytes(max_nodes, G, D, e4m3);
+  if (!workspace || workspace_bytes < need) return TL_ERR_WORKSPACE;
+  if (!aligned_to(16, q, k_cache, v_cache, out, workspace) || ldq % 8 || !aligned_to(8, tree_mask) ||
+      !aligned_to(4, table, q_start, kv_lens, lse) || (e4m3 && !aligned_to(16, k_scale, v_scale)))
+    return TL_ERR_ALIGN;
+  const size_t kv = cache_bytes(cache_dtype, pages * H * block, D), sc = e4m3 ? size_t(pages) * H * block * 4 : 0;
+  Span in[] = {{q, (size_t(T - 1) * ldq + H * G * D) * 2}, {k_cache, kv}, {v_cache, kv}, {k_scale, sc}, {v_scale, sc},
+               {table, size_t(R) * table_width * 4}, {q_start, size_t(R) * 4 + 4}, {kv_lens, size_t(R) * 4},
+               {tree_mask, tree_mask ? size_t(T) * 8 : 0}};
+  Span o[] = {{out, size_t(T) * H * G * D * 2}, {lse, lse ? size_t(T) * H * G * 4 : 0}, {workspace, need}};
+  if (any_alias(in, 9, o, 3)) return TL_ERR_ALIAS;
+  tl::TreeArgs a = {};
+  a.q = q;
+  a.k = static_cast<const char *>(k_cache);
+  a.v = static_cast<const char *>(v_cache);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.table = table;
+  a.q_start = q_start;
+  a.kv_lens = kv_lens;
+  a.tree_mask = tree_mask;
+  a.out = out;
+  a.lse = lse;
+  a.ldq = ldq;
+  a.T = int(T);
+  a.R = int(R);
+  a.H = int(H);
+  a.G = int(G);
+  a.pages = int(pages);
+  a.block_shift = log2_of(block);
+  a.table_width = int(table_width);
+  a.max_keys = int(table_width * block);
+  a.scale = scale;
+  return from_hip(tl::launch_tree_attention(a, D, e4m3, max_nodes, workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t tl_tree_verify_workspace_size(int64_t T, int64_t V) {
+  if (!count_ok(T) || V < 1 || V >= kMaxDim) return 0;
+  return size_t(T) * tl::verify_parts(T, V) * 8;
+}
+
+int tl_tree_verify(const void *logits, int logits_dtype, int64_t ld, int64_t T, int64_t V, const int32_t *draft,
+                   const int32_t *parents, const int32_t *q_start, int64_t R, int32_t *accepted, int32_t *path,
+                   int64_t path_width, int32_t *next, int32_t *target, void *workspace, size_t workspace_bytes,
+                   void *stream) {
+  if (logits_dtype != TL_BF16 && logits_dtype != TL_F32) return TL_ERR_DTYPE;
+  if (!count_ok(T) || R < 0 || R > TL_MAX_REQUESTS || V < 1 || V >= kMaxDim || ld < V || ld >= kMaxDim) return TL_ERR_SHAPE;
+  if (path_width < 1 || path_width > TL_TREE_NODES || T * tl::verify_parts(T, V) >= kMaxDim) return TL_ERR_SHAPE;
+  if (T == 0 && R == 0) return TL_OK;
+  if (!q_start || (T && any_null(logits, draft, parents, target)) || (R && any_null(accepted, path, next)))
+    return TL_ERR_NULLPTR;
+  const size_t need = tl_tree_verify_workspace_size(T, V), es = logits_dtype == TL_F32 ? 4 : 2;
+  if (need && (!workspace || workspace_bytes < need)) return TL_ERR_WORKSPACE;
+  if (!aligned_to(es, logits) || !aligned_to(16, workspace) ||
+      !aligned_to(4, draft, parents, q_start, accepted, path, next, target))
+    return TL_ERR_ALIGN;
+  const size_t r4 = size_t(R) * 4, t4 = size_t(T) * 4;
+  Span in[] = {{logits, T ? (size_t(T - 1) * ld + V) * es : 0}, {draft, t4}, {parents, t4}, {q_start, r4 + 4}};
+  Span out[] = {{accepted, r4}, {path, r4 * path_width}, {next, r4}, {target, t4}, {workspace, need}};
+  if (any_alias(in, 4, out, 5)) return TL_ERR_ALIAS;
+  tl::VerifyArgs a = {logits, draft, parents, q_start, accepted, path, next, target, static_cast<uint64_t *>(workspace),
+                      ld, V, int(T), int(R), int(path_width), tl::verify_parts(T, V)};
+  return from_hip(tl::launch_tree_verify(a, logits_dtype == TL_F32, static_cast<hipStream_t>(stream)));
+}
+
+int tl_kv_commit(const int32_t *accepted, const int32_t *path, int64_t path_width, const int32_t *ctx_lens,
+                 const int32_t *kv_lens, const int32_t *table, int64_t table_width, int64_t R, void *k_cache,
+                 void *v_cache, float *k_scale, float *v_scale, int cache_dtype, int64_t L, int64_t pages, int64_t H,
+                 int64_t block, int64_t D, int32_t *ctx_out, void *stream) {
+  if (int s = check_cache(cache_dtype, pages, H, block, D)) return s;
+  if (R < 0 || R > TL_MAX_REQUESTS || L < 1 || L > 4096 || path_width < 1 || path_width > TL_TREE_NODES) return TL_ERR_SHAPE;
+  if (table_width < 0 || table_width > (kMaxDim - 1) / block || L * R * H >= kMaxDim) return TL_ERR_SHAPE;
+  if (pages > (int64_t(1) << 50) / (L * H * block * D)) return TL_ERR_SHAPE;
+  if (R == 0) return TL_OK;
+  const bool e4m3 = cache_dtype == TL_E4M3;
+  if (any_null(accepted, path, ctx_lens, kv_lens, k_cache, v_cache, ctx_out) || (table_width && !table) ||
+      (e4m3 && any_null(k_scale, v_scale)))
+    return TL_ERR_NULLPTR;
+  if (!aligned_to(16, k_cache, v_cache) ||
+      !aligned_to(4, accepted, path, ctx_lens, kv_lens, table, k_scale, v_scale, ctx_out))
+    return TL_ERR_ALIGN;
+  const size_t r4 = size_t(R) * 4, tokens = size_t(L) * pages * H * block;
+  const size_t kv = cache_bytes(cache_dtype, int64_t(tokens), D), sc = e4m3 ? tokens * 4 : 0;
+  Span in[] = {{accepted, r4}, {path, r4 * path_width}, {ctx_lens, r4}, {kv_lens, r4}, {table, r4 * table_width}};
+  Span out[] = {{k_cache, kv}, {v_cache, kv}, {k_scale, sc}, {v_scale, sc}, {ctx_out, r4}};
+  if (any_alias(in, 5, out, 5)) return TL_ERR_ALIAS;
+  tl::CommitArgs a = {accepted, path, ctx_lens, kv_lens, table, static_cast<char *>(k_cache),
+                      static_cast<char *>(v_cache), k_scale, v_scale, ctx_out, pages * H * block, int(R), int(L),
+                      int(H), int(pages), log2_of(block), int(table_width), int(path_width)};
+  return from_hip(tl::launch_kv_commit(a, D, e4m3, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

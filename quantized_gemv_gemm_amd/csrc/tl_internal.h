@@ -99,6 +99,81 @@ hipError_t launch_gemm(const int8_t *xq, const float *tok_scale, int64_t M, int6
                        const uint32_t *packed, const int8_t *q, const float *row_scale, void *y,
                        int y_dtype, int32_t *acc_out, void *workspace, hipStream_t stream);
 
+// ---------------------------------------------------------------------------
+// one step of speculative decoding over a paged cache
+constexpr int kMaxRequests = 4096;  // their prefix sums sit in LDS
+
+// attention (k_tree.hip)
+struct TreeArgs {
+  const uint16_t *q;         // bf16 [T, H * G, D], tokens ldq elements apart
+  const char *k, *v;         // caches
+  const float *k_scale, *v_scale;
+  const int32_t *table, *q_start, *kv_lens;
+  const uint64_t *tree_mask;
+  uint16_t *out;             // bf16 [T, H * G, D]
+  float *lse;                // f32 [T, H * G] or NULL
+  float *part_o, *part_ml;   // workspace: partial sums, and their maximum and sum
+  int64_t ldq;
+  int T, R, H, G;            // tokens, requests, cache heads, query heads of each
+  int pages, block_shift, table_width;
+  int max_keys;              // table_width * block
+  float scale;
+};
+size_t tree_workspace_bytes(int64_t max_nodes, int64_t group, int64_t D, bool e4m3);
+hipError_t launch_tree_attention(TreeArgs a, int64_t D, bool e4m3, int64_t max_nodes, void *workspace,
+                                 hipStream_t stream);
+
+// block tables, slots, positions and tree masks (k_step.hip)
+struct StepArgs {
+  const int32_t *ctx_lens, *new_lens, *owned;
+  int32_t *table;
+  const int32_t *free_list, *free_head, *parents;
+  int32_t *q_start, *kv_lens;
+  int64_t *slots;
+  int32_t *positions;
+  uint64_t *tree_mask;
+  int32_t *owned_out, *free_head_out;
+  int64_t free_count;
+  int T, R, table_width, block;
+};
+hipError_t launch_step_plan(const StepArgs &a, hipStream_t stream);
+
+// cache rows (k_kv.hip)
+struct WriteArgs {
+  const uint16_t *q, *k, *v;  // bf16 [T, heads, D], tokens ldq / ldk / ldv elements apart
+  const int64_t *slots;
+  const int32_t *positions;
+  const float *cos_sin;       // f32 [max_pos, rot]: cosines, then sines
+  uint16_t *q_out;
+  void *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  int64_t ldq, ldk, ldv, slot_count;
+  int T, Hq, H, rot, max_pos, block_shift;
+};
+hipError_t launch_kv_write(const WriteArgs &a, int64_t D, bool e4m3, hipStream_t stream);
+
+struct CommitArgs {
+  const int32_t *accepted, *path, *ctx_lens, *kv_lens, *table;
+  char *k_cache, *v_cache;
+  float *k_scale, *v_scale;
+  int32_t *ctx_out;
+  int64_t layer_tokens;       // pages * heads * block
+  int R, L, H, pages, block_shift, table_width, path_width;
+};
+hipError_t launch_kv_commit(const CommitArgs &a, int64_t D, bool e4m3, hipStream_t stream);
+
+// greedy check of drafted trees (k_verify.hip)
+struct VerifyArgs {
+  const void *logits;         // [T, V], rows ld elements apart
+  const int32_t *draft, *parents, *q_start;
+  int32_t *accepted, *path, *next, *target;
+  uint64_t *best;             // workspace [T][parts]
+  int64_t ld, V;
+  int T, R, path_width, parts;
+};
+int verify_parts(int64_t T, int64_t V);
+hipError_t launch_tree_verify(const VerifyArgs &a, bool f32, hipStream_t stream);
+
 // whole layer from the raw input (tl_api.cpp): the checks that need no workspace,
 // then the workspace checks and the launches on the path tl_linear_path names
 size_t linear_scratch_bytes(int64_t T, int64_t K, int64_t N);
