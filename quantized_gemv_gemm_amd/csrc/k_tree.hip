@@ -11,8 +11,6 @@
 // 32 keys leave a lane with 8 consecutive keys of one query row (the cache's order of K
 // rows sees to that), so the row's maximum, sum and rescale factor are plain per-lane
 // scalars, and the probabilities are, as they lie, the B operand of O^T = V^T P^T.
-// K and V go from memory straight into operand registers in 1 KB loads; LDS only joins
-// the four waves of a workgroup.
 //
 // Work is cut into units of kUnitKeys keys of one (request, cache head, row block), and
 // workgroup w of W takes units [w U / W, (w + 1) U / W): lengths live on the device, so
@@ -20,8 +18,12 @@
 // An item that falls to several workgroups leaves partial sums in the workspace, which
 // tree_combine_kernel adds in a fixed order.
 //
-// Two forms: `split` (few rows) gives the four waves of a workgroup the same rows and
-// different keys; `share` (many rows) gives them different rows and the same keys.
+// Two kernels.  `split` (up to 32 rows of a cache head): bound by the cache's bytes.  The
+// four waves of a workgroup hold the same rows and take different keys; K and V go from
+// memory straight into operand registers, and LDS only joins the waves' sums at the end.
+// `share` (more rows): bound by the matrix cores and the exponentials.  The waves hold
+// different rows and take the same keys, which are staged in LDS two steps deep, so that
+// memory is read once for 64 or 128 rows.
 //
 // Rounding: q.k and p.v are sums of bf16 products in f32; the probabilities are
 // rounded once to bf16 for the product with V (relative 2^-9 each, with errors of both
@@ -167,15 +169,34 @@ __device__ __forceinline__ Item locate(const TreeArgs &a, int rows, const int *p
   return it;
 }
 
-// first unit of workgroup w of 2^grid_log
-__device__ __forceinline__ int first_unit(int w, int total, int grid_log) {
-  return int((int64_t(total) * w) >> grid_log);
+// first unit of workgroup w of W; with fewer units than workgroups the first ones get one each
+__device__ __forceinline__ int first_unit(int w, int W, int total) {
+  return total >= W ? int(int64_t(total) * w / W) : min(w, total);
 }
 
-// Workgroups are dealt to the eight XCDs in turn: workgroup indices are renamed so that
-// an XCD gets neighbouring units, whose row blocks read the same keys from its own L2.
-__device__ __forceinline__ int renamed(int id, int grid_log) {
-  return ((id & 7) << (grid_log - 3)) + (id >> 3);
+// Workgroups are dealt to the eight XCDs in turn.  Where each has several units, their
+// indices are renamed so that an XCD gets neighbouring units, whose row blocks read the
+// same keys from its own L2; where there are few, they stay spread over the chip.
+__device__ __forceinline__ int renamed(int id, int W, int total) {
+  return total >= W ? (id & 7) * (W >> 3) + (id >> 3) : id;
+}
+
+// What the joining kernel has to know of workgroup w's first unit: nothing (parts = 0)
+// unless it is the first border between workgroups inside its item.
+struct Border {
+  int r, h, b, n;
+  int slot0, parts;    // the item's partial sums: slot0, then 2 w, 2 (w + 1), ...
+  int pad[2];
+};
+__device__ __forceinline__ Border border_of(const Item &it, int w, int W, int total) {
+  Border d = {it.r, it.h, it.b, it.n, 0, 0, {0, 0}};
+  const int u0 = int(it.first), u1 = u0 + it.units;
+  const int before = w > 0 ? first_unit(w - 1, W, total) : 0;
+  if (it.at == 0 || before > u0) return d;
+  d.slot0 = 2 * (w - 1) + (before == u0 ? 0 : 1);
+  const int end = total >= W ? int((int64_t(u1) * W + total - 1) / total) : u1;  // first workgroup past the item
+  d.parts = 1 + end - w;
+  return d;
 }
 
 // ---------------------------------------------------------------------------
@@ -220,10 +241,9 @@ struct Tiles {
 
   // K: `at` is the lane's place in chunk 0 of its tile (lanes m < 8 the first tile, the
   // others the second); the second product's tokens are 8 places on
-  template <int FROM = 0, int TO = C / 2>
   __device__ __forceinline__ void load_k(const char *at) {
 #pragma unroll
-    for (int c = FROM; c < TO; ++c) {
+    for (int c = 0; c < C / 2; ++c) {
       w[2 * c] = *reinterpret_cast<const u32x4 *>(at + 1024 * c);
       w[2 * c + 1] = *reinterpret_cast<const u32x4 *>(at + 1024 * c + 128);
     }
@@ -316,503 +336,771 @@ template <int D, int RT>
 struct Rows {
   f32x4 o[D / 16][RT];  // lane (n, g): query row n of row tile t, d = 16 j + 4 g + i
   float m[RT], l[RT];   // running maximum (raw scores) and the lane's share of the sum
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      m[t] = kNegInf;
+      l[t] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) o[j][t] = f32x4{0, 0, 0, 0};
+    }
+  }
 };
 
-template <int D, bool E4M3, int RT, bool SHARE>
-struct Variant {
-  static constexpr int rows = 16 * RT * (SHARE ? kWaves : 1);
-  // workgroups a compute unit holds, by registers: where it is one, 512 of them a lane
-  static constexpr int occupancy = D * (E4M3 ? 1 : 2) * RT > 512 || D * RT > 256 || D * (E4M3 ? 1 : 2) > 256 ? 1 : 2;
-  static constexpr int grid_log = occupancy == 1 ? 8 : 9;
+// A segment: the run of units of one item that a workgroup has; all values are uniform.
+struct Segment {
+  int r, h, n, kv, blk;
+  int ctx, key_end, q0;
+  int s0, s1;          // steps
+  bool whole, flat;    // the whole item; <= 64 nodes
+  int slot;            // of the partial sums
 };
+__device__ __forceinline__ Segment segment_of(const TreeArgs &a, const Item &it, int rows, int take, int slot) {
+  Segment g;
+  g.r = __builtin_amdgcn_readfirstlane(it.r);
+  g.h = __builtin_amdgcn_readfirstlane(it.h);
+  g.n = __builtin_amdgcn_readfirstlane(it.n);
+  g.kv = __builtin_amdgcn_readfirstlane(it.kv);
+  g.blk = __builtin_amdgcn_readfirstlane(it.b);
+  const int at = __builtin_amdgcn_readfirstlane(it.at);
+  g.whole = take == __builtin_amdgcn_readfirstlane(it.units);
+  g.slot = slot;
+  g.flat = g.n <= kTreeNodes;
+  g.ctx = g.kv - g.n;
+  g.key_end = block_keys(g.n, g.kv, g.blk, a.G, rows);
+  g.q0 = max(a.q_start[g.r], 0);
+  g.s0 = at * kUnitSteps;
+  g.s1 = max(min((at + take) * kUnitSteps, (g.key_end + kStepKeys - 1) / kStepKeys), g.s0);
+  return g;
+}
 
-// ---------------------------------------------------------------------------
-template <int D, bool E4M3, int RT, bool SHARE>
-__global__ __launch_bounds__(kThreads, (Variant<D, E4M3, RT, SHARE>::occupancy)) void tree_attention_kernel(const TreeArgs a) {
-  constexpr int ROWS = Variant<D, E4M3, RT, SHARE>::rows;
-  constexpr int QC = D / 32, OC = D / 16;
-  // the four waves' sums are joined in rounds of at most 64 KB of LDS
-  constexpr int ROUNDS = RT * D > 256 ? RT * D / 256 : 1;
-  constexpr int JT = OC / ROUNDS;                      // 16-d tiles joined in a round
-  constexpr int JW = JT / kWaves;                      // of which each wave finishes this many
-  static_assert(JW * kWaves * ROUNDS == OC, "rounds");
-  extern __shared__ __align__(16) char lds[];
-  f32x4 *join = reinterpret_cast<f32x4 *>(lds);        // [wave][JT][RT][64] (split form only)
-  float *stat = reinterpret_cast<float *>(lds + (SHARE ? 0 : kWaves * JT * RT * 1024));  // [wave][2][RT * 16]
-  int *pre = reinterpret_cast<int *>(stat + (SHARE ? 0 : kWaves * 2 * RT * 16));
-  __shared__ int red[kWaves];
+// The rows of a wave: what they see, and their queries as B operands.
+template <int D, bool E4M3, int RT>
+struct Queries {
+  bf16x8 q[D / 32][RT];
+  uint64_t sees[RT];   // flat: nodes the row may see
+  int node[RT];        // of query row (lane & 15) of row tile t; n or more: there is none
 
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int row16 = lane & 15, g = lane >> 4;
-  constexpr int LOG = Variant<D, E4M3, RT, SHARE>::grid_log;
-  const int w = renamed(blockIdx.x, LOG);
-  unit_prefix(a, ROWS, pre, red);
-  const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
-  const int u_begin = first_unit(w, total, LOG), u_end = first_unit(w + 1, total, LOG);
-  const float c2 = a.scale * 1.44269504088896340736f;  // scores to powers of two
-
-  for (int u = u_begin; u < u_end;) {
-    const Item it = locate(a, ROWS, pre, u);
-    const int r = __builtin_amdgcn_readfirstlane(it.r), h = __builtin_amdgcn_readfirstlane(it.h);
-    const int n = __builtin_amdgcn_readfirstlane(it.n), kv = __builtin_amdgcn_readfirstlane(it.kv);
-    const int blk = __builtin_amdgcn_readfirstlane(it.b), units = __builtin_amdgcn_readfirstlane(it.units);
-    const int at = __builtin_amdgcn_readfirstlane(it.at);
-    const int take = min(units - at, u_end - u);
-    const bool whole = take == units;
-    const int slot = 2 * w + (u == u_begin ? 0 : 1);   // of this workgroup's partial sums
-    u += take;
-
-    // this wave's rows
-    const bool flat = n <= kTreeNodes;
-    const int ctx = kv - n;
-    const int q0 = max(a.q_start[r], 0);
-    const int row0 = blk * ROWS + (SHARE ? wave * 16 * RT : 0);
-    bf16x8 q[QC][RT];
-    uint64_t sees[RT];                                 // flat: nodes the row may see
-    int node[RT];
+  __device__ __forceinline__ void load(const TreeArgs &a, const Segment &s, int row0, int row16, int g) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const int row = row0 + 16 * t + row16;
       node[t] = row / a.G;
-      const bool there = node[t] < n;
-      const int64_t tok = q0 + (there ? node[t] : 0);
+      const bool there = node[t] < s.n;
+      const int64_t tok = s.q0 + (there ? node[t] : 0);
       sees[t] = 0;
-      if (flat && there)
-        sees[t] = a.tree_mask ? a.tree_mask[tok] : (~uint64_t(0) >> (63 - node[t]));
-      const uint16_t *src = a.q + tok * a.ldq + int64_t(h * a.G + (there ? row - node[t] * a.G : 0)) * D;
+      if (s.flat && there) sees[t] = a.tree_mask ? a.tree_mask[tok] : (~uint64_t(0) >> (63 - node[t]));
+      const uint16_t *src = a.q + tok * a.ldq + int64_t(s.h * a.G + (there ? row - node[t] * a.G : 0)) * D;
 #pragma unroll
-      for (int j = 0; j < QC; ++j) {
+      for (int j = 0; j < D / 32; ++j) {
         const int d = E4M3 ? 64 * (j >> 1) + 16 * g + 8 * (j & 1) : 32 * j + 8 * g;
         u32x4 v = *reinterpret_cast<const u32x4 *>(src + d);
         if (!there) v = u32x4{0, 0, 0, 0};
         q[j][t] = __builtin_bit_cast(bf16x8, v);
       }
     }
-    // keys that all of the wave's rows see come first: below `clear` no mask is looked at
-    const int clear = flat ? ctx : ctx + row0 / a.G + 1;
-    const int key_end = block_keys(n, kv, blk, a.G, ROWS);
+  }
 
-    Rows<D, RT> acc;
+  // which of the lane's eight keys from position `pos` on row tile t sees, if they are there
+  __device__ __forceinline__ uint32_t visible(int t, const Segment &s, int pos) const {
+    const int j0 = pos - s.ctx;                        // the node of the first key
+    if (s.flat)
+      return (j0 <= -8 ? 255u : j0 < 0 ? uint32_t(sees[t] << -j0) | ((1u << -j0) - 1u)
+                                       : j0 < 64 ? uint32_t(sees[t] >> j0) : 0u) & 255u;
+    return (1u << min(max(node[t] - j0 + 1, 0), 8)) - 1u;
+  }
+};
+
+// The pages of a segment: 64 page numbers at a time in a register's lanes.
+struct Pages {
+  const int32_t *table;
+  int base, ids;
+
+  __device__ __forceinline__ void begin(const TreeArgs &a, const Segment &s, int step, int lane) {
+    table = a.table + int64_t(s.r) * a.table_width;
+    base = (step * kStepKeys) >> a.block_shift;
+    ids = base + lane < a.table_width ? table[base + lane] : -1;
+  }
+  // tile t of a step: its first token in the cache (in tokens; its elements are at D times
+  // this), and how many of its keys there are.  Steps come in rising order.
+  __device__ __forceinline__ void place(const TreeArgs &a, const Segment &s, int step, int t, int lane, int64_t &tile,
+                                        int &lim) {
+    const int pos = step * kStepKeys + 16 * t;
+    int page = (pos >> a.block_shift) - base;
+    if (page >= 64) {                                  // uniform
+      base += page;
+      ids = base + lane < a.table_width ? table[base + lane] : -1;
+      page = 0;
+    }
+    int id = __builtin_amdgcn_readlane(ids, page);
+    lim = min(max(s.key_end - pos, 0), 16);
+    if (lim == 0 || uint32_t(id) >= uint32_t(a.pages)) {
+      id = 0;
+      lim = 0;
+    }
+    tile = ((int64_t(id) * a.H + s.h) << a.block_shift) + (pos & ((1 << a.block_shift) - 1));
+  }
+};
+
+// e4m3: the scales of the lane's eight keys
+struct Scales {
+  f32x4 k[2], v[2];
+  __device__ __forceinline__ void load(const TreeArgs &a, int64_t t0, int64_t t1, int g) {
+    const int64_t at = (g < 2 ? t0 : t1) + 8 * (g & 1);
+    k[0] = *reinterpret_cast<const f32x4 *>(a.k_scale + at);
+    k[1] = *reinterpret_cast<const f32x4 *>(a.k_scale + at + 4);
+    v[0] = *reinterpret_cast<const f32x4 *>(a.v_scale + at);
+    v[1] = *reinterpret_cast<const f32x4 *>(a.v_scale + at + 4);
+  }
+  // absent keys' scales are not used; whether one of the others' is not finite (it counts as 0 then)
+  __device__ __forceinline__ bool keep_v(uint32_t have) {
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float x = have >> i & 1 ? v[i >> 2][i & 3] : 0.0f;
+      const bool bad = !(fabsf(x) < __builtin_inff());
+      odd |= bad;
+      v[i >> 2][i & 3] = bad ? 0.0f : x;
+    }
+    return odd;
+  }
+};
+
+// The lane's keys that are there (a bit each) of two tiles with lim0 and lim1 keys.
+__device__ __forceinline__ uint32_t present(int lim0, int lim1, int g) {
+  const int left = min(max((g < 2 ? lim0 : lim1) - 8 * (g & 1), 0), 8);
+  return (1u << left) - 1u;
+}
+
+// An operand of V (2-byte elements) without absent keys (a bit of `keep` for each of the
+// eight) and without infinities and NaN, whose top bits are gathered in `odd`.
+__device__ __forceinline__ bf16x8 clean(bf16x8 x, const uint32_t *keep, uint32_t &odd) {
+  u32x4 w = __builtin_bit_cast(u32x4, x);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    w[e] &= keep[e];
+    const uint32_t b = ((w[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    odd |= b;
+    w[e] &= ~((b >> 15) * 0xFFFFu);
+  }
+  return __builtin_bit_cast(bf16x8, w);
+}
+
+// Scores of one row tile to weights: raises the running maximum (rescaling the sums
+// where it grew), adds to the running sum, and gives the B operand of the second product.
+// zero: a bit for each key whose weight is 0.
+template <int D, bool E4M3, int RT, bool MASKED>
+__device__ __forceinline__ bf16x8 weigh(const f32x4 &s0, const f32x4 &s1, const f32x4 *vs, float c2, int t,
+                                        Rows<D, RT> &acc, uint32_t &zero) {
+  float top = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])), fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
+  top = fmaxf(row_max(top), acc.m[t]);
+  if (__any(top > acc.m[t])) {
+    const float f = top > acc.m[t] ? __builtin_amdgcn_exp2f((acc.m[t] - top) * c2) : 1.0f;
+    acc.l[t] *= f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) acc.o[j][t] *= f;
+    acc.m[t] = top;
+  }
+  const float mc = top == kNegInf ? 0.0f : top * c2;
+  float e[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s0[i], c2, -mc));
+    e[4 + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s1[i], c2, -mc));
+  }
+  acc.l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+  if constexpr (MASKED) {
+    zero = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) zero |= uint32_t(e[i] == 0.0f) << i;
+  }
+  if constexpr (E4M3) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] *= vs[i >> 2][i & 3];
+  }
+  return as_operand(pack2(e[0], e[1]), pack2(e[2], e[3]), pack2(e[4], e[5]), pack2(e[6], e[7]));
+}
+
+// An infinity or NaN of a node that some rows do not see must not reach them through
+// 0 * inf: the products go without such values, and this adds them key by key where the
+// row sees the key.
+template <int D, bool E4M3, int RT>
+__device__ __forceinline__ void add_not_finite(const TreeArgs &a, int64_t t0, int64_t t1, int lim0, int lim1,
+                                               const uint32_t *vis, const uint32_t *zero, int row16, int g,
+                                               Rows<D, RT> &acc) {
+  constexpr int ES = E4M3 ? 1 : 2;
+  for (int kk = 0; kk < kStepKeys; ++kk) {
+    const int token = kk & 15;
+    if (token >= (kk < 16 ? lim0 : lim1)) continue;
+    const int64_t at = kk < 16 ? t0 : t1;
+    const char *tile = a.v + (at * D + kv_tile_v(token, 4 * g, ES)) * ES;
+    const float scale = E4M3 ? a.v_scale[at + token] : 1.0f;
+    const int from = row16 + 16 * (kk >> 3), e = kk & 7;
+    float with[RT];                                    // NaN: 0 * inf; 0: not seen
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      acc.m[t] = kNegInf;
-      acc.l[t] = 0.0f;
+      const int on = __shfl(int(vis[t]), from, 64) >> e & 1, none = __shfl(int(zero[t]), from, 64) >> e & 1;
+      with[t] = !on ? 0.0f : none ? __builtin_nanf("") : 1.0f;
+    }
 #pragma unroll
-      for (int j = 0; j < OC; ++j) acc.o[j][t] = f32x4{0, 0, 0, 0};
+    for (int j = 0; j < D / 16; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float v = v_element<E4M3>(tile, j, i) * scale;
+        const bool finite = fabsf(v) < __builtin_inff();
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc.o[j][t][i] += finite || with[t] == 0.0f ? 0.0f : with[t] * v;
+      }
+      __builtin_amdgcn_sched_barrier(0);               // few registers: the loop hardly ever runs
     }
+  }
+}
 
-    // this wave's steps of the segment
-    const int steps_end = min((at + take) * kUnitSteps, (key_end + kStepKeys - 1) / kStepKeys);
-    int s0 = at * kUnitSteps, s1 = max(steps_end, s0);
-    if (SHARE) {
-      if (row0 >= n * a.G) s1 = s0;                    // a wave past the last row
+// Where a row's results go; `lead` lanes also store its maximum and sum, or its lse.
+template <int D, int RT>
+struct Results {
+  float inv[RT];
+  int64_t to[RT];                                      // element offset of the lane's d's, in out or part_o
+  bool there[RT];
+
+  __device__ __forceinline__ void begin(const TreeArgs &a, const Segment &s, int rows, int row0, int row16, int g,
+                                        const int *node, const float *top, const float *sum, float c2, bool lead) {
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int row = row0 + 16 * t + row16;
+      there[t] = node[t] < s.n;
+      inv[t] = !s.whole || sum[t] == 0.0f ? 0.0f : 1.0f / sum[t];
+      const int64_t line = s.whole ? int64_t(s.q0 + node[t]) * a.H * a.G + s.h * a.G + (row - node[t] * a.G)
+                                   : int64_t(s.slot) * rows + row - s.blk * rows;
+      to[t] = line * D + 4 * g;
+      if (there[t] && g == 0 && lead) {
+        if (!s.whole) {
+          a.part_ml[2 * line] = top[t];
+          a.part_ml[2 * line + 1] = sum[t];
+        } else if (a.lse) {
+          a.lse[line] = log_sum(top[t], sum[t], c2);
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ float log_sum(float top, float sum, float c2) {
+    return top == kNegInf ? kNegInf : (top * c2 + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
+  }
+  __device__ __forceinline__ void put(const TreeArgs &a, bool whole, int j, int t, f32x4 v) const {
+    if (whole) {
+      const uint2 o = {pack2(v[0] * inv[t], v[1] * inv[t]), pack2(v[2] * inv[t], v[3] * inv[t])};
+      *reinterpret_cast<uint2 *>(a.out + to[t] + 16 * j) = o;
     } else {
-      const int len = s1 - s0, base = s0;
-      s0 = base + len * wave / kWaves;
-      s1 = base + len * (wave + 1) / kWaves;
+      *reinterpret_cast<f32x4 *>(a.part_o + to[t] + 16 * j) = v;
     }
-    const int shift = a.block_shift;                   // tokens of a page, as a power of two
-    const int32_t *table = a.table + int64_t(r) * a.table_width;
-    int page_base = (s0 * kStepKeys) >> shift;
-    int page_ids = page_base + lane < a.table_width ? table[page_base + lane] : -1;
+  }
+};
 
-    // tile number 2 s + t: where it is, and how many of its keys there are
-    auto place = [&](int s, int t, int64_t &tile, int &lim) {
-      const int pos = s * kStepKeys + 16 * t;
-      int page = (pos >> shift) - page_base;
-      if (page >= 64) {                                // uniform
-        page_base += page;
-        page_ids = page_base + lane < a.table_width ? table[page_base + lane] : -1;
-        page = 0;
-      }
-      int id = __builtin_amdgcn_readlane(page_ids, page);
-      lim = min(max(key_end - pos, 0), 16);
-      if (lim == 0 || uint32_t(id) >= uint32_t(a.pages)) {
-        id = 0;
-        lim = 0;
-      }
-      // in tokens: the cache's element offset is this times D
-      tile = ((int64_t(id) * a.H + h) << shift) + (pos & ((1 << shift) - 1));
-    };
-    constexpr int ES = E4M3 ? 1 : 2;
+// ---------------------------------------------------------------------------
+// few rows: the waves of a workgroup take different keys
+template <int D, bool E4M3, int RT>
+struct Split {
+  static constexpr int rows = 16 * RT;
+  // workgroups a compute unit holds, by registers: where it is one, 512 of them a lane
+  static constexpr int occupancy = D * RT > 256 || D * (E4M3 ? 1 : 2) > 256 ? 1 : 2;
+  static constexpr int grid = 256 * occupancy;
+  // the four waves' sums are joined in rounds of at most 64 KB of LDS
+  static constexpr int rounds = RT * D > 256 ? RT * D / 256 : 1;
+  static constexpr int join_tiles = D / 16 / rounds;   // 16-d tiles joined in a round
+  static constexpr size_t lds = kWaves * join_tiles * RT * 1024 + kWaves * 2 * RT * 16 * 4;
+};
+
+template <int D, bool E4M3, int RT>
+__global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tree_split_kernel(const TreeArgs a) {
+  using S = Split<D, E4M3, RT>;
+  constexpr int ROWS = S::rows, QC = D / 32, OC = D / 16, JT = S::join_tiles, JW = JT / kWaves, W = S::grid;
+  constexpr int ES = E4M3 ? 1 : 2;
+  static_assert(JW * kWaves * S::rounds == OC, "rounds");
+  extern __shared__ __align__(16) char lds[];
+  f32x4 *join = reinterpret_cast<f32x4 *>(lds);        // [wave][JT][RT][64]
+  float *stat = reinterpret_cast<float *>(lds + kWaves * JT * RT * 1024);  // [wave][2][RT * 16]
+  int *pre = reinterpret_cast<int *>(stat + kWaves * 2 * RT * 16);
+  __shared__ int red[kWaves];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row16 = lane & 15, g = lane >> 4;
+  unit_prefix(a, ROWS, pre, red);
+  const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
+  const int w = renamed(blockIdx.x, W, total);
+  const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
+  const float c2 = a.scale * 1.44269504088896340736f;  // scores to powers of two
+  if (u_begin == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
+
+  for (int u = u_begin; u < u_end;) {
+    const Item it = locate(a, ROWS, pre, u);
+    if (u == u_begin && threadIdx.x == 0) reinterpret_cast<Border *>(a.borders)[w] = border_of(it, w, W, total);
+    const int take = min(__builtin_amdgcn_readfirstlane(it.units - it.at), u_end - u);
+    const Segment seg = segment_of(a, it, ROWS, take, 2 * w + (u == u_begin ? 0 : 1));
+    u += take;
+    const int row0 = seg.blk * ROWS;
+    Queries<D, E4M3, RT> qs;
+    qs.load(a, seg, row0, row16, g);
+    // keys that all rows see come first: below `clear` no mask is looked at
+    const int clear = seg.flat ? seg.ctx : seg.ctx + row0 / a.G + 1;
+    Rows<D, RT> acc;
+    acc.clear();
+
+    const int len = seg.s1 - seg.s0;                   // this wave's steps
+    const int s1 = seg.s0 + len * (wave + 1) / kWaves;
+    int s = seg.s0 + len * wave / kWaves;
+    Pages pages;
+    pages.begin(a, seg, s, lane);
     const int k_lane = 256 * g + 16 * (row16 & 7), v_lane = 256 * (g & 1) + 16 * row16;
     // one step, tokens at t0 and t1; the second form looks at masks, at keys that are not
     // there and at values that are not finite, the first knows that all rows see all keys
-    auto step = [&](int s, int64_t t0, int64_t t1, [[maybe_unused]] int lim0, [[maybe_unused]] int lim1,
-                    auto mask_tag) {
+    auto step = [&](int64_t t0, int64_t t1, [[maybe_unused]] int lim0, [[maybe_unused]] int lim1, auto mask_tag) {
       constexpr bool MASKED = decltype(mask_tag)::value;
       Tiles<D, E4M3> kt, vt;
-      // all loads are on their way before the first wait; where that takes too many
-      // registers, K's second half and V take the place of K's first
-      constexpr bool LATE_V = D * ES * RT > 512;
-      const char *k_at = a.k + (row16 < 8 ? t0 : t1) * (D * ES) + k_lane;
-      const char *v_at = a.v + (g < 2 ? t0 : t1) * (D * ES) + v_lane;
-      if constexpr (LATE_V)
-        kt.template load_k<0, D / 64>(k_at);
-      else
-        kt.load_k(k_at);
-      f32x4 ks[2], vs[2];                              // e4m3: the scales of the lane's tokens
-      if constexpr (E4M3) {
-        const int64_t at = (g < 2 ? t0 : t1) + 8 * (g & 1);
-        ks[0] = *reinterpret_cast<const f32x4 *>(a.k_scale + at);
-        ks[1] = *reinterpret_cast<const f32x4 *>(a.k_scale + at + 4);
-        vs[0] = *reinterpret_cast<const f32x4 *>(a.v_scale + at);
-        vs[1] = *reinterpret_cast<const f32x4 *>(a.v_scale + at + 4);
-      }
-      if constexpr (!LATE_V) vt.load_v(v_at);
+      Scales sl;
+      // all loads are on their way before the first wait
+      kt.load_k(a.k + (row16 < 8 ? t0 : t1) * (D * ES) + k_lane);
+      if constexpr (E4M3) sl.load(a, t0, t1, g);
+      vt.load_v(a.v + (g < 2 ? t0 : t1) * (D * ES) + v_lane);
       __builtin_amdgcn_sched_barrier(0);
       f32x4 sc[2][RT];
 #pragma unroll
       for (int t = 0; t < RT; ++t) sc[0][t] = sc[1][t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int j = 0; j < QC; ++j) {
-        if (LATE_V && j == QC / 2) {
-          __builtin_amdgcn_sched_barrier(0);
-          kt.template load_k<D / 64, D / 32>(k_at);
-        }
+      for (int j = 0; j < QC; ++j)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const bf16x8 ka = kt.k_operand(i, j);
 #pragma unroll
-          for (int t = 0; t < RT; ++t) sc[i][t] = mfma(ka, q[j][t], sc[i][t]);
+          for (int t = 0; t < RT; ++t) sc[i][t] = mfma(ka, qs.q[j][t], sc[i][t]);
         }
-      }
-      if constexpr (LATE_V) {
-        __builtin_amdgcn_sched_barrier(0);
-        vt.load_v(v_at);
-      }
       if constexpr (E4M3) {
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            sc[0][t][i] *= ks[0][i];
-            sc[1][t][i] *= ks[1][i];
-          }
+        for (int t = 0; t < RT; ++t) {
+          sc[0][t] *= sl.k[0];
+          sc[1][t] *= sl.k[1];
+        }
       }
-      [[maybe_unused]] const int pos = s * kStepKeys;
       [[maybe_unused]] uint32_t vis[RT];               // a bit for each of the lane's eight keys
       [[maybe_unused]] bool rare = false;
-      [[maybe_unused]] uint32_t zero[RT];              // as vis: its probability is 0
       if constexpr (MASKED) {
-        const int left = min(max((g < 2 ? lim0 : lim1) - 8 * (g & 1), 0), 8);
-        const uint32_t have = (1u << left) - 1u;
-        const int j0 = pos + 8 * g - ctx;              // the node of the lane's first key
+        const uint32_t have = present(lim0, lim1, g);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          if (flat) {
-            vis[t] = j0 <= -8 ? 255u : j0 < 0 ? uint32_t(sees[t] << -j0) | ((1u << -j0) - 1u)
-                                              : j0 < 64 ? uint32_t(sees[t] >> j0) : 0u;
-          } else {
-            vis[t] = (1u << min(max(node[t] - j0 + 1, 0), 8)) - 1u;
-          }
-          vis[t] &= have;
+          vis[t] = qs.visible(t, seg, s * kStepKeys + 8 * g) & have;
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             if (!(vis[t] >> i & 1)) sc[i >> 2][t][i & 3] = kNegInf;
         }
         vt.keep_keys(have);
         bool odd = vt.not_finite();
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {                // what the scales of absent tokens hold is not used
-            const float x = have >> i & 1 ? vs[i >> 2][i & 3] : 0.0f;
-            const bool bad = !(fabsf(x) < __builtin_inff());
-            odd |= bad;
-            vs[i >> 2][i & 3] = bad ? 0.0f : x;
-          }
-        }
+        if constexpr (E4M3) odd |= sl.keep_v(have);
         rare = __any(odd);
         if (rare) vt.drop_not_finite();
       }
-
       bf16x8 p[RT];
+      uint32_t zero[RT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        float top = fmaxf(fmaxf(fmaxf(sc[0][t][0], sc[0][t][1]), fmaxf(sc[0][t][2], sc[0][t][3])),
-                          fmaxf(fmaxf(sc[1][t][0], sc[1][t][1]), fmaxf(sc[1][t][2], sc[1][t][3])));
-        top = fmaxf(row_max(top), acc.m[t]);
-        if (__any(top > acc.m[t])) {
-          const float f = top > acc.m[t] ? __builtin_amdgcn_exp2f((acc.m[t] - top) * c2) : 1.0f;
-          acc.l[t] *= f;
-#pragma unroll
-          for (int j = 0; j < OC; ++j) acc.o[j][t] *= f;
-          acc.m[t] = top;
-        }
-        const float mc = top == kNegInf ? 0.0f : top * c2;
-        float e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[i >> 2][t][i & 3], c2, -mc));
-        acc.l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-        if constexpr (MASKED) {
-          zero[t] = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) zero[t] |= uint32_t(e[i] == 0.0f) << i;
-        }
-        if constexpr (E4M3) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] *= vs[i >> 2][i & 3];
-        }
-        p[t] = as_operand(pack2(e[0], e[1]), pack2(e[2], e[3]), pack2(e[4], e[5]), pack2(e[6], e[7]));
-      }
-
+      for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
 #pragma unroll
       for (int j = 0; j < OC; ++j) {
         const bf16x8 va = vt.v_operand(j);
 #pragma unroll
         for (int t = 0; t < RT; ++t) acc.o[j][t] = mfma(va, p[t], acc.o[j][t]);
       }
-      if constexpr (MASKED) {
-        // An infinity or NaN of a node that some rows do not see must not reach them
-        // through 0 * inf: the products above went without it, and it is added key by
-        // key where the row sees the key.
-        if (rare)
-          for (int kk = 0; kk < kStepKeys; ++kk) {
-            const int token = kk & 15;
-            if (token >= (kk < 16 ? lim0 : lim1)) continue;
-            const int64_t at = kk < 16 ? t0 : t1;
-            const char *tile = a.v + (at * D + kv_tile_v(token, 4 * g, ES)) * ES;
-            const float scale = E4M3 ? a.v_scale[at + token] : 1.0f;
-            const int from = row16 + 16 * (kk >> 3), e = kk & 7;
-            float with[RT];                            // NaN: 0 * inf; 0: not seen
-#pragma unroll
-            for (int t = 0; t < RT; ++t) {
-              const int on = __shfl(int(vis[t]), from, 64) >> e & 1, none = __shfl(int(zero[t]), from, 64) >> e & 1;
-              with[t] = !on ? 0.0f : none ? __builtin_nanf("") : 1.0f;
-            }
-#pragma unroll
-            for (int j = 0; j < OC; ++j) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float v = v_element<E4M3>(tile, j, i) * scale;
-                const bool finite = fabsf(v) < __builtin_inff();
-#pragma unroll
-                for (int t = 0; t < RT; ++t) acc.o[j][t][i] += finite || with[t] == 0.0f ? 0.0f : with[t] * v;
-              }
-              __builtin_amdgcn_sched_barrier(0);       // few registers: the loop hardly ever runs
-            }
-          }
-      }
+      if constexpr (MASKED)
+        if (rare) add_not_finite<D, E4M3, RT>(a, t0, t1, lim0, lim1, vis, zero, row16, g, acc);
     };
     // the keys that every row sees; from the first page that is not one, or the first node
     // on, the careful form
-    int s = s0;
     int64_t t0, t1;
     int lim0, lim1;
     for (; s < s1; ++s) {
-      place(s, 0, t0, lim0);
-      place(s, 1, t1, lim1);
+      pages.place(a, seg, s, 0, lane, t0, lim0);
+      pages.place(a, seg, s, 1, lane, t1, lim1);
       if (s * kStepKeys + kStepKeys > clear || lim0 + lim1 < 32) break;
-      step(s, t0, t1, 16, 16, std::false_type());
+      step(t0, t1, 16, 16, std::false_type());
     }
     for (; s < s1; ++s) {
-      place(s, 0, t0, lim0);
-      place(s, 1, t1, lim1);
-      step(s, t0, t1, lim0, lim1, std::true_type());
+      pages.place(a, seg, s, 0, lane, t0, lim0);
+      pages.place(a, seg, s, 1, lane, t1, lim1);
+      step(t0, t1, lim0, lim1, std::true_type());
     }
 
-    // ---- the segment's results
-#pragma unroll
-    for (int t = 0; t < RT; ++t) acc.l[t] = row_sum(acc.l[t]);
-    float top[RT], total_l[RT];
-    if constexpr (SHARE) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        top[t] = acc.m[t];
-        total_l[t] = acc.l[t];
-      }
-    } else {
-      __syncthreads();                                 // the last segment's readers are done
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-        if (g == 0) {
-          stat[(wave * 2 + 0) * RT * 16 + 16 * t + row16] = acc.m[t];
-          stat[(wave * 2 + 1) * RT * 16 + 16 * t + row16] = acc.l[t];
-        }
-      __syncthreads();
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        float mw[kWaves];
-        top[t] = kNegInf;
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
-          mw[v] = stat[(v * 2 + 0) * RT * 16 + 16 * t + row16];
-          top[t] = fmaxf(top[t], mw[v]);
-        }
-        total_l[t] = 0.0f;
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
-          const float f = mw[v] == top[t] ? 1.0f : __builtin_amdgcn_exp2f((mw[v] - top[t]) * c2);
-          total_l[t] += f * stat[(v * 2 + 1) * RT * 16 + 16 * t + row16];
-        }
-        const float f = acc.m[t] == top[t] ? 1.0f : __builtin_amdgcn_exp2f((acc.m[t] - top[t]) * c2);
-#pragma unroll
-        for (int j = 0; j < OC; ++j) acc.o[j][t] *= f;
-      }
-    }
-
-    // where the lane's values go: four d's of row n in each 16-d tile
-    float inv[RT];
-    int64_t to[RT];                                    // element offset of the row, in out or part_o
-    bool there[RT];
+    // ---- the four waves' sums
+    __syncthreads();                                   // the last segment's readers are done
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      const int row = row0 + 16 * t + row16;
-      there[t] = node[t] < n;
-      inv[t] = !whole || total_l[t] == 0.0f ? 0.0f : 1.0f / total_l[t];
-      const int64_t line = whole ? int64_t(q0 + node[t]) * a.H * a.G + h * a.G + (row - node[t] * a.G)
-                                 : int64_t(slot) * ROWS + row - blk * ROWS;
-      to[t] = line * D + 4 * g;
-      if (there[t] && g == 0 && (SHARE || wave == 0)) {
-        if (!whole) {
-          a.part_ml[2 * line] = top[t];
-          a.part_ml[2 * line + 1] = total_l[t];
-        } else if (a.lse) {
-          a.lse[line] = top[t] == kNegInf
-                            ? kNegInf
-                            : (top[t] * c2 + __builtin_amdgcn_logf(total_l[t])) * 0.693147180559945309f;
-        }
+      acc.l[t] = row_sum(acc.l[t]);
+      if (g == 0) {
+        stat[(wave * 2 + 0) * RT * 16 + 16 * t + row16] = acc.m[t];
+        stat[(wave * 2 + 1) * RT * 16 + 16 * t + row16] = acc.l[t];
       }
     }
-    auto put = [&](int j, int t, f32x4 v) {
-      if (whole) {
-        const uint2 o = {pack2(v[0] * inv[t], v[1] * inv[t]), pack2(v[2] * inv[t], v[3] * inv[t])};
-        *reinterpret_cast<uint2 *>(a.out + to[t] + 16 * j) = o;
-      } else {
-        *reinterpret_cast<f32x4 *>(a.part_o + to[t] + 16 * j) = v;
+    __syncthreads();
+    float top[RT], sum[RT];
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      float mw[kWaves];
+      top[t] = kNegInf;
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) {
+        mw[v] = stat[(v * 2 + 0) * RT * 16 + 16 * t + row16];
+        top[t] = fmaxf(top[t], mw[v]);
       }
-    };
-    if constexpr (SHARE) {
+      sum[t] = 0.0f;
 #pragma unroll
-      for (int t = 0; t < RT; ++t)
-        if (there[t]) {
-          if (whole) {
+      for (int v = 0; v < kWaves; ++v) {
+        const float f = mw[v] == top[t] ? 1.0f : __builtin_amdgcn_exp2f((mw[v] - top[t]) * c2);
+        sum[t] += f * stat[(v * 2 + 1) * RT * 16 + 16 * t + row16];
+      }
+      const float f = acc.m[t] == top[t] ? 1.0f : __builtin_amdgcn_exp2f((acc.m[t] - top[t]) * c2);
 #pragma unroll
-            for (int j = 0; j < OC; ++j) put(j, t, acc.o[j][t]);
-          } else {
+      for (int j = 0; j < OC; ++j) acc.o[j][t] *= f;
+    }
+    Results<D, RT> res;
+    res.begin(a, seg, ROWS, row0, row16, g, qs.node, top, sum, c2, wave == 0);
 #pragma unroll
-            for (int j = 0; j < OC; ++j) put(j, t, acc.o[j][t]);
-          }
+    for (int round = 0; round < S::rounds; ++round) {
+      if (round) __syncthreads();
+#pragma unroll
+      for (int j = 0; j < JT; ++j)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) join[((wave * JT + j) * RT + t) * 64 + lane] = acc.o[round * JT + j][t];
+      __syncthreads();
+#pragma unroll
+      for (int jj = 0; jj < JW; ++jj)
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const int j = wave * JW + jj;
+          f32x4 v = join[(j * RT + t) * 64 + lane];
+#pragma unroll
+          for (int x = 1; x < kWaves; ++x) v += join[((x * JT + j) * RT + t) * 64 + lane];
+          if (res.there[t]) res.put(a, seg.whole, round * JT + j, t, v);
         }
-    } else {
-#pragma unroll
-      for (int round = 0; round < ROUNDS; ++round) {
-        if (round) __syncthreads();
-#pragma unroll
-        for (int j = 0; j < JT; ++j)
-#pragma unroll
-          for (int t = 0; t < RT; ++t) join[((wave * JT + j) * RT + t) * 64 + lane] = acc.o[round * JT + j][t];
-        __syncthreads();
-#pragma unroll
-        for (int jj = 0; jj < JW; ++jj)
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const int j = wave * JW + jj;
-            f32x4 v = join[(j * RT + t) * 64 + lane];
-#pragma unroll
-            for (int x = 1; x < kWaves; ++x) v += join[((x * JT + j) * RT + t) * 64 + lane];
-            if (there[t]) put(round * JT + j, t, v);
-          }
-      }
     }
   }
 }
 
-// Adds the partial sums of items that several workgroups share.  Workgroup w looks at
-// the first unit of main workgroup w: it is the owner of the item if that is the first
-// such border inside it.  blockIdx.y takes every gridDim.y-th row.
-__global__ __launch_bounds__(kThreads) void tree_combine_kernel(const TreeArgs a, int rows, int D, int grid_log) {
+// ---------------------------------------------------------------------------
+// many rows: the waves of a workgroup take different rows and share the keys through LDS
+template <int D, bool E4M3, int RT>
+struct Share {
+  static constexpr int rows = 16 * RT * kWaves;
+  static constexpr int occupancy = 2;
+  static constexpr int grid = 256 * occupancy;
+  static constexpr int half = kStepKeys * D * 2;       // bytes of K, or of V, of a step (2-byte elements)
+  static constexpr size_t lds = 2 * 2 * half;          // two steps of both
+};
+
+// An LDS step holds the tiles as a 2-byte cache does: K, then V, each [tile][16 * D].
+template <int D, bool E4M3>
+struct Stage {
+  static constexpr int units = E4M3 ? D / 64 : D / 32; // 1 KB pieces of a tile in the cache
+  static constexpr int mine = 4 * units / kWaves;      // pieces a wave brings: of two tiles of K and of V
+  u32x4 r[E4M3 ? mine : 1];
+
+  // begins to bring a step; 2-byte elements go straight to LDS
+  __device__ __forceinline__ void begin(const TreeArgs &a, int64_t t0, int64_t t1, char *buf, int wave, int lane) {
+    constexpr int ES = E4M3 ? 1 : 2;
+#pragma unroll
+    for (int i = 0; i < mine; ++i) {
+      const int p = wave * mine + i, of = p / units, c = p % units;  // of: K0, K1, V0, V1
+      const char *src = (of < 2 ? a.k : a.v) + (of & 1 ? t1 : t0) * (D * ES) + 1024 * c + 16 * lane;
+      if constexpr (E4M3) {
+        r[i] = *reinterpret_cast<const u32x4 *>(src);
+      } else {
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void *)src,
+            (__attribute__((address_space(3))) void *)(buf + 1024 * p), 16, 0, 0);
+      }
+    }
+  }
+  // e4m3: the pieces, as bf16, to LDS
+  __device__ __forceinline__ void finish(char *buf, int wave, int lane) {
+    if constexpr (E4M3) {
+#pragma unroll
+      for (int i = 0; i < mine; ++i) {
+        const int p = wave * mine + i, of = p / units, c = p % units;
+        const u32x4 x = r[i];
+        const u32x4 lo = {e4m3_lo(x[0]), e4m3_hi(x[0]), e4m3_lo(x[1]), e4m3_hi(x[1])};
+        const u32x4 hi = {e4m3_lo(x[2]), e4m3_hi(x[2]), e4m3_lo(x[3]), e4m3_hi(x[3])};
+        // K: 16 d's of a token are halves of two 32-d pieces; V: 8 tokens of two 16-d tiles,
+        // of which a piece has four
+        char *dst = buf + of * (32 * D) + 2048 * c + (of < 2 ? 16 * lane : 1024 * (lane >> 5) + 16 * (lane & 31));
+        *reinterpret_cast<u32x4 *>(dst) = lo;
+        *reinterpret_cast<u32x4 *>(dst + (of < 2 ? 1024 : 512)) = hi;
+      }
+    }
+  }
+};
+
+template <int D, bool E4M3, int RT>
+__global__ __launch_bounds__(kThreads, (Share<D, E4M3, RT>::occupancy)) void tree_share_kernel(const TreeArgs a) {
+  using S = Share<D, E4M3, RT>;
+  constexpr int ROWS = S::rows, QC = D / 32, OC = D / 16, W = S::grid;
   extern __shared__ __align__(16) char lds[];
-  int *pre = reinterpret_cast<int *>(lds);
+  int *pre = reinterpret_cast<int *>(lds + S::lds);
   __shared__ int red[kWaves];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int row16 = lane & 15, g = lane >> 4;
+  unit_prefix(a, ROWS, pre, red);
+  const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
+  const int w = renamed(blockIdx.x, W, total);
+  const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
+  const float c2 = a.scale * 1.44269504088896340736f;
+  if (u_begin == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
+  // operands in a step: K of 32 d's number j, tokens of product i; V of 16 d's number j
+  const int k_lane = (row16 >> 3) * (32 * D) + 256 * g + 16 * (row16 & 7);
+  const int v_lane = 2 * (32 * D) + (g >> 1) * (32 * D) + 256 * (g & 1) + 16 * row16;
+
+  for (int u = u_begin; u < u_end;) {
+    const Item it = locate(a, ROWS, pre, u);
+    if (u == u_begin && threadIdx.x == 0) reinterpret_cast<Border *>(a.borders)[w] = border_of(it, w, W, total);
+    const int take = min(__builtin_amdgcn_readfirstlane(it.units - it.at), u_end - u);
+    const Segment seg = segment_of(a, it, ROWS, take, 2 * w + (u == u_begin ? 0 : 1));
+    u += take;
+    const int row0 = seg.blk * ROWS + wave * 16 * RT;
+    const bool idle = row0 >= seg.n * a.G;             // a wave past the last row only helps to stage
+    Queries<D, E4M3, RT> qs;
+    qs.load(a, seg, row0, row16, g);
+    const int clear = seg.flat ? seg.ctx : seg.ctx + row0 / a.G + 1;
+    Rows<D, RT> acc;
+    acc.clear();
+    Pages pages;
+    pages.begin(a, seg, seg.s0, lane);
+    Stage<D, E4M3> stage;
+    Scales sl, sl_next;
+    int64_t t0 = 0, t1 = 0, n0 = 0, n1 = 0;
+    int lim0 = 0, lim1 = 0, nl0 = 0, nl1 = 0;
+    __syncthreads();                                   // the last segment's readers are done
+    if (seg.s0 < seg.s1) {
+      pages.place(a, seg, seg.s0, 0, lane, n0, nl0);
+      pages.place(a, seg, seg.s0, 1, lane, n1, nl1);
+      char *buf = lds + (seg.s0 & 1) * (2 * S::half);
+      stage.begin(a, n0, n1, buf, wave, lane);
+      if constexpr (E4M3) sl_next.load(a, n0, n1, g);
+      stage.finish(buf, wave, lane);
+    }
+    auto step = [&](int s, const char *buf, auto mask_tag) {
+      constexpr bool MASKED = decltype(mask_tag)::value;
+      f32x4 sc[2][RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) sc[0][t] = sc[1][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < QC; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const bf16x8 ka = *reinterpret_cast<const bf16x8 *>(buf + k_lane + 1024 * j + 128 * i);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) sc[i][t] = mfma(ka, qs.q[j][t], sc[i][t]);
+        }
+      if constexpr (E4M3) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          sc[0][t] *= sl.k[0];
+          sc[1][t] *= sl.k[1];
+        }
+      }
+      [[maybe_unused]] uint32_t vis[RT], keep[4], odd = 0;
+      if constexpr (MASKED) {
+        const uint32_t have = present(lim0, lim1, g);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          vis[t] = qs.visible(t, seg, s * kStepKeys + 8 * g) & have;
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (!(vis[t] >> i & 1)) sc[i >> 2][t][i & 3] = kNegInf;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          keep[e] = (have >> (2 * e) & 1 ? 0xFFFFu : 0u) | (have >> (2 * e + 1) & 1 ? 0xFFFF0000u : 0u);
+        if constexpr (E4M3) odd = sl.keep_v(have);
+      }
+      bf16x8 p[RT];
+      uint32_t zero[RT];
+#pragma unroll
+      for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
+#pragma unroll
+      for (int j = 0; j < OC; ++j) {
+        bf16x8 va = *reinterpret_cast<const bf16x8 *>(buf + v_lane + 512 * j);
+        if constexpr (MASKED) va = clean(va, keep, odd);
+#pragma unroll
+        for (int t = 0; t < RT; ++t) acc.o[j][t] = mfma(va, p[t], acc.o[j][t]);
+      }
+      if constexpr (MASKED)
+        if (__any(odd != 0)) add_not_finite<D, E4M3, RT>(a, t0, t1, lim0, lim1, vis, zero, row16, g, acc);
+    };
+    // one step: the staged one is published, the next one begun, then the products
+    auto turn = [&](int s, auto mask_tag) {
+      char *buf = lds + (s & 1) * (2 * S::half), *other = lds + (~s & 1) * (2 * S::half);
+      if (s + 1 < seg.s1) {
+        stage.begin(a, n0, n1, other, wave, lane);
+        if constexpr (E4M3) sl_next.load(a, n0, n1, g);
+      }
+      if (!idle) step(s, buf, mask_tag);
+      if (s + 1 < seg.s1) stage.finish(other, wave, lane);
+    };
+    auto publish = [&](int s) {
+      // the wave's own pieces have arrived, and every wave is past its reads of the other buffer
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      t0 = n0;
+      t1 = n1;
+      lim0 = nl0;
+      lim1 = nl1;
+      if constexpr (E4M3) sl = sl_next;
+      if (s + 1 < seg.s1) {
+        pages.place(a, seg, s + 1, 0, lane, n0, nl0);
+        pages.place(a, seg, s + 1, 1, lane, n1, nl1);
+      }
+    };
+    int s = seg.s0;
+    bool open = false;                                 // step s is published
+    for (; s < seg.s1; ++s) {
+      publish(s);
+      open = true;
+      if (s * kStepKeys + kStepKeys > clear || lim0 + lim1 < 32) break;
+      turn(s, std::false_type());
+      open = false;
+    }
+    for (; s < seg.s1; ++s) {
+      if (!open) publish(s);
+      open = false;
+      turn(s, std::true_type());
+    }
+
+#pragma unroll
+    for (int t = 0; t < RT; ++t) acc.l[t] = row_sum(acc.l[t]);
+    Results<D, RT> res;
+    res.begin(a, seg, ROWS, row0, row16, g, qs.node, acc.m, acc.l, c2, true);
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      if (res.there[t]) {
+        if (seg.whole) {
+#pragma unroll
+          for (int j = 0; j < OC; ++j) res.put(a, true, j, t, acc.o[j][t]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < OC; ++j) res.put(a, false, j, t, acc.o[j][t]);
+        }
+      }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Adds the partial sums of an item that several workgroups share; workgroup w has the
+// item whose first border inside it is the beginning of main workgroup w, if there is
+// one.  Four parts at a time are on their way; blockIdx.y takes every gridDim.y-th row.
+__global__ __launch_bounds__(kThreads) void tree_combine_kernel(const TreeArgs a, int rows, int D) {
   const int w = blockIdx.x;
-  unit_prefix(a, rows, pre, red);
-  const int total = pre[a.R], s = first_unit(w, total, grid_log);
-  if (s == 0 || s >= total || s == first_unit(w + 1, total, grid_log)) return;
-  int w0 = w - 1;                                      // the workgroup before that has any units
-  while (first_unit(w0, total, grid_log) == s) --w0;
-  const Item it = locate(a, rows, pre, s);
-  const int u0 = int(it.first), u1 = u0 + it.units;
-  if (s == u0 || first_unit(w0, total, grid_log) > u0) return;
-  // parts: the end of workgroup w0, and the beginnings of w, w + 1, ... inside the item
-  const int slot0 = 2 * w0 + (first_unit(w0, total, grid_log) == u0 ? 0 : 1);
+  const Border d = reinterpret_cast<const Border *>(a.borders)[w];
+  if (d.parts == 0) return;
   const float c2 = a.scale * 1.44269504088896340736f;
   const int threads_a_row = D / 4, lane = threadIdx.x % threads_a_row;
   const int per_pass = kThreads / threads_a_row;
-  const int q0 = max(a.q_start[it.r], 0);
+  const int q0 = max(a.q_start[d.r], 0);
   for (int row = blockIdx.y * per_pass + threadIdx.x / threads_a_row; row < rows; row += gridDim.y * per_pass) {
-    const int64_t all = int64_t(it.b) * rows + row;
+    const int64_t all = int64_t(d.b) * rows + row;
     const int node = int(all / a.G);
-    if (node >= it.n) continue;
-    float top = a.part_ml[(int64_t(slot0) * rows + row) * 2];
-    for (int x = w; x < int(gridDim.x) && first_unit(x, total, grid_log) < u1; ++x)
-      if (first_unit(x, total, grid_log) < first_unit(x + 1, total, grid_log))
-        top = fmaxf(top, a.part_ml[(int64_t(2 * x) * rows + row) * 2]);
+    if (node >= d.n) break;
+    float m = kNegInf, l = 0.0f;
     f32x4 o = {0, 0, 0, 0};
-    float l = 0.0f;
-    auto add = [&](int64_t slot) {
-      const float m = a.part_ml[(slot * rows + row) * 2];
-      const float f = m == top ? 1.0f : __builtin_amdgcn_exp2f((m - top) * c2);
-      l += f * a.part_ml[(slot * rows + row) * 2 + 1];
-      o += f * *reinterpret_cast<const f32x4 *>(a.part_o + (slot * rows + row) * D + 4 * lane);
-    };
-    add(slot0);
-    for (int x = w; x < int(gridDim.x) && first_unit(x, total, grid_log) < u1; ++x)
-      if (first_unit(x, total, grid_log) < first_unit(x + 1, total, grid_log)) add(2 * x);
+    for (int p = 0; p < d.parts; p += 4) {
+      float2 ml[4];
+      f32x4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int part = min(p + i, d.parts - 1);
+        const int64_t line = int64_t(part == 0 ? d.slot0 : 2 * (w + part - 1)) * rows + row;
+        ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * line);
+        v[i] = *reinterpret_cast<const f32x4 *>(a.part_o + line * D + 4 * lane);
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, ml[i].x);
+      const float keep = m == top ? 1.0f : __builtin_amdgcn_exp2f((m - top) * c2);
+      l *= keep;
+      o *= keep;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = p + i >= d.parts ? 0.0f : ml[i].x == top ? 1.0f : __builtin_amdgcn_exp2f((ml[i].x - top) * c2);
+        if (p + i < d.parts) {
+          l += f * ml[i].y;
+          o += f * v[i];
+        }
+      }
+      m = top;
+    }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t at = int64_t(q0 + node) * a.H * a.G + it.h * a.G + (all - int64_t(node) * a.G);
-    const uint2 v = {pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv)};
-    *reinterpret_cast<uint2 *>(a.out + at * D + 4 * lane) = v;
-    if (a.lse && lane == 0)
-      a.lse[at] = top == kNegInf ? kNegInf : (top * c2 + __builtin_amdgcn_logf(l)) * 0.693147180559945309f;
+    const int64_t at = int64_t(q0 + node) * a.H * a.G + d.h * a.G + (all - int64_t(node) * a.G);
+    const uint2 x = {pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv)};
+    *reinterpret_cast<uint2 *>(a.out + at * D + 4 * lane) = x;
+    if (a.lse && lane == 0) a.lse[at] = Results<64, 1>::log_sum(m, l, c2);
   }
 }
 
-template <int D, bool E4M3, int RT, bool SHARE>
-hipError_t launch(const TreeArgs &a, const char *name, hipStream_t stream) {
-  constexpr int ROWS = Variant<D, E4M3, RT, SHARE>::rows;
-  constexpr int ROUNDS = RT * D > 256 ? RT * D / 256 : 1;
-  constexpr size_t join = SHARE ? 0 : kWaves * (D / 16 / ROUNDS) * RT * 1024 + kWaves * 2 * RT * 16 * 4;
-  const size_t prefix = size_t(a.R + 1) * 4;
+void combine(const TreeArgs &a, int grid, int rows, int D, hipStream_t stream) {
+  hipLaunchKernelGGL(tree_combine_kernel, dim3(grid, 4), dim3(kThreads), 0, stream, a, rows, D);
+}
+
+template <int D, bool E4M3, int RT>
+hipError_t launch_split(const TreeArgs &a, const char *name, hipStream_t stream) {
+  using S = Split<D, E4M3, RT>;
   (void)hipGetLastError();
-  constexpr int LOG = Variant<D, E4M3, RT, SHARE>::grid_log;
-  hipLaunchKernelGGL((tree_attention_kernel<D, E4M3, RT, SHARE>), dim3(1 << LOG), dim3(kThreads), join + prefix, stream, a);
-  hipLaunchKernelGGL(tree_combine_kernel, dim3(1 << LOG, 4), dim3(kThreads), prefix, stream, a, ROWS, D, LOG);
+  hipLaunchKernelGGL((tree_split_kernel<D, E4M3, RT>), dim3(S::grid), dim3(kThreads), S::lds + size_t(a.R + 1) * 4,
+                     stream, a);
+  combine(a, S::grid, S::rows, D, stream);
+  set_last_kernel(name);
+  return hipGetLastError();
+}
+
+template <int D, bool E4M3, int RT>
+hipError_t launch_share(const TreeArgs &a, const char *name, hipStream_t stream) {
+  using S = Share<D, E4M3, RT>;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL((tree_share_kernel<D, E4M3, RT>), dim3(S::grid), dim3(kThreads), S::lds + size_t(a.R + 1) * 4,
+                     stream, a);
+  combine(a, S::grid, S::rows, D, stream);
   set_last_kernel(name);
   return hipGetLastError();
 }
 
 // Rows of one cache head in the step's longest request decide the form: up to 32 rows
 // every row sits in each wave and the waves split the keys; above, they share the keys.
-// 2-byte elements of 256-wide heads leave registers for 16 rows a wave.
+// 2-byte elements of 256-wide heads leave the split form registers for 16 rows a wave.
 struct Form {
   bool share;
   int tiles;  // of 16 rows a wave
 };
 Form tree_form(int64_t rows, int64_t D, bool e4m3) {
-  const int most = D == 256 && !e4m3 ? 1 : 2;
-  return {rows > 32, rows <= 16 ? 1 : most};
+  if (rows > 32) return {true, rows <= 64 || D == 256 ? 1 : 2};
+  return {false, rows <= 16 || (D == 256 && !e4m3) ? 1 : 2};
 }
 int form_rows(Form f) { return 16 * f.tiles * (f.share ? kWaves : 1); }
 
 template <int D, bool E4M3>
 hipError_t pick(const TreeArgs &a, Form f, hipStream_t stream) {
-  if (!f.share && f.tiles == 1)
-    return launch<D, E4M3, 1, false>(a, E4M3 ? "tree_attention_e4m3_split16" : "tree_attention_bf16_split16", stream);
-  if constexpr (D == 256 && !E4M3) {
-    return launch<D, E4M3, 1, true>(a, "tree_attention_bf16_share64", stream);
-  } else {
-    if (f.share)
-      return launch<D, E4M3, 2, true>(a, E4M3 ? "tree_attention_e4m3_share128" : "tree_attention_bf16_share128", stream);
-    return launch<D, E4M3, 2, false>(a, E4M3 ? "tree_attention_e4m3_split32" : "tree_attention_bf16_split32", stream);
+  if (f.share) {
+    if constexpr (D != 256) {
+      if (f.tiles == 2)
+        return launch_share<D, E4M3, 2>(a, E4M3 ? "tree_attention_e4m3_share128" : "tree_attention_bf16_share128", stream);
+    }
+    return launch_share<D, E4M3, 1>(a, E4M3 ? "tree_attention_e4m3_share64" : "tree_attention_bf16_share64", stream);
   }
+  if constexpr (D != 256 || E4M3) {
+    if (f.tiles == 2)
+      return launch_split<D, E4M3, 2>(a, E4M3 ? "tree_attention_e4m3_split32" : "tree_attention_bf16_split32", stream);
+  }
+  return launch_split<D, E4M3, 1>(a, E4M3 ? "tree_attention_e4m3_split16" : "tree_attention_bf16_split16", stream);
 }
 
 }  // namespace
 
+// partial sums of two segments a workgroup, then their maxima and sums, then the borders
 size_t tree_workspace_bytes(int64_t max_nodes, int64_t group, int64_t D, bool e4m3) {
-  return size_t(2 * kMaxGrid) * form_rows(tree_form(max_nodes * group, D, e4m3)) * (D + 2) * 4;
+  return size_t(2 * kMaxGrid) * form_rows(tree_form(max_nodes * group, D, e4m3)) * (D + 2) * 4 + kMaxGrid * sizeof(Border);
 }
 
 hipError_t launch_tree_attention(TreeArgs a, int64_t D, bool e4m3, int64_t max_nodes, void *workspace,
@@ -820,6 +1108,7 @@ hipError_t launch_tree_attention(TreeArgs a, int64_t D, bool e4m3, int64_t max_n
   const Form f = tree_form(max_nodes * a.G, D, e4m3);
   a.part_o = static_cast<float *>(workspace);
   a.part_ml = a.part_o + int64_t(2 * kMaxGrid) * form_rows(f) * D;
+  a.borders = reinterpret_cast<int32_t *>(a.part_ml + int64_t(2 * kMaxGrid) * form_rows(f) * 2);
   if (e4m3) return D == 64 ? pick<64, true>(a, f, stream) : D == 128 ? pick<128, true>(a, f, stream) : pick<256, true>(a, f, stream);
   return D == 64 ? pick<64, false>(a, f, stream) : D == 128 ? pick<128, false>(a, f, stream) : pick<256, false>(a, f, stream);
 }

@@ -113,6 +113,7 @@ struct TreeArgs {
   uint16_t *out;             // bf16 [T, H * G, D]
   float *lse;                // f32 [T, H * G] or NULL
   float *part_o, *part_ml;   // workspace: partial sums, and their maximum and sum
+  int32_t *borders;          // workspace: the items that workgroups share
   int64_t ldq;
   int T, R, H, G;            // tokens, requests, cache heads, query heads of each
   int pages, block_shift, table_width;
