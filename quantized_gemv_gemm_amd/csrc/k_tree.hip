@@ -79,10 +79,11 @@ __device__ __forceinline__ int block_units(int n, int kv, int b, int G, int rows
   return max((block_keys(n, kv, b, G, rows) + kUnitKeys - 1) / kUnitKeys, 1);
 }
 
-// pre[r] = units of the requests before r (R + 1 entries), by the whole workgroup.
+// pre[r] = units of the requests before r (R + 1 entries), by a whole workgroup of NT threads.
+template <int NT>
 __device__ __forceinline__ void unit_prefix(const TreeArgs &a, int rows, int *pre, int *red) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (a.R + kThreads - 1) / kThreads, r0 = tid * per;
+  const int per = (a.R + NT - 1) / NT, r0 = tid * per;
   int sum = 0;
   for (int j = 0; j < per; ++j) {  // the same count in every lane: the loop below needs them all
     const int r = r0 + j;
@@ -412,34 +413,46 @@ struct Queries {
   }
 };
 
-// The pages of a segment: 64 page numbers at a time in a register's lanes.
+// The tiles of a segment from a step on, in order: page numbers are held 64 at a time in a
+// register's lanes, and looked at where a page begins.
 struct Pages {
   const int32_t *table;
-  int base, ids;
+  int ids, base;       // page numbers base .. base + 63
+  int pos;             // of the next tile
+  int64_t tile;        // the last tile's first token in the cache; its elements are at D times this
+  bool good;           // its page is one
 
-  __device__ __forceinline__ void begin(const TreeArgs &a, const Segment &s, int step, int lane) {
-    table = a.table + int64_t(s.r) * a.table_width;
-    base = (step * kStepKeys) >> a.block_shift;
+  __device__ __forceinline__ void fetch(const TreeArgs &a, int lane) {
     ids = base + lane < a.table_width ? table[base + lane] : -1;
+    asm volatile("" : "+v"(ids));                      // waited for here, not at every use
   }
-  // tile t of a step: its first token in the cache (in tokens; its elements are at D times
-  // this), and how many of its keys there are.  Steps come in rising order.
-  __device__ __forceinline__ void place(const TreeArgs &a, const Segment &s, int step, int t, int lane, int64_t &tile,
-                                        int &lim) {
-    const int pos = step * kStepKeys + 16 * t;
+  __device__ __forceinline__ void enter(const TreeArgs &a, const Segment &s, int lane) {
     int page = (pos >> a.block_shift) - base;
     if (page >= 64) {                                  // uniform
       base += page;
-      ids = base + lane < a.table_width ? table[base + lane] : -1;
+      fetch(a, lane);
       page = 0;
     }
-    int id = __builtin_amdgcn_readlane(ids, page);
-    lim = min(max(s.key_end - pos, 0), 16);
-    if (lim == 0 || uint32_t(id) >= uint32_t(a.pages)) {
-      id = 0;
-      lim = 0;
-    }
-    tile = ((int64_t(id) * a.H + s.h) << a.block_shift) + (pos & ((1 << a.block_shift) - 1));
+    const int id = __builtin_amdgcn_readlane(ids, page);
+    good = uint32_t(id) < uint32_t(a.pages);
+    tile = (((good ? int64_t(id) : 0) * a.H + s.h) << a.block_shift) + (pos & ((1 << a.block_shift) - 1)) - 16;
+  }
+  __device__ __forceinline__ void begin(const TreeArgs &a, const Segment &s, int step, int lane) {
+    table = a.table + int64_t(s.r) * a.table_width;
+    pos = step * kStepKeys;
+    base = pos >> a.block_shift;
+    fetch(a, lane);
+    enter(a, s, lane);
+  }
+  // the next tile, and how many of its keys there are (where there are none it is some
+  // tile of the cache all the same)
+  __device__ __forceinline__ int64_t next(const TreeArgs &a, const Segment &s, int lane, int &lim) {
+    if (pos < s.key_end && (pos & ((1 << a.block_shift) - 1)) == 0) enter(a, s, lane);
+    const int left = min(s.key_end - pos, 16);
+    pos += 16;
+    if (left > 0) tile += 16;
+    lim = good && left > 0 ? left : 0;
+    return left > 0 ? tile : s.h << a.block_shift;     // of page 0
   }
 };
 
@@ -487,14 +500,14 @@ __device__ __forceinline__ bf16x8 clean(bf16x8 x, const uint32_t *keep, uint32_t
   return __builtin_bit_cast(bf16x8, w);
 }
 
-// Scores of one row tile to weights: raises the running maximum (rescaling the sums
-// where it grew), adds to the running sum, and gives the B operand of the second product.
-// zero: a bit for each key whose weight is 0.
-template <int D, bool E4M3, int RT, bool MASKED>
-__device__ __forceinline__ bf16x8 weigh(const f32x4 &s0, const f32x4 &s1, const f32x4 *vs, float c2, int t,
-                                        Rows<D, RT> &acc, uint32_t &zero) {
-  float top = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])), fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
-  top = fmaxf(row_max(top), acc.m[t]);
+// The running maximum of one row tile with new scores: the new maximum, not yet taken over.
+__device__ __forceinline__ float row_top(const f32x4 &s0, const f32x4 &s1, float before) {
+  const float top = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])), fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
+  return fmaxf(row_max(top), before);
+}
+// Takes a new maximum over, rescaling the sums where it grew.
+template <int D, int RT>
+__device__ __forceinline__ void take_top(float top, float c2, int t, Rows<D, RT> &acc) {
   if (__any(top > acc.m[t])) {
     const float f = top > acc.m[t] ? __builtin_amdgcn_exp2f((acc.m[t] - top) * c2) : 1.0f;
     acc.l[t] *= f;
@@ -502,7 +515,13 @@ __device__ __forceinline__ bf16x8 weigh(const f32x4 &s0, const f32x4 &s1, const 
     for (int j = 0; j < D / 16; ++j) acc.o[j][t] *= f;
     acc.m[t] = top;
   }
-  const float mc = top == kNegInf ? 0.0f : top * c2;
+}
+// Scores of one row tile to weights under the running maximum: adds to the running sum, and
+// gives the B operand of the second product.  zero: a bit for each key whose weight is 0.
+template <int D, bool E4M3, int RT, bool MASKED>
+__device__ __forceinline__ bf16x8 weigh(const f32x4 &s0, const f32x4 &s1, const f32x4 *vs, float c2, int t,
+                                        Rows<D, RT> &acc, uint32_t &zero) {
+  const float mc = acc.m[t] == kNegInf ? 0.0f : acc.m[t] * c2;
   float e[8];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -625,7 +644,7 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row16 = lane & 15, g = lane >> 4;
-  unit_prefix(a, ROWS, pre, red);
+  unit_prefix<kThreads>(a, ROWS, pre, red);
   const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
   const int w = renamed(blockIdx.x, W, total);
   const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
@@ -701,7 +720,10 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
       bf16x8 p[RT];
       uint32_t zero[RT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
+      for (int t = 0; t < RT; ++t) {
+        take_top(row_top(sc[0][t], sc[1][t], acc.m[t]), c2, t, acc);
+        p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
+      }
 #pragma unroll
       for (int j = 0; j < OC; ++j) {
         const bf16x8 va = vt.v_operand(j);
@@ -716,15 +738,16 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
     int64_t t0, t1;
     int lim0, lim1;
     for (; s < s1; ++s) {
-      pages.place(a, seg, s, 0, lane, t0, lim0);
-      pages.place(a, seg, s, 1, lane, t1, lim1);
+      t0 = pages.next(a, seg, lane, lim0);
+      t1 = pages.next(a, seg, lane, lim1);
       if (s * kStepKeys + kStepKeys > clear || lim0 + lim1 < 32) break;
       step(t0, t1, 16, 16, std::false_type());
     }
-    for (; s < s1; ++s) {
-      pages.place(a, seg, s, 0, lane, t0, lim0);
-      pages.place(a, seg, s, 1, lane, t1, lim1);
+    while (s < s1) {
       step(t0, t1, lim0, lim1, std::true_type());
+      if (++s == s1) break;
+      t0 = pages.next(a, seg, lane, lim0);
+      t1 = pages.next(a, seg, lane, lim1);
     }
 
     // ---- the four waves' sums
@@ -786,74 +809,148 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
 // many rows: the waves of a workgroup take different rows and share the keys through LDS
 template <int D, bool E4M3, int RT>
 struct Share {
-  static constexpr int rows = 16 * RT * kWaves;
-  static constexpr int occupancy = 2;
-  static constexpr int grid = 256 * occupancy;
-  static constexpr int half = kStepKeys * D * 2;       // bytes of K, or of V, of a step (2-byte elements)
-  static constexpr size_t lds = 2 * 2 * half;          // two steps of both
+  // one workgroup with eight waves where LDS does not hold two with four
+  static constexpr int waves = D == 256 && E4M3 ? 8 : 4;
+  static constexpr int threads = 64 * waves;
+  static constexpr int rows = 16 * RT * waves;
+  static constexpr int grid = 2048 / waves;            // eight waves a compute unit
+  static constexpr int ring = D == 256 ? 2 : 4;        // steps on their way or in use
+  static constexpr int tile = 16 * D * (E4M3 ? 1 : 2); // bytes of a tile in the cache
+  static constexpr int units = tile / 1024;            // its 1 KB pieces
+  // pieces a wave brings of a step's K and of its V; where there are fewer pieces than waves,
+  // the first half of the waves bring K and the others V
+  static constexpr bool halves = 2 * units < waves;
+  static constexpr int mine = halves ? 1 : 2 * units / waves;
+  // The second tile lies 128 bytes off a multiple of the first: lanes 0-7 and 8-15 read
+  // one of K each, and would meet in the same 32 of the 64 banks.
+  static constexpr int gap = 128;
+  static constexpr int raw = 2 * tile + gap;           // bytes of a step of K, or of V, as the cache has it
+  static constexpr int wide = 2 * 16 * D * 2 + gap;    // and as bf16
+  static constexpr int scales = E4M3 ? waves * 256 : 0;  // of a step, a copy for each wave
+  static constexpr size_t lds = ring * (2 * raw + scales) + (E4M3 ? 4 * wide : 0);
+  // loads of a wave for a step: what the waits count
+  static constexpr int loads = (halves ? 1 : 2) * mine + (E4M3 ? 1 : 0);
 };
 
-// An LDS step holds the tiles as a 2-byte cache does: K, then V, each [tile][16 * D].
-template <int D, bool E4M3>
-struct Stage {
-  static constexpr int units = E4M3 ? D / 64 : D / 32; // 1 KB pieces of a tile in the cache
-  static constexpr int mine = 4 * units / kWaves;      // pieces a wave brings: of two tiles of K and of V
-  u32x4 r[E4M3 ? mine : 1];
+// s_waitcnt vmcnt(N), the other counters free
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4 << 14) | 0x0F70);
+}
+// all waves: LDS writes done before are seen after; loads on their way go on
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+__device__ __forceinline__ void load_to_lds16(const char *from, char *to) {  // to: uniform; lane i writes at 16 i
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                   (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+}
 
-  // begins to bring a step; 2-byte elements go straight to LDS
-  __device__ __forceinline__ void begin(const TreeArgs &a, int64_t t0, int64_t t1, char *buf, int wave, int lane) {
-    constexpr int ES = E4M3 ? 1 : 2;
+// The staging of steps.  K and V have a ring of `ring` steps in LDS, as the cache has them
+// ([tile][16 D]), filled by loads that go to LDS directly.  e4m3 steps are widened to bf16
+// (in a bf16 cache's order) a turn before they are used.
+template <int D, bool E4M3, int RT>
+struct Stage {
+  using S = Share<D, E4M3, RT>;
+  static constexpr int ES = E4M3 ? 1 : 2;
+  char *lds;
+  int wave, lane;
+
+  __device__ __forceinline__ char *raw_k(int step) const { return lds + (step & (S::ring - 1)) * (2 * S::raw); }
+  __device__ __forceinline__ char *raw_v(int step) const { return raw_k(step) + S::raw; }
+  __device__ __forceinline__ char *wide_k(int step) const {
+    return lds + S::ring * (2 * S::raw + S::scales) + (step & 1) * (2 * S::wide);
+  }
+  // this wave's scales of a step: [32] of K, [32] of V
+  __device__ __forceinline__ char *marks(int step) const {
+    return lds + S::ring * 2 * S::raw + (step & (S::ring - 1)) * S::scales + wave * 256;
+  }
+  __device__ __forceinline__ const char *use_k(int step) const { return E4M3 ? wide_k(step) : raw_k(step); }
+  __device__ __forceinline__ const char *use_v(int step) const { return use_k(step) + (E4M3 ? S::wide : S::raw); }
+
+  // this wave's first piece of K or V, or -1: it has none
+  template <bool V>
+  __device__ __forceinline__ int first() const {
+    if constexpr (!S::halves) return wave * S::mine;
+    const int p = V ? wave - S::waves / 2 : wave;
+    return p >= 0 && p < S::waves / 2 ? p : -1;
+  }
+  // this wave's pieces of two tiles at t0 and t1
+  template <bool V>
+  __device__ __forceinline__ void bring(const char *cache, int64_t t0, int64_t t1, char *to) const {
+    if (first<V>() < 0) return;
 #pragma unroll
-    for (int i = 0; i < mine; ++i) {
-      const int p = wave * mine + i, of = p / units, c = p % units;  // of: K0, K1, V0, V1
-      const char *src = (of < 2 ? a.k : a.v) + (of & 1 ? t1 : t0) * (D * ES) + 1024 * c + 16 * lane;
-      if constexpr (E4M3) {
-        r[i] = *reinterpret_cast<const u32x4 *>(src);
-      } else {
-        __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void *)src,
-            (__attribute__((address_space(3))) void *)(buf + 1024 * p), 16, 0, 0);
-      }
+    for (int i = 0; i < S::mine; ++i) {
+      const int p = first<V>() + i, of = p / S::units, c = p % S::units;
+      load_to_lds16(cache + (of ? t1 : t0) * (D * ES) + 1024 * c + 16 * lane, to + of * S::gap + 1024 * p);
     }
   }
-  // e4m3: the pieces, as bf16, to LDS
-  __device__ __forceinline__ void finish(char *buf, int wave, int lane) {
+  __device__ __forceinline__ void bring(const TreeArgs &a, int step, int64_t t0, int64_t t1) const {
+    bring<false>(a.k, t0, t1, raw_k(step));
+    bring<true>(a.v, t0, t1, raw_v(step));
     if constexpr (E4M3) {
-#pragma unroll
-      for (int i = 0; i < mine; ++i) {
-        const int p = wave * mine + i, of = p / units, c = p % units;
-        const u32x4 x = r[i];
-        const u32x4 lo = {e4m3_lo(x[0]), e4m3_hi(x[0]), e4m3_lo(x[1]), e4m3_hi(x[1])};
-        const u32x4 hi = {e4m3_lo(x[2]), e4m3_hi(x[2]), e4m3_lo(x[3]), e4m3_hi(x[3])};
-        // K: 16 d's of a token are halves of two 32-d pieces; V: 8 tokens of two 16-d tiles,
-        // of which a piece has four
-        char *dst = buf + of * (32 * D) + 2048 * c + (of < 2 ? 16 * lane : 1024 * (lane >> 5) + 16 * (lane & 31));
-        *reinterpret_cast<u32x4 *>(dst) = lo;
-        *reinterpret_cast<u32x4 *>(dst + (of < 2 ? 1024 : 512)) = hi;
-      }
+      const int64_t at = (lane & 16 ? t1 : t0) + (lane & 15);
+      __builtin_amdgcn_global_load_lds(
+          (const __attribute__((address_space(1))) void *)((lane < 32 ? a.k_scale : a.v_scale) + at),
+          (__attribute__((address_space(3))) void *)marks(step), 4, 0, 0);
     }
+  }
+  // this wave's pieces of a step, as bf16; only its own loads need to have arrived
+  template <bool V>
+  __device__ __forceinline__ void widen(const char *from, char *to) const {
+    if (first<V>() < 0) return;
+#pragma unroll
+    for (int i = 0; i < S::mine; ++i) {
+      const int p = first<V>() + i, of = p / S::units, c = p % S::units;
+      const u32x4 x = *reinterpret_cast<const u32x4 *>(from + of * S::gap + 1024 * p + 16 * lane);
+      const u32x4 lo = {e4m3_lo(x[0]), e4m3_hi(x[0]), e4m3_lo(x[1]), e4m3_hi(x[1])};
+      const u32x4 hi = {e4m3_lo(x[2]), e4m3_hi(x[2]), e4m3_lo(x[3]), e4m3_hi(x[3])};
+      // K: 16 d's of a token are halves of two 32-d pieces; V: 8 tokens of two 16-d tiles,
+      // of which a piece has four
+      char *dst = to + of * (32 * D + S::gap) + 2048 * c + (V ? 1024 * (lane >> 5) + 16 * (lane & 31) : 16 * lane);
+      *reinterpret_cast<u32x4 *>(dst) = lo;
+      *reinterpret_cast<u32x4 *>(dst + (V ? 512 : 1024)) = hi;
+    }
+  }
+  __device__ __forceinline__ void widen(int step) const {
+    if constexpr (E4M3) {
+      widen<false>(raw_k(step), wide_k(step));
+      widen<true>(raw_v(step), wide_k(step) + S::wide);
+    }
+  }
+  // until this wave's loads of a step have arrived, `later` further steps being on their way
+  __device__ __forceinline__ void arrive(int later) const {
+    if (S::ring > 2 && later >= 2) wait_loads<2 * S::loads>();
+    else if (S::ring > 2 && later == 1) wait_loads<S::loads>();
+    else wait_loads<0>();
   }
 };
 
 template <int D, bool E4M3, int RT>
-__global__ __launch_bounds__(kThreads, (Share<D, E4M3, RT>::occupancy)) void tree_share_kernel(const TreeArgs a) {
+__global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_kernel(const TreeArgs a) {
   using S = Share<D, E4M3, RT>;
+  using St = Stage<D, E4M3, RT>;
   constexpr int ROWS = S::rows, QC = D / 32, OC = D / 16, W = S::grid;
+  static_assert(S::ring <= 4, "arrive() counts two later steps at most");
+  static_assert(!S::halves || 4 * S::units == S::waves, "a wave brings whole pieces");
   extern __shared__ __align__(16) char lds[];
   int *pre = reinterpret_cast<int *>(lds + S::lds);
-  __shared__ int red[kWaves];
+  __shared__ int red[S::waves];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int row16 = lane & 15, g = lane >> 4;
-  unit_prefix(a, ROWS, pre, red);
+  const St st = {lds, wave, lane};
+  unit_prefix<S::threads>(a, ROWS, pre, red);
   const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
   const int w = renamed(blockIdx.x, W, total);
   const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
   const float c2 = a.scale * 1.44269504088896340736f;
   if (u_begin == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
   // operands in a step: K of 32 d's number j, tokens of product i; V of 16 d's number j
-  const int k_lane = (row16 >> 3) * (32 * D) + 256 * g + 16 * (row16 & 7);
-  const int v_lane = 2 * (32 * D) + (g >> 1) * (32 * D) + 256 * (g & 1) + 16 * row16;
+  const int k_lane = (row16 >> 3) * (32 * D + S::gap) + 256 * g + 16 * (row16 & 7);
+  const int v_lane = (g >> 1) * (32 * D + S::gap) + 256 * (g & 1) + 16 * row16;
 
   for (int u = u_begin; u < u_end;) {
     const Item it = locate(a, ROWS, pre, u);
@@ -861,42 +958,70 @@ __global__ __launch_bounds__(kThreads, (Share<D, E4M3, RT>::occupancy)) void tre
     const int take = min(__builtin_amdgcn_readfirstlane(it.units - it.at), u_end - u);
     const Segment seg = segment_of(a, it, ROWS, take, 2 * w + (u == u_begin ? 0 : 1));
     u += take;
+    const int s1 = seg.s1;
     const int row0 = seg.blk * ROWS + wave * 16 * RT;
     const bool idle = row0 >= seg.n * a.G;             // a wave past the last row only helps to stage
     Queries<D, E4M3, RT> qs;
     qs.load(a, seg, row0, row16, g);
-    const int clear = seg.flat ? seg.ctx : seg.ctx + row0 / a.G + 1;
     Rows<D, RT> acc;
     acc.clear();
-    Pages pages;
-    pages.begin(a, seg, seg.s0, lane);
-    Stage<D, E4M3> stage;
-    Scales sl, sl_next;
-    int64_t t0 = 0, t1 = 0, n0 = 0, n1 = 0;
-    int lim0 = 0, lim1 = 0, nl0 = 0, nl1 = 0;
-    __syncthreads();                                   // the last segment's readers are done
-    if (seg.s0 < seg.s1) {
-      pages.place(a, seg, seg.s0, 0, lane, n0, nl0);
-      pages.place(a, seg, seg.s0, 1, lane, n1, nl1);
-      char *buf = lds + (seg.s0 & 1) * (2 * S::half);
-      stage.begin(a, n0, n1, buf, wave, lane);
-      if constexpr (E4M3) sl_next.load(a, n0, n1, g);
-      stage.finish(buf, wave, lane);
+
+    // steps before `plain` are seen by all rows, and every key of theirs is there
+    int plain = max(seg.flat ? seg.ctx : seg.ctx + row0 / a.G + 1, 0) / kStepKeys;
+    Pages ahead;
+    ahead.begin(a, seg, seg.s0, lane);
+    int issued = seg.s0;
+    auto bring = [&]() {
+      int x, y;
+      const int64_t t0 = ahead.next(a, seg, lane, x), t1 = ahead.next(a, seg, lane, y);
+      if (x + y < 32) plain = min(plain, issued);
+      st.bring(a, issued, t0, t1);
+      ++issued;
+    };
+    lds_barrier();                                     // the last segment's readers are done
+    for (int i = 0; i < S::ring - 1 && issued < s1; ++i) bring();
+    if constexpr (E4M3) {
+      if (seg.s0 < s1) {
+        st.arrive(issued - 1 - seg.s0);
+        st.widen(seg.s0);
+      }
     }
-    auto step = [&](int s, const char *buf, auto mask_tag) {
+    // One step.  Operands are read from LDS four at a time, the next four on their way
+    // while four are multiplied, and V's first four while the scores are weighed.
+    auto step = [&](int s, int64_t t0, int64_t t1, int lim0, int lim1, auto mask_tag) {
       constexpr bool MASKED = decltype(mask_tag)::value;
+      const char *kb = st.use_k(s) + k_lane, *vb = st.use_v(s) + v_lane;
+      bf16x8 f[2][4];
       f32x4 sc[2][RT];
 #pragma unroll
       for (int t = 0; t < RT; ++t) sc[0][t] = sc[1][t] = f32x4{0, 0, 0, 0};
+      auto read_k = [&](int n, bf16x8 (&to)[4]) {
 #pragma unroll
-      for (int j = 0; j < QC; ++j)
+        for (int i = 0; i < 4; ++i)
+          to[i] = *reinterpret_cast<const bf16x8 *>(kb + 1024 * ((4 * n + i) >> 1) + 128 * (i & 1));
+      };
+      auto read_v = [&](int n, bf16x8 (&to)[4]) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const bf16x8 ka = *reinterpret_cast<const bf16x8 *>(buf + k_lane + 1024 * j + 128 * i);
+        for (int i = 0; i < 4; ++i) to[i] = *reinterpret_cast<const bf16x8 *>(vb + 512 * (4 * n + i));
+      };
+      read_k(0, f[0]);
 #pragma unroll
-          for (int t = 0; t < RT; ++t) sc[i][t] = mfma(ka, qs.q[j][t], sc[i][t]);
-        }
+      for (int n = 0; n < QC / 2; ++n) {
+        if (n + 1 < QC / 2) read_k(n + 1, f[~n & 1]);
+        else read_v(0, f[~n & 1]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int t = 0; t < RT; ++t) sc[i & 1][t] = mfma(f[n & 1][i], qs.q[2 * n + (i >> 1)][t], sc[i & 1][t]);
+      }
+      Scales sl;
       if constexpr (E4M3) {
+        const f32x4 *sp = reinterpret_cast<const f32x4 *>(st.marks(s)) + 2 * g;
+        sl.k[0] = sp[0];
+        sl.k[1] = sp[1];
+        sl.v[0] = sp[8];
+        sl.v[1] = sp[9];
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
           sc[0][t] *= sl.k[0];
@@ -921,54 +1046,53 @@ __global__ __launch_bounds__(kThreads, (Share<D, E4M3, RT>::occupancy)) void tre
       bf16x8 p[RT];
       uint32_t zero[RT];
 #pragma unroll
+      for (int t = 0; t < RT; ++t) take_top(row_top(sc[0][t], sc[1][t], acc.m[t]), c2, t, acc);
+#pragma unroll
       for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
 #pragma unroll
-      for (int j = 0; j < OC; ++j) {
-        bf16x8 va = *reinterpret_cast<const bf16x8 *>(buf + v_lane + 512 * j);
-        if constexpr (MASKED) va = clean(va, keep, odd);
+      for (int n = 0; n < OC / 4; ++n) {
+        constexpr int at = (QC / 2) & 1;               // where V's first four went
+        if (n + 1 < OC / 4) read_v(n + 1, f[(n + 1 + at) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int t = 0; t < RT; ++t) acc.o[j][t] = mfma(va, p[t], acc.o[j][t]);
+        for (int i = 0; i < 4; ++i) {
+          bf16x8 va = f[(n + at) & 1][i];
+          if constexpr (MASKED) va = clean(va, keep, odd);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) acc.o[4 * n + i][t] = mfma(va, p[t], acc.o[4 * n + i][t]);
+        }
       }
       if constexpr (MASKED)
         if (__any(odd != 0)) add_not_finite<D, E4M3, RT>(a, t0, t1, lim0, lim1, vis, zero, row16, g, acc);
     };
-    // one step: the staged one is published, the next one begun, then the products
-    auto turn = [&](int s, auto mask_tag) {
-      char *buf = lds + (s & 1) * (2 * S::half), *other = lds + (~s & 1) * (2 * S::half);
-      if (s + 1 < seg.s1) {
-        stage.begin(a, n0, n1, other, wave, lane);
-        if constexpr (E4M3) sl_next.load(a, n0, n1, g);
-      }
-      if (!idle) step(s, buf, mask_tag);
-      if (s + 1 < seg.s1) stage.finish(other, wave, lane);
-    };
-    auto publish = [&](int s) {
-      // the wave's own pieces have arrived, and every wave is past its reads of the other buffer
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      t0 = n0;
-      t1 = n1;
-      lim0 = nl0;
-      lim1 = nl1;
-      if constexpr (E4M3) sl = sl_next;
-      if (s + 1 < seg.s1) {
-        pages.place(a, seg, s + 1, 0, lane, n0, nl0);
-        pages.place(a, seg, s + 1, 1, lane, n1, nl1);
+    // A turn: wait for the wave's own pieces of step s; the barrier makes everybody's
+    // visible and says that everybody is done with step s - 1, whose place is filled again.
+    auto turn = [&](int s, int64_t t0, int64_t t1, int lim0, int lim1, auto mask_tag) {
+      if constexpr (!E4M3) st.arrive(issued - 1 - s);
+      lds_barrier();
+      if (issued < s1) bring();
+      if (!idle) step(s, t0, t1, lim0, lim1, mask_tag);
+      if constexpr (E4M3) {
+        if (s + 1 < s1) {
+          st.arrive(issued - 2 - s);
+          st.widen(s + 1);
+        }
       }
     };
     int s = seg.s0;
-    bool open = false;                                 // step s is published
-    for (; s < seg.s1; ++s) {
-      publish(s);
-      open = true;
-      if (s * kStepKeys + kStepKeys > clear || lim0 + lim1 < 32) break;
-      turn(s, std::false_type());
-      open = false;
+    while (s < min(plain, s1)) {
+      turn(s, 0, 0, 16, 16, std::false_type());
+      ++s;
     }
-    for (; s < seg.s1; ++s) {
-      if (!open) publish(s);
-      open = false;
-      turn(s, std::true_type());
+    // the rest with care: masks, keys that are not there, values that are not finite
+    if (s < s1) {
+      Pages now;
+      now.begin(a, seg, s, lane);
+      for (; s < s1; ++s) {
+        int lim0, lim1;
+        const int64_t t0 = now.next(a, seg, lane, lim0), t1 = now.next(a, seg, lane, lim1);
+        turn(s, t0, t1, lim0, lim1, std::true_type());
+      }
     }
 
 #pragma unroll
@@ -992,7 +1116,7 @@ __global__ __launch_bounds__(kThreads, (Share<D, E4M3, RT>::occupancy)) void tre
 // ---------------------------------------------------------------------------
 // Adds the partial sums of an item that several workgroups share; workgroup w has the
 // item whose first border inside it is the beginning of main workgroup w, if there is
-// one.  Four parts at a time are on their way; blockIdx.y takes every gridDim.y-th row.
+// one.  Four parts at a time are on their way.  blockIdx.y: 1024 values of the rows.
 __global__ __launch_bounds__(kThreads) void tree_combine_kernel(const TreeArgs a, int rows, int D) {
   const int w = blockIdx.x;
   const Border d = reinterpret_cast<const Border *>(a.borders)[w];
@@ -1042,7 +1166,7 @@ __global__ __launch_bounds__(kThreads) void tree_combine_kernel(const TreeArgs a
 }
 
 void combine(const TreeArgs &a, int grid, int rows, int D, hipStream_t stream) {
-  hipLaunchKernelGGL(tree_combine_kernel, dim3(grid, 4), dim3(kThreads), 0, stream, a, rows, D);
+  hipLaunchKernelGGL(tree_combine_kernel, dim3(grid, rows * D / 1024), dim3(kThreads), 0, stream, a, rows, D);
 }
 
 template <int D, bool E4M3, int RT>
@@ -1060,7 +1184,7 @@ template <int D, bool E4M3, int RT>
 hipError_t launch_share(const TreeArgs &a, const char *name, hipStream_t stream) {
   using S = Share<D, E4M3, RT>;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((tree_share_kernel<D, E4M3, RT>), dim3(S::grid), dim3(kThreads), S::lds + size_t(a.R + 1) * 4,
+  hipLaunchKernelGGL((tree_share_kernel<D, E4M3, RT>), dim3(S::grid), dim3(S::threads), S::lds + size_t(a.R + 1) * 4,
                      stream, a);
   combine(a, S::grid, S::rows, D, stream);
   set_last_kernel(name);
@@ -1072,13 +1196,13 @@ hipError_t launch_share(const TreeArgs &a, const char *name, hipStream_t stream)
 // 2-byte elements of 256-wide heads leave the split form registers for 16 rows a wave.
 struct Form {
   bool share;
-  int tiles;  // of 16 rows a wave
+  int tiles, waves;  // of 16 rows a wave; with different rows
 };
 Form tree_form(int64_t rows, int64_t D, bool e4m3) {
-  if (rows > 32) return {true, rows <= 64 || D == 256 ? 1 : 2};
-  return {false, rows <= 16 || (D == 256 && !e4m3) ? 1 : 2};
+  if (rows <= 32) return {false, rows <= 16 || (D == 256 && !e4m3) ? 1 : 2, 1};
+  return {true, rows <= 64 || D == 256 ? 1 : 2, D == 256 && e4m3 ? 8 : 4};
 }
-int form_rows(Form f) { return 16 * f.tiles * (f.share ? kWaves : 1); }
+int form_rows(Form f) { return 16 * f.tiles * f.waves; }
 
 template <int D, bool E4M3>
 hipError_t pick(const TreeArgs &a, Form f, hipStream_t stream) {
