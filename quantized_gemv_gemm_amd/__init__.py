@@ -580,6 +580,13 @@ def hadamard_join(u_lo, u_hi, half, out=None):
 TREE_NODES = 64
 
 
+def _raw_stream(index):
+    """The current HIP stream of GPU ``index``, as an address (a step makes many short calls:
+    torch.cuda.current_stream builds an object for 2 us each time)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(index)
+
+
 def _given(t, name, dtype, shape, index):
     """A contiguous GPU tensor of this dtype and shape, on device number ``index``; its address."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
@@ -686,17 +693,17 @@ def step_plan(ctx_lens, new_lens, owned, block_table, free_list, free_head, toke
          _given(free_list, "free_list", i32, free_list.shape, i), _given(free_head, "free_head", i32, (1,), i),
          None if parents is None else _given(parents, "parents", i32, (T,), i)]
     dev = ctx_lens.device
-    q_start = torch.empty(R + 1, dtype=i32, device=dev)
-    kv_lens = torch.empty(R, dtype=i32, device=dev)
-    slots = torch.empty(T, dtype=torch.int64, device=dev)
-    positions = torch.empty(T, dtype=i32, device=dev)
-    mask = None if parents is None else torch.empty(T, dtype=torch.int64, device=dev)
-    owned_out = torch.empty(R, dtype=i32, device=dev)
-    head_out = torch.empty(1, dtype=i32, device=dev)
+    # the outputs share two allocations: each one alone would cost as much as the kernel
+    q_start, kv_lens, positions, owned_out, head_out = torch.empty(
+        3 * R + T + 2, dtype=i32, device=dev).split_with_sizes((R + 1, R, T, R, 1))
+    if parents is None:
+        slots, mask = torch.empty(T, dtype=torch.int64, device=dev), None
+    else:
+        slots, mask = torch.empty((2, T), dtype=torch.int64, device=dev).unbind()
     _check("tl_step_plan", lib().tl_step_plan(
         p[0], p[1], p[2], R, p[3], width, int(block), p[4], free_list.shape[0], p[5], p[6], T, q_start.data_ptr(),
         kv_lens.data_ptr(), slots.data_ptr(), positions.data_ptr(), None if mask is None else mask.data_ptr(),
-        owned_out.data_ptr(), head_out.data_ptr(), _stream(dev)))
+        owned_out.data_ptr(), head_out.data_ptr(), _raw_stream(i)))
     return q_start, kv_lens, slots, positions, mask, owned_out, head_out
 
 
@@ -734,7 +741,7 @@ def kv_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, q=None, 
         cp = _given(cos_sin, "cos_sin", torch.float32, (most, rot), i)
         pp = _given(positions, "positions", torch.int32, (T,), i)
     _check("tl_kv_write", lib().tl_kv_write(kp, ldk, vp, ldv, sp, T, H, D, qp, ldq, Hq, pp, cp, most, rot, qo, kc, vc,
-                                            ks, vs, code, pages, block, _stream(k.device)))
+                                            ks, vs, code, pages, block, _raw_stream(i)))
     return q_out
 
 
@@ -778,7 +785,7 @@ def tree_attention(q, k_cache, v_cache, block_table, q_start, kv_lens, tree_mask
     wp = _given(workspace, "workspace", torch.uint8, (workspace.numel(),), i)
     _check("tl_tree_attention", lib().tl_tree_attention(
         qp, ldq, T, H, G, D, kc, vc, ks, vs, code, pages, block, tp, width, R, sp, lp, mp,
-        D ** -0.5 if scale is None else scale, max_nodes, op, ep, wp, workspace.numel(), _stream(q.device)))
+        D ** -0.5 if scale is None else scale, max_nodes, op, ep, wp, workspace.numel(), _raw_stream(i)))
     return out if lse is None else (out, lse)
 
 
@@ -797,17 +804,16 @@ def tree_verify(logits, draft, parents, q_start, path_width=TREE_NODES, workspac
     pp = _given(parents, "parents", i32, (T,), i)
     sp = _given(q_start, "q_start", i32, (R + 1,), i)
     dev = logits.device
-    accepted = torch.empty(R, dtype=i32, device=dev)
-    path = torch.empty((R, path_width), dtype=i32, device=dev)
-    nxt = torch.empty(R, dtype=i32, device=dev)
-    target = torch.empty(T, dtype=i32, device=dev)
+    accepted, path, nxt, target = torch.empty(R * (path_width + 2) + T, dtype=i32, device=dev).split_with_sizes(
+        (R, R * path_width, R, T))
+    path = path.view(R, path_width)
     if workspace is None:
         need = lib().tl_tree_verify_workspace_size(T, V)
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     wp = _given(workspace, "workspace", torch.uint8, (workspace.numel(),), i)
     _check("tl_tree_verify", lib().tl_tree_verify(
         logits.data_ptr(), code, logits.stride(0) if T > 1 else V, T, V, dp, pp, sp, R, accepted.data_ptr(),
-        path.data_ptr(), path_width, nxt.data_ptr(), target.data_ptr(), wp, workspace.numel(), _stream(dev)))
+        path.data_ptr(), path_width, nxt.data_ptr(), target.data_ptr(), wp, workspace.numel(), _raw_stream(i)))
     return accepted, path, nxt, target
 
 
@@ -830,5 +836,5 @@ def kv_commit(accepted, path, ctx_lens, kv_lens, block_table, k_cache, v_cache, 
         _given(ctx_lens, "ctx_lens", i32, (R,), i), _given(kv_lens, "kv_lens", i32, (R,), i),
         _given(block_table, "block_table", i32, (R, block_table.shape[1]), i), block_table.shape[1], R, kc, vc, ks, vs,
         code, k_cache.shape[0] if layers else 1, pages, H, block, D, _given(ctx_out, "ctx_out", i32, (R,), i),
-        _stream(accepted.device)))
+        _raw_stream(i)))
     return ctx_out

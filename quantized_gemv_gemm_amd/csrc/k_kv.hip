@@ -229,15 +229,22 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
 
 // ---------------------------------------------------------------------------
 // Rows ctx + path[i] of a request go to ctx + i.  A workgroup takes one layer, request
-// and head and reads every row that moves before it writes one, so paths may overlap
-// their targets; at most 64 rows, usually a handful: what bounds it is the chain of
-// loads to the first row (lengths, path, page, row).
+// and head, and the elements lie in threads' registers while they move, up to 4096 of V at
+// a time: some d's of every row, all read before one is written, so paths may overlap
+// their targets.  What bounds it is the
+// chain of loads to the first row (lengths, path, page, row) and, over many requests and
+// layers, V's lines: a token's values are 2 (1) bytes of every 16, so moving one touches
+// the lines of eight.
 template <int D, bool E4M3>
 __global__ __launch_bounds__(kThreads) void kv_commit_kernel(const CommitArgs a) {
   constexpr int ES = E4M3 ? 1 : 2;
-  constexpr int KP = D * ES / 16;                        // 16-byte pieces of a K row
-  extern __shared__ __attribute__((aligned(16))) char rows[];  // K pieces, V elements, scales
-  __shared__ int64_t s_src[kTreeNodes], s_dst[kTreeNodes];     // tokens in the layer's cache, or -1
+  constexpr int VN = 16, KN = VN * ES / 16 > 0 ? VN * ES / 16 : 1;  // registers of a pass: elements of V, pieces of K
+  // of a move's source and target: the token, and its row's first byte in K and in V
+  struct Place {
+    int64_t token, k, v;
+  };
+  __shared__ Place s_src[kTreeNodes], s_dst[kTreeNodes];
+  __shared__ int s_count;
   const int tid = threadIdx.x;
   int b = blockIdx.x;
   const int head = b % a.H;
@@ -245,14 +252,13 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(const CommitArgs a)
   const int r = b % a.R, layer = b / a.R;
   const int ctx = max(a.ctx_lens[r], 0), n = max(a.kv_lens[r] - ctx, 0);  // not served: no new tokens
   const int block = 1 << a.block_shift, count = min(max(a.accepted[r], 0), n);
+  const int most = min(a.path_width, kTreeNodes);
+  const int from = tid < most ? a.path[int64_t(r) * a.path_width + tid] : -1;
   if (tid == 0 && head == 0 && layer == 0) a.ctx_out[r] = ctx + count;
-  const int moves = min(min(count, a.path_width), kTreeNodes);
-  if (n > kTreeNodes || moves == 0) return;
-  bool go = false;
-  if (tid < moves) {
-    const int from = a.path[int64_t(r) * a.path_width + tid];
+  if (n > kTreeNodes || count == 0) return;
+  if (tid < 64) {
     int64_t src = -1, dst = -1;
-    if (from > tid && from < n) {
+    if (tid < min(count, most) && from > tid && from < n) {
       auto token = [&](int pos) -> int64_t {
         const int page = pos >> a.block_shift;
         if (page >= a.table_width) return -1;
@@ -262,52 +268,75 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(const CommitArgs a)
       };
       src = token(ctx + from);
       dst = token(ctx + tid);
-      go = src >= 0 && dst >= 0;
     }
-    s_src[tid] = go ? src : -1;
-    s_dst[tid] = dst;
-  }
-  if (!__syncthreads_or(go)) return;
-
-  const int64_t base = layer * a.layer_tokens;           // tokens before this layer's cache
-  char *k_rows = rows, *v_rows = rows + moves * D * ES;
-  float *scales = reinterpret_cast<float *>(v_rows + moves * D * ES);
-  // byte offset of piece p of a K row, and of element d of a V row
-  auto k_at = [&](int64_t tok, int p) { return ((base + (tok & ~int64_t(15))) * D + kv_tile_k(int(tok & 15), p * (16 / ES), ES)) * ES; };
-  auto v_at = [&](int64_t tok, int d) { return ((base + (tok & ~int64_t(15))) * D + kv_tile_v(int(tok & 15), d, ES)) * ES; };
-  for (int u = tid; u < moves * KP; u += kThreads) {
-    const int i = u / KP, p = u % KP;
-    if (s_src[i] >= 0)
-      *reinterpret_cast<u32x4 *>(k_rows + 16 * u) = *reinterpret_cast<const u32x4 *>(a.k_cache + k_at(s_src[i], p));
-  }
-  for (int u = tid; u < moves * D; u += kThreads) {
-    const int i = u / D, d = u % D;
-    if (s_src[i] < 0) continue;
-    if constexpr (E4M3) v_rows[u] = a.v_cache[v_at(s_src[i], d)];
-    else reinterpret_cast<uint16_t *>(v_rows)[u] = *reinterpret_cast<const uint16_t *>(a.v_cache + v_at(s_src[i], d));
-  }
-  if constexpr (E4M3) {
-    if (tid < moves && s_src[tid] >= 0) {
-      scales[2 * tid] = a.k_scale[base + s_src[tid]];
-      scales[2 * tid + 1] = a.v_scale[base + s_src[tid]];
+    const bool go = src >= 0 && dst >= 0;
+    const uint64_t all = __ballot(go);
+    const int at = __popcll(all & ((uint64_t(1) << tid) - 1));   // the moves, without gaps
+    if (go) {
+      const int64_t base = layer * a.layer_tokens;       // tokens before this layer's cache
+      auto place = [&](int64_t tok) {
+        const int64_t tile = (base + (tok & ~int64_t(15))) * (D * ES);
+        return Place{base + tok, tile + kv_k_token(int(tok & 15)), tile + kv_v_token(int(tok & 15), ES)};
+      };
+      s_src[at] = place(src);
+      s_dst[at] = place(dst);
     }
+    if (tid == 0) s_count = __popcll(all);
   }
   __syncthreads();
-  for (int u = tid; u < moves * KP; u += kThreads) {
-    const int i = u / KP, p = u % KP;
-    if (s_src[i] >= 0)
-      *reinterpret_cast<u32x4 *>(a.k_cache + k_at(s_dst[i], p)) = *reinterpret_cast<const u32x4 *>(k_rows + 16 * u);
-  }
-  for (int u = tid; u < moves * D; u += kThreads) {
-    const int i = u / D, d = u % D;
-    if (s_src[i] < 0) continue;
-    if constexpr (E4M3) a.v_cache[v_at(s_dst[i], d)] = v_rows[u];
-    else *reinterpret_cast<uint16_t *>(a.v_cache + v_at(s_dst[i], d)) = reinterpret_cast<const uint16_t *>(v_rows)[u];
-  }
-  if constexpr (E4M3) {
-    if (tid < moves && s_src[tid] >= 0) {
-      a.k_scale[base + s_dst[tid]] = scales[2 * tid];
-      a.v_scale[base + s_dst[tid]] = scales[2 * tid + 1];
+  const int moves = s_count;
+  if (moves == 0) return;
+
+  int log_d = D == 64 ? 6 : D == 128 ? 7 : 8;            // d's of a pass, a power of two
+  while (moves << log_d > VN * kThreads) --log_d;
+  const int log_k = log_d + (E4M3 ? 0 : 1) - 4;          // 16-byte pieces of K
+  for (int d0 = 0; d0 < D; d0 += 1 << log_d) {
+    const int p0 = d0 * ES / 16;
+    u32x4 k[KN];
+    uint32_t v[VN];
+    float ks = 0, vs = 0;
+#pragma unroll
+    for (int i = 0; i < KN; ++i) {
+      if (i * kThreads >= moves << log_k) break;         // uniform
+      const int u = i * kThreads + tid, row = u >> log_k, p = p0 + u - (row << log_k);
+      if (row < moves) k[i] = *reinterpret_cast<const u32x4 *>(a.k_cache + s_src[row].k + kv_k_piece(p));
+    }
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      if (i * kThreads >= moves << log_d) break;
+      const int u = i * kThreads + tid, row = u >> log_d, d = d0 + u - (row << log_d);
+      if (row < moves) {
+        const char *p = a.v_cache + s_src[row].v + kv_v_element(d, ES);
+        if constexpr (E4M3) v[i] = *reinterpret_cast<const uint8_t *>(p);
+        else v[i] = *reinterpret_cast<const uint16_t *>(p);
+      }
+    }
+    const bool scales = E4M3 && d0 == 0 && tid < moves;
+    if (scales) {
+      ks = a.k_scale[s_src[tid].token];
+      vs = a.v_scale[s_src[tid].token];
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);                  // every load has returned
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < KN; ++i) {
+      if (i * kThreads >= moves << log_k) break;
+      const int u = i * kThreads + tid, row = u >> log_k, p = p0 + u - (row << log_k);
+      if (row < moves) *reinterpret_cast<u32x4 *>(a.k_cache + s_dst[row].k + kv_k_piece(p)) = k[i];
+    }
+#pragma unroll
+    for (int i = 0; i < VN; ++i) {
+      if (i * kThreads >= moves << log_d) break;
+      const int u = i * kThreads + tid, row = u >> log_d, d = d0 + u - (row << log_d);
+      if (row < moves) {
+        char *p = a.v_cache + s_dst[row].v + kv_v_element(d, ES);
+        if constexpr (E4M3) *reinterpret_cast<uint8_t *>(p) = uint8_t(v[i]);
+        else *reinterpret_cast<uint16_t *>(p) = uint16_t(v[i]);
+      }
+    }
+    if (scales) {
+      a.k_scale[s_dst[tid].token] = ks;
+      a.v_scale[s_dst[tid].token] = vs;
     }
   }
 }
@@ -327,10 +356,8 @@ template <int D, bool E4M3>
 hipError_t commit_rows(const CommitArgs &a, hipStream_t stream) {
   const int64_t grid = int64_t(a.L) * a.R * a.H;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  const int most = a.path_width < kTreeNodes ? a.path_width : kTreeNodes;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((kv_commit_kernel<D, E4M3>), dim3(unsigned(grid)), dim3(kThreads),
-                     size_t(most) * (2 * D * (E4M3 ? 1 : 2) + 8), stream, a);
+  hipLaunchKernelGGL((kv_commit_kernel<D, E4M3>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a);
   set_last_kernel(E4M3 ? "kv_commit_e4m3" : "kv_commit_bf16");
   return hipGetLastError();
 }

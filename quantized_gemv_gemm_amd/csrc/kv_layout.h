@@ -36,4 +36,13 @@ TL_HD int kv_tile_v(int t, int d, int bytes) {
   return d / w * (16 * w) + t / 8 * (8 * w) + d % 16 * (8 * u) + d % w / 16 * 8 + t % 8;
 }
 
+// The same in bytes, as a token's part and a d's part.  K: 16-byte piece p of a row;
+// V: element d.
+TL_HD int kv_k_token(int t) { return kv_place(t) * 16; }
+TL_HD int kv_k_piece(int p) { return p * 256; }
+TL_HD int kv_v_token(int t, int bytes) { return t / 8 * 256 + t % 8 * bytes; }
+TL_HD int kv_v_element(int d, int bytes) {
+  return bytes == 2 ? d / 16 * 512 + d % 16 * 16 : d / 32 * 512 + d % 16 * 16 + d / 16 % 2 * 8;
+}
+
 }  // namespace tl
