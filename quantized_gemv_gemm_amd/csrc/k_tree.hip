@@ -456,6 +456,31 @@ struct Pages {
   }
 };
 
+// The places of 64 tiles of a segment, a lane each: a step's are two readlanes, so that the
+// scalar work between two steps is short.
+struct Window {
+  int first;           // tile of lane 0
+  uint32_t lo, hi;     // first token in the cache (some tile of it where there is none)
+
+  // fills it from tile `from` on, and gives the first of its tiles that lacks a key
+  __device__ __forceinline__ int fill(const TreeArgs &a, const Segment &s, int from, int lane) {
+    first = from;
+    const int pos = (from + lane) * kKvTile, page = pos >> a.block_shift, mask = (1 << a.block_shift) - 1;
+    int id = -1;
+    if (pos < s.key_end && page < a.table_width) id = a.table[int64_t(s.r) * a.table_width + page];
+    const bool good = uint32_t(id) < uint32_t(a.pages);
+    const int64_t at = (((good ? int64_t(id) : 0) * a.H + s.h) << a.block_shift) + (good ? pos & mask : 0);
+    lo = uint32_t(at);
+    hi = uint32_t(at >> 32);
+    const uint64_t lacks = __ballot(!good || pos + kKvTile > s.key_end);
+    return lacks ? from + __builtin_ctzll(lacks) : 0x7FFFFFFF;
+  }
+  __device__ __forceinline__ int64_t tile(int i) const {  // i: uniform
+    const int at = i - first;
+    return int64_t(uint64_t(uint32_t(__builtin_amdgcn_readlane(hi, at))) << 32 | uint32_t(__builtin_amdgcn_readlane(lo, at)));
+  }
+};
+
 // e4m3: the scales of the lane's eight keys
 struct Scales {
   f32x4 k[2], v[2];
@@ -505,10 +530,13 @@ __device__ __forceinline__ float row_top(const f32x4 &s0, const f32x4 &s1, float
   const float top = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])), fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
   return fmaxf(row_max(top), before);
 }
-// Takes a new maximum over, rescaling the sums where it grew.
+// Takes a new maximum over, rescaling the sums, once it is past the old one by `slack`:
+// weights up to 2^8 are as exact as those up to 1, and a maximum still creeps up for long
+// after it is nearly reached (with the rescale at every rise a quarter of the steps over
+// 8192 keys had one).
 template <int D, int RT>
-__device__ __forceinline__ void take_top(float top, float c2, int t, Rows<D, RT> &acc) {
-  if (__any(top > acc.m[t])) {
+__device__ __forceinline__ void take_top(float top, float slack, float c2, int t, Rows<D, RT> &acc) {
+  if (__any(top > acc.m[t] + slack)) {
     const float f = top > acc.m[t] ? __builtin_amdgcn_exp2f((acc.m[t] - top) * c2) : 1.0f;
     acc.l[t] *= f;
 #pragma unroll
@@ -516,6 +544,8 @@ __device__ __forceinline__ void take_top(float top, float c2, int t, Rows<D, RT>
     acc.m[t] = top;
   }
 }
+// 8 as a power of two, in raw scores; finite, so that it leaves -inf as it is
+__device__ __forceinline__ float slack_of(float c2) { return fminf(8.0f / c2, 1e30f); }
 // Scores of one row tile to weights under the running maximum: adds to the running sum, and
 // gives the B operand of the second product.  zero: a bit for each key whose weight is 0.
 template <int D, bool E4M3, int RT, bool MASKED>
@@ -648,7 +678,7 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
   const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
   const int w = renamed(blockIdx.x, W, total);
   const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
-  const float c2 = a.scale * 1.44269504088896340736f;  // scores to powers of two
+  const float c2 = a.scale * 1.44269504088896340736f, slack = slack_of(c2);  // scores to powers of two
   if (u_begin == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
 
   for (int u = u_begin; u < u_end;) {
@@ -721,7 +751,7 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
       uint32_t zero[RT];
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        take_top(row_top(sc[0][t], sc[1][t], acc.m[t]), c2, t, acc);
+        take_top(row_top(sc[0][t], sc[1][t], acc.m[t]), slack, c2, t, acc);
         p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
       }
 #pragma unroll
@@ -946,7 +976,7 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
   const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
   const int w = renamed(blockIdx.x, W, total);
   const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
-  const float c2 = a.scale * 1.44269504088896340736f;
+  const float c2 = a.scale * 1.44269504088896340736f, slack = slack_of(c2);
   if (u_begin == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
   // operands in a step: K of 32 d's number j, tokens of product i; V of 16 d's number j
   const int k_lane = (row16 >> 3) * (32 * D + S::gap) + 256 * g + 16 * (row16 & 7);
@@ -968,14 +998,12 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
 
     // steps before `plain` are seen by all rows, and every key of theirs is there
     int plain = max(seg.flat ? seg.ctx : seg.ctx + row0 / a.G + 1, 0) / kStepKeys;
-    Pages ahead;
-    ahead.begin(a, seg, seg.s0, lane);
+    Window ahead;
+    plain = min(plain, ahead.fill(a, seg, 2 * seg.s0, lane) >> 1);
     int issued = seg.s0;
     auto bring = [&]() {
-      int x, y;
-      const int64_t t0 = ahead.next(a, seg, lane, x), t1 = ahead.next(a, seg, lane, y);
-      if (x + y < 32) plain = min(plain, issued);
-      st.bring(a, issued, t0, t1);
+      if (2 * issued - ahead.first >= 64) plain = min(plain, ahead.fill(a, seg, 2 * issued, lane) >> 1);
+      st.bring(a, issued, ahead.tile(2 * issued), ahead.tile(2 * issued + 1));
       ++issued;
     };
     lds_barrier();                                     // the last segment's readers are done
@@ -988,6 +1016,7 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
     }
     // One step.  Operands are read from LDS four at a time, the next four on their way
     // while four are multiplied, and V's first four while the scores are weighed.
+    // The next step is begun to be brought while the first operands come.
     auto step = [&](int s, int64_t t0, int64_t t1, int lim0, int lim1, auto mask_tag) {
       constexpr bool MASKED = decltype(mask_tag)::value;
       const char *kb = st.use_k(s) + k_lane, *vb = st.use_v(s) + v_lane;
@@ -1005,10 +1034,16 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
         for (int i = 0; i < 4; ++i) to[i] = *reinterpret_cast<const bf16x8 *>(vb + 512 * (4 * n + i));
       };
       read_k(0, f[0]);
+      if (QC > 2) read_k(1, f[1]);
+      else read_v(0, f[1]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (issued < s1) bring();
 #pragma unroll
       for (int n = 0; n < QC / 2; ++n) {
-        if (n + 1 < QC / 2) read_k(n + 1, f[~n & 1]);
-        else read_v(0, f[~n & 1]);
+        if (n > 0) {
+          if (n + 1 < QC / 2) read_k(n + 1, f[~n & 1]);
+          else read_v(0, f[~n & 1]);
+        }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -1046,7 +1081,7 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
       bf16x8 p[RT];
       uint32_t zero[RT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) take_top(row_top(sc[0][t], sc[1][t], acc.m[t]), c2, t, acc);
+      for (int t = 0; t < RT; ++t) take_top(row_top(sc[0][t], sc[1][t], acc.m[t]), slack, c2, t, acc);
 #pragma unroll
       for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
 #pragma unroll
@@ -1070,8 +1105,8 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
     auto turn = [&](int s, int64_t t0, int64_t t1, int lim0, int lim1, auto mask_tag) {
       if constexpr (!E4M3) st.arrive(issued - 1 - s);
       lds_barrier();
-      if (issued < s1) bring();
       if (!idle) step(s, t0, t1, lim0, lim1, mask_tag);
+      else if (issued < s1) bring();
       if constexpr (E4M3) {
         if (s + 1 < s1) {
           st.arrive(issued - 2 - s);
