@@ -839,12 +839,14 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
 // many rows: the waves of a workgroup take different rows and share the keys through LDS
 template <int D, bool E4M3, int RT>
 struct Share {
-  // one workgroup with eight waves where LDS does not hold two with four
-  static constexpr int waves = D == 256 && E4M3 ? 8 : 4;
+  // Two workgroups of four waves a compute unit; 256-wide heads, whose steps are twice as
+  // long in LDS and whose waves hold 16 rows, have one of eight, which reads memory once for
+  // 128 rows (prompt chunk 380 -> 357 us; for 128-wide heads eight waves measured 113 -> 117).
+  static constexpr int waves = D == 256 ? 8 : 4;
   static constexpr int threads = 64 * waves;
   static constexpr int rows = 16 * RT * waves;
   static constexpr int grid = 2048 / waves;            // eight waves a compute unit
-  static constexpr int ring = D == 256 ? 2 : 4;        // steps on their way or in use
+  static constexpr int ring = D == 256 && E4M3 ? 2 : 4;  // steps on their way or in use
   static constexpr int tile = 16 * D * (E4M3 ? 1 : 2); // bytes of a tile in the cache
   static constexpr int units = tile / 1024;            // its 1 KB pieces
   // pieces a wave brings of a step's K and of its V; where there are fewer pieces than waves,
@@ -1235,7 +1237,7 @@ struct Form {
 };
 Form tree_form(int64_t rows, int64_t D, bool e4m3) {
   if (rows <= 32) return {false, rows <= 16 || (D == 256 && !e4m3) ? 1 : 2, 1};
-  return {true, rows <= 64 || D == 256 ? 1 : 2, D == 256 && e4m3 ? 8 : 4};
+  return {true, rows <= 64 || D == 256 ? 1 : 2, D == 256 ? 8 : 4};
 }
 int form_rows(Form f) { return 16 * f.tiles * f.waves; }
 
@@ -1246,7 +1248,10 @@ hipError_t pick(const TreeArgs &a, Form f, hipStream_t stream) {
       if (f.tiles == 2)
         return launch_share<D, E4M3, 2>(a, E4M3 ? "tree_attention_e4m3_share128" : "tree_attention_bf16_share128", stream);
     }
-    return launch_share<D, E4M3, 1>(a, E4M3 ? "tree_attention_e4m3_share64" : "tree_attention_bf16_share64", stream);
+    if constexpr (D == 256)
+      return launch_share<D, E4M3, 1>(a, E4M3 ? "tree_attention_e4m3_share128" : "tree_attention_bf16_share128", stream);
+    else
+      return launch_share<D, E4M3, 1>(a, E4M3 ? "tree_attention_e4m3_share64" : "tree_attention_bf16_share64", stream);
   }
   if constexpr (D != 256 || E4M3) {
     if (f.tiles == 2)
