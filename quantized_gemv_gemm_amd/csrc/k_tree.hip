@@ -170,34 +170,37 @@ __device__ __forceinline__ Item locate(const TreeArgs &a, int rows, const int *p
   return it;
 }
 
-// first unit of workgroup w of W; with fewer units than workgroups the first ones get one each
-__device__ __forceinline__ int first_unit(int w, int W, int total) {
-  return total >= W ? int(int64_t(total) * w / W) : min(w, total);
-}
+// first unit of workgroup w of W (with fewer units than workgroups some have none)
+__device__ __forceinline__ int first_unit(int w, int W, int total) { return int(int64_t(total) * w / W); }
+// the workgroup that has unit u, with fewer units than workgroups: one each
+__device__ __forceinline__ int only_unit(int u, int W, int total) { return ((u + 1) * W + total - 1) / total - 1; }
 
-// Workgroups are dealt to the eight XCDs in turn.  Where each has several units, their
-// indices are renamed so that an XCD gets neighbouring units, whose row blocks read the
-// same keys from its own L2; where there are few, they stay spread over the chip.
-__device__ __forceinline__ int renamed(int id, int W, int total) {
-  return total >= W ? (id & 7) * (W >> 3) + (id >> 3) : id;
-}
+// Workgroups are dealt to the eight XCDs in turn: their indices are renamed so that an XCD
+// gets neighbouring units, whose row blocks read the same keys from its own L2.
+__device__ __forceinline__ int renamed(int id, int W) { return (id & 7) * (W >> 3) + (id >> 3); }
 
 // What the joining kernel has to know of workgroup w's first unit: nothing (parts = 0)
 // unless it is the first border between workgroups inside its item.
 struct Border {
   int r, h, b, n;
-  int slot0, parts;    // the item's partial sums: slot0, then 2 w, 2 (w + 1), ...
-  int pad[2];
+  int slot0, parts;    // the item's partial sums: slot0, then the first ones of the workgroups
+  int unit, total;     // that have `unit`, the units after it, ... of `total`
 };
 __device__ __forceinline__ Border border_of(const Item &it, int w, int W, int total) {
-  Border d = {it.r, it.h, it.b, it.n, 0, 0, {0, 0}};
-  const int u0 = int(it.first), u1 = u0 + it.units;
-  const int before = w > 0 ? first_unit(w - 1, W, total) : 0;
-  if (it.at == 0 || before > u0) return d;
-  d.slot0 = 2 * (w - 1) + (before == u0 ? 0 : 1);
-  const int end = total >= W ? int((int64_t(u1) * W + total - 1) / total) : u1;  // first workgroup past the item
-  d.parts = 1 + end - w;
+  const int unit = int(it.first) + it.at, u0 = int(it.first), u1 = u0 + it.units;
+  Border d = {it.r, it.h, it.b, it.n, 0, 0, unit, total};
+  if (it.at == 0) return d;
+  const int last = total < W ? only_unit(unit - 1, W, total) : w - 1;  // the workgroup before
+  const int before = total < W ? unit - 1 : first_unit(last, W, total);
+  if (before > u0) return d;
+  d.slot0 = 2 * last + (before == u0 ? 0 : 1);
+  const int end = total < W ? u1 - unit : int((int64_t(u1) * W + total - 1) / total) - w;  // workgroups to the item's end
+  d.parts = 1 + end;
   return d;
+}
+__device__ __forceinline__ int slot_of(const Border &d, int part, int w, int W) {
+  if (part == 0) return d.slot0;
+  return 2 * (d.total < W ? only_unit(d.unit + part - 1, W, d.total) : w + part - 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -676,7 +679,7 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
   const int row16 = lane & 15, g = lane >> 4;
   unit_prefix<kThreads>(a, ROWS, pre, red);
   const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
-  const int w = renamed(blockIdx.x, W, total);
+  const int w = renamed(blockIdx.x, W);
   const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
   const float c2 = a.scale * 1.44269504088896340736f, slack = slack_of(c2);  // scores to powers of two
   if (u_begin == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
@@ -976,7 +979,7 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
   const St st = {lds, wave, lane};
   unit_prefix<S::threads>(a, ROWS, pre, red);
   const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
-  const int w = renamed(blockIdx.x, W, total);
+  const int w = renamed(blockIdx.x, W);
   const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
   const float c2 = a.scale * 1.44269504088896340736f, slack = slack_of(c2);
   if (u_begin == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
@@ -1151,59 +1154,101 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
 }
 
 // ---------------------------------------------------------------------------
-// Adds the partial sums of an item that several workgroups share; workgroup w has the
-// item whose first border inside it is the beginning of main workgroup w, if there is
-// one.  Four parts at a time are on their way.  blockIdx.y: 1024 values of the rows.
-__global__ __launch_bounds__(kThreads) void tree_combine_kernel(const TreeArgs a, int rows, int D) {
-  const int w = blockIdx.x;
-  const Border d = reinterpret_cast<const Border *>(a.borders)[w];
-  if (d.parts == 0) return;
+// Adds the partial sums of the items that several workgroups share.  blockIdx.x takes its
+// share of the borders between the W main workgroups, of which those that are the first
+// inside their item have parts to add; blockIdx.y takes some values of the item's rows.  A
+// thread holds four neighbouring values, with four parts on their way at a time.  Where the
+// items are few, so that each has many parts, GROUPS = 4 groups of threads take every
+// fourth part: a long cache of few heads has over a hundred parts an item, and added in a
+// row they took longer than the attention (one request, 4 heads, 65536 keys, 16 rows: 60 us
+// in all with one group, 35 with four; sixteen trees over 8192 keys, two or three parts an
+// item: 114 with one, 135 with four).
+template <int GROUPS>
+__global__ __launch_bounds__(GROUPS == 1 ? 256 : 512) void tree_combine_kernel(const TreeArgs a, int rows, int D, int W) {
+  constexpr int kJoinGroup = GROUPS == 1 ? 256 : 512 / GROUPS;
+  __shared__ f32x4 s_o[GROUPS][GROUPS == 1 ? 1 : kJoinGroup];
+  __shared__ float2 s_ml[GROUPS][GROUPS == 1 ? 1 : kJoinGroup];
+  const int lane = threadIdx.x & 63, group = threadIdx.x / kJoinGroup, me = threadIdx.x % kJoinGroup;
   const float c2 = a.scale * 1.44269504088896340736f;
-  const int threads_a_row = D / 4, lane = threadIdx.x % threads_a_row;
-  const int per_pass = kThreads / threads_a_row;
-  const int q0 = max(a.q_start[d.r], 0);
-  for (int row = blockIdx.y * per_pass + threadIdx.x / threads_a_row; row < rows; row += gridDim.y * per_pass) {
-    const int64_t all = int64_t(d.b) * rows + row;
-    const int node = int(all / a.G);
-    if (node >= d.n) break;
-    float m = kNegInf, l = 0.0f;
-    f32x4 o = {0, 0, 0, 0};
-    for (int p = 0; p < d.parts; p += 4) {
-      float2 ml[4];
-      f32x4 v[4];
+  const int value = blockIdx.y * (4 * kJoinGroup) + 4 * me, row = value / D, d = value - row * D;
+  const Border *borders = reinterpret_cast<const Border *>(a.borders);
+  const int end = W / gridDim.x * (blockIdx.x + 1);
+  for (int base = W / gridDim.x * blockIdx.x; base < end; base += 64) {
+    uint64_t owners = __ballot(base + lane < end && borders[base + lane].parts != 0);
+    while (owners) {                                   // the same in every wave
+      const int w = base + __builtin_ctzll(owners);
+      owners &= owners - 1;
+      const Border b = borders[w];
+      const int64_t all = int64_t(b.b) * rows + row;
+      const int node = int(all / a.G);
+      const bool there = row < rows && node < b.n;
+      float m = kNegInf, l = 0.0f;
+      f32x4 o = {0, 0, 0, 0};
+      for (int p = group; there && p < b.parts; p += 4 * GROUPS) {
+        float2 ml[4];
+        f32x4 v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int part = min(p + i, d.parts - 1);
-        const int64_t line = int64_t(part == 0 ? d.slot0 : 2 * (w + part - 1)) * rows + row;
-        ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * line);
-        v[i] = *reinterpret_cast<const f32x4 *>(a.part_o + line * D + 4 * lane);
+        for (int i = 0; i < 4; ++i) {
+          const int part = min(p + i * GROUPS, b.parts - 1);
+          const int64_t line = int64_t(slot_of(b, part, w, W)) * rows + row;
+          ml[i] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * line);
+          v[i] = *reinterpret_cast<const f32x4 *>(a.part_o + line * D + d);
+        }
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (p + i * GROUPS < b.parts) top = fmaxf(top, ml[i].x);
+        const float keep = m == top ? 1.0f : __builtin_amdgcn_exp2f((m - top) * c2);
+        l *= keep;
+        o *= keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (p + i * GROUPS < b.parts) {
+            const float f = ml[i].x == top ? 1.0f : __builtin_amdgcn_exp2f((ml[i].x - top) * c2);
+            l += f * ml[i].y;
+            o += f * v[i];
+          }
+        m = top;
       }
       float top = m;
+      if constexpr (GROUPS > 1) {
+        s_o[group][me] = o;
+        s_ml[group][me] = make_float2(m, l);
+        __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, ml[i].x);
-      const float keep = m == top ? 1.0f : __builtin_amdgcn_exp2f((m - top) * c2);
-      l *= keep;
-      o *= keep;
+        for (int i = 0; i < GROUPS; ++i) top = fmaxf(top, s_ml[i][me].x);
+        l = 0.0f;
+        o = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = p + i >= d.parts ? 0.0f : ml[i].x == top ? 1.0f : __builtin_amdgcn_exp2f((ml[i].x - top) * c2);
-        if (p + i < d.parts) {
-          l += f * ml[i].y;
-          o += f * v[i];
+        for (int i = 0; i < GROUPS; ++i) {
+          const float2 x = s_ml[i][me];
+          const float f = x.x == top ? 1.0f : __builtin_amdgcn_exp2f((x.x - top) * c2);
+          l += f * x.y;
+          o += f * s_o[i][me];
         }
+        __syncthreads();
       }
-      m = top;
+      if (group == 0 && there) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int64_t at =
+            int64_t(max(a.q_start[b.r], 0) + node) * a.H * a.G + b.h * a.G + (all - int64_t(node) * a.G);
+        const uint2 x = {pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv)};
+        *reinterpret_cast<uint2 *>(a.out + at * D + d) = x;
+        if (a.lse && d == 0) a.lse[at] = Results<64, 1>::log_sum(top, l, c2);
+      }
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int64_t at = int64_t(q0 + node) * a.H * a.G + d.h * a.G + (all - int64_t(node) * a.G);
-    const uint2 x = {pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv)};
-    *reinterpret_cast<uint2 *>(a.out + at * D + 4 * lane) = x;
-    if (a.lse && lane == 0) a.lse[at] = Results<64, 1>::log_sum(m, l, c2);
   }
 }
 
-void combine(const TreeArgs &a, int grid, int rows, int D, hipStream_t stream) {
-  hipLaunchKernelGGL(tree_combine_kernel, dim3(grid, rows * D / 1024), dim3(kThreads), 0, stream, a, rows, D);
+void combine(const TreeArgs &a, int W, int rows, int D, hipStream_t stream) {
+  const int64_t items = a.H * (int64_t(a.T) * a.G / rows + a.R);  // there can be
+  if (8 * items > W) {
+    hipLaunchKernelGGL(tree_combine_kernel<1>, dim3(W, rows * D / 1024), dim3(256), 0, stream, a, rows, D, W);
+  } else {
+    int X = 8;                                         // columns: a power of two, enough for each item
+    while (X < items) X *= 2;
+    hipLaunchKernelGGL(tree_combine_kernel<4>, dim3(X, rows * D / 512), dim3(512), 0, stream, a, rows, D, W);
+  }
 }
 
 template <int D, bool E4M3, int RT>
