@@ -18,15 +18,15 @@
 // An item that falls to several workgroups leaves partial sums in the workspace, which
 // tree_combine_kernel adds in a fixed order.
 //
-// Two kernels.  `split` (up to 32 rows of a cache head): bound by the cache's bytes.  The
+// Two kernels.  `split` (few rows of a cache head): bound by the cache's bytes.  The
 // four waves of a workgroup hold the same rows and take different keys; K and V go from
 // memory straight into operand registers, and LDS only joins the waves' sums at the end.
 // `share` (more rows): bound by the matrix cores and the exponentials.  The waves hold
-// different rows and take the same keys, which are staged in LDS two steps deep, so that
-// memory is read once for 64 or 128 rows.
+// different rows and take the same keys, which are staged in LDS two or four steps deep, so
+// that memory is read once for 64 or 128 rows.
 //
 // Rounding: q.k and p.v are sums of bf16 products in f32; the probabilities are
-// rounded once to bf16 for the product with V (relative 2^-9 each, with errors of both
+// rounded once to bf16 for the product with V (off by 2^-8 of it at most, with errors of both
 // signs), while their sum is taken before that rounding.
 #include <type_traits>
 
@@ -1273,30 +1273,41 @@ hipError_t launch_share(const TreeArgs &a, const char *name, hipStream_t stream)
   return hipGetLastError();
 }
 
-// Rows of one cache head in the step's longest request decide the form: up to 32 rows
-// every row sits in each wave and the waves split the keys; above, they share the keys.
-// 2-byte elements of 256-wide heads leave the split form registers for 16 rows a wave.
+// Rows of one cache head in the step's longest request decide the form.  In the split form
+// every row of a block sits in each wave and the waves split the keys; blocks of 16 or 32
+// rows, of which several read the same keys.  In the share form they share the keys through
+// LDS in blocks of 64 or 128 rows.  Split and share, us, 8 cache heads (16 requests over
+// 8192 keys; 16 over 1024; one over 16384):
+//   bf16   64-wide,  64 rows   52  63 |  19  22 | 18 20    128 rows   80  80 |  20  31 | 21 25
+//   bf16  128-wide,  32 rows  112 106 |  26  27 | 25 25     64 rows  114 112 |  26  33 | 30 27
+//                                                           96 rows  233 122
+//   bf16  256-wide,  32 rows  209 202 |  30  38 | 31 33     64 rows  399 209 |  52  44 | 38 36
+//   e4m3   64-wide, 256 rows  158 162
+//   e4m3  128-wide, 128 rows  113 124 |  28  48 | 29 37    256 rows  215 210 |  47  58 | 46 50
+//   e4m3  256-wide,  64 rows  154 176                       96 rows  266 183
+// A step widened to two bytes in LDS for each block costs e4m3 more than bytes read again,
+// so its split form goes further.  2-byte elements of 256-wide heads leave the split form
+// registers for 16 rows a wave.
 struct Form {
   bool share;
   int tiles, waves;  // of 16 rows a wave; with different rows
 };
 Form tree_form(int64_t rows, int64_t D, bool e4m3) {
-  if (rows <= 32) return {false, rows <= 16 || (D == 256 && !e4m3) ? 1 : 2, 1};
-  return {true, rows <= 64 || D == 256 ? 1 : 2, D == 256 ? 8 : 4};
+  if (rows <= (e4m3 ? (D == 256 ? 64 : 256) : (D == 64 ? 64 : 32)))
+    return {false, rows <= 16 || (D == 256 && !e4m3) ? 1 : 2, 1};
+  // 64 rows in blocks of 128 leave half the waves idle: 116 us for 112
+  return {true, D == 256 || (rows <= 64 && D == 128) ? 1 : 2, D == 256 ? 8 : 4};
 }
 int form_rows(Form f) { return 16 * f.tiles * f.waves; }
 
 template <int D, bool E4M3>
 hipError_t pick(const TreeArgs &a, Form f, hipStream_t stream) {
   if (f.share) {
-    if constexpr (D != 256) {
-      if (f.tiles == 2)
-        return launch_share<D, E4M3, 2>(a, E4M3 ? "tree_attention_e4m3_share128" : "tree_attention_bf16_share128", stream);
+    if constexpr (D == 128 && !E4M3) {
+      if (f.tiles == 1) return launch_share<D, E4M3, 1>(a, "tree_attention_bf16_share64", stream);
     }
-    if constexpr (D == 256)
-      return launch_share<D, E4M3, 1>(a, E4M3 ? "tree_attention_e4m3_share128" : "tree_attention_bf16_share128", stream);
-    else
-      return launch_share<D, E4M3, 1>(a, E4M3 ? "tree_attention_e4m3_share64" : "tree_attention_bf16_share64", stream);
+    return launch_share<D, E4M3, D == 256 ? 1 : 2>(
+        a, E4M3 ? "tree_attention_e4m3_share128" : "tree_attention_bf16_share128", stream);
   }
   if constexpr (D != 256 || E4M3) {
     if (f.tiles == 2)

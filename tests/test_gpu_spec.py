@@ -625,3 +625,32 @@ def test_step_on_another_stream_and_in_a_graph(tl, torch):
         announce(f"  replay {seed}")
         for n, (a, b) in enumerate(zip(result(r), eager[seed])):
             assert torch.equal(a, b), f"output {n}"
+
+
+FORMS = [(64, False, 4, "bf16_split16"), (64, False, 16, "bf16_split32"), (64, False, 17, "bf16_share128"),
+         (128, False, 4, "bf16_split16"), (128, False, 8, "bf16_split32"), (128, False, 16, "bf16_share64"),
+         (128, False, 17, "bf16_share128"), (256, False, 8, "bf16_split16"), (256, False, 9, "bf16_share128"),
+         (64, True, 4, "e4m3_split16"), (64, True, 64, "e4m3_split32"), (64, True, 65, "e4m3_share128"),
+         (128, True, 4, "e4m3_split16"), (128, True, 64, "e4m3_split32"), (128, True, 65, "e4m3_share128"),
+         (256, True, 4, "e4m3_split16"), (256, True, 16, "e4m3_split32"), (256, True, 17, "e4m3_share128")]
+
+
+@pytest.mark.parametrize("D,e4m3,nodes,form", FORMS)
+def test_attention_each_form(tl, D, e4m3, nodes, form):
+    """Both sides of each border between the kernel's forms (4 query heads a cache head), with trees that fill a
+    block of rows and trees that do not, bad pages, empty rows and values that are not finite beside each tree."""
+    reqs = [(min(nodes, 64), 150), (1, 700), (3, 0), (min(nodes, 64) // 2, 300), (nodes, 65)]
+    c = Case(tl, reqs, 2, 4, D, e4m3, 32, seed=nodes + D)
+    c.table[1, 4] = -1
+    c.mask[c.q_start[2]:c.q_start[2] + 3] = [1, 0, 5]    # a node that sees nothing: there is no context either
+    nan = 0x7F if e4m3 else 0x7FC0
+    at = {w: ref.offsets(w, c.es, 32, D) for w in "kv"}
+    for r in range(len(reqs)):                           # tokens past the end of each last page
+        for pos in range(int(c.kv[r]), -(-int(c.kv[r]) // 32) * 32):
+            c.kbits[c.table[r, pos // 32], :].reshape(2, -1)[:, at["k"][pos % 32]] = nan
+            c.vbits[c.table[r, pos // 32], :].reshape(2, -1)[:, at["v"][pos % 32]] = nan
+    c.vbits[c.table[2, 0], 1].reshape(-1)[at["v"][2, 7]] = nan   # seen by its own node alone
+    c.call().check()
+    assert tl.last_kernel_name() == "tree_attention_" + form
+    got = values(raw(c.out))[c.q_start[2]:]
+    assert np.isnan(got[2, 4:, 7]).all() and np.isfinite(got[:2]).all() and (got[1] == 0).all()
