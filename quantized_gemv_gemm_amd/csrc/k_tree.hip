@@ -528,23 +528,31 @@ __device__ __forceinline__ bf16x8 clean(bf16x8 x, const uint32_t *keep, uint32_t
   return __builtin_bit_cast(bf16x8, w);
 }
 
-// The running maximum of one row tile with new scores: the new maximum, not yet taken over.
-__device__ __forceinline__ float row_top(const f32x4 &s0, const f32x4 &s1, float before) {
-  const float top = fmaxf(fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s0[2], s0[3])), fmaxf(fmaxf(s1[0], s1[1]), fmaxf(s1[2], s1[3])));
-  return fmaxf(row_max(top), before);
-}
-// Takes a new maximum over, rescaling the sums, once it is past the old one by `slack`:
-// weights up to 2^8 are as exact as those up to 1, and a maximum still creeps up for long
-// after it is nearly reached (with the rescale at every rise a quarter of the steps over
-// 8192 keys had one).
+// New scores: takes a row's new maximum over, rescaling the sums, once it is past the old
+// one by `slack`: weights up to 2^8 are as exact as those up to 1, and a maximum still
+// creeps up for long after it is nearly reached (with the rescale at every rise a quarter
+// of the steps over 8192 keys had one).  So a lane looks at its own eight scores alone, and
+// the four lanes of a row meet only where one of them is past it.
 template <int D, int RT>
-__device__ __forceinline__ void take_top(float top, float slack, float c2, int t, Rows<D, RT> &acc) {
-  if (__any(top > acc.m[t] + slack)) {
-    const float f = top > acc.m[t] ? __builtin_amdgcn_exp2f((acc.m[t] - top) * c2) : 1.0f;
+__device__ __forceinline__ void take_tops(const f32x4 (&s0)[RT], const f32x4 (&s1)[RT], float slack, float c2,
+                                          Rows<D, RT> &acc) {
+  float top[RT];
+  bool past = false;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    top[t] = fmaxf(fmaxf(fmaxf(s0[t][0], s0[t][1]), fmaxf(s0[t][2], s0[t][3])),
+                   fmaxf(fmaxf(s1[t][0], s1[t][1]), fmaxf(s1[t][2], s1[t][3])));
+    past |= top[t] > acc.m[t] + slack;
+  }
+  if (!__any(past)) return;
+#pragma unroll
+  for (int t = 0; t < RT; ++t) {
+    const float m = fmaxf(row_max(top[t]), acc.m[t]);
+    const float f = m > acc.m[t] ? __builtin_amdgcn_exp2f((acc.m[t] - m) * c2) : 1.0f;
     acc.l[t] *= f;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) acc.o[j][t] *= f;
-    acc.m[t] = top;
+    acc.m[t] = m;
   }
 }
 // 8 as a power of two, in raw scores; finite, so that it leaves -inf as it is
@@ -752,11 +760,9 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
       }
       bf16x8 p[RT];
       uint32_t zero[RT];
+      take_tops(sc[0], sc[1], slack, c2, acc);
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        take_top(row_top(sc[0][t], sc[1][t], acc.m[t]), slack, c2, t, acc);
-        p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
-      }
+      for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
 #pragma unroll
       for (int j = 0; j < OC; ++j) {
         const bf16x8 va = vt.v_operand(j);
@@ -1085,8 +1091,7 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
       }
       bf16x8 p[RT];
       uint32_t zero[RT];
-#pragma unroll
-      for (int t = 0; t < RT; ++t) take_top(row_top(sc[0][t], sc[1][t], acc.m[t]), slack, c2, t, acc);
+      take_tops(sc[0], sc[1], slack, c2, acc);
 #pragma unroll
       for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
 #pragma unroll
