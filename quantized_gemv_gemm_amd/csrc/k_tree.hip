@@ -66,47 +66,58 @@ __device__ __forceinline__ int request_nodes(const TreeArgs &a, int r) {
 __device__ __forceinline__ int request_keys(const TreeArgs &a, int r) {
   return min(max(a.kv_lens[r], 0), a.max_keys);
 }
-__device__ __forceinline__ int row_blocks(int n, int G, int rows) { return int((int64_t(n) * G + rows - 1) / rows); }
+// (n G stays below 2^31)
+__device__ __forceinline__ int row_blocks(int n, int G, int rows) { return (uint32_t(n) * G + rows - 1) / uint32_t(rows); }
 
 // A request of up to 64 nodes has the same keys for every row block; a longer one is a
 // chain, whose row block ends at its last node's own key.
 __device__ __forceinline__ int block_keys(int n, int kv, int b, int G, int rows) {
   if (n <= kTreeNodes) return kv;
-  const int last = int((min(int64_t(b + 1) * rows, int64_t(n) * G) - 1) / G);
+  const int last = min(int((uint32_t(b + 1) * rows - 1) / uint32_t(G)), n - 1);
   return max(kv - n + last + 1, 0);
 }
 __device__ __forceinline__ int block_units(int n, int kv, int b, int G, int rows) {
   return max((block_keys(n, kv, b, G, rows) + kUnitKeys - 1) / kUnitKeys, 1);
 }
 
-// pre[r] = units of the requests before r (R + 1 entries), by a whole workgroup of NT threads.
+// pre[r] = units of the requests before r (R + 1 entries), by a whole workgroup of NT
+// threads.  Requests are dealt to the waves in turn.  A chain's blocks are counted by its
+// own lane if they are few, else by the whole wave (64 prompts of 100 tokens, all of them
+// in one wave and that one counting each: 87 us of attention, of which 62 are left).
 template <int NT>
 __device__ __forceinline__ void unit_prefix(const TreeArgs &a, int rows, int *pre, int *red) {
+  constexpr int kOwnBlocks = 16, WAVES = NT / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (a.R + NT - 1) / NT, r0 = tid * per;
-  int sum = 0;
-  for (int j = 0; j < per; ++j) {  // the same count in every lane: the loop below needs them all
-    const int r = r0 + j;
-    int n = 0, kv = 0, units = 0;
+  for (int base = 0; base < a.R; base += NT) {
+    const int r = base + WAVES * lane + wave;
+    int n = 0, kv = 0, nb = 0, units = 0;
     if (r < a.R) {
       n = request_nodes(a, r);
       kv = request_keys(a, r);
-      if (n && n <= kTreeNodes) units = row_blocks(n, a.G, rows) * block_units(n, kv, 0, a.G, rows);
+      nb = row_blocks(n, a.G, rows);
+      if (n <= kTreeNodes) units = nb * block_units(n, kv, 0, a.G, rows);
+      else if (nb <= kOwnBlocks)
+        for (int b = 0; b < nb; ++b) units += block_units(n, kv, b, a.G, rows);
     }
-    uint64_t longs = __ballot(n > kTreeNodes);
+    uint64_t longs = __ballot(n > kTreeNodes && nb > kOwnBlocks);
     while (longs) {
       const int src = __builtin_ctzll(longs);
       longs &= longs - 1;
-      const int ln = __shfl(n, src, 64), lkv = __shfl(kv, src, 64), nb = row_blocks(ln, a.G, rows);
+      const int ln = __builtin_amdgcn_readlane(n, src), lkv = __builtin_amdgcn_readlane(kv, src);
+      const int blocks = __builtin_amdgcn_readlane(nb, src);
       int part = 0;
-      for (int b = lane; b < nb; b += 64) part += block_units(ln, lkv, b, a.G, rows);
+      for (int b = lane; b < blocks; b += 64) part += block_units(ln, lkv, b, a.G, rows);
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) part += __shfl_xor(part, off, 64);
       if (lane == src) units = part;
     }
-    sum += units * a.H;
-    if (r < a.R) pre[r + 1] = sum;  // within this thread so far
+    if (r < a.R) pre[r + 1] = units * a.H;
   }
+  __syncthreads();
+  const int per = (a.R + NT - 1) / NT, r0 = tid * per;
+  int sum = 0;
+  for (int j = 0; j < per; ++j)
+    if (r0 + j < a.R) pre[r0 + j + 1] = sum += pre[r0 + j + 1];  // within this thread so far
   int run = sum;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
@@ -194,7 +205,13 @@ __device__ __forceinline__ Border border_of(const Item &it, int w, int W, int to
   const int before = total < W ? unit - 1 : first_unit(last, W, total);
   if (before > u0) return d;
   d.slot0 = 2 * last + (before == u0 ? 0 : 1);
-  const int end = total < W ? u1 - unit : int((int64_t(u1) * W + total - 1) / total) - w;  // workgroups to the item's end
+  int end = u1 - unit;                                 // workgroups to the item's end
+  if (total >= W) {
+    int e = int(double(u1) * W / total);               // the first whose first unit is u1 or more, or one off
+    while (first_unit(e, W, total) < u1) ++e;
+    while (first_unit(e - 1, W, total) >= u1) --e;
+    end = e - w;
+  }
   d.parts = 1 + end;
   return d;
 }
@@ -393,8 +410,11 @@ struct Queries {
       node[t] = row / a.G;
       const bool there = node[t] < s.n;
       const int64_t tok = s.q0 + (there ? node[t] : 0);
-      sees[t] = 0;
-      if (s.flat && there) sees[t] = a.tree_mask ? a.tree_mask[tok] : (~uint64_t(0) >> (63 - node[t]));
+      // without a branch that lanes part at: the compiler has been seen to save registers that
+      // are needed later at the end of one, before the lanes that stayed away are back
+      uint64_t own = ~uint64_t(0) >> ((63 - node[t]) & 63);
+      if (a.tree_mask) own = a.tree_mask[tok];         // uniform
+      sees[t] = s.flat && there ? own : 0;
       const uint16_t *src = a.q + tok * a.ldq + int64_t(s.h * a.G + (there ? row - node[t] * a.G : 0)) * D;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
@@ -1184,8 +1204,8 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : 512) void tree_combine_kernel(c
       const int w = base + __builtin_ctzll(owners);
       owners &= owners - 1;
       const Border b = borders[w];
-      const int64_t all = int64_t(b.b) * rows + row;
-      const int node = int(all / a.G);
+      const uint32_t all = uint32_t(b.b) * rows + row;
+      const int node = all / uint32_t(a.G);
       const bool there = row < rows && node < b.n;
       float m = kNegInf, l = 0.0f;
       f32x4 o = {0, 0, 0, 0};
@@ -1236,7 +1256,7 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : 512) void tree_combine_kernel(c
       if (group == 0 && there) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int64_t at =
-            int64_t(max(a.q_start[b.r], 0) + node) * a.H * a.G + b.h * a.G + (all - int64_t(node) * a.G);
+            int64_t(max(a.q_start[b.r], 0) + node) * a.H * a.G + b.h * a.G + int(all - uint32_t(node) * a.G);
         const uint2 x = {pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv)};
         *reinterpret_cast<uint2 *>(a.out + at * D + d) = x;
         if (a.lse && d == 0) a.lse[at] = Results<64, 1>::log_sum(top, l, c2);
