@@ -181,6 +181,12 @@ __device__ __forceinline__ Item locate(const TreeArgs &a, int rows, const int *p
   return it;
 }
 
+// unit u, or the first of its item if that has `undivided` units at most
+__device__ __forceinline__ int whole_from(const TreeArgs &a, int rows, const int *pre, int u, int undivided) {
+  const Item it = locate(a, rows, pre, u);
+  return __builtin_amdgcn_readfirstlane(it.units <= undivided ? int(it.first) : u);
+}
+
 // first unit of workgroup w of W (with fewer units than workgroups some have none)
 __device__ __forceinline__ int first_unit(int w, int W, int total) { return int(int64_t(total) * w / W); }
 // the workgroup that has unit u, with fewer units than workgroups: one each
@@ -875,6 +881,12 @@ struct Share {
   static constexpr int threads = 64 * waves;
   static constexpr int rows = 16 * RT * waves;
   static constexpr int grid = 2048 / waves;            // eight waves a compute unit
+  // Items of up to three units stay whole, with the workgroup that has their last one: the
+  // partial sums of 128 rows, written and read again, cost more than a unit (64 trees over
+  // 300 keys 59 -> 52 us, a prompt of 300 tokens 34 -> 27, 128-wide heads; eight trees over
+  // 350 keys on average 33 -> 35).  With five, four prompts of 500 go from 57 to 42, but
+  // eight trees over 350 from 35 to 40 and one over 512 from 22 to 35.
+  static constexpr int undivided = 3;
   static constexpr int ring = D == 256 && E4M3 ? 2 : 4;  // steps on their way or in use
   static constexpr int tile = 16 * D * (E4M3 ? 1 : 2); // bytes of a tile in the cache
   static constexpr int units = tile / 1024;            // its 1 KB pieces
@@ -1006,14 +1018,19 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
   unit_prefix<S::threads>(a, ROWS, pre, red);
   const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
   const int w = renamed(blockIdx.x, W);
-  const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
+  int u = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
+  if (u < u_end) {
+    if (u_end < total) u_end = whole_from(a, ROWS, pre, u_end, S::undivided);
+    u = whole_from(a, ROWS, pre, u, S::undivided);
+  }
+  const int u_begin = u;
   const float c2 = a.scale * 1.44269504088896340736f, slack = slack_of(c2);
-  if (u_begin == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
+  if (u == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
   // operands in a step: K of 32 d's number j, tokens of product i; V of 16 d's number j
   const int k_lane = (row16 >> 3) * (32 * D + S::gap) + 256 * g + 16 * (row16 & 7);
   const int v_lane = (g >> 1) * (32 * D + S::gap) + 256 * (g & 1) + 16 * row16;
 
-  for (int u = u_begin; u < u_end;) {
+  while (u < u_end) {
     const Item it = locate(a, ROWS, pre, u);
     if (u == u_begin && threadIdx.x == 0) reinterpret_cast<Border *>(a.borders)[w] = border_of(it, w, W, total);
     const int take = min(__builtin_amdgcn_readfirstlane(it.units - it.at), u_end - u);
