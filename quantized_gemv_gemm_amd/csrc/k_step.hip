@@ -9,7 +9,9 @@
 //   slot  = table[r, pos / bs] * bs + pos % bs,  pos = ctx + i for the i-th new token
 //   position = ctx + depth(i), mask = bits of i and its ancestors   (trees of <= 64 nodes)
 //
-// One launch.  What bounds it is latency: a few dependent loads, whatever the sizes are.
+// One launch.  What bounds it is latency: a few dependent loads, whatever the sizes are
+// (one tree of 33 nodes 3.9 us, 512 requests with 68000 new tokens 8.6 us; a launch that
+// does nothing takes 1.8).
 // Every workgroup computes the two prefix sums over the requests for itself (R is small
 // and sits in L2) and then takes its share of tokens, so no workgroup waits for another
 // and no counter has to be cleared.  A tree is one wavefront: a lane holds a node, and

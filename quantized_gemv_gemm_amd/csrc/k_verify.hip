@@ -4,7 +4,9 @@
 //   walk: node 0 is given; from node c go to the lowest node whose parent is c and whose
 //   drafted token is target(c); accepted = nodes walked, next = target of the last one.
 //
-// What bounds it is reading the logits once.  Launch 1 cuts every row into `parts` so that
+// What bounds it is reading the logits once (512 rows of 248320 in bf16: 42 us, 6.1 TB/s,
+// where summing a large tensor reaches 5.9, and 4.8 for the walks; 17 rows in f32: 5.8 and
+// 4.2 us).  Launch 1 cuts every row into `parts` so that
 // a single tree also fills the chip.  A thread compares whole 16-byte loads: the largest of
 // their 8 (4) values against its own, and keeps the load that holds it: about 3 operations
 // a value, where comparing and remembering each one took 11 and was slower than the memory.
