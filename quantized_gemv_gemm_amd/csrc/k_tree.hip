@@ -54,6 +54,7 @@ constexpr int kUnitKeys = kStepKeys * kUnitSteps;
 constexpr int kThreads = 256, kWaves = 4;
 constexpr int kMaxGrid = 512;
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kSlack = 8;                            // of a running maximum, as a power of two
 
 // ---------------------------------------------------------------------------
 // which units there are
@@ -368,12 +369,17 @@ __device__ __forceinline__ float v_element(const char *at, int j, int i) {
 template <int D, int RT>
 struct Rows {
   f32x4 o[D / 16][RT];  // lane (n, g): query row n of row tile t, d = 16 j + 4 g + i
-  float m[RT], l[RT];   // running maximum (raw scores) and the lane's share of the sum
+  // Scores count as powers of two (times scale / ln 2).  m: what the weights are relative to,
+  // the running maximum within kSlack; past: how far above m a score may be; -inf (and m = 0)
+  // before there is any.  l: the lane's share of the sum.
+  float m[RT], past[RT], l[RT];
+  __device__ __forceinline__ float top(int t) const { return past[t] < 0.0f ? kNegInf : m[t]; }
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
-      m[t] = kNegInf;
+      m[t] = 0.0f;
+      past[t] = kNegInf;
       l[t] = 0.0f;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) o[j][t] = f32x4{0, 0, 0, 0};
@@ -560,47 +566,50 @@ __device__ __forceinline__ bf16x8 clean(bf16x8 x, const uint32_t *keep, uint32_t
   return __builtin_bit_cast(bf16x8, w);
 }
 
-// New scores: takes a row's new maximum over, rescaling the sums, once it is past the old
-// one by `slack`: weights up to 2^8 are as exact as those up to 1, and a maximum still
-// creeps up for long after it is nearly reached (with the rescale at every rise a quarter
-// of the steps over 8192 keys had one).  So a lane looks at its own eight scores alone, and
-// the four lanes of a row meet only where one of them is past it.
+// New scores, taken relative to the running maxima: e.  A row's new maximum is taken over,
+// rescaling the sums, once it is past the old one by kSlack: weights up to 2^8 are as exact
+// as those up to 1, and a maximum still creeps up for long after it is nearly reached (with
+// the rescale at every rise a quarter of the steps over 8192 keys had one).  So a lane looks
+// at its own eight scores alone, and the four lanes of a row meet only where one of them is
+// past it.  (The comparison takes e, not the scores: the compiler passes what comes out of a
+// matrix instruction through one more instruction each before it compares.)
 template <int D, int RT>
-__device__ __forceinline__ void take_tops(const f32x4 (&s0)[RT], const f32x4 (&s1)[RT], float slack, float c2,
-                                          Rows<D, RT> &acc) {
+__device__ __forceinline__ void relate(const f32x4 (&s0)[RT], const f32x4 (&s1)[RT], float c2, Rows<D, RT> &acc,
+                                       float (&e)[RT][8]) {
   float top[RT];
   bool past = false;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    top[t] = fmaxf(fmaxf(fmaxf(s0[t][0], s0[t][1]), fmaxf(s0[t][2], s0[t][3])),
-                   fmaxf(fmaxf(s1[t][0], s1[t][1]), fmaxf(s1[t][2], s1[t][3])));
-    past |= top[t] > acc.m[t] + slack;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e[t][i] = __builtin_fmaf(s0[t][i], c2, -acc.m[t]);
+      e[t][4 + i] = __builtin_fmaf(s1[t][i], c2, -acc.m[t]);
+    }
+    const float *x = e[t];
+    top[t] = fmaxf(fmaxf(fmaxf(fmaxf(x[0], x[1]), x[2]), fmaxf(fmaxf(x[3], x[4]), x[5])), fmaxf(x[6], x[7]));
+    past |= top[t] > acc.past[t];
   }
   if (!__any(past)) return;
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
-    const float m = fmaxf(row_max(top[t]), acc.m[t]);
-    const float f = m > acc.m[t] ? __builtin_amdgcn_exp2f((acc.m[t] - m) * c2) : 1.0f;
+    const float up = row_max(top[t]);
+    const bool none = acc.past[t] < 0.0f, rise = up > (none ? kNegInf : 0.0f);
+    const float by = rise ? up : 0.0f, f = none ? 1.0f : __builtin_amdgcn_exp2f(-by);
     acc.l[t] *= f;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) acc.o[j][t] *= f;
-    acc.m[t] = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[t][i] -= by;
+    acc.m[t] += by;
+    if (rise) acc.past[t] = kSlack;
   }
 }
-// 8 as a power of two, in raw scores; finite, so that it leaves -inf as it is
-__device__ __forceinline__ float slack_of(float c2) { return fminf(8.0f / c2, 1e30f); }
-// Scores of one row tile to weights under the running maximum: adds to the running sum, and
-// gives the B operand of the second product.  zero: a bit for each key whose weight is 0.
+// Relative scores of one row tile to weights: adds to the running sum, and gives the B
+// operand of the second product.  zero: a bit for each key whose weight is 0.
 template <int D, bool E4M3, int RT, bool MASKED>
-__device__ __forceinline__ bf16x8 weigh(const f32x4 &s0, const f32x4 &s1, const f32x4 *vs, float c2, int t,
-                                        Rows<D, RT> &acc, uint32_t &zero) {
-  const float mc = acc.m[t] == kNegInf ? 0.0f : acc.m[t] * c2;
-  float e[8];
+__device__ __forceinline__ bf16x8 weigh(float (&e)[8], const f32x4 *vs, int t, Rows<D, RT> &acc, uint32_t &zero) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    e[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s0[i], c2, -mc));
-    e[4 + i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s1[i], c2, -mc));
-  }
+  for (int i = 0; i < 8; ++i) e[i] = __builtin_amdgcn_exp2f(e[i]);
   acc.l[t] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
   if constexpr (MASKED) {
     zero = 0;
@@ -657,7 +666,7 @@ struct Results {
   bool there[RT];
 
   __device__ __forceinline__ void begin(const TreeArgs &a, const Segment &s, int rows, int row0, int row16, int g,
-                                        const int *node, const float *top, const float *sum, float c2, bool lead) {
+                                        const int *node, const float *top, const float *sum, bool lead) {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       const int row = row0 + 16 * t + row16;
@@ -671,13 +680,13 @@ struct Results {
           a.part_ml[2 * line] = top[t];
           a.part_ml[2 * line + 1] = sum[t];
         } else if (a.lse) {
-          a.lse[line] = log_sum(top[t], sum[t], c2);
+          a.lse[line] = log_sum(top[t], sum[t]);
         }
       }
     }
   }
-  static __device__ __forceinline__ float log_sum(float top, float sum, float c2) {
-    return top == kNegInf ? kNegInf : (top * c2 + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
+  static __device__ __forceinline__ float log_sum(float top, float sum) {
+    return top == kNegInf ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
   }
   __device__ __forceinline__ void put(const TreeArgs &a, bool whole, int j, int t, f32x4 v) const {
     if (whole) {
@@ -695,23 +704,20 @@ template <int D, bool E4M3, int RT>
 struct Split {
   static constexpr int rows = 16 * RT;
   // workgroups a compute unit holds, by registers: where it is one, 512 of them a lane
-  static constexpr int occupancy = D * RT > 256 || D * (E4M3 ? 1 : 2) > 256 ? 1 : 2;
+  static constexpr int occupancy = D * (E4M3 ? 1 : 2) > 256 ? 1 : 2;
   static constexpr int grid = 256 * occupancy;
-  // the four waves' sums are joined in rounds of at most 64 KB of LDS
-  static constexpr int rounds = RT * D > 256 ? RT * D / 256 : 1;
-  static constexpr int join_tiles = D / 16 / rounds;   // 16-d tiles joined in a round
-  static constexpr size_t lds = kWaves * join_tiles * RT * 1024 + kWaves * 2 * RT * 16 * 4;
+  // the four waves' sums are joined through LDS, up to 64 KB
+  static constexpr size_t lds = kWaves * (D / 16) * RT * 1024 + kWaves * 2 * RT * 16 * 4;
 };
 
 template <int D, bool E4M3, int RT>
 __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tree_split_kernel(const TreeArgs a) {
   using S = Split<D, E4M3, RT>;
-  constexpr int ROWS = S::rows, QC = D / 32, OC = D / 16, JT = S::join_tiles, JW = JT / kWaves, W = S::grid;
+  constexpr int ROWS = S::rows, QC = D / 32, OC = D / 16, JW = OC / kWaves, W = S::grid;
   constexpr int ES = E4M3 ? 1 : 2;
-  static_assert(JW * kWaves * S::rounds == OC, "rounds");
   extern __shared__ __align__(16) char lds[];
-  f32x4 *join = reinterpret_cast<f32x4 *>(lds);        // [wave][JT][RT][64]
-  float *stat = reinterpret_cast<float *>(lds + kWaves * JT * RT * 1024);  // [wave][2][RT * 16]
+  f32x4 *join = reinterpret_cast<f32x4 *>(lds);        // [wave][OC][RT][64]
+  float *stat = reinterpret_cast<float *>(lds + kWaves * OC * RT * 1024);  // [wave][2][RT * 16]
   int *pre = reinterpret_cast<int *>(stat + kWaves * 2 * RT * 16);
   __shared__ int red[kWaves];
 
@@ -721,7 +727,7 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
   const int total = __builtin_amdgcn_readfirstlane(pre[a.R]);
   const int w = renamed(blockIdx.x, W);
   const int u_begin = first_unit(w, W, total), u_end = first_unit(w + 1, W, total);
-  const float c2 = a.scale * 1.44269504088896340736f, slack = slack_of(c2);  // scores to powers of two
+  const float c2 = a.scale * 1.44269504088896340736f;  // scores to powers of two
   if (u_begin == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
 
   for (int u = u_begin; u < u_end;) {
@@ -792,9 +798,10 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
       }
       bf16x8 p[RT];
       uint32_t zero[RT];
-      take_tops(sc[0], sc[1], slack, c2, acc);
+      float e[RT][8];
+      relate(sc[0], sc[1], c2, acc, e);
 #pragma unroll
-      for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
+      for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(e[t], sl.v, t, acc, zero[t]);
 #pragma unroll
       for (int j = 0; j < OC; ++j) {
         const bf16x8 va = vt.v_operand(j);
@@ -827,7 +834,7 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
     for (int t = 0; t < RT; ++t) {
       acc.l[t] = row_sum(acc.l[t]);
       if (g == 0) {
-        stat[(wave * 2 + 0) * RT * 16 + 16 * t + row16] = acc.m[t];
+        stat[(wave * 2 + 0) * RT * 16 + 16 * t + row16] = acc.top(t);
         stat[(wave * 2 + 1) * RT * 16 + 16 * t + row16] = acc.l[t];
       }
     }
@@ -845,34 +852,30 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
       sum[t] = 0.0f;
 #pragma unroll
       for (int v = 0; v < kWaves; ++v) {
-        const float f = mw[v] == top[t] ? 1.0f : __builtin_amdgcn_exp2f((mw[v] - top[t]) * c2);
+        const float f = mw[v] == top[t] ? 1.0f : __builtin_amdgcn_exp2f(mw[v] - top[t]);
         sum[t] += f * stat[(v * 2 + 1) * RT * 16 + 16 * t + row16];
       }
-      const float f = acc.m[t] == top[t] ? 1.0f : __builtin_amdgcn_exp2f((acc.m[t] - top[t]) * c2);
+      const float f = acc.top(t) == top[t] ? 1.0f : __builtin_amdgcn_exp2f(acc.top(t) - top[t]);
 #pragma unroll
       for (int j = 0; j < OC; ++j) acc.o[j][t] *= f;
     }
     Results<D, RT> res;
-    res.begin(a, seg, ROWS, row0, row16, g, qs.node, top, sum, c2, wave == 0);
+    res.begin(a, seg, ROWS, row0, row16, g, qs.node, top, sum, wave == 0);
 #pragma unroll
-    for (int round = 0; round < S::rounds; ++round) {
-      if (round) __syncthreads();
+    for (int j = 0; j < OC; ++j)
 #pragma unroll
-      for (int j = 0; j < JT; ++j)
+      for (int t = 0; t < RT; ++t) join[((wave * OC + j) * RT + t) * 64 + lane] = acc.o[j][t];
+    __syncthreads();
 #pragma unroll
-        for (int t = 0; t < RT; ++t) join[((wave * JT + j) * RT + t) * 64 + lane] = acc.o[round * JT + j][t];
-      __syncthreads();
+    for (int jj = 0; jj < JW; ++jj)
 #pragma unroll
-      for (int jj = 0; jj < JW; ++jj)
+      for (int t = 0; t < RT; ++t) {
+        const int j = wave * JW + jj;
+        f32x4 v = join[(j * RT + t) * 64 + lane];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          const int j = wave * JW + jj;
-          f32x4 v = join[(j * RT + t) * 64 + lane];
-#pragma unroll
-          for (int x = 1; x < kWaves; ++x) v += join[((x * JT + j) * RT + t) * 64 + lane];
-          if (res.there[t]) res.put(a, seg.whole, round * JT + j, t, v);
-        }
-    }
+        for (int x = 1; x < kWaves; ++x) v += join[((x * OC + j) * RT + t) * 64 + lane];
+        if (res.there[t]) res.put(a, seg.whole, j, t, v);
+      }
   }
 }
 
@@ -1030,7 +1033,7 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
     u = whole_from(a, ROWS, pre, u, S::undivided);
   }
   const int u_begin = u;
-  const float c2 = a.scale * 1.44269504088896340736f, slack = slack_of(c2);
+  const float c2 = a.scale * 1.44269504088896340736f;
   if (u == u_end && threadIdx.x == 0) a.borders[8 * w + 5] = 0;
   // operands in a step: K of 32 d's number j, tokens of product i; V of 16 d's number j
   const int k_lane = (row16 >> 3) * (32 * D + S::gap) + 256 * g + 16 * (row16 & 7);
@@ -1104,6 +1107,8 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
 #pragma unroll
           for (int t = 0; t < RT; ++t) sc[i & 1][t] = mfma(f[n & 1][i], qs.q[2 * n + (i >> 1)][t], sc[i & 1][t]);
       }
+      constexpr int at = (QC / 2) & 1;                 // where V's first four went
+      read_v(1, f[~at & 1]);
       Scales sl;
       if constexpr (E4M3) {
         const f32x4 *sp = reinterpret_cast<const f32x4 *>(st.marks(s)) + 2 * g;
@@ -1134,13 +1139,13 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
       }
       bf16x8 p[RT];
       uint32_t zero[RT];
-      take_tops(sc[0], sc[1], slack, c2, acc);
+      float e[RT][8];
+      relate(sc[0], sc[1], c2, acc, e);
 #pragma unroll
-      for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(sc[0][t], sc[1][t], sl.v, c2, t, acc, zero[t]);
+      for (int t = 0; t < RT; ++t) p[t] = weigh<D, E4M3, RT, MASKED>(e[t], sl.v, t, acc, zero[t]);
 #pragma unroll
       for (int n = 0; n < OC / 4; ++n) {
-        constexpr int at = (QC / 2) & 1;               // where V's first four went
-        if (n + 1 < OC / 4) read_v(n + 1, f[(n + 1 + at) & 1]);
+        if (n > 0 && n + 1 < OC / 4) read_v(n + 1, f[(n + 1 + at) & 1]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1184,9 +1189,12 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
     }
 
 #pragma unroll
-    for (int t = 0; t < RT; ++t) acc.l[t] = row_sum(acc.l[t]);
+    for (int t = 0; t < RT; ++t) {
+      acc.l[t] = row_sum(acc.l[t]);
+      acc.m[t] = acc.top(t);
+    }
     Results<D, RT> res;
-    res.begin(a, seg, ROWS, row0, row16, g, qs.node, acc.m, acc.l, c2, true);
+    res.begin(a, seg, ROWS, row0, row16, g, qs.node, acc.m, acc.l, true);
 #pragma unroll
     for (int t = 0; t < RT; ++t)
       if (res.there[t]) {
@@ -1217,7 +1225,6 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : 512) void tree_combine_kernel(c
   __shared__ f32x4 s_o[GROUPS][GROUPS == 1 ? 1 : kJoinGroup];
   __shared__ float2 s_ml[GROUPS][GROUPS == 1 ? 1 : kJoinGroup];
   const int lane = threadIdx.x & 63, group = threadIdx.x / kJoinGroup, me = threadIdx.x % kJoinGroup;
-  const float c2 = a.scale * 1.44269504088896340736f;
   const int value = blockIdx.y * (4 * kJoinGroup) + 4 * me, row = value / D, d = value - row * D;
   const Border *borders = reinterpret_cast<const Border *>(a.borders);
   const int end = W / gridDim.x * (blockIdx.x + 1);
@@ -1246,13 +1253,13 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : 512) void tree_combine_kernel(c
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (p + i * GROUPS < b.parts) top = fmaxf(top, ml[i].x);
-        const float keep = m == top ? 1.0f : __builtin_amdgcn_exp2f((m - top) * c2);
+        const float keep = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
         l *= keep;
         o *= keep;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (p + i * GROUPS < b.parts) {
-            const float f = ml[i].x == top ? 1.0f : __builtin_amdgcn_exp2f((ml[i].x - top) * c2);
+            const float f = ml[i].x == top ? 1.0f : __builtin_amdgcn_exp2f(ml[i].x - top);
             l += f * ml[i].y;
             o += f * v[i];
           }
@@ -1270,7 +1277,7 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : 512) void tree_combine_kernel(c
 #pragma unroll
         for (int i = 0; i < GROUPS; ++i) {
           const float2 x = s_ml[i][me];
-          const float f = x.x == top ? 1.0f : __builtin_amdgcn_exp2f((x.x - top) * c2);
+          const float f = x.x == top ? 1.0f : __builtin_amdgcn_exp2f(x.x - top);
           l += f * x.y;
           o += f * s_o[i][me];
         }
@@ -1282,7 +1289,7 @@ __global__ __launch_bounds__(GROUPS == 1 ? 256 : 512) void tree_combine_kernel(c
             int64_t(max(a.q_start[b.r], 0) + node) * a.H * a.G + b.h * a.G + int(all - uint32_t(node) * a.G);
         const uint2 x = {pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv)};
         *reinterpret_cast<uint2 *>(a.out + at * D + d) = x;
-        if (a.lse && d == 0) a.lse[at] = Results<64, 1>::log_sum(top, l, c2);
+        if (a.lse && d == 0) a.lse[at] = Results<64, 1>::log_sum(top, l);
       }
     }
   }
@@ -1332,17 +1339,17 @@ hipError_t launch_share(const TreeArgs &a, const char *name, hipStream_t stream)
 //   bf16  256-wide,  32 rows  209 202 |  30  38 | 31 33     64 rows  399 209 |  52  44 | 38 36
 //   e4m3   64-wide, 256 rows  158 162
 //   e4m3  128-wide, 128 rows  113 124 |  28  48 | 29 37    256 rows  215 210 |  47  58 | 46 50
-//   e4m3  256-wide,  64 rows  154 176                       96 rows  266 183
+//   e4m3  256-wide,  32 rows  119 167                       64 rows  167 176 (48: 236 171)
 // A step widened to two bytes in LDS for each block costs e4m3 more than bytes read again,
-// so its split form goes further.  2-byte elements of 256-wide heads leave the split form
-// registers for 16 rows a wave.
+// so its split form goes further.  256-wide heads leave the split form registers for 16
+// rows a wave: 32 e4m3 ones are possible with all 512 registers of a lane (113 us for 119),
+// but the compiler does not come through there without spilling.
 struct Form {
   bool share;
   int tiles, waves;  // of 16 rows a wave; with different rows
 };
 Form tree_form(int64_t rows, int64_t D, bool e4m3) {
-  if (rows <= (e4m3 ? (D == 256 ? 64 : 256) : (D == 64 ? 64 : 32)))
-    return {false, rows <= 16 || (D == 256 && !e4m3) ? 1 : 2, 1};
+  if (rows <= (D == 256 ? 32 : e4m3 ? 256 : D == 64 ? 64 : 32)) return {false, rows <= 16 || D == 256 ? 1 : 2, 1};
   // 64 rows in blocks of 128 leave half the waves idle: 116 us for 112
   return {true, D == 256 || (rows <= 64 && D == 128) ? 1 : 2, D == 256 ? 8 : 4};
 }
@@ -1357,7 +1364,7 @@ hipError_t pick(const TreeArgs &a, Form f, hipStream_t stream) {
     return launch_share<D, E4M3, D == 256 ? 1 : 2>(
         a, E4M3 ? "tree_attention_e4m3_share128" : "tree_attention_bf16_share128", stream);
   }
-  if constexpr (D != 256 || E4M3) {
+  if constexpr (D != 256) {
     if (f.tiles == 2)
       return launch_split<D, E4M3, 2>(a, E4M3 ? "tree_attention_e4m3_split32" : "tree_attention_bf16_split32", stream);
   }
