@@ -1058,13 +1058,22 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
     Window ahead;
     plain = min(plain, ahead.fill(a, seg, 2 * seg.s0, lane) >> 1);
     int issued = seg.s0;
+    [[maybe_unused]] int ready = seg.s0;               // steps before are in LDS for all waves
     auto bring = [&]() {
       if (2 * issued - ahead.first >= 64) plain = min(plain, ahead.fill(a, seg, 2 * issued, lane) >> 1);
       st.bring(a, issued, ahead.tile(2 * issued), ahead.tile(2 * issued + 1));
       ++issued;
     };
+    // what there is room for: all waves are done with the steps before this turn's
+    auto refill = [&]() {
+      if constexpr (E4M3) {
+        if (issued < s1) bring();
+      } else {
+        while (issued < min(ready + 2, s1)) bring();
+      }
+    };
     lds_barrier();                                     // the last segment's readers are done
-    for (int i = 0; i < S::ring - 1 && issued < s1; ++i) bring();
+    for (int i = 0; i < (E4M3 ? S::ring - 1 : 2) && issued < s1; ++i) bring();
     if constexpr (E4M3) {
       if (seg.s0 < s1) {
         st.arrive(issued - 1 - seg.s0);
@@ -1072,8 +1081,8 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
       }
     }
     // One step.  Operands are read from LDS four at a time, the next four on their way
-    // while four are multiplied, and V's first four while the scores are weighed.
-    // The next step is begun to be brought while the first operands come.
+    // while four are multiplied, and V's first eight while the scores are weighed.
+    // Later steps are begun to be brought while the first operands come.
     auto step = [&](int s, int64_t t0, int64_t t1, int lim0, int lim1, auto mask_tag) {
       constexpr bool MASKED = decltype(mask_tag)::value;
       const char *kb = st.use_k(s) + k_lane, *vb = st.use_v(s) + v_lane;
@@ -1094,7 +1103,7 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
       if (QC > 2) read_k(1, f[1]);
       else read_v(0, f[1]);
       __builtin_amdgcn_sched_barrier(0);
-      if (issued < s1) bring();
+      refill();
 #pragma unroll
       for (int n = 0; n < QC / 2; ++n) {
         if (n > 0) {
@@ -1108,7 +1117,7 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
           for (int t = 0; t < RT; ++t) sc[i & 1][t] = mfma(f[n & 1][i], qs.q[2 * n + (i >> 1)][t], sc[i & 1][t]);
       }
       constexpr int at = (QC / 2) & 1;                 // where V's first four went
-      read_v(1, f[~at & 1]);
+      if constexpr (OC > 4) read_v(1, f[~at & 1]);
       Scales sl;
       if constexpr (E4M3) {
         const f32x4 *sp = reinterpret_cast<const f32x4 *>(st.marks(s)) + 2 * g;
@@ -1158,13 +1167,19 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_k
       if constexpr (MASKED)
         if (__any(odd != 0)) add_not_finite<D, E4M3, RT>(a, t0, t1, lim0, lim1, vis, zero, row16, g, acc);
     };
-    // A turn: wait for the wave's own pieces of step s; the barrier makes everybody's
-    // visible and says that everybody is done with step s - 1, whose place is filled again.
+    // A turn: wait for the wave's own pieces; the barrier makes everybody's visible and says
+    // that everybody is done with the steps before, whose places are filled again.  bf16
+    // takes two steps a turn, with the next two on their way meanwhile (with one step a turn
+    // and three on their way a tree batch took 113 us for 109, a prompt chunk 350 to 371 on
+    // several cards for 348 to 363); e4m3 takes one, which is widened a turn before.
     auto turn = [&](int s, int64_t t0, int64_t t1, int lim0, int lim1, auto mask_tag) {
-      if constexpr (!E4M3) st.arrive(issued - 1 - s);
-      lds_barrier();
+      if (E4M3 || s == ready) {
+        if constexpr (!E4M3) wait_loads<0>();
+        lds_barrier();
+        ready = issued;
+      }
       if (!idle) step(s, t0, t1, lim0, lim1, mask_tag);
-      else if (issued < s1) bring();
+      else refill();
       if constexpr (E4M3) {
         if (s + 1 < s1) {
           st.arrive(issued - 2 - s);
