@@ -18,10 +18,10 @@
 // An item that falls to several workgroups leaves partial sums in the workspace, which
 // tree_combine_kernel adds in a fixed order.
 //
-// Measured, main and joining launch: one token over 1000 keys 9.5 + 3.9 us; 4 trees of 8 over
-// 131071 e4m3 keys, 8 heads of 128, 194 + 5.5 us (5.5 TB/s; reading alone reaches 5.9); 16
-// trees of 64, 4 query heads, over up to 8192 bf16 keys 104 + 13 us (2.7 TB/s, 470 TFLOP/s);
-// 2 prompts of 2048 on 2048, 24 query heads of 256, 343 + 17 us (860 TFLOP/s; a large
+// Measured, main and joining launch: one token over 1000 keys 9.7 + 3.9 us; 4 trees of 8 over
+// 131071 e4m3 keys, 8 heads of 128, 194 + 5.4 us (5.5 TB/s; reading alone reaches 5.9); 16
+// trees of 64, 4 query heads, over up to 8192 bf16 keys 97 + 13 us (2.8 TB/s, 490 TFLOP/s);
+// 2 prompts of 2048 on 2048, 24 query heads of 256, 341 + 17 us (870 TFLOP/s; a large
 // library product reaches 1205).
 //
 // Two kernels.  `split` (few rows of a cache head): bound by the cache's bytes.  The
