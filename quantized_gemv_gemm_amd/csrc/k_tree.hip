@@ -88,17 +88,20 @@ __device__ __forceinline__ int block_units(int n, int kv, int b, int G, int rows
 }
 
 // pre[r] = units of the requests before r (R + 1 entries), by a whole workgroup of NT
-// threads.  Requests are dealt to the waves in turn.  A chain's blocks are counted by its
+// threads.  Their sum stays below 2^31 because the requests' tokens do not overlap: where
+// q_start is not ascending there are no units at all.  Requests are dealt to the waves in turn.  A chain's blocks are counted by its
 // own lane if they are few, else by the whole wave (64 prompts of 100 tokens, all of them
 // in one wave and that one counting each: 87 us of attention, of which 62 are left).
 template <int NT>
 __device__ __forceinline__ void unit_prefix(const TreeArgs &a, int rows, int *pre, int *red) {
   constexpr int kOwnBlocks = 16, WAVES = NT / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  bool falls = false;
   for (int base = 0; base < a.R; base += NT) {
     const int r = base + WAVES * lane + wave;
     int n = 0, kv = 0, nb = 0, units = 0;
     if (r < a.R) {
+      falls |= a.q_start[r + 1] < a.q_start[r];
       n = request_nodes(a, r);
       kv = request_keys(a, r);
       nb = row_blocks(n, a.G, rows);
@@ -120,11 +123,11 @@ __device__ __forceinline__ void unit_prefix(const TreeArgs &a, int rows, int *pr
     }
     if (r < a.R) pre[r + 1] = units * a.H;
   }
-  __syncthreads();
+  const bool bad = __syncthreads_or(falls);
   const int per = (a.R + NT - 1) / NT, r0 = tid * per;
   int sum = 0;
   for (int j = 0; j < per; ++j)
-    if (r0 + j < a.R) pre[r0 + j + 1] = sum += pre[r0 + j + 1];  // within this thread so far
+    if (r0 + j < a.R) pre[r0 + j + 1] = sum += bad ? 0 : pre[r0 + j + 1];  // within this thread so far
   int run = sum;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {

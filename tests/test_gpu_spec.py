@@ -654,3 +654,12 @@ def test_attention_each_form(tl, D, e4m3, nodes, form):
     assert tl.last_kernel_name() == "tree_attention_" + form
     got = values(raw(c.out))[c.q_start[2]:]
     assert np.isnan(got[2, 4:, 7]).all() and np.isfinite(got[:2]).all() and (got[1] == 0).all()
+
+
+@pytest.mark.parametrize("D,hint", [(64, 1), (128, 40), (256, 12)])
+def test_attention_requests_out_of_order(tl, D, hint):
+    """Request starts that do not ascend: nothing is attended to, and nothing written."""
+    c = Case(tl, [(3, 20), (4, 200), (5, 40)], 1, 4, D, False, 16, seed=21)
+    c.q_start = np.array([0, 7, 3, 12], dtype=np.int32)
+    c.call(max_nodes=hint)
+    assert (values(raw(c.out)) == 776.0).all() and (c.lse == 777.0).all()
