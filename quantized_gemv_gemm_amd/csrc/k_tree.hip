@@ -52,7 +52,6 @@ constexpr int kStepKeys = 32;                 // keys of one step of a wave: two
 constexpr int kUnitSteps = 4;
 constexpr int kUnitKeys = kStepKeys * kUnitSteps;
 constexpr int kThreads = 256, kWaves = 4;
-constexpr int kMaxGrid = 512;
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kSlack = 8;                            // of a running maximum, as a power of two
 
@@ -89,9 +88,10 @@ __device__ __forceinline__ int block_units(int n, int kv, int b, int G, int rows
 
 // pre[r] = units of the requests before r (R + 1 entries), by a whole workgroup of NT
 // threads.  Their sum stays below 2^31 because the requests' tokens do not overlap: where
-// q_start is not ascending there are no units at all.  Requests are dealt to the waves in turn.  A chain's blocks are counted by its
-// own lane if they are few, else by the whole wave (64 prompts of 100 tokens, all of them
-// in one wave and that one counting each: 87 us of attention, of which 62 are left).
+// q_start falls there are no units at all.  Requests are dealt to the waves in turn.  A
+// chain's blocks are counted by its own lane if they are few, else by the whole wave (64
+// prompts of 100 tokens, all of them in one wave and that one counting each: 87 us of
+// attention, of which 62 are left).
 template <int NT>
 __device__ __forceinline__ void unit_prefix(const TreeArgs &a, int rows, int *pre, int *red) {
   constexpr int kOwnBlocks = 16, WAVES = NT / 64;
@@ -706,8 +706,10 @@ struct Results {
 template <int D, bool E4M3, int RT>
 struct Split {
   static constexpr int rows = 16 * RT;
-  // workgroups a compute unit holds, by registers: where it is one, 512 of them a lane
-  static constexpr int occupancy = D * (E4M3 ? 1 : 2) > 256 ? 1 : 2;
+  // workgroups a compute unit holds, by registers: where it is one, 512 of them a lane; a
+  // third one where a step has least to load (64-wide e4m3, 16 trees of 64 over up to 8192
+  // keys 92 -> 75 us, 64 of 4 over 500 27 -> 23; in bf16 16 trees of 8 go from 36 to 37)
+  static constexpr int occupancy = D * (E4M3 ? 1 : 2) > 256 ? 1 : D == 64 && E4M3 ? 3 : 2;
   static constexpr int grid = 256 * occupancy;
   // the four waves' sums are joined through LDS, up to 64 KB
   static constexpr size_t lds = kWaves * (D / 16) * RT * 1024 + kWaves * 2 * RT * 16 * 4;
@@ -892,7 +894,10 @@ struct Share {
   static constexpr int waves = D == 256 ? 8 : 4;
   static constexpr int threads = 64 * waves;
   static constexpr int rows = 16 * RT * waves;
-  static constexpr int grid = 2048 / waves;            // eight waves a compute unit
+  // waves a SIMD, by registers: a third one takes 64-wide heads, whose softmax is the longer
+  // part of a step, from 396 us to 364 (a prompt of 8192, bf16) and from 550 to 481 (e4m3)
+  static constexpr int occupancy = D == 64 ? 3 : 2;
+  static constexpr int grid = 1024 * occupancy / waves;
   // Items of up to three units stay whole, with the workgroup that has their last one: the
   // partial sums of 128 rows, written and read again, cost more than a unit (64 trees over
   // 300 keys 59 -> 52 us, a prompt of 300 tokens 34 -> 27, 128-wide heads; eight trees over
@@ -1014,7 +1019,7 @@ struct Stage {
 };
 
 template <int D, bool E4M3, int RT>
-__global__ __launch_bounds__((Share<D, E4M3, RT>::threads), 2) void tree_share_kernel(const TreeArgs a) {
+__global__ __launch_bounds__((Share<D, E4M3, RT>::threads), (Share<D, E4M3, RT>::occupancy)) void tree_share_kernel(const TreeArgs a) {
   using S = Share<D, E4M3, RT>;
   using St = Stage<D, E4M3, RT>;
   constexpr int ROWS = S::rows, QC = D / 32, OC = D / 16, W = S::grid;
@@ -1389,19 +1394,24 @@ hipError_t pick(const TreeArgs &a, Form f, hipStream_t stream) {
   return launch_split<D, E4M3, 1>(a, E4M3 ? "tree_attention_e4m3_split16" : "tree_attention_bf16_split16", stream);
 }
 
+// the most workgroups a kernel for width D has
+int64_t most_workgroups(int64_t D) { return D == 64 ? 768 : 512; }
+
 }  // namespace
 
 // partial sums of two segments a workgroup, then their maxima and sums, then the borders
 size_t tree_workspace_bytes(int64_t max_nodes, int64_t group, int64_t D, bool e4m3) {
-  return size_t(2 * kMaxGrid) * form_rows(tree_form(max_nodes * group, D, e4m3)) * (D + 2) * 4 + kMaxGrid * sizeof(Border);
+  const size_t W = most_workgroups(D);
+  return 2 * W * form_rows(tree_form(max_nodes * group, D, e4m3)) * (D + 2) * 4 + W * sizeof(Border);
 }
 
 hipError_t launch_tree_attention(TreeArgs a, int64_t D, bool e4m3, int64_t max_nodes, void *workspace,
                                  hipStream_t stream) {
   const Form f = tree_form(max_nodes * a.G, D, e4m3);
+  const int64_t lines = 2 * most_workgroups(D) * form_rows(f);
   a.part_o = static_cast<float *>(workspace);
-  a.part_ml = a.part_o + int64_t(2 * kMaxGrid) * form_rows(f) * D;
-  a.borders = reinterpret_cast<int32_t *>(a.part_ml + int64_t(2 * kMaxGrid) * form_rows(f) * 2);
+  a.part_ml = a.part_o + lines * D;
+  a.borders = reinterpret_cast<int32_t *>(a.part_ml + lines * 2);
   if (e4m3) return D == 64 ? pick<64, true>(a, f, stream) : D == 128 ? pick<128, true>(a, f, stream) : pick<256, true>(a, f, stream);
   return D == 64 ? pick<64, false>(a, f, stream) : D == 128 ? pick<128, false>(a, f, stream) : pick<256, false>(a, f, stream);
 }
