@@ -1356,13 +1356,15 @@ hipError_t launch_share(const TreeArgs &a, const char *name, hipStream_t stream)
 // rows, of which several read the same keys.  In the share form they share the keys through
 // LDS in blocks of 64 or 128 rows.  Split and share, us, 8 cache heads (16 requests over
 // 8192 keys; 16 over 1024; one over 16384):
-//   bf16   64-wide,  64 rows   52  63 |  19  22 | 18 20    128 rows   80  80 |  20  31 | 21 25
-//   bf16  128-wide,  32 rows  112 106 |  26  27 | 25 25     64 rows  114 112 |  26  33 | 30 27
-//                                                           96 rows  233 122
-//   bf16  256-wide,  32 rows  209 202 |  30  38 | 31 33     64 rows  399 209 |  52  44 | 38 36
-//   e4m3   64-wide, 256 rows  158 162
-//   e4m3  128-wide, 128 rows  113 124 |  28  48 | 29 37    256 rows  215 210 |  47  58 | 46 50
-//   e4m3  256-wide,  32 rows  119 167                       64 rows  167 176 (48: 236 171)
+//   bf16   64-wide,  64 rows   53  59 | 20 26 | 19 26      128 rows   79  70 | 21 33 | 22 29
+//   bf16  128-wide,  32 rows  110 108 | 28 28 | 26 26       64 rows  121 124 | 27 34 | 31 28
+//                                                           96 rows  236 125 | 39 43 | 37 31
+//   bf16  256-wide,  32 rows  207 195 | 31 40 | 32 35       64 rows  402 211 | 54 45 | 38 37
+//   e4m3   64-wide, 256 rows  152 143 | 39 41 | 33 40
+//   e4m3  128-wide, 128 rows  118 134 | 28 51 | 30 39      256 rows  228 219 | 47 60 | 46 53
+//   e4m3  256-wide,  32 rows  121 169 | 28 37 | 31 32       48 rows  239 177 | 40 40 | 38 34
+// 64 rows of 128-wide bf16 heads are a draw here, but one request over 65536 keys takes 52
+// in the split form and 38 in the other.
 // A step widened to two bytes in LDS for each block costs e4m3 more than bytes read again,
 // so its split form goes further.  256-wide heads leave the split form registers for 16
 // rows a wave: 32 e4m3 ones are possible with all 512 registers of a lane (113 us for 119),
