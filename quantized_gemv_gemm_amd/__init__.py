@@ -598,8 +598,8 @@ def _given(t, name, dtype, shape, index):
 
 
 def _rows(t, name, index):
-    """A bf16 [tokens, heads, D] tensor with whole rows next to each other, tokens any distance
-    apart: its address and that distance."""
+    """A bf16 [tokens, heads, D] tensor with a token's heads next to each other, tokens a row or
+    more apart: its address and that distance."""
     import torch
     if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.get_device() != index:
         _need(t.contiguous(), name, torch.bfloat16, 3)
@@ -608,7 +608,11 @@ def _rows(t, name, index):
     ld, sh, sd = t.stride()
     if sd != 1 and D > 1 or sh != D and H > 1:
         raise ValueError(f"{name}'s heads must lie next to each other (strides {t.stride()})")
-    return t.data_ptr(), max(ld, H * D) if T > 1 else H * D
+    if T < 2:
+        return t.data_ptr(), H * D
+    if ld < H * D:
+        raise ValueError(f"{name}'s tokens must not overlap (strides {t.stride()}): copy a broadcast tensor first")
+    return t.data_ptr(), ld
 
 
 def _index_of(t, name):
@@ -709,7 +713,7 @@ def step_plan(ctx_lens, new_lens, owned, block_table, free_list, free_head, toke
 
 def kv_write(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, q=None, positions=None, cos_sin=None,
              q_out=None):
-    """Writes rows k, v bf16 [T, H, D] (any token distance) to the cache at slots int64 [T] and
+    """Writes rows k, v bf16 [T, H, D] (tokens a row or more apart) to the cache at slots int64 [T] and
     returns q_out bf16 [T, Hq, D] if q is given.  With positions int32 [T] and cos_sin f32
     [max_pos, rot] (cosines, then sines) the first rot elements of q and k are rotated first.
     An e4m3 cache gets codes and scales."""
@@ -754,7 +758,7 @@ def tree_attention_workspace_size(max_nodes: int, group: int, D: int, dtype=None
 
 def tree_attention(q, k_cache, v_cache, block_table, q_start, kv_lens, tree_mask=None, k_scale=None, v_scale=None,
                    scale=None, max_nodes=None, out=None, lse=None, workspace=None):
-    """Attention of q bf16 [T, Hq, D] (any token distance) over the paged cache: request r's tokens
+    """Attention of q bf16 [T, Hq, D] (tokens a row or more apart) over the paged cache: request r's tokens
     q_start[r] .. q_start[r+1]-1 see its first kv_lens[r] - n keys and, of its own n, those that
     tree_mask int64 [T] names (or, without a mask or above 64 tokens, those up to themselves).
     Returns out bf16 [T, Hq, D], or (out, lse) if ``lse`` f32 [T, Hq] is given (True: made here).

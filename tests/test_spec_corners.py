@@ -1,0 +1,38 @@
+"""Corners of the speculative-decoding operators without a GPU: views whose tokens overlap."""
+from __future__ import annotations
+
+import os
+
+import pytest
+
+import quantized_gemv_gemm_amd as tl
+
+pytestmark = pytest.mark.skipif(not os.path.exists(tl.LIB_PATH), reason="libtl.so not built")
+
+
+# --------------------------------------------------------------------------- rows of q, k and v
+def test_rows_closer_than_a_row_are_refused():
+    """Tokens that share elements (a broadcast token, a sliding window) have no distance the kernels take."""
+    torch = pytest.importorskip("torch")
+    one = torch.zeros((1, 4, 128), dtype=torch.bfloat16)
+    flat = torch.zeros(40 * 128, dtype=torch.bfloat16)
+    for view in (one.expand(8, 4, 128), flat.as_strided((8, 4, 128), (128, 128, 1)),
+                 flat.as_strided((8, 4, 128), (4 * 128 - 8, 128, 1)), one[:, :1].expand(2, 1, 128)):
+        for name in ("q", "k", "v"):
+            with pytest.raises(ValueError, match=name):
+                tl._rows(view, name, -1)
+
+
+def test_rows_give_their_own_distance():
+    torch = pytest.importorskip("torch")
+    wide = torch.zeros((6, 20 * 64), dtype=torch.bfloat16)
+    assert tl._rows(wide.unflatten(1, (20, 64)), "q", -1) == (wide.data_ptr(), 20 * 64)
+    part = wide[:, 128:128 + 4 * 64].unflatten(1, (4, 64))
+    assert tl._rows(part, "k", -1) == (part.data_ptr(), 20 * 64)
+    assert tl._rows(part[::3], "k", -1)[1] == 60 * 64
+    # one token or none: whatever the stride says, nothing is stepped over
+    assert tl._rows(part[:1].expand(1, 4, 64), "k", -1)[1] == 4 * 64
+    assert tl._rows(wide.as_strided((1, 4, 64), (0, 64, 1)), "k", -1)[1] == 4 * 64
+    assert tl._rows(part[:0], "k", -1)[1] == 4 * 64
+    # one head: the distance of heads does not matter
+    assert tl._rows(wide.as_strided((3, 1, 64), (128, 7, 1)), "v", -1)[1] == 128
