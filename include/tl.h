@@ -495,7 +495,8 @@ int tl_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, 
  *                aligned, contents free; calls that overlap in time must not share it
  * What lies in keys a token does not see (infinities and NaN among it) does not reach it.
  * Rows of out and lse of tokens that belong to no request are left as they are.
- * Requires scale > 0 and finite, 1 <= G <= 64, max_nodes >= 1, 0 <= R <= 4096.
+ * Requires scale > 0 and finite, 1 <= G <= 64, max_nodes >= 1, 0 <= R <= 4096, and
+ * table_width * block <= 2^31 - 4096.
  */
 size_t tl_tree_attention_workspace_size(int64_t max_nodes, int64_t G, int64_t D, int cache_dtype);
 int tl_tree_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H, int64_t G, int64_t D, const void *k_cache,

@@ -46,6 +46,9 @@ int from_hip(hipError_t e) {
 }
 
 constexpr int64_t kMaxDim = int64_t(1) << 31;  // rows, tokens and K stay below 2^31
+// keys of a request's table: the attention counts positions in 32 bits, and looks for the
+// tiles of a segment 64 at a time, so up to 1024 positions past the last key
+constexpr int64_t kMostKeys = kMaxDim - 4096;
 
 // one step of speculative decoding over a paged cache
 bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -566,7 +569,7 @@ int tl_tree_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H, int6
   if (!count_ok(T) || R < 0 || R > TL_MAX_REQUESTS || G < 1 || G > 64 || max_nodes < 1 || max_nodes >= kMaxDim)
     return TL_ERR_SHAPE;
   if (ldq < H * G * D || ldq >= kMaxDim || T * G >= kMaxDim) return TL_ERR_SHAPE;
-  if (table_width < 0 || table_width > (kMaxDim - 1) / block) return TL_ERR_SHAPE;
+  if (table_width < 0 || table_width > kMostKeys / block) return TL_ERR_SHAPE;
   if (!(scale > 0.0f && scale < __builtin_inff())) return TL_ERR_SHAPE;
   if (T == 0 || R == 0) return TL_OK;
   // the units of work the kernel counts stay below 2^31

@@ -1,6 +1,8 @@
-"""Corners of the speculative-decoding operators without a GPU: views whose tokens overlap."""
+"""Corners of the speculative-decoding operators without a GPU: views whose tokens overlap, and
+sizes at the edge of what the kernels' integers hold."""
 from __future__ import annotations
 
+import ctypes
 import os
 
 import pytest
@@ -36,3 +38,19 @@ def test_rows_give_their_own_distance():
     assert tl._rows(part[:0], "k", -1)[1] == 4 * 64
     # one head: the distance of heads does not matter
     assert tl._rows(wide.as_strided((3, 1, 64), (128, 7, 1)), "v", -1)[1] == 128
+
+
+# --------------------------------------------------------------------------- sizes
+def attention_status(T=1, H=1, G=1, D=64, block=16, width=4, R=1):
+    """Status of a call without a workspace: 7 if nothing before it is refused."""
+    P = lambda n: ctypes.c_void_p((n + 1) << 40)
+    return tl.lib().tl_tree_attention(P(0), H * G * D, T, H, G, D, P(1), P(2), None, None, tl.TL_BF16, 9, block, P(3), width,
+                                      R, P(4), P(5), None, 0.1, 1, P(6), None, None, 0, None)
+
+
+@pytest.mark.parametrize("block", [16, 64, 4096])
+def test_attention_positions_stay_in_31_bits(block):
+    """Keys are counted in 32 bits, up to 64 tiles past the last one: wider tables would give negative positions."""
+    most = ((1 << 31) - 4096) // block
+    assert attention_status(block=block, width=most) == 7
+    assert attention_status(block=block, width=most + 1) == 2
