@@ -440,9 +440,10 @@ int64_t tl_kv_offset(int which, int cache_dtype, int64_t H, int64_t D, int64_t b
  * out positions  int32 [T]      ctx + depth in the tree, or ctx + number of the token
  * out tree_mask  uint64 [T]     (with parents) the node and its ancestors, a bit each
  * out owned_out  int32 [R], free_head_out int32 [1]: both after this step
- * A request is served if its tokens fit table_width pages and the pages it needs beyond
- * `owned` are free after those of the requests before it; one that is not served gets
- * slots of -1 and takes no page.  With parents, requests of more than 64 new tokens are
+ * A request is served if its tokens fit table_width pages, the pages it needs beyond
+ * `owned` are free after those of the requests before it, and its tokens are among the T
+ * (with those of the requests before it); one that is not served gets slots of -1 and
+ * takes no page.  With parents, requests of more than 64 new tokens are
  * chains (mask 0).  Tokens from q_start[R] on get slot -1, position 0 and mask 0.
  * No output may be an input; table is the only in-out argument.
  * Requires 0 <= R <= 4096, T and free_count < 2^31, table_width * block < 2^31.

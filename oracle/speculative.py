@@ -86,13 +86,15 @@ def step_plan(ctx, new, owned, table, free, head, T, block, parents=None):
     pos_out, mask_out, owned_out = np.zeros(T, np.int64), np.zeros(T, np.uint64), owned.copy()
     at = max(head, 0)
     left = len(free) if head >= 0 else 0
-    pages_asked = 0
+    pages_asked = tokens_asked = 0
     for r in range(R):
         c, n, o = max(int(ctx[r]), 0), max(int(new[r]), 0), max(int(owned[r]), 0)
         owned_out[r] = o
         want = -(-(c + n) // block)
         need = max(0, want - o) if want <= width else 0
-        served = want <= width and (need == 0 or (head >= 0 and head + pages_asked + need <= left))
+        tokens_asked += n
+        room = tokens_asked <= T or (n == 0 and need == 0)
+        served = want <= width and room and (need == 0 or (head >= 0 and head + pages_asked + need <= left))
         if served:
             for j in range(need):
                 table[r, o + j] = free[head + pages_asked + j]

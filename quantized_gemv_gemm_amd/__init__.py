@@ -683,7 +683,8 @@ def step_plan(ctx_lens, new_lens, owned, block_table, free_list, free_head, toke
     """Metadata of a step from the request lengths (int32 [R] each), on the GPU: takes pages from
     ``free_list`` into ``block_table`` int32 [R, width] (in place) and returns (q_start [R+1],
     kv_lens [R], slots int64 [tokens], positions [tokens], tree_mask int64 [tokens] or None,
-    owned [R], free_head [1]).  ``tokens`` is the step's token count or more (a graph's capacity)."""
+    owned [R], free_head [1]).  ``tokens`` is the step's token count or more (a graph's capacity); a
+    request that does not fit it, the table or the free pages is not served (kv_lens 0, slots -1)."""
     import torch
     i32 = torch.int32
     i = _index_of(ctx_lens, "ctx_lens")

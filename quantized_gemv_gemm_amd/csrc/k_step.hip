@@ -4,10 +4,14 @@
 // free_head on:
 //   want  = ceil((ctx + new) / bs),  need = max(0, want - owned)   (0 if want > table width)
 //   first = sum of need over the requests before r
-//   served = want fits the table and (need = 0 or free_head + first + need <= F)
+//   room = all tokens up to r's last are among the T, or it has neither tokens nor need
+//   served = room, want fits the table and (need = 0 or free_head + first + need <= F)
 //   table[r, owned + j] = free_list[free_head + first + j]          (served, j < need)
 //   slot  = table[r, pos / bs] * bs + pos % bs,  pos = ctx + i for the i-th new token
 //   position = ctx + depth(i), mask = bits of i and its ancestors   (trees of <= 64 nodes)
+// A request whose last tokens are past the T could not be attended to: its cache length
+// would count rows that nobody writes.  Where room or pages end they end for all later
+// requests that need any, so the pages that are granted are the first ones of the list.
 //
 // One launch.  What bounds it is latency: a few dependent loads, whatever the sizes are
 // (one tree of 33 nodes 3.9 us, 512 requests with 68000 new tokens 8.6 us; a launch that
@@ -86,7 +90,8 @@ __global__ __launch_bounds__(kThreads) void step_plan_kernel(const StepArgs a) {
     const int fresh = max(a.new_lens[r], 0), ctx = max(a.ctx_lens[r], 0), owned = max(a.owned[r], 0);
     const int64_t need = pages_needed(a, ctx, fresh, owned, fits);
     bq += fresh;
-    const bool served = fits && (need == 0 || bn + need <= left);
+    const bool room = bq <= a.T || (fresh == 0 && need == 0);
+    const bool served = fits && room && (need == 0 || bn + need <= left);
     bn += need;
     q_pre[r + 1] = int(min(bq, int64_t(a.T)));
     n_pre[r + 1] = int(min(bn, kMost));
@@ -135,7 +140,8 @@ __global__ __launch_bounds__(kThreads) void step_plan_kernel(const StepArgs a) {
     const int64_t need = pages_needed(a, ctx, fresh, owned, fits);
     const int64_t pos = int64_t(ctx) + (t - q_pre[lo]);
     int64_t slot = -1;
-    if (fits && (need == 0 || n_pre[lo] + need <= left)) {
+    const bool room = int64_t(q_pre[lo]) + fresh <= a.T;
+    if (fits && room && (need == 0 || n_pre[lo] + need <= left)) {
       const int64_t page = pos / a.block;
       const int id = page < owned ? a.table[int64_t(lo) * a.table_width + page]
                                   : a.free_list[head + n_pre[lo] + (page - owned)];

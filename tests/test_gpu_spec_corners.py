@@ -1,0 +1,55 @@
+"""Corners of the speculative-decoding operators on the GPU: steps larger than their capacity."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+from gpu_common import announce, dev
+from test_gpu_spec import Case, raw, run_plan, tl, torch, values  # noqa: F401 (fixtures among them)
+
+pytestmark = pytest.mark.gpu
+
+
+# --------------------------------------------------------------------------- more tokens than the capacity
+@pytest.mark.parametrize("R,block,tree", [(2, 16, True), (2, 16, False), (40, 16, True), (700, 32, True), (700, 64, False)])
+def test_plan_beyond_capacity(tl, torch, R, block, tree):
+    """Capacities below the step's tokens: at a request's border, inside one, at the first token, none at all."""
+    rng = np.random.default_rng(R + block)
+    new = rng.choice([0, 1, 5, 33, 64, 90], R)
+    new[0] = 5
+    ctx = rng.integers(0, 200, R)
+    owned = np.maximum(-(-ctx // block) - (rng.random(R) < 0.2), 0)
+    width = int((-(-(ctx + new) // block)).max())
+    table = np.arange(R * width).reshape(R, width)
+    free = np.arange(R * width, 2 * R * width)
+    total = int(new.sum())
+    for T in sorted({0, 1, 4, 5, 6, total // 2, int(new[:R // 2].sum()), total - 1, total}):
+        announce(f"step_plan R={R} tokens={total} capacity={T}")
+        parents = rng.integers(-1, 30, T) if tree else None
+        run_plan(tl, torch, ctx, new, owned, table, free, 0, T, block, parents)
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_step_beyond_capacity(tl, torch, e4m3, tree):
+    """A request that does not fit the step's tokens is not served: nothing of what its pages held before
+    is seen, no page is taken, nothing is committed; the requests before it are as they would be alone."""
+    announce(f"a step beyond its capacity, e4m3={e4m3} tree={tree}")
+    d, H, G, D, block, T = dev(), 2, 2, 128, 16, 10
+    ctx, new, parents = [20, 30, 12], [5, 8, 3], [-1, 0, 0, 1, 1] + [-1, 0, 1, 2, 3]
+    c = Case(tl, [(5, 20), (5, 33), (0, 12)], H, G, D, e4m3, block, tree=tree, seed=31)
+    i32 = lambda a: torch.tensor(np.asarray(a), dtype=torch.int32, device=d)
+    owned = [2, 2, 1]                                  # request 1 needs one page more
+    free = np.setdiff1d(np.arange(c.pages), c.table[c.table < c.pages])
+    table = i32(np.where(c.table < c.pages, c.table, 0))
+    q_start, kv, slots, _, mask, owned_out, head = tl.step_plan(
+        i32(ctx), i32(new), i32(owned), table, i32(free), i32([0]), T, block, parents=i32(parents) if tree else None)
+    assert q_start.tolist() == [0, 5, 10, 10] and kv.tolist() == [25, 0, 0]
+    assert owned_out.tolist() == owned and head.tolist() == [0] and (slots[5:] == -1).all()
+    c.kv = np.array([25, 0, 0], dtype=np.int32)
+    c.mask = mask.cpu().numpy().view(np.uint64) if tree else None
+    c.call(block_table=table, q_start=q_start, kv_lens=kv).check(only=[0])
+    assert (values(raw(c.out))[5:] == 0).all() and torch.isneginf(c.lse[5:]).all()
+    done = tl.kv_commit(i32([1, 4, 1]), i32([[0, -1, -1, -1], [0, 1, 2, 4], [0, -1, -1, -1]]), i32(ctx), kv, table,
+                        c.args["k_cache"], c.args["v_cache"], c.args["k_scale"], c.args["v_scale"])
+    assert done.tolist() == [21, 30, 12]

@@ -1,12 +1,14 @@
-"""Corners of the speculative-decoding operators without a GPU: views whose tokens overlap, and
-sizes at the edge of what the kernels' integers hold."""
+"""Corners of the speculative-decoding operators without a GPU: views whose tokens overlap,
+sizes at the edge of what the kernels' integers hold, and the plain definitions beside them."""
 from __future__ import annotations
 
 import ctypes
 import os
 
+import numpy as np
 import pytest
 
+import oracle.speculative as ref
 import quantized_gemv_gemm_amd as tl
 
 pytestmark = pytest.mark.skipif(not os.path.exists(tl.LIB_PATH), reason="libtl.so not built")
@@ -54,3 +56,16 @@ def test_attention_positions_stay_in_31_bits(block):
     most = ((1 << 31) - 4096) // block
     assert attention_status(block=block, width=most) == 7
     assert attention_status(block=block, width=most + 1) == 2
+
+
+# --------------------------------------------------------------------------- the plain definitions, by hand
+def test_plan_beyond_capacity_by_hand():
+    """Request 1's tokens pass the capacity: it and the later ones with tokens or a need of pages are not served."""
+    table = np.zeros((5, 3), dtype=np.int64)
+    got = ref.step_plan(np.array([14, 10, 16, 20, 8]), np.array([3, 8, 0, 0, 1]), np.array([1, 1, 1, 1, 1]), table,
+                        np.array([9, 8, 7, 6]), 0, 10, 16, np.array([-1, 0, 0] + [-1, 0, 1, 2, 3, 4, 5]))
+    q_start, kv, slots, pos, mask, owned, head, out = got
+    assert q_start.tolist() == [0, 3, 10, 10, 10, 10]
+    assert kv.tolist() == [17, 0, 16, 0, 0] and owned.tolist() == [2, 1, 1, 1, 1] and head == 1
+    assert out[0].tolist() == [0, 9, 0] and not out[1:].any()
+    assert slots.tolist() == [14, 15, 9 * 16] + [-1] * 7 and mask[9] == 127 and pos[9] == 16
