@@ -489,7 +489,8 @@ int tl_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, 
  *                tokens and, with a mask in a request of up to 64 tokens, the own token j
  *                where bit j is set; else the own tokens up to itself.
  * out out        bf16 [T, H * G, D]: softmax(scale q K^T) V over the keys it sees, 0 if none
- * out lse        f32 [T, H * G] or NULL: log of the sum of exponentials, -inf if none
+ * out lse        f32 [T, H * G] or NULL: log of the sum of exponentials, -inf if none; NaN
+ *                (as out) where a score is NaN
  * max_nodes      the most tokens a request has, as far as the caller knows: it chooses the
  *                kernel and sizes the workspace; lengths above it are still right
  * workspace      tl_tree_attention_workspace_size(max_nodes, G, D, cache_dtype) bytes, 16-byte

@@ -688,8 +688,10 @@ struct Results {
       }
     }
   }
+  // no key seen: a sum of 0, -inf + log 0.  Scores that are all NaN leave no maximum either,
+  // but a sum that is NaN.
   static __device__ __forceinline__ float log_sum(float top, float sum) {
-    return top == kNegInf ? kNegInf : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
+    return (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945309f;
   }
   __device__ __forceinline__ void put(const TreeArgs &a, bool whole, int j, int t, f32x4 v) const {
     if (whole) {

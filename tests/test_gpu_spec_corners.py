@@ -1,4 +1,5 @@
-"""Corners of the speculative-decoding operators on the GPU: steps larger than their capacity."""
+"""Corners of the speculative-decoding operators on the GPU: steps larger than their capacity, and
+scores that are all NaN."""
 from __future__ import annotations
 
 import numpy as np
@@ -53,3 +54,29 @@ def test_step_beyond_capacity(tl, torch, e4m3, tree):
     done = tl.kv_commit(i32([1, 4, 1]), i32([[0, -1, -1, -1], [0, 1, 2, 4], [0, -1, -1, -1]]), i32(ctx), kv, table,
                         c.args["k_cache"], c.args["v_cache"], c.args["k_scale"], c.args["v_scale"])
     assert done.tolist() == [21, 30, 12]
+
+
+# --------------------------------------------------------------------------- rows whose scores are all NaN
+@pytest.mark.parametrize("D,e4m3,nodes,context", [(64, False, 3, 40), (128, False, 8, 100), (128, False, 16, 70),
+                                                  (256, False, 20, 9), (64, True, 64, 300), (256, True, 12, 50),
+                                                  (128, False, 2, 9000), (128, True, 40, 6000),
+                                                  (128, False, 40, 3000), (256, False, 20, 3000)])
+def test_attention_queries_that_are_nan(tl, D, e4m3, nodes, context):
+    """A query with a NaN has a NaN result and a NaN lse, which -inf (nothing seen) is not; its neighbours have theirs."""
+    c = Case(tl, [(nodes, context), (1, 0), (nodes, 0)], 1, 4, D, e4m3, 32, seed=D + nodes)
+    bad = [(0, 1), (nodes - 1, 3), (nodes, 0), (nodes + 1, 2)]
+    for t, h in bad:
+        c.q[t, h, (7 * t) % D] = np.nan
+    c.mask[nodes + 1 + nodes - 1] = 0                  # sees nothing: -inf, also with a NaN in its query
+    c.q[-1, 1, 0] = np.nan
+    c.call()
+    c.q[-1, 1, 0] = 0.0                                # check() counts its bounds from q; this row is exactly 0 below
+    c.check()
+    lse, out = c.lse.cpu().numpy(), values(raw(c.out))
+    nan = np.zeros(lse.shape, bool)
+    for t, h in bad:
+        nan[t, h] = True
+    nan[-1] = False
+    np.testing.assert_array_equal(np.isnan(lse), nan)
+    np.testing.assert_array_equal(np.isnan(out).all(-1), nan)
+    assert np.isneginf(lse[-1]).all() and (out[-1] == 0).all()
