@@ -538,7 +538,9 @@ int tl_tree_verify(const void *logits, int logits_dtype, int64_t ld, int64_t T, 
  * io  k_cache, v_cache [L, pages, H, block, D] and, for e4m3, the scales: for each layer and
  *                head the row of position ctx + path[i] goes to ctx + i, for i < accepted;
  *                every source is read before it is overwritten
- * out ctx_out    int32 [R]: ctx + accepted; ctx for a request that was not served
+ * out ctx_out    int32 [R]: ctx + accepted; ctx for a request that was not served.  Of a request
+ *                of up to 64 tokens no more than path_width nodes are committed and counted:
+ *                where the later ones' rows lie is not known
  * Entries of path that do not move a row forward inside the request are skipped.
  */
 int tl_kv_commit(const int32_t *accepted, const int32_t *path, int64_t path_width, const int32_t *ctx_lens,

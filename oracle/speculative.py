@@ -195,10 +195,12 @@ def commit_moves(accepted, path, ctx, kv, table, pages, block):
         c = max(int(ctx[r]), 0)
         n = max(int(kv[r]) - c, 0)
         count = min(max(int(accepted[r]), 0), n)
+        if n <= NODES:
+            count = min(count, path.shape[1])  # further nodes are not known
         out.append(c + count)
         if n > NODES:
             continue
-        for i in range(min(count, path.shape[1])):
+        for i in range(count):
             p = int(path[r, i])
             if not i < p < n:
                 continue

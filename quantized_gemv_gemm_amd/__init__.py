@@ -826,7 +826,8 @@ def kv_commit(accepted, path, ctx_lens, kv_lens, block_table, k_cache, v_cache, 
               ctx_out=None):
     """Moves the rows of the accepted nodes (tree_verify's accepted [R] and path [R, width]) to the
     positions after the context, in a cache layer [pages, H, block, D] or all of them
-    [L, pages, H, block, D]; returns the new context lengths int32 [R]."""
+    [L, pages, H, block, D]; returns the new context lengths int32 [R] (a tree's accepted nodes past the
+    path's width are not committed)."""
     import torch
     i = _index_of(accepted, "accepted")
     layers = k_cache.dim() == 5

@@ -229,7 +229,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
 }
 
 // ---------------------------------------------------------------------------
-// Rows ctx + path[i] of a request go to ctx + i.  A workgroup takes one layer, request
+// Rows ctx + path[i] of a request go to ctx + i, as many as the path has.  A workgroup takes one layer, request
 // and head, and the elements lie in threads' registers while they move, up to 4096 of V at
 // a time: some d's of every row, all read before one is written, so paths may overlap
 // their targets.  What bounds it is the chain of loads to the first row (lengths, path,
@@ -252,14 +252,15 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(const CommitArgs a)
   b /= a.H;
   const int r = b % a.R, layer = b / a.R;
   const int ctx = max(a.ctx_lens[r], 0), n = max(a.kv_lens[r] - ctx, 0);  // not served: no new tokens
-  const int block = 1 << a.block_shift, count = min(max(a.accepted[r], 0), n);
-  const int most = min(a.path_width, kTreeNodes);
-  const int from = tid < most ? a.path[int64_t(r) * a.path_width + tid] : -1;
+  const int block = 1 << a.block_shift;
+  // a tree's accepted nodes as far as the path names them (a chain's lie where they belong)
+  const int count = min(max(a.accepted[r], 0), n <= kTreeNodes ? min(n, a.path_width) : n);
+  const int from = tid < a.path_width ? a.path[int64_t(r) * a.path_width + tid] : -1;
   if (tid == 0 && head == 0 && layer == 0) a.ctx_out[r] = ctx + count;
   if (n > kTreeNodes || count == 0) return;
   if (tid < 64) {
     int64_t src = -1, dst = -1;
-    if (tid < min(count, most) && from > tid && from < n) {
+    if (tid < count && from > tid && from < n) {
       auto token = [&](int pos) -> int64_t {
         const int page = pos >> a.block_shift;
         if (page >= a.table_width) return -1;

@@ -1,11 +1,12 @@
-"""Corners of the speculative-decoding operators on the GPU: steps larger than their capacity, and
-scores that are all NaN."""
+"""Corners of the speculative-decoding operators on the GPU: steps larger than their capacity,
+scores that are all NaN, and paths cut short."""
 from __future__ import annotations
 
 import numpy as np
 import pytest
 
-from gpu_common import announce, dev
+import oracle.speculative as ref
+from gpu_common import announce, dev, to_dev
 from test_gpu_spec import Case, raw, run_plan, tl, torch, values  # noqa: F401 (fixtures among them)
 
 pytestmark = pytest.mark.gpu
@@ -80,3 +81,37 @@ def test_attention_queries_that_are_nan(tl, D, e4m3, nodes, context):
     np.testing.assert_array_equal(np.isnan(lse), nan)
     np.testing.assert_array_equal(np.isnan(out).all(-1), nan)
     assert np.isneginf(lse[-1]).all() and (out[-1] == 0).all()
+
+
+# --------------------------------------------------------------------------- commits
+def commit(tl, torch, accepted, path, ctx, kv, block=16, D=64, H=2, e4m3=False, seed=0):
+    """kv_commit against the moves of the plain definition; returns the new lengths."""
+    d, rng, R = dev(), np.random.default_rng(seed), len(ctx)
+    width = 12
+    table = rng.permutation(R * width).reshape(R, width).astype(np.int32)
+    path, i32 = np.array(path, dtype=np.int32), lambda a: to_dev(np.array(a, dtype=np.int32), d)
+    kind = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    k, v, ks, vs = tl.kv_cache(R * width, H, block, D, dtype=kind, device=d)
+    for c in (k, v):
+        c.view(torch.uint8).copy_(torch.from_numpy(rng.integers(0, 256, c.view(torch.uint8).shape, dtype=np.uint8)))
+    before = [raw(c).copy() for c in (k, v)]
+    got = tl.kv_commit(i32(accepted), to_dev(path, d), i32(ctx), i32(kv), to_dev(table, d), k, v, ks, vs)
+    torch.cuda.synchronize()
+    moves, want = ref.commit_moves(accepted, path, ctx, kv, table, R * width, block)
+    for c, old, which in ((k, before[0], "k"), (v, before[1], "v")):
+        at = ref.offsets(which, 1 if e4m3 else 2, block, D)
+        new = old.copy().reshape(old.shape[:2] + (-1,))
+        for _, pa, ta, pb, tb in moves:
+            new[pb][..., at[tb]] = old.reshape(new.shape)[pa][..., at[ta]]
+        np.testing.assert_array_equal(raw(c).reshape(new.shape), new)
+    np.testing.assert_array_equal(got.cpu().numpy(), want)
+    return got.tolist()
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_commit_of_a_path_cut_short(tl, torch, e4m3):
+    """Nodes past the path's width are not known, so they are not committed; a prompt needs no path."""
+    announce(f"kv_commit, paths narrower than the accepted nodes, e4m3={e4m3}")
+    path = [[0, 2, 3], [0, 1, 2], [0, 4, -1], [-1, -1, -1]]
+    got = commit(tl, torch, [5, 3, 2, 100], path, [20, 31, 7, 9], [36, 40, 17, 109], e4m3=e4m3)
+    assert got == [23, 34, 9, 109]

@@ -69,3 +69,9 @@ def test_plan_beyond_capacity_by_hand():
     assert kv.tolist() == [17, 0, 16, 0, 0] and owned.tolist() == [2, 1, 1, 1, 1] and head == 1
     assert out[0].tolist() == [0, 9, 0] and not out[1:].any()
     assert slots.tolist() == [14, 15, 9 * 16] + [-1] * 7 and mask[9] == 127 and pos[9] == 16
+
+
+def test_commit_of_a_path_cut_short_by_hand():
+    """Five accepted nodes, three of them on the path; a prompt of 100 tokens needs none."""
+    moves, ctx = ref.commit_moves([5, 100], np.array([[0, 2, 3], [-1, -1, -1]]), [15, 4], [25, 104], np.zeros((2, 8)), 3, 16)
+    assert moves == [(0, 0, 1, 0, 0), (0, 0, 2, 0, 1)] and ctx.tolist() == [18, 104]
