@@ -251,7 +251,7 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(const CommitArgs a)
   const int head = b % a.H;
   b /= a.H;
   const int r = b % a.R, layer = b / a.R;
-  const int ctx = max(a.ctx_lens[r], 0), n = max(a.kv_lens[r] - ctx, 0);  // not served: no new tokens
+  const int ctx = max(a.ctx_lens[r], 0), n = max(max(a.kv_lens[r], 0) - ctx, 0);  // not served: no new tokens
   const int block = 1 << a.block_shift;
   // a tree's accepted nodes as far as the path names them (a chain's lie where they belong)
   const int count = min(max(a.accepted[r], 0), n <= kTreeNodes ? min(n, a.path_width) : n);

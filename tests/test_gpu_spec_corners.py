@@ -1,5 +1,5 @@
 """Corners of the speculative-decoding operators on the GPU: steps larger than their capacity,
-scores that are all NaN, and paths cut short."""
+scores that are all NaN, paths cut short, and lengths of the type's lowest value."""
 from __future__ import annotations
 
 import numpy as np
@@ -115,3 +115,11 @@ def test_commit_of_a_path_cut_short(tl, torch, e4m3):
     path = [[0, 2, 3], [0, 1, 2], [0, 4, -1], [-1, -1, -1]]
     got = commit(tl, torch, [5, 3, 2, 100], path, [20, 31, 7, 9], [36, 40, 17, 109], e4m3=e4m3)
     assert got == [23, 34, 9, 109]
+
+
+def test_commit_of_lengths_of_the_lowest_value(tl, torch):
+    """Negative lengths count as 0, down to the type's lowest."""
+    announce("kv_commit, lowest lengths")
+    low = -2 ** 31
+    got = commit(tl, torch, [3, 3, low, 2], [[0, 2, 3]] * 4, [5, low, 8, 40], [low, 9, 14, low + 3])
+    assert got == [5, 3, 8, 40]
