@@ -715,6 +715,7 @@ struct Split {
   static constexpr int grid = 256 * occupancy;
   // the four waves' sums are joined through LDS, up to 64 KB
   static constexpr size_t lds = kWaves * (D / 16) * RT * 1024 + kWaves * 2 * RT * 16 * 4;
+  static_assert(fits_lds(lds), "the most requests' prefix sums lie behind it");
 };
 
 template <int D, bool E4M3, int RT>
@@ -920,6 +921,7 @@ struct Share {
   static constexpr int wide = 2 * 16 * D * 2 + gap;    // and as bf16
   static constexpr int scales = E4M3 ? waves * 256 : 0;  // of a step, a copy for each wave
   static constexpr size_t lds = ring * (2 * raw + scales) + (E4M3 ? 4 * wide : 0);
+  static_assert(fits_lds(lds), "the most requests' prefix sums lie behind it");
   // loads of a wave for a step: what the waits count
   static constexpr int loads = (halves ? 1 : 2) * mine + (E4M3 ? 1 : 0);
 };
@@ -1335,7 +1337,7 @@ template <int D, bool E4M3, int RT>
 hipError_t launch_split(const TreeArgs &a, const char *name, hipStream_t stream) {
   using S = Split<D, E4M3, RT>;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((tree_split_kernel<D, E4M3, RT>), dim3(S::grid), dim3(kThreads), S::lds + size_t(a.R + 1) * 4,
+  hipLaunchKernelGGL((tree_split_kernel<D, E4M3, RT>), dim3(S::grid), dim3(kThreads), S::lds + prefix_bytes(a.R),
                      stream, a);
   combine(a, S::grid, S::rows, D, stream);
   set_last_kernel(name);
@@ -1346,7 +1348,7 @@ template <int D, bool E4M3, int RT>
 hipError_t launch_share(const TreeArgs &a, const char *name, hipStream_t stream) {
   using S = Share<D, E4M3, RT>;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((tree_share_kernel<D, E4M3, RT>), dim3(S::grid), dim3(S::threads), S::lds + size_t(a.R + 1) * 4,
+  hipLaunchKernelGGL((tree_share_kernel<D, E4M3, RT>), dim3(S::grid), dim3(S::threads), S::lds + prefix_bytes(a.R),
                      stream, a);
   combine(a, S::grid, S::rows, D, stream);
   set_last_kernel(name);

@@ -504,7 +504,7 @@ int tl_step_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t
                  const int32_t *free_head, const int32_t *parents, int64_t T, int32_t *q_start, int32_t *kv_lens,
                  int64_t *slots, int32_t *positions, uint64_t *tree_mask, int32_t *owned_out,
                  int32_t *free_head_out, void *stream) {
-  if (R < 0 || R > TL_MAX_REQUESTS || !count_ok(T) || !count_ok(free_count) || !block_ok(block)) return TL_ERR_SHAPE;
+  if (R < 0 || R > tl::kMaxRequests || !count_ok(T) || !count_ok(free_count) || !block_ok(block)) return TL_ERR_SHAPE;
   if (table_width < 0 || table_width > (kMaxDim - 1) / block) return TL_ERR_SHAPE;
   if (any_null(free_head, q_start, free_head_out)) return TL_ERR_NULLPTR;
   if (R && (any_null(ctx_lens, new_lens, owned, kv_lens, owned_out) || (table_width && !table))) return TL_ERR_NULLPTR;
@@ -566,7 +566,7 @@ int tl_tree_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H, int6
                       int64_t max_nodes, uint16_t *out, float *lse, void *workspace, size_t workspace_bytes,
                       void *stream) {
   if (int s = check_cache(cache_dtype, pages, H, block, D)) return s;
-  if (!count_ok(T) || R < 0 || R > TL_MAX_REQUESTS || G < 1 || G > 64 || max_nodes < 1 || max_nodes >= kMaxDim)
+  if (!count_ok(T) || R < 0 || R > tl::kMaxRequests || G < 1 || G > 64 || max_nodes < 1 || max_nodes >= kMaxDim)
     return TL_ERR_SHAPE;
   if (ldq < H * G * D || ldq >= kMaxDim || T * G >= kMaxDim) return TL_ERR_SHAPE;
   if (table_width < 0 || table_width > kMostKeys / block) return TL_ERR_SHAPE;
@@ -623,7 +623,7 @@ int tl_tree_verify(const void *logits, int logits_dtype, int64_t ld, int64_t T, 
                    int64_t path_width, int32_t *next, int32_t *target, void *workspace, size_t workspace_bytes,
                    void *stream) {
   if (logits_dtype != TL_BF16 && logits_dtype != TL_F32) return TL_ERR_DTYPE;
-  if (!count_ok(T) || R < 0 || R > TL_MAX_REQUESTS || V < 1 || V >= kMaxDim || ld < V || ld >= kMaxDim) return TL_ERR_SHAPE;
+  if (!count_ok(T) || R < 0 || R > tl::kMaxRequests || V < 1 || V >= kMaxDim || ld < V || ld >= kMaxDim) return TL_ERR_SHAPE;
   if (path_width < 1 || path_width > TL_TREE_NODES || T * tl::verify_parts(T, V) >= kMaxDim) return TL_ERR_SHAPE;
   if (T == 0 && R == 0) return TL_OK;
   if (!q_start || (T && any_null(logits, draft, parents, target)) || (R && any_null(accepted, path, next)))
@@ -647,7 +647,7 @@ int tl_kv_commit(const int32_t *accepted, const int32_t *path, int64_t path_widt
                  void *v_cache, float *k_scale, float *v_scale, int cache_dtype, int64_t L, int64_t pages, int64_t H,
                  int64_t block, int64_t D, int32_t *ctx_out, void *stream) {
   if (int s = check_cache(cache_dtype, pages, H, block, D)) return s;
-  if (R < 0 || R > TL_MAX_REQUESTS || L < 1 || L > 4096 || path_width < 1 || path_width > TL_TREE_NODES) return TL_ERR_SHAPE;
+  if (R < 0 || R > tl::kMaxRequests || L < 1 || L > 4096 || path_width < 1 || path_width > TL_TREE_NODES) return TL_ERR_SHAPE;
   if (table_width < 0 || table_width > (kMaxDim - 1) / block || L * R * H >= kMaxDim) return TL_ERR_SHAPE;
   if (pages > (int64_t(1) << 50) / (L * H * block * D)) return TL_ERR_SHAPE;
   if (R == 0) return TL_OK;

@@ -101,7 +101,12 @@ hipError_t launch_gemm(const int8_t *xq, const float *tok_scale, int64_t M, int6
 
 // ---------------------------------------------------------------------------
 // one step of speculative decoding over a paged cache
-constexpr int kMaxRequests = 4096;  // their prefix sums sit in LDS
+constexpr int kMaxRequests = TL_MAX_REQUESTS;
+// Their prefix sums sit in LDS: behind what an attention kernel stages, and with its static
+// variables (272 to 288 bytes by the compiler's report) within a compute unit's 160 KB.
+constexpr size_t kLdsBytes = 160 * 1024, kStaticLds = 512;
+constexpr size_t prefix_bytes(int R) { return size_t(R + 1) * 4; }
+constexpr bool fits_lds(size_t staged) { return staged + prefix_bytes(kMaxRequests) + kStaticLds <= kLdsBytes; }
 
 // attention (k_tree.hip)
 struct TreeArgs {

@@ -1,5 +1,5 @@
 """Corners of the speculative-decoding operators on the GPU: steps larger than their capacity,
-scores that are all NaN, paths cut short, and lengths of the type's lowest value."""
+scores that are all NaN, paths cut short, lengths of the type's lowest value, the most requests."""
 from __future__ import annotations
 
 import numpy as np
@@ -123,3 +123,18 @@ def test_commit_of_lengths_of_the_lowest_value(tl, torch):
     low = -2 ** 31
     got = commit(tl, torch, [3, 3, low, 2], [[0, 2, 3]] * 4, [5, low, 8, 40], [low, 9, 14, low + 3])
     assert got == [5, 3, 8, 40]
+
+
+# --------------------------------------------------------------------------- the most requests
+@pytest.mark.parametrize("D,e4m3,G,nodes,form", [(256, False, 5, 8, "bf16_share128"), (256, True, 5, 8, "e4m3_share128"),
+                                                 (64, False, 5, 16, "bf16_share128"), (64, True, 3, 4, "e4m3_split16"),
+                                                 (256, False, 2, 4, "bf16_split16")])
+def test_attention_of_the_most_requests(tl, D, e4m3, G, nodes, form):
+    """4096 requests, most of them without tokens, in forms whose prefix sums lie behind the largest LDS rings."""
+    rng = np.random.default_rng(D + G)
+    reqs = [(0, int(c)) for c in rng.choice([0, 0, 0, 9], 4096)]
+    for r in [0, 1, 255, 256, 511, 512, 513, 2047, 4094, 4095] + rng.integers(0, 4096, 30).tolist():
+        reqs[r] = (int(rng.integers(1, nodes + 1)), int(rng.integers(0, 90)))
+    reqs[777] = (nodes, 2500)                          # one that several workgroups share
+    c = Case(tl, reqs, 1, G, D, e4m3, 16, seed=D + G).call(max_nodes=nodes).check()
+    assert tl.last_kernel_name() == "tree_attention_" + form

@@ -3,7 +3,9 @@ sizes at the edge of what the kernels' integers hold, and the plain definitions 
 from __future__ import annotations
 
 import ctypes
+import json
 import os
+import re
 
 import numpy as np
 import pytest
@@ -75,3 +77,14 @@ def test_commit_of_a_path_cut_short_by_hand():
     """Five accepted nodes, three of them on the path; a prompt of 100 tokens needs none."""
     moves, ctx = ref.commit_moves([5, 100], np.array([[0, 2, 3], [-1, -1, -1]]), [15, 4], [25, 104], np.zeros((2, 8)), 3, 16)
     assert moves == [(0, 0, 1, 0, 0), (0, 0, 2, 0, 1)] and ctx.tolist() == [18, 104]
+
+
+def test_attention_kernels_fit_lds_at_the_most_requests():
+    """The compiler's count of static LDS stays within what the sources keep free for it beside the ring
+    and the prefix sums of 4096 requests."""
+    from quantized_gemv_gemm_amd import _build
+    with open(_build.RESOURCES) as f:
+        figs = {k: v["lds"] for k, v in json.load(f).items() if "tree_split_kernel" in k or "tree_share_kernel" in k}
+    with open(os.path.join(_build.CSRC, "tl_internal.h")) as f:
+        free = int(re.search(r"kStaticLds = (\d+);", f.read()).group(1))
+    assert len(figs) > 10 and max(figs.values()) <= free
