@@ -414,7 +414,11 @@ int tl_linear_apply_noalloc(const uint16_t *x, int64_t T, int64_t K, int64_t N, 
  * outside [0, pages) is a page whose tokens are not there; a slot outside
  * [0, pages * block) is not written.
  *
- * Metadata arrays (lengths, tables, slots, masks, paths) need natural alignment only.
+ * Metadata arrays (lengths, tables, slots, masks, paths) need natural alignment only; q, k,
+ * v, out, caches and cos_sin 16 bytes, as the scales do where tl_tree_attention reads them.
+ * Beside what each call requires: 1 <= H <= 65536, 1 <= pages < 2^31,
+ * pages * H * block * D <= 2^50, T < 2^31, and distances of tokens at least a token's
+ * elements and below 2^31.  What breaks a limit is refused with TL_ERR_SHAPE.
  */
 #define TL_MAX_REQUESTS 4096
 #define TL_TREE_NODES 64 /* nodes of a drafted tree */
@@ -468,7 +472,7 @@ int tl_step_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t
  * io  k_cache, v_cache and, for e4m3, k_scale, v_scale: the tokens' rows.  e4m3: scale =
  *                fl32(amax / 448) of the (rotated, rounded) row, code = RNE(fl32(x / scale)),
  *                both 0 for a row of zeros.
- * Requires rot a multiple of 16, at most D; finite inputs.
+ * Requires rot a multiple of 16, at most D; max_pos < 2^31; Hq <= 65536; finite inputs.
  */
 int tl_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t T,
                 int64_t H, int64_t D, const uint16_t *q, int64_t ldq, int64_t Hq, const int32_t *positions,
@@ -497,8 +501,12 @@ int tl_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, 
  *                aligned, contents free; calls that overlap in time must not share it
  * What lies in keys a token does not see (infinities and NaN among it) does not reach it.
  * Rows of out and lse of tokens that belong to no request are left as they are.
- * Requires scale > 0 and finite, 1 <= G <= 64, max_nodes >= 1, 0 <= R <= 4096, and
- * table_width * block <= 2^31 - 4096.
+ * Requires scale > 0 and finite, 1 <= G <= 64, 1 <= max_nodes < 2^31, 0 <= R <= 4096,
+ * T * G < 2^31, table_width * block <= 2^31 - 4096, and
+ *   H * (T * G / 16 + R) * (table_width * block / 128 + 1) < 2^31:
+ * the kernels count their work (16 rows by 128 keys a unit, or more) in 32 bits, and the
+ * host knows the most there can be.  A longer step is several calls, over fewer of its
+ * requests or heads each.
  */
 size_t tl_tree_attention_workspace_size(int64_t max_nodes, int64_t G, int64_t D, int cache_dtype);
 int tl_tree_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H, int64_t G, int64_t D, const void *k_cache,
@@ -522,7 +530,8 @@ int tl_tree_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H, int6
  * A request of more than 64 tokens is a prompt: all its tokens count as accepted, path is
  * -1, next its last token's target.
  * workspace      tl_tree_verify_workspace_size(T, V) bytes, 16-byte aligned, contents free
- * Requires 1 <= path_width <= 64, 1 <= V < 2^31, 0 <= R <= 4096.
+ * Requires 1 <= path_width <= 64, 1 <= V <= ld < 2^31, 0 <= R <= 4096, and T times the parts
+ * of a row (at most 64) below 2^31.
  */
 size_t tl_tree_verify_workspace_size(int64_t T, int64_t V);
 int tl_tree_verify(const void *logits, int logits_dtype, int64_t ld, int64_t T, int64_t V, const int32_t *draft,
@@ -542,6 +551,8 @@ int tl_tree_verify(const void *logits, int logits_dtype, int64_t ld, int64_t T, 
  *                of up to 64 tokens no more than path_width nodes are committed and counted:
  *                where the later ones' rows lie is not known
  * Entries of path that do not move a row forward inside the request are skipped.
+ * Requires 1 <= path_width <= 64, 1 <= L <= 4096, 0 <= R <= 4096, L * R * H < 2^31,
+ * L * pages * H * block * D <= 2^50, table_width * block < 2^31.
  */
 int tl_kv_commit(const int32_t *accepted, const int32_t *path, int64_t path_width, const int32_t *ctx_lens,
                  const int32_t *kv_lens, const int32_t *table, int64_t table_width, int64_t R, void *k_cache,

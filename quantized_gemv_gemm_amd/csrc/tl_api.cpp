@@ -572,7 +572,8 @@ int tl_tree_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H, int6
   if (table_width < 0 || table_width > kMostKeys / block) return TL_ERR_SHAPE;
   if (!(scale > 0.0f && scale < __builtin_inff())) return TL_ERR_SHAPE;
   if (T == 0 || R == 0) return TL_OK;
-  // the units of work the kernel counts stay below 2^31
+  // the units of work the kernel counts stay below 2^31, whichever form it takes: 16 rows are
+  // the fewest of a block
   if (double(H) * (double(T) * G / 16 + R) * (double(table_width) * block / 128 + 1) >= 2147483648.0) return TL_ERR_SHAPE;
   const bool e4m3 = cache_dtype == TL_E4M3;
   if (any_null(q, k_cache, v_cache, q_start, kv_lens, out) || (table_width && !table)) return TL_ERR_NULLPTR;

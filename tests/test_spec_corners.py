@@ -6,6 +6,7 @@ import ctypes
 import json
 import os
 import re
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -88,3 +89,17 @@ def test_attention_kernels_fit_lds_at_the_most_requests():
     with open(os.path.join(_build.CSRC, "tl_internal.h")) as f:
         free = int(re.search(r"kStaticLds = (\d+);", f.read()).group(1))
     assert len(figs) > 10 and max(figs.values()) <= free
+
+
+@pytest.mark.parametrize("H,T,G,R,block", [(1, 1 << 17, 16, 4096, 64), (8, 65536, 8, 1, 16), (64, 4096, 64, 64, 4096),
+                                           (65536, 16, 1, 7, 128)])
+def test_attention_units_stay_in_31_bits(H, T, G, R, block):
+    """The documented limit, H (T G / 16 + R) (width block / 128 + 1) < 2^31, at its two sides."""
+    def units(width):
+        return Fraction(H) * (Fraction(T * G, 16) + R) * (Fraction(width * block, 128) + 1)
+    lo, hi = 0, ((1 << 31) - 4096) // block + 1
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        lo, hi = (mid, hi) if units(mid) < 1 << 31 else (lo, mid)
+    assert attention_status(T=T, H=H, G=G, R=R, block=block, width=lo) == 7
+    assert attention_status(T=T, H=H, G=G, R=R, block=block, width=hi) == 2
