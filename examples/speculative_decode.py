@@ -119,8 +119,10 @@ def draft_tree(history, nodes, depth=6, branches=4):
 def generate(model, prompts, count, nodes=16, cache=torch.bfloat16, draft=draft_tree):
     """`count` tokens after each prompt, with trees of up to `nodes` tokens (1: one token a step).
     Returns the tokens, for each its logit's lead over the next best, and the steps taken."""
-    R = len(prompts)
-    state = State(model, R, max(map(len, prompts)) + count + 2 * nodes, dtype=cache)
+    R, capacity = len(prompts), max(map(len, prompts)) + count + 2 * nodes
+    if capacity > len(model.cos_sin):                    # kv_write clamps positions to the table
+        raise ValueError(f"{capacity} positions are needed, the model's rotary table has {len(model.cos_sin)}")
+    state = State(model, R, capacity, dtype=cache)
     ints = state.ints
 
     def verify(logits, tokens, parents, q_start):

@@ -5,13 +5,32 @@ import numpy as np
 import pytest
 
 pytest.importorskip("torch")
-from decoder_common import TOL, TOL_E4M3, VOCAB, apart, load_example, models  # noqa: E402
+from decoder_common import MAX_POS, TOL, TOL_E4M3, VOCAB, apart, load_example, models  # noqa: E402
 
 
 @pytest.fixture(scope="module")
-def plain():
+def example():
+    return load_example()
+
+
+@pytest.fixture(scope="module")
+def both(example):
     with pytest.MonkeyPatch.context() as m:
-        return models(load_example(), m, "cpu", pack=lambda codes, scales: (None, None, None))[1]
+        return models(example, m, "cpu", pack=lambda codes, scales: (None, None, None))
+
+
+@pytest.fixture(scope="module")
+def plain(both):
+    return both[1]
+
+
+def test_the_example_refuses_what_its_rotary_table_lacks(example, both):
+    """Positions past the table would all be turned as its last one is."""
+    prompts = [[1, 2, 3], [4] * 200]
+    with pytest.raises(ValueError, match="positions"):
+        example.generate(both[0], prompts, MAX_POS - 200 - 16 + 1, nodes=8)
+    with pytest.raises(ValueError, match="positions"):
+        example.generate(both[0], [[0] * MAX_POS], 1, nodes=1)
 
 
 def test_tokens_one_at_a_time_are_tokens_at_once(plain):
