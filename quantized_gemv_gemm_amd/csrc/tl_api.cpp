@@ -492,8 +492,8 @@ int tl_linear_apply(const uint16_t *x, int64_t T, int64_t K, int64_t N, const in
 // one step of speculative decoding over a paged cache
 int64_t tl_kv_offset(int which, int cache_dtype, int64_t H, int64_t D, int64_t block, int64_t page, int64_t head,
                      int64_t token, int64_t d) {
-  if (check_cache(cache_dtype, 1, H, block, D) || (which != 0 && which != 1)) return -1;
-  if (page < 0 || page >= kMaxDim || head < 0 || head >= H || token < 0 || token >= block || d < 0 || d >= D) return -1;
+  if (page < 0 || page >= kMaxDim || check_cache(cache_dtype, page + 1, H, block, D)) return -1;
+  if ((which != 0 && which != 1) || head < 0 || head >= H || token < 0 || token >= block || d < 0 || d >= D) return -1;
   const int es = cache_dtype == TL_BF16 ? 2 : 1, t = int(token & (tl::kKvTile - 1));
   const int in_tile = which ? tl::kv_tile_v(t, int(d), es) : tl::kv_tile_k(t, int(d), es);
   return ((page * H + head) * block + token - t) * D + in_tile;

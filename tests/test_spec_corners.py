@@ -103,3 +103,13 @@ def test_attention_units_stay_in_31_bits(H, T, G, R, block):
         lo, hi = (mid, hi) if units(mid) < 1 << 31 else (lo, mid)
     assert attention_status(T=T, H=H, G=G, R=R, block=block, width=lo) == 7
     assert attention_status(T=T, H=H, G=G, R=R, block=block, width=hi) == 2
+
+
+def test_offset_refuses_caches_beyond_the_limit():
+    """pages * H * block * D stays within 2^50: past it an offset would not fit its type."""
+    L = tl.lib()
+    page = (1 << 50) // (65536 * 4096 * 256) - 1
+    assert L.tl_kv_offset(0, tl.TL_E4M3, 65536, 256, 4096, page, 65535, 4095, 255) == (1 << 50) - 1
+    for far in (page + 1, 1 << 30, (1 << 31) - 1):
+        assert L.tl_kv_offset(0, tl.TL_E4M3, 65536, 256, 4096, far, 65535, 4095, 255) == -1
+    assert L.tl_kv_offset(1, tl.TL_BF16, 1, 64, 16, (1 << 31) - 2, 0, 15, 63) == ((1 << 31) - 1) * 1024 - 1
