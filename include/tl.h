@@ -487,8 +487,9 @@ int tl_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, 
  * in  table      int32 [R, table_width]
  * in  q_start    int32 [R + 1], kv_lens int32 [R]: request r's tokens are q_start[r] ..
  *                q_start[r + 1] - 1 (n of them), its keys the positions 0 .. kv_lens[r] - 1,
- *                of which the last n are its own tokens.  q_start must not fall: where it
- *                does, nothing is written at all
+ *                of which the last n are its own tokens; positions past the table (and in
+ *                table entries that are no page) are not there.  q_start must not fall: where
+ *                it does, nothing is written at all
  * in  tree_mask  uint64 [T] or NULL.  A token sees every key before its request's own
  *                tokens and, with a mask in a request of up to 64 tokens, the own token j
  *                where bit j is set; else the own tokens up to itself.

@@ -59,7 +59,7 @@ constexpr float kSlack = 8;                            // of a running maximum, 
 // which units there are
 struct Item {
   int r, h, b;         // request, cache head, row block
-  int n, kv;           // the request's nodes and cache length (its nodes' keys among them)
+  int n, kv;           // the request's nodes and length (its nodes' keys among them)
   int units;           // of this item
   int at;              // unit inside the item
   int64_t first;       // global index of the item's first unit
@@ -69,21 +69,20 @@ __device__ __forceinline__ int request_nodes(const TreeArgs &a, int r) {
   const int lo = max(a.q_start[r], 0), hi = min(a.q_start[r + 1], a.T);
   return max(hi - lo, 0);
 }
-__device__ __forceinline__ int request_keys(const TreeArgs &a, int r) {
-  return min(max(a.kv_lens[r], 0), a.max_keys);
-}
+__device__ __forceinline__ int request_keys(const TreeArgs &a, int r) { return max(a.kv_lens[r], 0); }
 // (n G stays below 2^31)
 __device__ __forceinline__ int row_blocks(int n, int G, int rows) { return (uint32_t(n) * G + rows - 1) / uint32_t(rows); }
 
 // A request of up to 64 nodes has the same keys for every row block; a longer one is a
-// chain, whose row block ends at its last node's own key.
-__device__ __forceinline__ int block_keys(int n, int kv, int b, int G, int rows) {
-  if (n <= kTreeNodes) return kv;
-  const int last = min(int((uint32_t(b + 1) * rows - 1) / uint32_t(G)), n - 1);
-  return max(kv - n + last + 1, 0);
+// chain, whose row block ends at its last node's own key.  A length may pass the table: the
+// keys that the table has no page for are not there, whosever they are.
+__device__ __forceinline__ int block_keys(const TreeArgs &a, int n, int kv, int b, int rows) {
+  if (n <= kTreeNodes) return min(kv, a.max_keys);
+  const int last = min(int((uint32_t(b + 1) * rows - 1) / uint32_t(a.G)), n - 1);
+  return min(max(kv - n + last + 1, 0), a.max_keys);
 }
-__device__ __forceinline__ int block_units(int n, int kv, int b, int G, int rows) {
-  return max((block_keys(n, kv, b, G, rows) + kUnitKeys - 1) / kUnitKeys, 1);
+__device__ __forceinline__ int block_units(const TreeArgs &a, int n, int kv, int b, int rows) {
+  return max((block_keys(a, n, kv, b, rows) + kUnitKeys - 1) / kUnitKeys, 1);
 }
 
 // pre[r] = units of the requests before r (R + 1 entries), by a whole workgroup of NT
@@ -105,9 +104,9 @@ __device__ __forceinline__ void unit_prefix(const TreeArgs &a, int rows, int *pr
       n = request_nodes(a, r);
       kv = request_keys(a, r);
       nb = row_blocks(n, a.G, rows);
-      if (n <= kTreeNodes) units = nb * block_units(n, kv, 0, a.G, rows);
+      if (n <= kTreeNodes) units = nb * block_units(a, n, kv, 0, rows);
       else if (nb <= kOwnBlocks)
-        for (int b = 0; b < nb; ++b) units += block_units(n, kv, b, a.G, rows);
+        for (int b = 0; b < nb; ++b) units += block_units(a, n, kv, b, rows);
     }
     uint64_t longs = __ballot(n > kTreeNodes && nb > kOwnBlocks);
     while (longs) {
@@ -116,7 +115,7 @@ __device__ __forceinline__ void unit_prefix(const TreeArgs &a, int rows, int *pr
       const int ln = __builtin_amdgcn_readlane(n, src), lkv = __builtin_amdgcn_readlane(kv, src);
       const int blocks = __builtin_amdgcn_readlane(nb, src);
       int part = 0;
-      for (int b = lane; b < blocks; b += 64) part += block_units(ln, lkv, b, a.G, rows);
+      for (int b = lane; b < blocks; b += 64) part += block_units(a, ln, lkv, b, rows);
 #pragma unroll
       for (int off = 32; off > 0; off >>= 1) part += __shfl_xor(part, off, 64);
       if (lane == src) units = part;
@@ -160,7 +159,7 @@ __device__ __forceinline__ Item locate(const TreeArgs &a, int rows, const int *p
   it.h = local / per_head;
   int v = local - it.h * per_head;
   if (it.n <= kTreeNodes) {
-    it.units = block_units(it.n, it.kv, 0, a.G, rows);
+    it.units = block_units(a, it.n, it.kv, 0, rows);
     it.b = v / it.units;
     v -= it.b * it.units;
   } else {
@@ -168,7 +167,7 @@ __device__ __forceinline__ Item locate(const TreeArgs &a, int rows, const int *p
     it.b = 0;
     it.units = 0;
     for (int base = 0; base < nb; base += 64) {
-      const int mine = base + lane < nb ? block_units(it.n, it.kv, base + lane, a.G, rows) : 0;
+      const int mine = base + lane < nb ? block_units(a, it.n, it.kv, base + lane, rows) : 0;
       int run = mine;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
@@ -410,7 +409,7 @@ __device__ __forceinline__ Segment segment_of(const TreeArgs &a, const Item &it,
   g.slot = slot;
   g.flat = g.n <= kTreeNodes;
   g.ctx = g.kv - g.n;
-  g.key_end = block_keys(g.n, g.kv, g.blk, a.G, rows);
+  g.key_end = block_keys(a, g.n, g.kv, g.blk, rows);
   g.q0 = max(a.q_start[g.r], 0);
   g.s0 = at * kUnitSteps;
   g.s1 = max(min((at + take) * kUnitSteps, (g.key_end + kStepKeys - 1) / kStepKeys), g.s0);
@@ -449,7 +448,7 @@ struct Queries {
 
   // which of the lane's eight keys from position `pos` on row tile t sees, if they are there
   __device__ __forceinline__ uint32_t visible(int t, const Segment &s, int pos) const {
-    const int j0 = pos - s.ctx;                        // the node of the first key
+    const int j0 = max(pos - s.ctx, -8);               // the node of the first key; further back all are seen
     if (s.flat)
       return (j0 <= -8 ? 255u : j0 < 0 ? uint32_t(sees[t] << -j0) | ((1u << -j0) - 1u)
                                        : j0 < 64 ? uint32_t(sees[t] >> j0) : 0u) & 255u;
@@ -748,7 +747,7 @@ __global__ __launch_bounds__(kThreads, (Split<D, E4M3, RT>::occupancy)) void tre
     Queries<D, E4M3, RT> qs;
     qs.load(a, seg, row0, row16, g);
     // keys that all rows see come first: below `clear` no mask is looked at
-    const int clear = seg.flat ? seg.ctx : seg.ctx + row0 / a.G + 1;
+    const int clear = seg.flat ? seg.ctx : seg.ctx + min(row0 / a.G + 1, seg.n);
     Rows<D, RT> acc;
     acc.clear();
 
@@ -1066,7 +1065,7 @@ __global__ __launch_bounds__((Share<D, E4M3, RT>::threads), (Share<D, E4M3, RT>:
     acc.clear();
 
     // steps before `plain` are seen by all rows, and every key of theirs is there
-    int plain = max(seg.flat ? seg.ctx : seg.ctx + row0 / a.G + 1, 0) / kStepKeys;
+    int plain = max(seg.flat ? seg.ctx : seg.ctx + min(row0 / a.G + 1, seg.n), 0) / kStepKeys;
     Window ahead;
     plain = min(plain, ahead.fill(a, seg, 2 * seg.s0, lane) >> 1);
     int issued = seg.s0;

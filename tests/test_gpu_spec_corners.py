@@ -138,3 +138,26 @@ def test_attention_of_the_most_requests(tl, D, e4m3, G, nodes, form):
     reqs[777] = (nodes, 2500)                          # one that several workgroups share
     c = Case(tl, reqs, 1, G, D, e4m3, 16, seed=D + G).call(max_nodes=nodes).check()
     assert tl.last_kernel_name() == "tree_attention_" + form
+
+
+# --------------------------------------------------------------------------- lengths past the table
+@pytest.mark.parametrize("D,e4m3,G,n,tree", [(64, False, 2, 6, True), (128, False, 4, 5, True), (128, False, 4, 16, True),
+                                             (128, True, 4, 40, True), (256, False, 3, 12, True), (256, True, 5, 9, False),
+                                             (64, True, 2, 100, False), (128, False, 3, 150, False)])
+def test_attention_lengths_past_the_table(tl, D, e4m3, G, n, tree):
+    """Positions that the table has no page for are not there, and move nothing: a request's own tokens are still
+    the last n of its length, be they in the table or not."""
+    c = Case(tl, [(n, 100), (n, 37), (1, 60)], 2, G, D, e4m3, 16, tree=tree, seed=41)
+    width = (100 + n // 2) // 16                       # ends inside request 0's own tokens
+    kernel = to_dev(c.table[:, :width].copy(), dev())
+    c.table[:, width:] = -1                            # what the plain definition goes by
+    c.call(block_table=kernel).check()
+    # lengths of which not even the context fits, up to the type's largest
+    c.kv[0] = 16 * width + n
+    c.table = np.concatenate([c.table, np.full((3, -(-int(c.kv[0]) // 16)), -1, np.int32)], 1)
+    c.call(block_table=kernel).check()
+    out, lse = c.out.clone(), c.lse.clone()
+    for far in (16 * width + n + 1, 1 << 30, (1 << 31) - 1):
+        c.kv[0] = far
+        c.call(block_table=kernel)
+        assert c.out.equal(out) and c.lse.equal(lse), far
