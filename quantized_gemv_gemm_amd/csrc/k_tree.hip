@@ -20,9 +20,9 @@
 //
 // Measured, main and joining launch: one token over 1000 keys 9.7 + 3.9 us; 4 trees of 8 over
 // 131071 e4m3 keys, 8 heads of 128, 194 + 5.4 us (5.5 TB/s; reading alone reaches 5.9); 16
-// trees of 64, 4 query heads, over up to 8192 bf16 keys 97 + 13 us (2.8 TB/s, 490 TFLOP/s);
-// 2 prompts of 2048 on 2048, 24 query heads of 256, 341 + 17 us (870 TFLOP/s; a large
-// library product reaches 1205).
+// trees of 64, 4 query heads, over up to 8192 bf16 keys 99 + 14 us (2.7 TB/s, 475 TFLOP/s),
+// e4m3 140 + 7; 2 prompts of 2048 on 2048, 24 query heads of 256, 345 + 17 us in bf16 (855
+// TFLOP/s; a large library product reaches 1205), 403 + 17 in e4m3.
 //
 // Two kernels.  `split` (few rows of a cache head): bound by the cache's bytes.  The
 // four waves of a workgroup hold the same rows and take different keys; K and V go from
@@ -31,9 +31,12 @@
 // different rows and take the same keys, which are staged in LDS two or four steps deep, so
 // that memory is read once for 64 or 128 rows.
 //
-// Rounding: q.k and p.v are sums of bf16 products in f32; the probabilities are
-// rounded once to bf16 for the product with V (off by 2^-8 of it at most, with errors of both
-// signs), while their sum is taken before that rounding.
+// Rounding: q.k and p.v are sums of bf16 products in f32; the probabilities (in e4m3 times
+// V's scale) are rounded once to bf16 for the product with V (off by 2^-8 of it at most, with
+// errors of both signs), while their sum is taken before that rounding.  It is the one place
+// between the inputs and the result with fewer than 32 bits, and what the matrix instruction
+// takes: outputs are off by 0.0023 of their size in the mean square, where their own rounding
+// to bf16 alone makes 0.0017.
 #include <type_traits>
 
 #include "kv_layout.h"
@@ -1357,17 +1360,22 @@ hipError_t launch_share(const TreeArgs &a, const char *name, hipStream_t stream)
 // Rows of one cache head in the step's longest request decide the form.  In the split form
 // every row of a block sits in each wave and the waves split the keys; blocks of 16 or 32
 // rows, of which several read the same keys.  In the share form they share the keys through
-// LDS in blocks of 64 or 128 rows.  Split and share, us, 8 cache heads (16 requests over
-// 8192 keys; 16 over 1024; one over 16384):
-//   bf16   64-wide,  64 rows   53  59 | 20 26 | 19 26      128 rows   79  70 | 21 33 | 22 29
-//   bf16  128-wide,  32 rows  110 108 | 28 28 | 26 26       64 rows  121 124 | 27 34 | 31 28
-//                                                           96 rows  236 125 | 39 43 | 37 31
-//   bf16  256-wide,  32 rows  207 195 | 31 40 | 32 35       64 rows  402 211 | 54 45 | 38 37
-//   e4m3   64-wide, 256 rows  152 143 | 39 41 | 33 40
-//   e4m3  128-wide, 128 rows  118 134 | 28 51 | 30 39      256 rows  228 219 | 47 60 | 46 53
-//   e4m3  256-wide,  32 rows  121 169 | 28 37 | 31 32       48 rows  239 177 | 40 40 | 38 34
-// 64 rows of 128-wide bf16 heads are a draw here, but one request over 65536 keys takes 52
-// in the split form and 38 in the other.
+// LDS in blocks of 64 or 128 rows.  Split and share, us a call, 8 cache heads (16 requests
+// over 8192 keys; 16 over 1024; one over 16384):
+//   bf16   64-wide,  64 rows   53  59 | 20 26 | 19 25      128 rows   79  71 | 21 33 | 23 29
+//   bf16  128-wide,  32 rows  111 108 | 28 28 | 26 25       64 rows  118 120 | 27 34 | 31 28
+//                    48 rows  113 113 | 26 31 | 29 26       96 rows  234 127 | 40 42 | 36 31
+//   bf16  256-wide,  32 rows  212 201 | 31 40 | 32 35       64 rows  405 208 | 54 45 | 38 38
+//   e4m3   64-wide, 256 rows  154 142 | 39 41 | 33 40
+//   e4m3  128-wide, 128 rows  119 133 | 29 50 | 30 39      256 rows  228 219 | 46 59 | 44 51
+//   e4m3  256-wide,  32 rows  120 168 | 27 37 | 31 32       48 rows  239 177 | 40 40 | 38 34
+// One request over 65536 keys, 128-wide bf16, 64 rows: 86 and 56 with 8 heads, 52 and 39 with 4.
+// The rule knows rows, width and type alone, so each border is a balance of these columns:
+// bf16 borders lie where many requests over long caches gain, and short caches lose up to a
+// third there (64-wide, 128 rows: 33 for 21; 128-wide, 64 rows: 34 for 27); e4m3 ones lie
+// where short caches gain, and long ones lose up to 8 % (64-wide, 256 rows: 154 for 142).  The
+// longest request speaks for all of a call: a chunk of 512 tokens with 32 single tokens
+// beside it, all over 8192 keys, takes 246 us in bf16 (in two calls 300) and 281 in e4m3 (235).
 // A step widened to two bytes in LDS for each block costs e4m3 more than bytes read again,
 // so its split form goes further.  256-wide heads leave the split form registers for 16
 // rows a wave: 32 e4m3 ones are possible with all 512 registers of a lane (113 us for 119),
@@ -1378,7 +1386,7 @@ struct Form {
 };
 Form tree_form(int64_t rows, int64_t D, bool e4m3) {
   if (rows <= (D == 256 ? 32 : e4m3 ? 256 : D == 64 ? 64 : 32)) return {false, rows <= 16 || D == 256 ? 1 : 2, 1};
-  // 64 rows in blocks of 128 leave half the waves idle: 116 us for 112
+  // 64 rows in blocks of 128 leave half the waves idle: 118 us for 115, over 1024 keys 38 for 35
   return {true, D == 256 || (rows <= 64 && D == 128) ? 1 : 2, D == 256 ? 8 : 4};
 }
 int form_rows(Form f) { return 16 * f.tiles * f.waves; }
