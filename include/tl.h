@@ -530,6 +530,8 @@ int tl_tree_attention(const uint16_t *q, int64_t ldq, int64_t T, int64_t H, int6
  * out next       int32 [R]  target of the last accepted node (-1 for a request of no tokens)
  * A request of more than 64 tokens is a prompt: all its tokens count as accepted, path is
  * -1, next its last token's target.
+ * Which requests were served is not known here: where tl_step_plan left kv_lens at 0 (and
+ * tl_kv_commit leaves the context as it was) the logits, and so these outputs, mean nothing.
  * workspace      tl_tree_verify_workspace_size(T, V) bytes, 16-byte aligned, contents free
  * Requires 1 <= path_width <= 64, 1 <= V <= ld < 2^31, 0 <= R <= 4096, and T times the parts
  * of a row (at most 64) below 2^31.

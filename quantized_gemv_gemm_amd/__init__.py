@@ -796,7 +796,8 @@ def tree_attention(q, k_cache, v_cache, block_table, q_start, kv_lens, tree_mask
 
 def tree_verify(logits, draft, parents, q_start, path_width=TREE_NODES, workspace=None):
     """Greedy check of drafted trees: logits bf16 or f32 [T, V] (any row distance), draft and parents
-    int32 [T], q_start int32 [R+1] -> (accepted [R], path [R, path_width], next [R], target [T])."""
+    int32 [T], q_start int32 [R+1] -> (accepted [R], path [R, path_width], next [R], target [T]).  What
+    it says of a request that step_plan did not serve (kv_lens 0) means nothing."""
     import torch
     i = _index_of(logits, "logits")
     code = _out_code(logits.dtype)
