@@ -562,6 +562,131 @@ int tl_kv_commit(const int32_t *accepted, const int32_t *path, int64_t path_widt
                  void *v_cache, float *k_scale, float *v_scale, int cache_dtype, int64_t L, int64_t pages, int64_t H,
                  int64_t block, int64_t D, int32_t *ctx_out, void *stream);
 
+/*
+ * tl_kv_write_norm -- tl_kv_write for layers that normalise the heads of q and k, with
+ * positions of one or several axes (time, height and width of images and video).
+ * in  k, v, slots, cos_sin, q_out, caches and scales as in tl_kv_write
+ * in  q          bf16, or NULL: tokens ldq and heads q_head elements apart (q_head = 2 D where
+ *                every head's gate lies beside it); multiples of 8, q_head >= D
+ * in  q_weight, k_weight  f32 [D] or NULL (ones).  Every row x of q and k becomes
+ *                x w / sqrt(mean of x^2 + eps), then is rotated as in tl_kv_write, all in f32;
+ *                q and a bf16 cache get it rounded once, an e4m3 cache takes scale and codes
+ *                from the f32 values.  v is written as in tl_kv_write.
+ * in  positions  int32 [axes, T], axis_of int32 [rot/2]: the axis whose positions turn the
+ *                pair (d, d + rot/2); clamped to the axes.  axis_of may be NULL with one axis.
+ * Requires 1 <= axes <= 16, eps >= 0 and finite; otherwise as tl_kv_write.
+ */
+int tl_kv_write_norm(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t T,
+                     int64_t H, int64_t D, const uint16_t *q, int64_t ldq, int64_t q_head, int64_t Hq,
+                     const float *q_weight, const float *k_weight, float eps, const int32_t *positions, int64_t axes,
+                     const int32_t *axis_of, const float *cos_sin, int64_t max_pos, int64_t rot, uint16_t *q_out,
+                     void *k_cache, void *v_cache, float *k_scale, float *v_scale, int cache_dtype, int64_t pages,
+                     int64_t block, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Layers that keep a state of fixed size for each request in the place of a cache: a short
+ * causal convolution and the gated delta rule, in the same steps (trees, single tokens,
+ * prompt chunks) and with the same lengths on the device:
+ *   tl_step_plan
+ *   (per layer)        the linear layer, tl_short_conv, tl_delta_rule, the output layer, ...
+ *   tl_tree_verify, tl_kv_commit (attention layers), tl_delta_commit (these layers)
+ * q_start int32 [R + 1] and kv_lens int32 [R] are tl_step_plan's; request r's states are row
+ * state_slots[r] (int32 [R]) of the states.  n = q_start[r + 1] - q_start[r] is the request's
+ * number of tokens in the step.
+ *   A request with kv_lens <= n has just begun: it starts from a state of zeros, whatever
+ * its row holds.  One with kv_lens <= 0, or a row outside [0, states), is not served: its
+ * tokens' outputs are zeros and its state is left alone.  A request without tokens leaves its
+ * state alone.  Served requests of a call must not share a row.  Where q_start falls, or
+ * leaves [0, T], nothing is written at all.  Outputs of tokens that belong to no request are
+ * left as they are.
+ *   tree_mask uint64 [T] or NULL: with it, requests of up to 64 tokens are drafted trees; a
+ * token's bits up to its own name its ancestors (its own is always among them), and the
+ * states are not changed: tl_delta_commit takes them along the accepted branch.  Longer
+ * requests, and all without a mask, are chains, and their states are those after their
+ * last token when the call is done.
+ *   Pointers need 16-byte alignment, gates and metadata their natural one.  0 <= R <= 4096,
+ * T < 2^31, 0 <= states < 2^31, distances below 2^31 and at least a row; all states of a call
+ * together have at most 2^50 elements.
+ */
+
+/*
+ * tl_short_conv -- y[t, c] = bias[c] + sum over j < taps of weight[c, taps - 1 - j] x[j back, c],
+ * then y / (1 + exp(-y)); "j back" is j tokens back along the chain or the branch, before the
+ * step's tokens the state's rows.
+ * in  x          bf16 [T, C], rows ldx elements apart (a multiple of 8)
+ * in  weight     f32 [C, taps], bias f32 [C] or NULL
+ * in  norm_heads, norm_dim, eps: the first norm_heads heads of norm_dim channels (q and k) are
+ *                divided by sqrt(sum of the head's y^2 + eps); 0 heads: none
+ * out out        bf16 [T, C], rows ldo elements apart (a multiple of 8); sums and norms in f32,
+ *                rounded once
+ * io  state      bf16 [states, taps - 1, C]: the last taps - 1 rows of x, the oldest first
+ * Requires taps 2, 3 or 4, C a multiple of 8 up to 2^20, norm_dim 64, 128 or 256, finite inputs.
+ */
+int tl_short_conv(const uint16_t *x, int64_t ldx, int64_t T, int64_t C, const float *weight, int64_t taps,
+                  const float *bias, const int32_t *q_start, const int32_t *kv_lens, const int32_t *state_slots,
+                  int64_t R, const uint64_t *tree_mask, int64_t norm_heads, int64_t norm_dim, float eps,
+                  uint16_t *state, int64_t states, uint16_t *out, int64_t ldo, void *stream);
+
+/*
+ * tl_delta_rule -- for each value head h, with its state S [Dk, Dv] and token by token:
+ *   S <- exp(g) S + k (b (v - exp(g) S^T k))^T,   out = scale S^T q
+ * (a tree's token starts from its parent's state).  Value heads h G .. h G + G - 1 share the
+ * key head h.
+ * in  q, k       bf16 [T, Hk, Dk], v bf16 [T, Hk * G, Dv], tokens ldq, ldk, ldv elements apart
+ *                (multiples of 8)
+ * in  a, b       f32 [T, Hk * G], rows lda, ldb apart; with a_log and dt_bias f32 [Hk * G]:
+ *                g = -exp(a_log) log(1 + exp(a + dt_bias)), b = 1 / (1 + exp(-b));
+ *                with both NULL a is the log decay g and b the step b
+ * out out        bf16 [T, Hk * G, Dv]
+ * io  state      f32 [states, Hk * G, Dk, Dv]; computed as exactly as f32 products and sums are
+ * max_nodes      the most tokens a request has, as far as the caller knows: it chooses the
+ *                kernel and sizes the workspace; lengths above it are still right
+ * workspace      tl_delta_rule_workspace_size(T, R, Hk, G, Dk, max_nodes, tree) bytes (tree: not 0
+ *                with a tree_mask), contents free, may be NULL where that is 0; calls that
+ *                overlap in time must not share it
+ * With a tree_mask whose bits are no tree's, D_i being the sum of g over token i's bits, the
+ * result is that of u_i = b_i (v_i - exp(D_i) S^T k_i - sum over i's other bits j of
+ * exp(D_i - D_j) (k_i k_j) u_j), out_i = scale (exp(D_i) S^T q_i + sum over i's bits of
+ * exp(D_i - D_j) (q_i k_j) u_j).
+ * Requires Dk 64 or 128, Dv a multiple of 16 up to 65536, Hk * G <= 65535,
+ * R * Hk * G * Dv / 16 < 2^31, max_nodes < 2^31, finite scale.  What is not finite in a token's k, v,
+ * g or b leaves nothing finite in the results of the tokens that see it and in the state after it,
+ * and changes nothing else; -inf is a log decay like any other: one below -10^4 counts as
+ * -10^4, whose exp is 0.
+ */
+size_t tl_delta_rule_workspace_size(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_t Dk, int64_t max_nodes,
+                                    int tree);
+int tl_delta_rule(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                  const float *a, int64_t lda, const float *b, int64_t ldb, const float *a_log, const float *dt_bias,
+                  int64_t T, int64_t Hk, int64_t G, int64_t Dk, int64_t Dv, const int32_t *q_start,
+                  const int32_t *kv_lens, const int32_t *state_slots, int64_t R, const uint64_t *tree_mask, float scale,
+                  float *state, int64_t states, int64_t max_nodes, uint16_t *out, void *workspace,
+                  size_t workspace_bytes, void *stream);
+
+/*
+ * tl_delta_commit -- the states of a tree step taken along the accepted branches, in L layers.
+ * in  accepted   int32 [R], path int32 [R, path_width] from tl_tree_verify; entries that name no
+ *                token of the request are skipped, and accepted counts up to path_width
+ * in  q_start, kv_lens, state_slots  the step's
+ * in  k, v, a, b  the step's inputs of tl_delta_rule in every layer, tokens ldk, ldv, lda, ldb and
+ *                layers k_layer, v_layer, a_layer, b_layer elements apart; a_log, dt_bias f32
+ *                [L, Hk * G] or both NULL
+ * io  state      f32 [L, states, Hk * G, Dk, Dv]
+ * in  x          bf16 [L, T, C], the step's input of tl_short_conv, rows ldx and layers x_layer
+ *                apart, or NULL; io conv_state bf16 [L, states, taps - 1, C] (with x)
+ * Requests of more than 64 tokens, that are not served or of which nothing is accepted are
+ * left alone.
+ * Requires 1 <= path_width <= 64, 1 <= L <= 4096, L * R * (Hk * G * Dv / 32 + C / 2048) < 2^31;
+ * otherwise as tl_delta_rule and tl_short_conv.
+ */
+int tl_delta_commit(const int32_t *accepted, const int32_t *path, int64_t path_width, const int32_t *q_start,
+                    const int32_t *kv_lens, const int32_t *state_slots, int64_t R, int64_t T, int64_t L,
+                    const uint16_t *k, int64_t ldk, int64_t k_layer, const uint16_t *v, int64_t ldv, int64_t v_layer,
+                    const float *a, int64_t lda, int64_t a_layer, const float *b, int64_t ldb, int64_t b_layer,
+                    const float *a_log, const float *dt_bias, int64_t Hk, int64_t G, int64_t Dk, int64_t Dv,
+                    float *state, int64_t states, const uint16_t *x, int64_t ldx, int64_t x_layer, int64_t C,
+                    int64_t taps, uint16_t *conv_state, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -75,6 +75,17 @@ _SIGS = {
                                       _c_i64, _c_p, _c_p, _c_p, _c_sz, _c_p]),
     "tl_kv_commit": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p,
                                     ctypes.c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p]),
+    "tl_kv_write_norm": (ctypes.c_int, [_c_p, _c_i64, _c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i64,
+                                        _c_i64, _c_p, _c_p, ctypes.c_float, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_i64,
+                                        _c_p, _c_p, _c_p, _c_p, _c_p, ctypes.c_int, _c_i64, _c_i64, _c_p]),
+    "tl_short_conv": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p,
+                                     _c_i64, _c_i64, ctypes.c_float, _c_p, _c_i64, _c_p, _c_i64, _c_p]),
+    "tl_delta_rule_workspace_size": (_c_sz, [_c_i64] * 6 + [ctypes.c_int]),
+    "tl_delta_rule": (ctypes.c_int, [_c_p, _c_i64] * 5 + [_c_p, _c_p] + [_c_i64] * 5 + [_c_p, _c_p, _c_p, _c_i64, _c_p,
+                                    ctypes.c_float, _c_p, _c_i64, _c_i64, _c_p, _c_p, _c_sz, _c_p]),
+    "tl_delta_commit": (ctypes.c_int, [_c_p, _c_p, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64]
+                        + [_c_p, _c_i64, _c_i64] * 4 + [_c_p, _c_p] + [_c_i64] * 4
+                        + [_c_p, _c_i64, _c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p]),
     "tl_linear_apply_noalloc": (ctypes.c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p,
                                                _c_p, ctypes.c_int, _c_p]),
 }
@@ -587,6 +598,15 @@ def _raw_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _call(name, index, *args):
+    """Calls the library on GPU ``index`` and its current stream (appended), whichever GPU is current."""
+    import torch
+    if torch._C._cuda_getDevice() != index:
+        with torch.cuda.device(index):
+            return _check(name, getattr(lib(), name)(*args, _raw_stream(index)))
+    return _check(name, getattr(lib(), name)(*args, _raw_stream(index)))
+
+
 def _given(t, name, dtype, shape, index):
     """A contiguous GPU tensor of this dtype and shape, on device number ``index``; its address."""
     if t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
@@ -845,3 +865,227 @@ def kv_commit(accepted, path, ctx_lens, kv_lens, block_table, k_cache, v_cache, 
         code, k_cache.shape[0] if layers else 1, pages, H, block, D, _given(ctx_out, "ctx_out", i32, (R,), i),
         _raw_stream(i)))
     return ctx_out
+
+
+def _q_rows(t, name, index):
+    """A bf16 [tokens, heads, D] tensor whose heads may be more than a head apart (q beside its gate): its address,
+    and the distances of tokens and of heads."""
+    import torch
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.get_device() != index:
+        _need(t.contiguous(), name, torch.bfloat16, 3)
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    T, H, D = t.shape
+    ld, sh, sd = t.stride()
+    if sd != 1 and D > 1:
+        raise ValueError(f"{name}'s elements must lie next to each other (strides {t.stride()})")
+    sh = sh if H > 1 else D
+    ld = ld if T > 1 else max(H - 1, 0) * sh + D
+    if sh < D or ld < max(H - 1, 0) * sh + D:
+        raise ValueError(f"{name}'s rows must not overlap (strides {t.stride()}): copy a broadcast tensor first")
+    return t.data_ptr(), ld, sh
+
+
+def kv_write_norm(k, v, slots, k_cache, v_cache, k_scale=None, v_scale=None, q=None, q_weight=None, k_weight=None,
+                  eps=1e-6, positions=None, cos_sin=None, axis_of=None, q_out=None):
+    """kv_write for layers that normalise every head of q and k: rows become x w / sqrt(mean x^2 + eps), with
+    q_weight and k_weight f32 [D] (None: ones), before they are rotated; q's heads may be more than a head apart.
+    positions int32 [T], or [axes, T] with axis_of int32 [rot/2]: the axis that turns each pair.  q and a
+    bfloat16 cache get the rows rounded once; an e4m3 cache takes scales and codes from the f32 rows."""
+    import torch
+    i = _index_of(k, "k")
+    code, kc, vc, ks, vs = _cache_args(k_cache, v_cache, k_scale, v_scale, i)
+    pages, H, block, D = k_cache.shape
+    kp, ldk = _rows(k, "k", i)
+    vp, ldv = _rows(v, "v", i)
+    T = k.shape[0]
+    if k.shape != (T, H, D) or v.shape != (T, H, D):
+        raise ValueError(f"k and v must be [T, {H}, {D}]")
+    sp = _given(slots, "slots", torch.int64, (T,), i)
+    f32 = torch.float32
+    kw = None if k_weight is None else _given(k_weight, "k_weight", f32, (D,), i)
+    qw = None if q_weight is None else _given(q_weight, "q_weight", f32, (D,), i)
+    qp, ldq, hq, Hq, qo = None, 0, D, 0, None
+    if q is not None:
+        qp, ldq, hq = _q_rows(q, "q", i)
+        Hq = q.shape[1]
+        if q.shape != (T, Hq, D):
+            raise ValueError(f"q must be [{T}, heads, {D}]")
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
+        qo = _given(q_out, "q_out", torch.bfloat16, (T, Hq, D), i)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight need q")
+    pp, cp, xp, most, rot, axes = None, None, None, 0, 0, 1
+    if cos_sin is not None:
+        if positions is None or cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be [max_pos, rot] and needs positions")
+        most, rot = cos_sin.shape
+        cp = _given(cos_sin, "cos_sin", f32, (most, rot), i)
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        pp = _given(positions, "positions", torch.int32, (axes, T) if positions.dim() == 2 else (T,), i)
+        if axis_of is not None:
+            xp = _given(axis_of, "axis_of", torch.int32, (rot // 2,), i)
+        elif axes != 1:
+            raise ValueError("positions of several axes need axis_of")
+    elif axis_of is not None:
+        raise ValueError("axis_of needs cos_sin")
+    _call("tl_kv_write_norm", i,
+        kp, ldk, vp, ldv, sp, T, H, D, qp, ldq, hq, Hq, qw, kw, eps, pp, axes, xp, cp, most, rot, qo, kc, vc, ks, vs, code,
+        pages, block)
+    return q_out
+
+
+# ---------------------------------------------------------------------------
+# layers that keep a state per request
+# ---------------------------------------------------------------------------
+def _columns(t, name, dtype, shape, index):
+    """A tensor of this shape whose last dimension is contiguous and whose rows lie apart: its address and the
+    distances of rows and, with three dimensions, of layers."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != index:
+        _need(t.contiguous(), name, dtype, len(shape))
+        if t.get_device() != index:
+            raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    *lead, ld, one = t.stride()
+    rows, cols = shape[-2:]
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name}'s columns must lie next to each other (strides {t.stride()})")
+    ld = ld if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name}'s rows must not overlap (strides {t.stride()}): copy a broadcast tensor first")
+    return (t.data_ptr(), ld) if len(shape) == 2 else (t.data_ptr(), ld, lead[0] if shape[0] > 1 else 0)
+
+
+def _heads(t, name, index, layers):
+    """A bf16 [tokens, heads, D] tensor, or [layers, tokens, heads, D], as _columns of its heads' elements."""
+    import torch
+    if t.dim() != (4 if layers else 3):
+        raise ValueError(f"{name} must be [{'layers, ' if layers else ''}tokens, heads, D], got {list(t.shape)}")
+    H, D = t.shape[-2:]
+    if t.stride(-1) != 1 and D > 1 or t.stride(-2) != D and H > 1:
+        raise ValueError(f"{name}'s heads must lie next to each other (strides {t.stride()})")
+    flat = t.as_strided((*t.shape[:-2], H * D), (*t.stride()[:-2], 1))
+    return _columns(flat, name, torch.bfloat16, flat.shape, index)
+
+
+def _step_args(q_start, kv_lens, state_slots, tree_mask, T, index):
+    import torch
+    R, i32 = kv_lens.shape[0], torch.int32
+    return (R, _given(q_start, "q_start", i32, (R + 1,), index), _given(kv_lens, "kv_lens", i32, (R,), index),
+            _given(state_slots, "state_slots", i32, (R,), index),
+            None if tree_mask is None else _given(tree_mask, "tree_mask", torch.int64, (T,), index))
+
+
+def short_conv(x, weight, q_start, kv_lens, state_slots, state, bias=None, tree_mask=None, norm_heads=0, norm_dim=128,
+               eps=1e-6, out=None):
+    """Causal convolution of x bf16 [T, C] (rows a row or more apart) with weight f32 [C, taps] along each request (or,
+    with tree_mask int64 [T], each tree's branches), then SiLU; the first norm_heads heads of norm_dim channels are
+    divided by their length.  state bf16 [states, taps - 1, C] holds the rows before the step, request r's at
+    state_slots[r], and is brought up to date for chains.  Returns out bf16 [T, C]."""
+    import torch
+    i = _index_of(x, "x")
+    if x.dim() != 2 or weight.dim() != 2 or state.dim() != 3:
+        raise ValueError("short_conv needs x [T, C], weight [C, taps] and state [states, taps - 1, C]")
+    (T, C), taps, bf16, f32 = x.shape, weight.shape[1], torch.bfloat16, torch.float32
+    xp, ldx = _columns(x, "x", bf16, (T, C), i)
+    R, sp, lp, np_, mp = _step_args(q_start, kv_lens, state_slots, tree_mask, T, i)
+    out = torch.empty((T, C), dtype=bf16, device=x.device) if out is None else out
+    op, ldo = _columns(out, "out", bf16, (T, C), i)
+    _call("tl_short_conv", i,
+        xp, ldx, T, C, _given(weight, "weight", f32, (C, taps), i), taps,
+        None if bias is None else _given(bias, "bias", f32, (C,), i), sp, lp, np_, R, mp, norm_heads, norm_dim, eps,
+        _given(state, "state", bf16, (state.shape[0], taps - 1, C), i), state.shape[0], op, ldo)
+    return out
+
+
+def delta_rule_workspace_size(tokens: int, requests: int, key_heads: int, group: int, Dk: int, max_nodes: int,
+                              tree=False) -> int:
+    """Bytes of workspace delta_rule needs; tree: whether it gets a tree_mask."""
+    return int(lib().tl_delta_rule_workspace_size(tokens, requests, key_heads, group, Dk, max_nodes, int(tree)))
+
+
+def _gates(a, b, a_log, dt_bias, shape, index):
+    import torch
+    f32 = torch.float32
+    if (a_log is None) != (dt_bias is None):
+        raise ValueError("a_log and dt_bias come together")
+    lead = shape[:-2] + shape[-1:]
+    return (_columns(a, "a", f32, shape, index), _columns(b, "b", f32, shape, index),
+            None if a_log is None else _given(a_log, "a_log", f32, lead, index),
+            None if a_log is None else _given(dt_bias, "dt_bias", f32, lead, index))
+
+
+def delta_rule(q, k, v, a, b, q_start, kv_lens, state_slots, state, a_log=None, dt_bias=None, tree_mask=None, scale=None,
+               max_nodes=None, out=None, workspace=None):
+    """The gated delta rule, S <- exp(g) S + k (b (v - exp(g) S^T k))^T and out = scale S^T q, along each request (or, with
+    tree_mask int64 [T], each tree's branches).  q, k bf16 [T, Hk, Dk] and v bf16 [T, Hv, Dv] (tokens a row or more apart);
+    a, b f32 [T, Hv]: with a_log and dt_bias f32 [Hv], g = -exp(a_log) softplus(a + dt_bias) and b = sigmoid(b), else g = a.
+    state f32 [states, Hv, Dk, Dv], request r's at state_slots[r], is brought up to date for chains.  Returns out bf16
+    [T, Hv, Dv].  ``max_nodes``: the most tokens of a request, as far as known (chooses the kernel)."""
+    import torch
+    i = _index_of(q, "q")
+    if state.dim() != 4:
+        raise ValueError("state must be [states, value heads, Dk, Dv]")
+    qp, ldq = _heads(q, "q", i, False)
+    kp, ldk = _heads(k, "k", i, False)
+    vp, ldv = _heads(v, "v", i, False)
+    (T, Hk, Dk), (states, Hv, _, Dv) = q.shape, state.shape
+    if k.shape != q.shape or v.shape != (T, Hv, Dv) or Hk == 0 or Hv % Hk or Hv == 0:
+        raise ValueError(f"k must be {list(q.shape)} and v [T, a multiple of {Hk}, Dv] as the state has them")
+    R, sp, lp, np_, mp = _step_args(q_start, kv_lens, state_slots, tree_mask, T, i)
+    (ap, lda), (bp, ldb), gp, dp = _gates(a, b, a_log, dt_bias, (T, Hv), i)
+    tp = _given(state, "state", torch.float32, (states, Hv, Dk, Dv), i)
+    out = torch.empty((T, Hv, Dv), dtype=torch.bfloat16, device=q.device) if out is None else out
+    op = _given(out, "out", torch.bfloat16, (T, Hv, Dv), i)
+    if max_nodes is None:
+        max_nodes = max(1, -(-T // max(R, 1)))
+    wp, size = None, 0
+    if workspace is None:
+        size = lib().tl_delta_rule_workspace_size(T, R, Hk, Hv // Hk, Dk, max_nodes, mp is not None)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        size = workspace.numel()
+        wp = _given(workspace, "workspace", torch.uint8, (size,), i)
+    _call("tl_delta_rule", i,
+        qp, ldq, kp, ldk, vp, ldv, ap, lda, bp, ldb, gp, dp, T, Hk, Hv // Hk, Dk, Dv, sp, lp, np_, R, mp,
+        Dk ** -0.5 if scale is None else scale, tp, states, max_nodes, op, wp, size)
+    return out
+
+
+def delta_commit(accepted, path, q_start, kv_lens, state_slots, k, v, a, b, state, a_log=None, dt_bias=None, x=None,
+                 conv_state=None):
+    """Takes the states of a tree step along the accepted branches (tree_verify's accepted [R] and path [R, width]): state
+    f32 [L, states, Hv, Dk, Dv] with the step's k [L, T, Hk, Dk], v [L, T, Hv, Dv], a, b [L, T, Hv] (a_log, dt_bias [L, Hv]),
+    and conv_state bf16 [L, states, taps - 1, C] with the convolution's input x [L, T, C], of all L layers, or of one
+    without the leading dimension."""
+    import torch
+    i = _index_of(accepted, "accepted")
+    if state.dim() not in (4, 5):
+        raise ValueError("state must be [states, value heads, Dk, Dv], with or without layers before")
+    if state.dim() == 4:
+        one = lambda t: None if t is None else t.unsqueeze(0)
+        k, v, a, b, state, a_log, dt_bias, x, conv_state = map(one, (k, v, a, b, state, a_log, dt_bias, x, conv_state))
+    L, states, Hv, Dk, Dv = state.shape
+    kp = _heads(k, "k", i, True)
+    vp = _heads(v, "v", i, True)
+    _, T, Hk, _ = k.shape
+    if k.shape != (L, T, Hk, Dk) or v.shape != (L, T, Hv, Dv) or Hk == 0 or Hv % Hk or Hv == 0:
+        raise ValueError(f"k must be [{L}, T, heads, {Dk}] and v [{L}, T, {Hv}, {Dv}]")
+    R, sp, lp, np_, _ = _step_args(q_start, kv_lens, state_slots, None, T, i)
+    ap, bp, gp, dp = _gates(a, b, a_log, dt_bias, (L, T, Hv), i)
+    if path.dim() != 2:
+        raise ValueError("path must be [R, width]")
+    xp, C, taps, cp = (None, 0, 0), 0, 0, None
+    if x is not None:
+        if conv_state is None or x.dim() != 3 or conv_state.dim() != 4:
+            raise ValueError("x [T, C] and conv_state [states, taps - 1, C] come together")
+        C, taps = x.shape[2], conv_state.shape[2] + 1
+        xp = _columns(x, "x", torch.bfloat16, (L, T, C), i)
+        cp = _given(conv_state, "conv_state", torch.bfloat16, (L, states, taps - 1, C), i)
+    elif conv_state is not None:
+        raise ValueError("x [T, C] and conv_state [states, taps - 1, C] come together")
+    _call("tl_delta_commit", i,
+        _given(accepted, "accepted", torch.int32, (R,), i), _given(path, "path", torch.int32, (R, path.shape[1]), i),
+        path.shape[1], sp, lp, np_, R, T, L, *kp, *vp, *ap, *bp, gp, dp, Hk, Hv // Hk, Dk, Dv,
+        _given(state, "state", torch.float32, (L, states, Hv, Dk, Dv), i), states, *xp, C, taps, cp)
+    return state

@@ -1,0 +1,149 @@
+// The short causal convolution of a layer that keeps a state: for each channel c and token t
+//   y = bias[c] + sum over j < W of w[c, W - 1 - j] x[j tokens back, c],   y <- y / (1 + exp(-y)),
+// and the first norm_heads heads of D channels are divided by sqrt(sum of their y^2 + eps).
+// "j tokens back" goes along the request (a chain) or along the tree's branch, and past the
+// step's first token into the request's state: its last W - 1 rows of x, the oldest first.
+//
+// A thread holds 8 neighbouring channels of a run of tokens; D / 8 neighbouring lanes hold a head.
+#include "kv_layout.h"
+#include "mixer_dev.h"
+
+namespace tl {
+namespace {
+
+constexpr int kRun = 16;   // tokens of a run
+constexpr int kAhead = 4;  // rows of a run on their way together
+
+struct Row8 {
+  float v[8];
+};
+__device__ __forceinline__ Row8 widen(u32x4 w) {
+  Row8 x;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x.v[2 * e] = lo_bf16(w[e]);
+    x.v[2 * e + 1] = hi_bf16(w[e]);
+  }
+  return x;
+}
+
+template <int W>
+__global__ __launch_bounds__(kMixerThreads) void short_conv_kernel(const ConvArgs a) {
+  const Piece p = find_piece<kRun>(a.q_start, a.R, a.T, int(blockIdx.x));
+  if (p.r < 0) return;
+  const int c0 = (int(blockIdx.y) * kMixerThreads + threadIdx.x) * 8;
+  if (c0 >= a.C) return;                                 // heads are whole: their lanes agree
+  const int i0 = p.part * kRun, count = min(kRun, p.n - i0);
+  uint16_t *out = a.out + int64_t(p.first + i0) * a.ldo + c0;
+  const int row = state_row(a.kv_lens, a.slots, a.state_count, p.r);
+  if (row < 0) {
+    for (int i = 0; i < count; ++i) *reinterpret_cast<u32x4 *>(out + int64_t(i) * a.ldo) = u32x4{0, 0, 0, 0};
+    return;
+  }
+  const bool tree = a.tree_mask && p.n <= kTreeNodes, fresh = a.kv_lens[p.r] <= p.n;
+  uint16_t *state = a.state + int64_t(row) * (W - 1) * a.C + c0;
+  const uint16_t *x = a.x + int64_t(p.first) * a.ldx + c0;
+  auto load_row = [&](int at) -> u32x4 {                 // token `at`, or for at < 0 the state's row at + W - 1
+    if (at < 0 && fresh) return u32x4{0, 0, 0, 0};
+    return *reinterpret_cast<const u32x4 *>(at >= 0 ? x + int64_t(at) * a.ldx : state + int64_t(at + W - 1) * a.C);
+  };
+  float w[W][8], bias[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    bias[e] = a.bias ? a.bias[c0 + e] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) w[j][e] = a.weight[int64_t(c0 + e) * W + j];
+  }
+  auto finish = [&](float (&y)[8], int i) {              // SiLU, the head's length, rounding
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504f * y[e]));
+      sum = fmaf(y[e], y[e], sum);
+    }
+    if (c0 < a.norm_channels) {
+      for (int off = a.norm_dim / 16; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+      const float by = 1.0f / sqrtf(sum + a.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] *= by;
+    }
+    u32x4 o;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
+    *reinterpret_cast<u32x4 *>(out + int64_t(i) * a.ldo) = o;
+  };
+  if (tree) {
+    for (int i = 0; i < count; ++i) {
+      const uint64_t word = a.tree_mask[p.first + i0 + i];
+      u32x4 raw[W];
+      int at = i0 + i;
+#pragma unroll
+      for (int j = W - 1; j >= 0; --j) {
+        raw[j] = load_row(at);
+        if (at > 0) {                                    // the nearest ancestor, or the row before the step
+          const uint64_t less = word & ((uint64_t(1) << at) - 1);
+          at = less ? 63 - __clzll(less) : -1;
+        } else {
+          --at;
+        }
+      }
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = bias[e];
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        const Row8 r = widen(raw[j]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = fmaf(w[j][e], r.v[e], y[e]);
+      }
+      finish(y, i);
+    }
+    return;
+  }
+  Row8 rows[W - 1 + kAhead];                             // the last W - 1 rows, and the next ones
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) rows[j] = widen(load_row(i0 - (W - 1) + j));
+  for (int i = 0; i < count; i += kAhead) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) rows[W - 1 + u] = widen(load_row(min(i0 + i + u, p.n - 1)));
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (i + u >= count) break;                         // uniform
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = bias[e];
+#pragma unroll
+      for (int j = 0; j < W; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = fmaf(w[j][e], rows[u + j].v[e], y[e]);
+      finish(y, i + u);
+    }
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) rows[j] = rows[kAhead + j];
+  }
+  if (i0 == 0) {                                         // the thread that has read the old rows
+    u32x4 next[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) next[j] = load_row(p.n - (W - 1) + j);
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<u32x4 *>(state + int64_t(j) * a.C) = next[j];
+  }
+}
+
+template <int W>
+hipError_t run(const ConvArgs &a, hipStream_t stream) {
+  const int64_t pieces = int64_t(a.T) / kRun + a.R;
+  (void)hipGetLastError();
+  hipLaunchKernelGGL((short_conv_kernel<W>), dim3(unsigned(pieces), unsigned((a.C + 2047) / 2048)), dim3(kMixerThreads), 0,
+                     stream, a);
+  set_last_kernel("short_conv");
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_short_conv(const ConvArgs &a, int64_t taps, hipStream_t stream) {
+  return taps == 2 ? run<2>(a, stream) : taps == 3 ? run<3>(a, stream) : run<4>(a, stream);
+}
+
+}  // namespace tl

@@ -1,0 +1,719 @@
+// The gated delta rule.  Each request keeps for each value head a state S [Dk, Dv] in f32;
+// token by token, with log decay g and step b,
+//   S <- exp(g) S + k u^T,   u = b (v - exp(g) S^T k),   out = scale S^T q.
+//
+// Few tokens (delta_step_kernel): token by token, the state in registers.
+//
+// Many tokens and drafted trees: chunks of 64.  With D_i the sum of the log decays of token i
+// and its ancestors (all before it, in a chain) and j running over i's ancestors,
+//   u_i = b_i (v_i - exp(D_i) S^T k_i - sum_j exp(D_i - D_j) (k_i k_j) u_j),
+// so U = T (V - exp(D) K S) with T = (I + A)^-1 diag(b), A_ij = b_i exp(D_i - D_j) k_i k_j, and
+//   out_i = scale (exp(D_i) S^T q_i + sum_j P_ij u_j),  P_ij = exp(D_i - D_j) q_i k_j (j = i too),
+//   S <- exp(D_last) S + sum_j k_j (exp(D_last - D_j) u_j)^T.
+// T and P need no state: delta_prep_kernel makes them for all chunks at once, and
+// delta_scan_kernel walks a request's chunks with 32 columns of a head's state in registers.
+//
+// Products run on the bf16 matrix instructions.  q and k are bf16; an f32 operand is the sum
+// of three bf16 parts of 8 bits each, cut off exactly (x = hi + mid + lo), and its products
+// are added part by part in f32: S and u are as exact as f32 products would make them, at
+// three instructions (six for T times an f32 operand, without the terms below 2^-24) where
+// f32 matrix instructions would take eight times the cycles.  What only reaches the bf16
+// output, P and S^T q, takes two parts: 16 bits.
+//
+// A product with a masked zero would still spread what is not finite to tokens that do not see
+// it.  So tokens with such a k, g or b, and elements of v, count as zeros in the products, and
+// the results of those that do see them, and the state, become NaN at the end.
+#include "kv_layout.h"
+#include "mixer_dev.h"
+
+namespace tl {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kThreads = kMixerThreads;
+constexpr int kChunk = 64;          // tokens of a chunk: a tree's most
+static_assert(kChunk == kTreeNodes, "a tree is one chunk");
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// the upper 16 bits of two floats
+__device__ __forceinline__ uint32_t upper(float x, float y) {
+  return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302);
+}
+__device__ __forceinline__ float below(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xFFFF0000u); }
+
+// log decay and step of token t and value head h
+struct Gate {
+  float g, b;
+};
+__device__ __forceinline__ Gate gate_of(const DeltaArgs &a, const float *pa, const float *pb, int64_t t, int h, int layer) {
+  const float x = pa[t * a.lda + h], y = pb[t * a.ldb + h];
+  if (!a.a_log) return {x, y};
+  const float z = x + a.dt_bias[int64_t(layer) * a.Hv + h];
+  return {-expf(a.a_log[int64_t(layer) * a.Hv + h]) * (z > 20.0f ? z : log1pf(expf(z))), 1.0f / (1.0f + expf(-y))};
+}
+
+// ---------------------------------------------------------------------------
+// Token by token.  A workgroup takes one request, head and 32 columns; a thread holds 4
+// columns of Dk / 32 rows.  S^T k and S^T q of the old state are summed together: the new
+// state's S^T q is exp(g) S^T q + (q k) u.
+template <int DK, bool COMMIT>
+__global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a, int conv_groups) {
+  constexpr int N = DK / 32;
+  __shared__ float s_k[DK], s_q[DK];
+  __shared__ float s_sum[4][8][9];
+  __shared__ int s_token[kTreeNodes];
+  __shared__ int s_count;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int blocks = (a.Dv + 31) / 32;
+  int id = blockIdx.x;
+  const bool conv = COMMIT && id >= a.L * a.R * a.Hv * blocks;
+  int cb, h = 0, r, layer;
+  if (conv) {
+    id -= a.L * a.R * a.Hv * blocks;
+    cb = id % conv_groups;
+    id /= conv_groups;
+  } else {
+    cb = id % blocks;
+    id /= blocks;
+    h = id % a.Hv;
+    id /= a.Hv;
+  }
+  r = id % a.R;
+  layer = id / a.R;
+  if (!starts_rise(a.q_start, a.R, a.T)) return;
+  const int first = a.q_start[r], n = a.q_start[r + 1] - first;
+  if (n <= 0) return;
+  const int srow = state_row(a.kv_lens, a.slots, a.state_count, r);
+  const bool fresh = a.kv_lens[r] <= n;
+  const int col = cb * 32 + 4 * (lane & 7);
+  const bool live = col < a.Dv;
+  int count = n;
+  if constexpr (COMMIT) {
+    if (srow < 0 || n > kTreeNodes) return;
+    if (wave == 0) {
+      const int most = min(min(max(a.accepted[r], 0), a.path_width), n);
+      const int at = lane < most ? a.path[int64_t(r) * a.path_width + lane] : -1;
+      const bool on = at >= 0 && at < n;
+      const uint64_t all = __ballot(on);
+      if (on) s_token[__popcll(all & ((uint64_t(1) << lane) - 1))] = at;
+      if (lane == 0) s_count = __popcll(all);
+    }
+    __syncthreads();
+    count = s_count;
+    if (count == 0) return;
+    if (conv) {                                          // the last rows of x along the branch
+      const int c = (cb * kThreads + tid) * 8, W = a.taps;
+      if (c >= a.C) return;
+      uint16_t *st = a.conv_state + (int64_t(layer) * a.state_count + srow) * (W - 1) * a.C + c;
+      const uint16_t *x = a.x + int64_t(layer) * a.x_layer + int64_t(first) * a.ldx + c;
+      u32x4 next[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        next[j] = u32x4{0, 0, 0, 0};
+        const int back = count - (W - 1) + j;
+        if (j < W - 1) {
+          if (back >= 0) next[j] = *reinterpret_cast<const u32x4 *>(x + int64_t(s_token[back]) * a.ldx);
+          else if (!fresh) next[j] = *reinterpret_cast<const u32x4 *>(st + int64_t(back + W - 1) * a.C);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j < W - 1) *reinterpret_cast<u32x4 *>(st + int64_t(j) * a.C) = next[j];
+      return;
+    }
+  } else if (srow < 0) {
+    if (live)
+      for (int i = wave * 8 + (lane >> 3); i < n; i += 32)
+        *reinterpret_cast<u32x2 *>(a.out + (int64_t(first + i) * a.Hv + h) * a.Dv + col) = u32x2{0, 0};
+    return;
+  }
+  const int kh = h / a.G;
+  float *state = a.state + ((int64_t(layer) * a.state_count + srow) * a.Hv + h) * DK * a.Dv + col;
+  f32x4 S[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    S[i] = f32x4{0, 0, 0, 0};
+    if (!fresh && live) S[i] = *reinterpret_cast<const f32x4 *>(state + int64_t(32 * i + 8 * wave + (lane >> 3)) * a.Dv);
+  }
+  const uint16_t *pq = a.q, *pk = a.k + int64_t(layer) * a.k_layer, *pv = a.v + int64_t(layer) * a.v_layer;
+  const float *pa = a.a + int64_t(layer) * a.a_layer, *pb = a.b + int64_t(layer) * a.b_layer;
+  for (int i = 0; i < count; ++i) {
+    const int64_t t = first + (COMMIT ? s_token[i] : i);
+    if (tid < DK) s_k[tid] = bf16_bits_to_float(pk[t * a.ldk + kh * DK + tid]);
+    if (!COMMIT && tid >= 128 && tid < 128 + DK) s_q[tid - 128] = bf16_bits_to_float(pq[t * a.ldq + kh * DK + tid - 128]);
+    const Gate gate = gate_of(a, pa, pb, t, h, layer);
+    u32x2 vw = {0, 0};
+    if (live) vw = *reinterpret_cast<const u32x2 *>(pv + t * a.ldv + int64_t(h) * a.Dv + col);
+    const float v[4] = {lo_bf16(vw[0]), hi_bf16(vw[0]), lo_bf16(vw[1]), hi_bf16(vw[1])};
+    const float decay = expf(gate.g);
+    __syncthreads();
+    float kk[N], sum[9];
+#pragma unroll
+    for (int e = 0; e < 9; ++e) sum[e] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int row = 32 * j + 8 * wave + (lane >> 3);
+      kk[j] = s_k[row];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = fmaf(S[j][e], kk[j], sum[e]);
+      if constexpr (!COMMIT) {
+        const float qq = s_q[row];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[4 + e] = fmaf(S[j][e], qq, sum[4 + e]);
+        sum[8] = fmaf(kk[j], qq, sum[8]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < (COMMIT ? 4 : 9); ++e) {
+#pragma unroll
+      for (int off = 8; off < 64; off <<= 1) sum[e] += __shfl_xor(sum[e], off, 64);
+      if (lane < 8) s_sum[wave][lane][e] = sum[e];
+    }
+    __syncthreads();
+    float u[4];
+#pragma unroll
+    for (int e = 0; e < (COMMIT ? 4 : 9); ++e)
+      sum[e] = s_sum[0][lane & 7][e] + s_sum[1][lane & 7][e] + (s_sum[2][lane & 7][e] + s_sum[3][lane & 7][e]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      u[e] = gate.b * (v[e] - decay * sum[e]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) S[j][e] = fmaf(kk[j], u[e], decay * S[j][e]);
+    }
+    if constexpr (!COMMIT) {
+      if (tid < 8 && live) {
+        float o[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = a.scale * fmaf(sum[8], u[e], decay * sum[4 + e]);
+        *reinterpret_cast<u32x2 *>(a.out + (t * a.Hv + h) * a.Dv + col) = u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+      }
+    }
+  }
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      *reinterpret_cast<f32x4 *>(state + int64_t(32 * i + 8 * wave + (lane >> 3)) * a.Dv) = S[i];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Chunks.  The workspace holds, for each chunk and value head, T and P as the matrix
+// instructions take their first operand, and the decays; for each chunk and key head, K
+// transposed.  A 16x16x32 operand is 64 lanes of 16 bytes: lane 16 g + m holds row m, columns
+// 8 g .. 8 g + 7 of 32.  Its result's lane 16 g + m holds column m, rows 4 g .. 4 g + 3.  Rows
+// are dealt to pairs of tiles so that a pair's results are the next product's second operand
+// as they stand: row m of tile 2 s + p is token (or element of k)
+//   32 s + 8 (m / 4) + 4 p + m % 4,
+// and the lane's 4 + 4 values of a pair are the 8 consecutive ones 32 s + 8 g ...
+__host__ __device__ constexpr int dealt(int tile, int m) { return 32 * (tile >> 1) + 8 * (m >> 2) + 4 * (tile & 1) + (m & 3); }
+
+constexpr int kTile = 1024;                              // bytes of an operand
+// tile i of T or P has its columns of 32 up to s = i / 2: 6 operands for each part
+__host__ __device__ constexpr int tri_at(int i, int s) { return (i < 2 ? i : 2 * (i - 1)) + s; }
+constexpr int kTriangle = 6;
+constexpr int kTParts = 3, kPParts = 2;
+constexpr int kDecays = (kTParts + kPParts) * kTriangle * kTile;  // behind T and P: three lists of 64
+constexpr int kHeadBytes = kDecays + 3 * kChunk * 4;      // the third: exp(D_last) and a word of tokens
+__host__ __device__ constexpr int key_bytes(int DK) { return kChunk * DK * 2; }
+
+// three (PARTS = 3) or two bf16 parts of 8 floats, as an operand's lane holds them
+template <int PARTS>
+__device__ __forceinline__ void cut(const float (&x)[8], u32x4 (&o)[PARTS]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float p = x[2 * e], q = x[2 * e + 1];
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) {
+      o[part][e] = PARTS == 2 && part == 1 ? pack_bf16(p, q) : upper(p, q);
+      p = below(p);
+      q = below(q);
+    }
+  }
+}
+
+template <int DK>
+__global__ __launch_bounds__(kThreads) void delta_prep_kernel(const DeltaArgs a) {
+  constexpr int NS = DK / 32, PITCH = kChunk + 4;
+  __shared__ __attribute__((aligned(16))) float s_A[kChunk * PITCH], s_T[kChunk * PITCH];
+  __shared__ double s_total[kChunk];
+  __shared__ float s_g[kChunk], s_b[kChunk];
+  __shared__ uint64_t s_seen[kChunk];
+  __shared__ uint32_t s_bad[2];                          // tokens whose k, g or b is not finite
+  static_assert(sizeof(s_T) >= kChunk * (DK + 8) * 2, "K passes through s_T");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
+  const int number = blockIdx.x, h = blockIdx.y, kh = h / a.G;
+  if (tid < 2) s_bad[tid] = 0;
+  const Piece piece = find_piece<kChunk>(a.q_start, a.R, a.T, number);
+  if (piece.r < 0 || state_row(a.kv_lens, a.slots, a.state_count, piece.r) < 0) return;
+  const int64_t t0 = int64_t(piece.first) + piece.part * kChunk;
+  const int n = min(kChunk, piece.n - piece.part * kChunk);
+  const bool tree = a.tree_mask && piece.n <= kTreeNodes;
+  char *head = a.heads + (int64_t(number) * a.Hv + h) * kHeadBytes;
+
+  // K transposed, once for the value heads that share it
+  if (h % a.G == 0 && !tree) {
+    uint16_t *rows = reinterpret_cast<uint16_t *>(s_T);
+    constexpr int ROW = DK + 8;
+    for (int u = tid; u < kChunk * DK / 8; u += kThreads) {
+      const int i = u / (DK / 8), d = u % (DK / 8) * 8;
+      u32x4 x = {0, 0, 0, 0};
+      if (i < n) x = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + d);
+      *reinterpret_cast<u32x4 *>(rows + i * ROW + d) = x;
+    }
+    __syncthreads();
+    u32x4 *to = reinterpret_cast<u32x4 *>(a.keys + (int64_t(number) * a.Hk + kh) * key_bytes(DK));
+    for (int u = wave; u < DK / 16 * 2; u += 4) {        // tile of d's, 32 tokens
+      const int d = dealt(u >> 1, m), i0 = 32 * (u & 1) + 8 * g;
+      u32x4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = rows[(i0 + 2 * e) * ROW + d] | uint32_t(rows[(i0 + 2 * e + 1) * ROW + d]) << 16;
+      to[u * 64 + lane] = x;
+    }
+    __syncthreads();
+  }
+
+  // a lane holds token i = dealt(wave, m): its k and q, 8 elements of every 32
+  const int i = dealt(wave, m), last = wave >> 1;
+  u32x4 ki[NS], qi[NS];
+#pragma unroll
+  for (int c = 0; c < NS; ++c) {
+    ki[c] = qi[c] = u32x4{0, 0, 0, 0};
+    if (i < n) {
+      ki[c] = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + 32 * c + 8 * g);
+      qi[c] = *reinterpret_cast<const u32x4 *>(a.q + (t0 + i) * a.ldq + kh * DK + 32 * c + 8 * g);
+    }
+  }
+  if (tid < kChunk) {
+    Gate gate = {0.0f, 0.0f};
+    if (tid < n) gate = gate_of(a, a.a, a.b, t0 + tid, h, 0);
+    // exp of less is 0 either way, and sums of finite numbers can be subtracted
+    if (gate.g < -1.0e4f) gate.g = -1.0e4f;
+    if (!__builtin_isfinite(gate.g) || !__builtin_isfinite(gate.b)) {
+      atomicOr(&s_bad[tid >> 5], 1u << (tid & 31));
+      gate = {0.0f, 0.0f};
+    }
+    s_g[tid] = gate.g;
+    s_b[tid] = gate.b;
+    const uint64_t own = uint64_t(1) << tid, upto = own | (own - 1);
+    s_seen[tid] = tree ? ((tid < n ? a.tree_mask[t0 + tid] : 0) | own) & upto : upto;
+  }
+  bool off = false;
+#pragma unroll
+  for (int c = 0; c < NS; ++c)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) off |= (ki[c][e] & 0x7F80u) == 0x7F80u || (ki[c][e] & 0x7F800000u) == 0x7F800000u;
+  if (off) atomicOr(&s_bad[i >> 5], 1u << (i & 31));
+  __syncthreads();
+  const uint64_t bad = s_bad[0] | uint64_t(s_bad[1]) << 32;
+  if (tid < kChunk) {
+    const uint64_t seen = s_seen[tid];
+    double total = 0.0;
+    for (int j = 0; j < n; ++j)
+      if (seen >> j & 1) total += double(s_g[j]);
+    s_total[tid] = total;
+  }
+  __syncthreads();
+
+  // (K K^T)^T and (Q K^T)^T: token i against 8 consecutive j's
+  if (32 * last < n) {
+    if (bad >> i & 1) {
+#pragma unroll
+      for (int c = 0; c < NS; ++c) ki[c] = u32x4{0, 0, 0, 0};
+    }
+    const double total = s_total[i];
+    const float step = s_b[i];
+    const uint64_t seen = s_seen[i];
+    for (int s = 0; s <= last; ++s) {
+      float kk[8], qk[8];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int j = dealt(2 * s + p, m);
+        f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < NS; ++c) {
+          u32x4 kj = {0, 0, 0, 0};
+          if (j < n && !(bad >> j & 1)) kj = *reinterpret_cast<const u32x4 *>(a.k + (t0 + j) * a.ldk + kh * DK + 32 * c + 8 * g);
+          x = mfma(kj, ki[c], x);
+          y = mfma(kj, qi[c], y);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          kk[4 * p + e] = x[e];
+          qk[4 * p + e] = y[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = 32 * s + 8 * g + e;
+        const bool on = i < n && j <= i && (seen >> j & 1);
+        const float decay = expf(float(total - s_total[j]));
+        kk[e] = on && j < i ? step * decay * kk[e] : 0.0f;
+        qk[e] = on ? decay * qk[e] : 0.0f;
+      }
+      f32x4 *to = reinterpret_cast<f32x4 *>(s_A + i * PITCH + 32 * s + 8 * g);
+      to[0] = f32x4{kk[0], kk[1], kk[2], kk[3]};
+      to[1] = f32x4{kk[4], kk[5], kk[6], kk[7]};
+      u32x4 part[kPParts];
+      cut<kPParts>(qk, part);
+      u32x4 *P = reinterpret_cast<u32x4 *>(head + kTParts * kTriangle * kTile);
+#pragma unroll
+      for (int e = 0; e < kPParts; ++e) P[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = part[e];
+    }
+  }
+  __syncthreads();
+
+  // T's diagonal blocks of 16: a lane solves one column, row by row
+  const int tiles = (n + 15) / 16;
+  if (wave < tiles) {
+    const float *A = s_A + (16 * wave) * PITCH + 16 * wave;
+    float t[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      float sum = x == m ? 1.0f : 0.0f;
+#pragma unroll
+      for (int y = 0; y < x; ++y) sum = fmaf(-A[x * PITCH + y], t[y], sum);
+      t[x] = sum;
+    }
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      if (x >> 2 == g) s_T[(16 * wave + x) * PITCH + 16 * wave + m] = t[x];
+  }
+  __syncthreads();
+  // the blocks below: T_ij = -T_ii sum over k of A_ik T_kj, a diagonal after the other
+  for (int off = 1; off < tiles; ++off) {
+    if (wave + off < tiles) {
+      const int bi = wave + off, bj = wave;
+      f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+      for (int bk = bj; bk < bi; ++bk)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          x = __builtin_amdgcn_mfma_f32_16x16x4f32(s_A[(16 * bi + m) * PITCH + 16 * bk + 4 * c + g],
+                                                   s_T[(16 * bk + 4 * c + g) * PITCH + 16 * bj + m], x, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)                        // x's lane holds rows 4 g + c
+        y = __builtin_amdgcn_mfma_f32_16x16x4f32(s_T[(16 * bi + m) * PITCH + 16 * bi + 4 * g + c], x[c], y, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s_T[(16 * bi + 4 * g + c) * PITCH + 16 * bj + m] = -y[c];
+    }
+    __syncthreads();
+  }
+  if (32 * last < n) {
+    u32x4 *T = reinterpret_cast<u32x4 *>(head);
+    for (int s = 0; s <= last; ++s) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = 32 * s + 8 * g + e;
+        x[e] = i < n && j <= i ? s_T[i * PITCH + j] * s_b[j] : 0.0f;
+      }
+      u32x4 part[kTParts];
+      cut<kTParts>(x, part);
+#pragma unroll
+      for (int e = 0; e < kTParts; ++e) T[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = part[e];
+    }
+  }
+  if (tid < kChunk) {
+    float *to = reinterpret_cast<float *>(head + kDecays);
+    const double end = s_total[n - 1];
+    to[tid] = tid < n ? expf(float(s_total[tid])) : 0.0f;
+    to[kChunk + tid] = tid < n ? expf(float(end - s_total[tid])) : 0.0f;
+    if (tid == 0) {
+      to[2 * kChunk] = expf(float(end));
+      reinterpret_cast<uint32_t *>(to)[2 * kChunk + 2] = s_bad[0];
+      reinterpret_cast<uint32_t *>(to)[2 * kChunk + 3] = s_bad[1];
+    }
+  }
+}
+
+// A workgroup walks the chunks of one request, head and 16 CT columns.  Wave w takes row tile
+// w of the chunk's tokens and, of the state, the rows 32 w .. 32 w + 31 (a pair of tiles).
+// Column m of tile c is column CT m + c: a lane's columns are neighbours.
+template <int DK, int CT>
+__global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a) {
+  constexpr int NS = DK / 32;
+  static_assert(NS <= 4, "a wave holds at most one pair of state tiles");
+  __shared__ __attribute__((aligned(16))) u32x4 s_S[3][CT][NS][64], s_R[3][CT][2][64], s_U[2][CT][2][64], s_W[3][CT][2][64];
+  __shared__ uint32_t s_bad[16 * CT][2];                 // of each column: tokens whose v is not finite
+  __shared__ int s_some;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
+  const int blocks = (a.Dv + 16 * CT - 1) / (16 * CT);
+  int id = blockIdx.x;
+  const int cb = id % blocks;
+  id /= blocks;
+  const int h = id % a.Hv, r = id / a.Hv, kh = h / a.G;
+  // a chain's state is NaN from such a token on, so the words need no clearing for later chunks
+  if (tid < 32 * CT) s_bad[tid >> 1][tid & 1] = 0;
+  if (tid == 0) s_some = 0;
+  if (!starts_rise(a.q_start, a.R, a.T)) return;
+  const int first = a.q_start[r], n = a.q_start[r + 1] - first;
+  if (n <= 0) return;
+  const int col = 16 * CT * cb + CT * m;
+  const bool live = col < a.Dv;
+  const int srow = state_row(a.kv_lens, a.slots, a.state_count, r);
+  auto store = [&](int64_t t, const float *o) {
+    uint16_t *to = a.out + (t * a.Hv + h) * a.Dv + col;
+    if constexpr (CT == 2) *reinterpret_cast<uint32_t *>(to) = pack_bf16(o[0], o[1]);
+    else *to = uint16_t(pack_bf16(o[0], 0.0f));
+  };
+  if (srow < 0) {
+    const float zero[2] = {0.0f, 0.0f};
+    if (live)
+      for (int i = 4 * wave + g; i < n; i += 16) store(int64_t(first) + i, zero);
+    return;
+  }
+  const bool tree = a.tree_mask && n <= kTreeNodes, fresh = a.kv_lens[r] <= n;
+  float *state = a.state + ((int64_t(srow) * a.Hv + h) * DK + 32 * wave + 8 * g) * a.Dv + col;
+  const bool holds = wave < NS;
+  f32x4 S[2][CT];                                        // [p][c][e]: row 32 w + 8 g + 4 p + e
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) S[p][c][e] = holds && live && !fresh ? state[int64_t(4 * p + e) * a.Dv + c] : 0.0f;
+
+  const int64_t number = int64_t(first) / kChunk + r;
+  const int row0 = 32 * (wave >> 1) + 8 * g + 4 * (wave & 1), pairs = (wave >> 1) + 1;
+  for (int part = 0; int64_t(part) * kChunk < n; ++part) {
+    const int64_t t0 = int64_t(first) + part * kChunk;
+    const int here = min(kChunk, n - part * kChunk);
+    const bool rows = 32 * (wave >> 1) < here;           // this wave has tokens
+    const char *head = a.heads + ((number + part) * a.Hv + h) * kHeadBytes;
+    const u32x4 *T = reinterpret_cast<const u32x4 *>(head), *P = T + kTParts * kTriangle * 64;
+    const float *decays = reinterpret_cast<const float *>(head + kDecays);
+    const u32x4 *keys = reinterpret_cast<const u32x4 *>(a.keys + ((number + part) * a.Hk + kh) * key_bytes(DK));
+    if (holds) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const float x[8] = {S[0][c][0], S[0][c][1], S[0][c][2], S[0][c][3], S[1][c][0], S[1][c][1], S[1][c][2], S[1][c][3]};
+        u32x4 o[3];
+        cut<3>(x, o);
+#pragma unroll
+        for (int e = 0; e < 3; ++e) s_S[e][c][wave][lane] = o[e];
+      }
+    }
+    __syncthreads();
+    f32x4 ks[CT], o[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) ks[c] = o[c] = f32x4{0, 0, 0, 0};
+    const uint64_t bad = *reinterpret_cast<const uint64_t *>(decays + 2 * kChunk + 2);
+    const f32x4 grown = *reinterpret_cast<const f32x4 *>(decays + row0);
+    if (rows) {
+      const int i = dealt(wave, m);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        u32x4 ki = {0, 0, 0, 0}, qi = {0, 0, 0, 0};
+        if (i < here) {
+          ki = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + 32 * s + 8 * g);
+          qi = *reinterpret_cast<const u32x4 *>(a.q + (t0 + i) * a.ldq + kh * DK + 32 * s + 8 * g);
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          ks[c] = mfma(ki, s_S[0][c][s][lane], ks[c]);
+          ks[c] = mfma(ki, s_S[1][c][s][lane], ks[c]);
+          ks[c] = mfma(ki, s_S[2][c][s][lane], ks[c]);
+          o[c] = mfma(qi, s_S[0][c][s][lane], o[c]);
+          o[c] = mfma(qi, s_S[1][c][s][lane], o[c]);
+        }
+      }
+      // R = V - exp(D) K S
+      float v[4][CT];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool there = live && row0 + e < here;
+        const uint16_t *from = a.v + (t0 + row0 + e) * a.ldv + int64_t(h) * a.Dv + col;
+        if constexpr (CT == 2) {
+          const uint32_t w = there ? *reinterpret_cast<const uint32_t *>(from) : 0;
+          v[e][0] = lo_bf16(w);
+          v[e][1] = hi_bf16(w);
+        } else {
+          v[e][0] = there ? bf16_bits_to_float(*from) : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = fmaf(-grown[e], ks[c][e], v[e][c]);
+          if (!__builtin_isfinite(v[e][c])) {
+            atomicOr(&s_bad[CT * m + c][(row0 + e) >> 5], 1u << ((row0 + e) & 31));
+            s_some = 1;
+            x[e] = 0.0f;
+          }
+          if (bad >> (row0 + e) & 1) x[e] = 0.0f;
+          o[c][e] *= grown[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          const u32x2 w = {upper(x[0], x[1]), upper(x[2], x[3])};
+          reinterpret_cast<u32x2 *>(&s_R[e][c][wave >> 1][lane])[wave & 1] = w;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = below(x[j]);
+        }
+      }
+    }
+    __syncthreads();
+    uint64_t gone[CT];                                   // tokens that a column's results must not have seen
+    const bool some = s_some || bad;
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+      gone[c] = some ? bad | s_bad[CT * m + c][0] | uint64_t(s_bad[CT * m + c][1]) << 32 : 0;
+    if (rows) {                                          // U = T R
+      f32x4 u[CT];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) u[c] = f32x4{0, 0, 0, 0};
+      for (int s = 0; s < pairs; ++s) {
+        const u32x4 *t = T + tri_at(wave, s) * 64 + lane;
+        const u32x4 hi = t[0], mid = t[kTriangle * 64], lo = t[2 * kTriangle * 64];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const u32x4 x = s_R[0][c][s][lane], y = s_R[1][c][s][lane], z = s_R[2][c][s][lane];
+          u[c] = mfma(lo, x, u[c]);
+          u[c] = mfma(mid, y, u[c]);
+          u[c] = mfma(hi, z, u[c]);
+          u[c] = mfma(mid, x, u[c]);
+          u[c] = mfma(hi, y, u[c]);
+          u[c] = mfma(hi, x, u[c]);
+        }
+      }
+      const f32x4 left = *reinterpret_cast<const f32x4 *>(decays + kChunk + row0);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        float x[4], y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[e] = u[c][e];
+          y[e] = left[e] * u[c][e];
+        }
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          const u32x2 w = {upper(x[0], x[1]), upper(x[2], x[3])}, z = {upper(y[0], y[1]), upper(y[2], y[3])};
+          if (e < 2) reinterpret_cast<u32x2 *>(&s_U[e][c][wave >> 1][lane])[wave & 1] = w;
+          reinterpret_cast<u32x2 *>(&s_W[e][c][wave >> 1][lane])[wave & 1] = z;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            x[j] = below(x[j]);
+            y[j] = below(y[j]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (rows) {                                          // out = scale (exp(D) Q S + P U)
+      for (int s = 0; s < pairs; ++s) {
+        const u32x4 *t = P + tri_at(wave, s) * 64 + lane;
+        const u32x4 hi = t[0], lo = t[kTriangle * 64];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          o[c] = mfma(lo, s_U[0][c][s][lane], o[c]);
+          o[c] = mfma(hi, s_U[1][c][s][lane], o[c]);
+          o[c] = mfma(hi, s_U[0][c][s][lane], o[c]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float x[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) x[c] = a.scale * o[c][e];
+        if (some) {
+          const int i = row0 + e;
+          const uint64_t own = uint64_t(1) << i, upto = own | (own - 1);
+          const uint64_t seen = tree ? ((i < here ? a.tree_mask[t0 + i] : 0) | own) & upto : upto;
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+            if (seen & gone[c]) x[c] = __builtin_nanf("");
+        }
+        if (live && row0 + e < here) store(t0 + row0 + e, x);
+      }
+    }
+    if (holds && !tree) {                                // S = exp(D_last) S + K^T (exp(D_last - D) U)
+      const float end = decays[2 * kChunk];
+      const int half = here > 32 ? 2 : 1;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) S[p][c] *= end;
+      for (int s = 0; s < half; ++s)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const u32x4 kt = keys[((2 * wave + p) * 2 + s) * 64 + lane];
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            S[p][c] = mfma(kt, s_W[2][c][s][lane], S[p][c]);
+            S[p][c] = mfma(kt, s_W[1][c][s][lane], S[p][c]);
+            S[p][c] = mfma(kt, s_W[0][c][s][lane], S[p][c]);
+          }
+        }
+      if (some) {
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+            if (gone[c]) S[p][c] = S[p][c] + __builtin_nanf("");
+      }
+    }
+  }
+  if (holds && live && !tree) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) state[int64_t(4 * p + e) * a.Dv + c] = S[p][c][e];
+  }
+}
+
+// Few tokens a request: token by token.
+constexpr int64_t kStepTokens = 8;
+bool by_chunks(int64_t max_nodes, bool tree) { return tree || max_nodes > kStepTokens; }
+size_t up(size_t n) { return (n + 255) / 256 * 256; }
+int64_t chunks_of(int64_t T, int64_t R) { return T / kChunk + R; }
+
+template <int DK>
+hipError_t run(DeltaArgs a, bool chunks, hipStream_t stream) {
+  (void)hipGetLastError();
+  if (!chunks) {
+    const int64_t grid = int64_t(a.R) * a.Hv * ((a.Dv + 31) / 32);
+    hipLaunchKernelGGL((delta_step_kernel<DK, false>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a, 1);
+    set_last_kernel("delta_step");
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(unsigned(chunks_of(a.T, a.R)), unsigned(a.Hv)), dim3(kThreads), 0, stream, a);
+  if (hipError_t e = hipGetLastError()) return e;
+  const int64_t grid = int64_t(a.R) * a.Hv * ((a.Dv + 31) / 32);
+  hipLaunchKernelGGL((delta_scan_kernel<DK, 2>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a);
+  set_last_kernel("delta_scan");
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t delta_workspace_bytes(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_t Dk, int64_t max_nodes, bool tree) {
+  if (!by_chunks(max_nodes, tree)) return 0;
+  const size_t n = size_t(chunks_of(T, R));
+  return up(n * size_t(Hk * G) * kHeadBytes) + n * size_t(Hk) * key_bytes(int(Dk));
+}
+
+hipError_t launch_delta_rule(DeltaArgs a, int64_t Dk, int64_t max_nodes, void *workspace, hipStream_t stream) {
+  const bool chunks = by_chunks(max_nodes, a.tree_mask != nullptr);
+  a.heads = static_cast<char *>(workspace);
+  a.keys = a.heads + up(size_t(chunks_of(a.T, a.R)) * size_t(a.Hv) * kHeadBytes);
+  return Dk == 64 ? run<64>(a, chunks, stream) : run<128>(a, chunks, stream);
+}
+
+hipError_t launch_delta_commit(const DeltaArgs &a, int64_t Dk, hipStream_t stream) {
+  const int64_t items = int64_t(a.L) * a.R, conv = a.x ? (a.C + 2047) / 2048 : 0;
+  const int64_t grid = items * a.Hv * ((a.Dv + 31) / 32) + items * conv;
+  (void)hipGetLastError();
+  if (Dk == 64) hipLaunchKernelGGL((delta_step_kernel<64, true>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a, int(conv));
+  else hipLaunchKernelGGL((delta_step_kernel<128, true>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a, int(conv));
+  set_last_kernel("delta_commit");
+  return hipGetLastError();
+}
+
+}  // namespace tl

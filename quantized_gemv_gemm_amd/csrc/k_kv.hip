@@ -5,6 +5,9 @@
 //   x'[d] = x[d] c[d] - x[d + h] s[d],  x'[d + h] = x[d + h] c[d] + x[d] s[d]   (d < h)
 //   x'[d] = x[d] (d >= rot), rounded to bf16, for q (to q_out) and k; v as it is;
 //   e4m3: scale = max |x'| / 448, code = e4m3(x' / scale) for each token and head.
+// kv_write_norm (NORM) takes x w / sqrt(mean of the head's x^2 + eps) in the place of x for q and
+// k, an axis of positions for each pair of elements, and rounds only what it stores: an e4m3
+// row's scale and codes are those of the f32 values.
 // Products and sums are rounded one by one (no fused multiply-add) and the divisions are
 // IEEE ones, so the codes are those of the plain formula.
 //
@@ -89,7 +92,88 @@ __device__ __forceinline__ uint32_t codes4(uint32_t w0, uint32_t w1, float scale
   return uint32_t(c);
 }
 
-template <int D, bool E4M3>
+// A piece of a row in f32: elements lo .. lo + 7 and hi .. hi + 7.
+struct Piece16 {
+  float a[8], b[8];
+};
+
+__device__ __forceinline__ void load8(const float *from, float (&to)[8]) {
+  const float4 x = reinterpret_cast<const float4 *>(from)[0], y = reinterpret_cast<const float4 *>(from)[1];
+  to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w, to[4] = y.x, to[5] = y.y, to[6] = y.z, to[7] = y.w;
+}
+
+// Piece p of token t's row, normalised and turned.  The P lanes of a row call it together.
+template <int P>
+__device__ __forceinline__ Piece16 normed(const Row16 &x, const WriteArgs &a, const float *weight, int t, int p, int lo,
+                                          int hi) {
+  Piece16 y;
+  float sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y.a[2 * e] = lo_bf16(x.a[e]), y.a[2 * e + 1] = hi_bf16(x.a[e]);
+    y.b[2 * e] = lo_bf16(x.b[e]), y.b[2 * e + 1] = hi_bf16(x.b[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum = fmaf(y.a[e], y.a[e], fmaf(y.b[e], y.b[e], sum));
+#pragma unroll
+  for (int off = P / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  const float by = 1.0f / sqrtf(sum / float(16 * P) + a.eps);
+  float wa[8], wb[8];
+  if (weight) {
+    load8(weight + lo, wa);
+    load8(weight + hi, wb);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    y.a[e] = y.a[e] * by * (weight ? wa[e] : 1.0f);
+    y.b[e] = y.b[e] * by * (weight ? wb[e] : 1.0f);
+  }
+  if (16 * p < a.rot) {                                  // pairs lo .. lo + 7
+    float c[8], s[8];
+    if (a.axis_of) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int axis = min(max(a.axis_of[lo + e], 0), a.axes - 1);
+        const int pos = min(max(a.positions[int64_t(axis) * a.T + t], 0), a.max_pos - 1);
+        const float *at = a.cos_sin + int64_t(pos) * a.rot + lo + e;
+        c[e] = at[0];
+        s[e] = at[a.rot / 2];
+      }
+    } else {
+      const float *at = angles(a, t) + lo;
+      load8(at, c);
+      load8(at + a.rot / 2, s);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float u = y.a[e], v = y.b[e];
+      y.a[e] = u * c[e] - v * s[e];
+      y.b[e] = v * c[e] + u * s[e];
+    }
+  }
+  return y;
+}
+
+__device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
+  return u32x4{pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
+}
+
+__device__ __forceinline__ u32x2 codes8(const float (&x)[8], float scale) {
+  const bool some = scale > 0.0f;
+  u32x2 o;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    float y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) y[j] = some ? x[4 * e + j] / scale : 0.0f;
+    int c = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
+    c = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], c, true);
+    o[e] = uint32_t(c);
+  }
+  return o;
+}
+
+template <int D, bool E4M3, bool NORM>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, int cache_groups) {
   constexpr int P = D / 16;                              // pieces (lanes) of a row
   constexpr int ES = E4M3 ? 1 : 2;
@@ -100,9 +184,14 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
     const int t = int(row / a.Hq), head = int(row - int64_t(t) * a.Hq), p = tid % P;
     int lo, hi;
     piece(p, a.rot, lo, hi);
-    const uint16_t *src = a.q + t * a.ldq + int64_t(head) * D;
+    const uint16_t *src = a.q + t * a.ldq + int64_t(head) * (NORM ? a.q_head : D);
     Row16 x = {*reinterpret_cast<const u32x4 *>(src + lo), *reinterpret_cast<const u32x4 *>(src + hi)};
-    if (16 * p < a.rot) rotate(x, angles(a, t), h, lo);
+    if constexpr (NORM) {
+      const Piece16 y = normed<P>(x, a, a.q_weight, t, p, lo, hi);
+      x = {pack8(y.a), pack8(y.b)};
+    } else if (16 * p < a.rot) {
+      rotate(x, angles(a, t), h, lo);
+    }
     uint16_t *dst = a.q_out + row * D;
     *reinterpret_cast<u32x4 *>(dst + lo) = x.a;
     *reinterpret_cast<u32x4 *>(dst + hi) = x.b;
@@ -162,10 +251,28 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
     if (live) {
       const uint16_t *src = a.k + t * a.ldk + int64_t(head) * D;
       k = {*reinterpret_cast<const u32x4 *>(src + lo), *reinterpret_cast<const u32x4 *>(src + hi)};
-      if (16 * p < a.rot) rotate(k, angles(a, t), h, lo);
+      if (!NORM && 16 * p < a.rot) rotate(k, angles(a, t), h, lo);
     }
     const int in_tile = int(slot & 15);
-    if constexpr (E4M3) {
+    Piece16 y;
+    if constexpr (NORM) {                                // rows that are not there are zeros, of an existing token
+      y = normed<P>(k, a, a.k_weight, min(t, a.T - 1), p, lo, hi);
+      if constexpr (!E4M3) k = {pack8(y.a), pack8(y.b)};
+    }
+    if constexpr (E4M3 && NORM) {
+      float m = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(fmaxf(m, fabsf(y.a[e])), fabsf(y.b[e]));
+#pragma unroll
+      for (int off = P / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
+      const float scale = m / 448.0f;
+      if (live) {
+        if (p == 0) a.k_scale[scale_of(slot)] = scale;
+        char *dst = static_cast<char *>(a.k_cache) + tile_of(slot);
+        *reinterpret_cast<u32x2 *>(dst + kv_tile_k(in_tile, lo, 1)) = codes8(y.a, scale);
+        *reinterpret_cast<u32x2 *>(dst + kv_tile_k(in_tile, hi, 1)) = codes8(y.b, scale);
+      }
+    } else if constexpr (E4M3) {
       float m = largest(k);
 #pragma unroll
       for (int off = P / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
@@ -343,14 +450,14 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(const CommitArgs a)
   }
 }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool NORM>
 hipError_t write_rows(const WriteArgs &a, hipStream_t stream) {
   const int64_t cache = (int64_t(a.T) + kTokens - 1) / kTokens * a.H;
   const int64_t q = a.q ? (int64_t(a.T) * a.Hq + kThreads / (D / 16) - 1) / (kThreads / (D / 16)) : 0;
   if (cache + q > 0x7FFFFFFF) return hipErrorInvalidValue;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((kv_write_kernel<D, E4M3>), dim3(unsigned(cache + q)), dim3(kThreads), 0, stream, a, int(cache));
-  set_last_kernel(E4M3 ? "kv_write_e4m3" : "kv_write_bf16");
+  hipLaunchKernelGGL((kv_write_kernel<D, E4M3, NORM>), dim3(unsigned(cache + q)), dim3(kThreads), 0, stream, a, int(cache));
+  set_last_kernel(NORM ? E4M3 ? "kv_write_norm_e4m3" : "kv_write_norm_bf16" : E4M3 ? "kv_write_e4m3" : "kv_write_bf16");
   return hipGetLastError();
 }
 
@@ -366,9 +473,16 @@ hipError_t commit_rows(const CommitArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-hipError_t launch_kv_write(const WriteArgs &a, int64_t D, bool e4m3, hipStream_t stream) {
-  if (e4m3) return D == 64 ? write_rows<64, true>(a, stream) : D == 128 ? write_rows<128, true>(a, stream) : write_rows<256, true>(a, stream);
-  return D == 64 ? write_rows<64, false>(a, stream) : D == 128 ? write_rows<128, false>(a, stream) : write_rows<256, false>(a, stream);
+template <bool E4M3, bool NORM>
+static hipError_t write_of(const WriteArgs &a, int64_t D, hipStream_t stream) {
+  return D == 64    ? write_rows<64, E4M3, NORM>(a, stream)
+         : D == 128 ? write_rows<128, E4M3, NORM>(a, stream)
+                    : write_rows<256, E4M3, NORM>(a, stream);
+}
+
+hipError_t launch_kv_write(const WriteArgs &a, int64_t D, bool e4m3, bool norm, hipStream_t stream) {
+  if (norm) return e4m3 ? write_of<true, true>(a, D, stream) : write_of<false, true>(a, D, stream);
+  return e4m3 ? write_of<true, false>(a, D, stream) : write_of<false, false>(a, D, stream);
 }
 
 hipError_t launch_kv_commit(const CommitArgs &a, int64_t D, bool e4m3, hipStream_t stream) {

@@ -527,30 +527,75 @@ int tl_step_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t
   return from_hip(tl::launch_step_plan(a, static_cast<hipStream_t>(stream)));
 }
 
+// both cache writers: what tl_kv_write takes, and the norms' arguments
+namespace {
+int kv_write(tl::WriteArgs a, int64_t T, int64_t H, int64_t D, int64_t Hq, int64_t axes, int64_t max_pos, int64_t rot,
+             int cache_dtype, int64_t pages, int64_t block, bool norm, void *stream) {
+  if (int s = check_cache(cache_dtype, pages, H, block, D)) return s;
+  if (!count_ok(T) || a.ldk < H * D || a.ldv < H * D || a.ldk >= kMaxDim || a.ldv >= kMaxDim) return TL_ERR_SHAPE;
+  if (a.q && (Hq < 1 || Hq > 65536 || a.q_head < D || a.q_head >= kMaxDim || a.ldq < (Hq - 1) * a.q_head + D ||
+              a.ldq >= kMaxDim))
+    return TL_ERR_SHAPE;
+  if (a.cos_sin && (rot < 16 || rot % 16 || rot > D || max_pos < 1 || max_pos >= kMaxDim)) return TL_ERR_SHAPE;
+  if (a.cos_sin && (axes < 1 || axes > 16)) return TL_ERR_SHAPE;
+  if (norm && !(a.eps >= 0.0f && a.eps < __builtin_inff())) return TL_ERR_SHAPE;
+  if (T == 0) return TL_OK;
+  const bool e4m3 = cache_dtype == TL_E4M3;
+  if (any_null(a.k, a.v, a.slots, a.k_cache, a.v_cache) || (a.q && !a.q_out) || (a.cos_sin && !a.positions))
+    return TL_ERR_NULLPTR;
+  if (a.cos_sin && axes > 1 && !a.axis_of) return TL_ERR_NULLPTR;
+  if (e4m3 && any_null(a.k_scale, a.v_scale)) return TL_ERR_NULLPTR;
+  if (!aligned_to(16, a.k, a.v, a.q, a.q_out, a.cos_sin, a.k_cache, a.v_cache, a.q_weight, a.k_weight) || a.ldk % 8 ||
+      a.ldv % 8 || (a.q && (a.ldq % 8 || a.q_head % 8)) || !aligned_to(8, a.slots) ||
+      !aligned_to(4, a.positions, a.axis_of, a.k_scale, a.v_scale))
+    return TL_ERR_ALIGN;
+  const size_t kv = cache_bytes(cache_dtype, pages * H * block, D), sc = e4m3 ? size_t(pages) * H * block * 4 : 0;
+  Span in[] = {{a.k, (size_t(T - 1) * a.ldk + H * D) * 2},
+               {a.v, (size_t(T - 1) * a.ldv + H * D) * 2},
+               {a.slots, size_t(T) * 8},
+               {a.q, a.q ? (size_t(T - 1) * a.ldq + (Hq - 1) * a.q_head + D) * 2 : 0},
+               {a.positions, a.cos_sin ? size_t(T) * axes * 4 : 0},
+               {a.cos_sin, a.cos_sin ? size_t(max_pos) * rot * 4 : 0},
+               {a.q_weight, a.q ? size_t(D) * 4 : 0},
+               {a.k_weight, size_t(D) * 4},
+               {a.axis_of, a.cos_sin ? size_t(rot) * 2 : 0}};
+  Span out[] = {{a.k_cache, kv}, {a.v_cache, kv}, {a.k_scale, sc}, {a.v_scale, sc},
+                {a.q_out, a.q ? size_t(T) * Hq * D * 2 : 0}};
+  if (any_alias(in, 9, out, 5)) return TL_ERR_ALIAS;
+  a.slot_count = pages * block;
+  a.T = int(T);
+  a.Hq = int(Hq);
+  a.H = int(H);
+  a.rot = a.cos_sin ? int(rot) : 0;
+  a.max_pos = int(max_pos);
+  a.block_shift = log2_of(block);
+  a.axes = int(axes);
+  return from_hip(tl::launch_kv_write(a, D, e4m3, norm, static_cast<hipStream_t>(stream)));
+}
+}  // namespace
+
 int tl_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t T,
                 int64_t H, int64_t D, const uint16_t *q, int64_t ldq, int64_t Hq, const int32_t *positions,
                 const float *cos_sin, int64_t max_pos, int64_t rot, uint16_t *q_out, void *k_cache, void *v_cache,
                 float *k_scale, float *v_scale, int cache_dtype, int64_t pages, int64_t block, void *stream) {
-  if (int s = check_cache(cache_dtype, pages, H, block, D)) return s;
-  if (!count_ok(T) || ldk < H * D || ldv < H * D || ldk >= kMaxDim || ldv >= kMaxDim) return TL_ERR_SHAPE;
-  if (q && (Hq < 1 || Hq > 65536 || ldq < Hq * D || ldq >= kMaxDim)) return TL_ERR_SHAPE;
-  if (cos_sin && (rot < 16 || rot % 16 || rot > D || max_pos < 1 || max_pos >= kMaxDim)) return TL_ERR_SHAPE;
-  if (T == 0) return TL_OK;
-  const bool e4m3 = cache_dtype == TL_E4M3;
-  if (any_null(k, v, slots, k_cache, v_cache) || (q && !q_out) || (cos_sin && !positions)) return TL_ERR_NULLPTR;
-  if (e4m3 && any_null(k_scale, v_scale)) return TL_ERR_NULLPTR;
-  if (!aligned_to(16, k, v, q, q_out, cos_sin, k_cache, v_cache) || ldk % 8 || ldv % 8 || (q && ldq % 8) ||
-      !aligned_to(8, slots) || !aligned_to(4, positions, k_scale, v_scale))
-    return TL_ERR_ALIGN;
-  const size_t kv = cache_bytes(cache_dtype, pages * H * block, D), sc = e4m3 ? size_t(pages) * H * block * 4 : 0;
-  Span in[] = {{k, (size_t(T - 1) * ldk + H * D) * 2}, {v, (size_t(T - 1) * ldv + H * D) * 2}, {slots, size_t(T) * 8},
-               {q, q ? (size_t(T - 1) * ldq + Hq * D) * 2 : 0}, {positions, cos_sin ? size_t(T) * 4 : 0},
-               {cos_sin, cos_sin ? size_t(max_pos) * rot * 4 : 0}};
-  Span out[] = {{k_cache, kv}, {v_cache, kv}, {k_scale, sc}, {v_scale, sc}, {q_out, q ? size_t(T) * Hq * D * 2 : 0}};
-  if (any_alias(in, 6, out, 5)) return TL_ERR_ALIAS;
-  tl::WriteArgs a = {q, k, v, slots, positions, cos_sin, q_out, k_cache, v_cache, k_scale, v_scale, ldq, ldk, ldv,
-                     pages * block, int(T), int(Hq), int(H), cos_sin ? int(rot) : 0, int(max_pos), log2_of(block)};
-  return from_hip(tl::launch_kv_write(a, D, e4m3, static_cast<hipStream_t>(stream)));
+  tl::WriteArgs a = {q, k, v, slots, positions, cos_sin, q_out, k_cache, v_cache, k_scale, v_scale, ldq, ldk, ldv};
+  a.q_head = D;
+  return kv_write(a, T, H, D, Hq, 1, max_pos, rot, cache_dtype, pages, block, false, stream);
+}
+
+int tl_kv_write_norm(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t T,
+                     int64_t H, int64_t D, const uint16_t *q, int64_t ldq, int64_t q_head, int64_t Hq,
+                     const float *q_weight, const float *k_weight, float eps, const int32_t *positions, int64_t axes,
+                     const int32_t *axis_of, const float *cos_sin, int64_t max_pos, int64_t rot, uint16_t *q_out,
+                     void *k_cache, void *v_cache, float *k_scale, float *v_scale, int cache_dtype, int64_t pages,
+                     int64_t block, void *stream) {
+  tl::WriteArgs a = {q, k, v, slots, positions, cos_sin, q_out, k_cache, v_cache, k_scale, v_scale, ldq, ldk, ldv};
+  a.q_head = q_head;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.axis_of = axis_of;
+  a.eps = eps;
+  return kv_write(a, T, H, D, Hq, axes, max_pos, rot, cache_dtype, pages, block, true, stream);
 }
 
 size_t tl_tree_attention_workspace_size(int64_t max_nodes, int64_t G, int64_t D, int cache_dtype) {
@@ -668,6 +713,135 @@ int tl_kv_commit(const int32_t *accepted, const int32_t *path, int64_t path_widt
                       static_cast<char *>(v_cache), k_scale, v_scale, ctx_out, pages * H * block, int(R), int(L),
                       int(H), int(pages), log2_of(block), int(table_width), int(path_width)};
   return from_hip(tl::launch_kv_commit(a, D, e4m3, static_cast<hipStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// layers that keep a state per request
+namespace {
+constexpr int64_t kMostState = int64_t(1) << 50;  // elements
+bool requests_ok(int64_t T, int64_t R, int64_t states) {
+  return count_ok(T) && R >= 0 && R <= tl::kMaxRequests && states >= 0 && states < kMaxDim;
+}
+bool delta_heads_ok(int64_t Hk, int64_t G, int64_t Dk, int64_t Dv) {
+  return Hk >= 1 && G >= 1 && Hk <= 65535 && G <= 65535 && Hk * G <= 65535 && (Dk == 64 || Dk == 128) && Dv >= 16 &&
+         Dv <= 65536 && Dv % 16 == 0;
+}
+bool distance_ok(int64_t ld, int64_t least) { return ld >= least && ld < kMaxDim; }
+}  // namespace
+
+int tl_short_conv(const uint16_t *x, int64_t ldx, int64_t T, int64_t C, const float *weight, int64_t taps,
+                  const float *bias, const int32_t *q_start, const int32_t *kv_lens, const int32_t *state_slots,
+                  int64_t R, const uint64_t *tree_mask, int64_t norm_heads, int64_t norm_dim, float eps,
+                  uint16_t *state, int64_t states, uint16_t *out, int64_t ldo, void *stream) {
+  if (!requests_ok(T, R, states) || C < 8 || C > (1 << 20) || C % 8 || taps < 2 || taps > 4) return TL_ERR_SHAPE;
+  if (!distance_ok(ldx, C) || !distance_ok(ldo, C)) return TL_ERR_SHAPE;
+  if (norm_heads < 0 || (norm_heads && (!width_ok(norm_dim) || norm_heads > C / norm_dim))) return TL_ERR_SHAPE;
+  if (norm_heads && !(eps >= 0.0f && eps < __builtin_inff())) return TL_ERR_SHAPE;
+  if (states > kMostState / (3 * C)) return TL_ERR_SHAPE;
+  if (T == 0 || R == 0) return TL_OK;
+  if (any_null(x, weight, q_start, kv_lens, state_slots, out) || (states && !state)) return TL_ERR_NULLPTR;
+  if (!aligned_to(16, x, state, out, weight, bias) || ldx % 8 || ldo % 8 || !aligned_to(8, tree_mask) ||
+      !aligned_to(4, q_start, kv_lens, state_slots))
+    return TL_ERR_ALIGN;
+  const size_t r4 = size_t(R) * 4, row = size_t(C) * 2;
+  Span in[] = {{x, size_t(T - 1) * ldx * 2 + row}, {weight, size_t(C) * taps * 4}, {bias, bias ? size_t(C) * 4 : 0},
+               {q_start, r4 + 4}, {kv_lens, r4}, {state_slots, r4}, {tree_mask, tree_mask ? size_t(T) * 8 : 0}};
+  Span o[] = {{state, size_t(states) * (taps - 1) * row}, {out, size_t(T - 1) * ldo * 2 + row}};
+  if (any_alias(in, 7, o, 2)) return TL_ERR_ALIAS;
+  tl::ConvArgs a = {x, weight, bias, q_start, kv_lens, state_slots, tree_mask, state, out, ldx, ldo, states,
+                    int(T), int(R), int(C), norm_heads ? int(norm_heads * norm_dim) : 0, int(norm_dim), eps};
+  return from_hip(tl::launch_short_conv(a, taps, static_cast<hipStream_t>(stream)));
+}
+
+size_t tl_delta_rule_workspace_size(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_t Dk, int64_t max_nodes,
+                                    int tree) {
+  if (!requests_ok(T, R, 0) || !delta_heads_ok(Hk, G, Dk, 16) || max_nodes < 1 || max_nodes >= kMaxDim) return 0;
+  return tl::delta_workspace_bytes(T, R, Hk, G, Dk, max_nodes, tree != 0);
+}
+
+int tl_delta_rule(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv,
+                  const float *a, int64_t lda, const float *b, int64_t ldb, const float *a_log, const float *dt_bias,
+                  int64_t T, int64_t Hk, int64_t G, int64_t Dk, int64_t Dv, const int32_t *q_start,
+                  const int32_t *kv_lens, const int32_t *state_slots, int64_t R, const uint64_t *tree_mask, float scale,
+                  float *state, int64_t states, int64_t max_nodes, uint16_t *out, void *workspace,
+                  size_t workspace_bytes, void *stream) {
+  if (!requests_ok(T, R, states) || !delta_heads_ok(Hk, G, Dk, Dv) || max_nodes < 1 || max_nodes >= kMaxDim)
+    return TL_ERR_SHAPE;
+  const int64_t Hv = Hk * G;
+  if (!distance_ok(ldq, Hk * Dk) || !distance_ok(ldk, Hk * Dk) || !distance_ok(ldv, Hv * Dv) || !distance_ok(lda, Hv) ||
+      !distance_ok(ldb, Hv))
+    return TL_ERR_SHAPE;
+  if (states > kMostState / (Hv * Dk * Dv) || R * Hv * ((Dv + 15) / 16) >= kMaxDim) return TL_ERR_SHAPE;
+  if (!(scale > -__builtin_inff() && scale < __builtin_inff())) return TL_ERR_SHAPE;
+  if (T == 0 || R == 0) return TL_OK;
+  if (any_null(q, k, v, a, b, q_start, kv_lens, state_slots, out) || (states && !state) || !a_log != !dt_bias)
+    return TL_ERR_NULLPTR;
+  const size_t need = tl::delta_workspace_bytes(T, R, Hk, G, Dk, max_nodes, tree_mask != nullptr);
+  if (need && (!workspace || workspace_bytes < need)) return TL_ERR_WORKSPACE;
+  if (!aligned_to(16, q, k, v, state, out, workspace) || ldq % 8 || ldk % 8 || ldv % 8 || !aligned_to(8, tree_mask) ||
+      !aligned_to(4, a, b, a_log, dt_bias, q_start, kv_lens, state_slots))
+    return TL_ERR_ALIGN;
+  const size_t r4 = size_t(R) * 4, h4 = size_t(Hv) * 4, last = size_t(T - 1);
+  Span in[] = {{q, (last * ldq + Hk * Dk) * 2}, {k, (last * ldk + Hk * Dk) * 2}, {v, (last * ldv + Hv * Dv) * 2},
+               {a, last * lda * 4 + h4}, {b, last * ldb * 4 + h4}, {a_log, a_log ? h4 : 0}, {dt_bias, a_log ? h4 : 0},
+               {q_start, r4 + 4}, {kv_lens, r4}, {state_slots, r4}, {tree_mask, tree_mask ? size_t(T) * 8 : 0}};
+  Span o[] = {{state, size_t(states) * Hv * Dk * Dv * 4}, {out, size_t(T) * Hv * Dv * 2}, {workspace, need}};
+  if (any_alias(in, 11, o, 3)) return TL_ERR_ALIAS;
+  tl::DeltaArgs d = {};
+  d.q = q, d.k = k, d.v = v, d.a = a, d.b = b, d.a_log = a_log, d.dt_bias = dt_bias;
+  d.q_start = q_start, d.kv_lens = kv_lens, d.slots = state_slots, d.tree_mask = tree_mask;
+  d.state = state, d.out = out;
+  d.ldq = ldq, d.ldk = ldk, d.ldv = ldv, d.lda = lda, d.ldb = ldb, d.state_count = states;
+  d.T = int(T), d.R = int(R), d.Hk = int(Hk), d.G = int(G), d.Hv = int(Hv), d.Dv = int(Dv);
+  d.scale = scale;
+  d.L = 1;
+  return from_hip(tl::launch_delta_rule(d, Dk, max_nodes, workspace, static_cast<hipStream_t>(stream)));
+}
+
+int tl_delta_commit(const int32_t *accepted, const int32_t *path, int64_t path_width, const int32_t *q_start,
+                    const int32_t *kv_lens, const int32_t *state_slots, int64_t R, int64_t T, int64_t L,
+                    const uint16_t *k, int64_t ldk, int64_t k_layer, const uint16_t *v, int64_t ldv, int64_t v_layer,
+                    const float *a, int64_t lda, int64_t a_layer, const float *b, int64_t ldb, int64_t b_layer,
+                    const float *a_log, const float *dt_bias, int64_t Hk, int64_t G, int64_t Dk, int64_t Dv,
+                    float *state, int64_t states, const uint16_t *x, int64_t ldx, int64_t x_layer, int64_t C,
+                    int64_t taps, uint16_t *conv_state, void *stream) {
+  if (!requests_ok(T, R, states) || !delta_heads_ok(Hk, G, Dk, Dv) || L < 1 || L > 4096) return TL_ERR_SHAPE;
+  if (path_width < 1 || path_width > TL_TREE_NODES) return TL_ERR_SHAPE;
+  const int64_t Hv = Hk * G;
+  if (!distance_ok(ldk, Hk * Dk) || !distance_ok(ldv, Hv * Dv) || !distance_ok(lda, Hv) || !distance_ok(ldb, Hv))
+    return TL_ERR_SHAPE;
+  if (x && (C < 8 || C > (1 << 20) || C % 8 || taps < 2 || taps > 4 || !distance_ok(ldx, C))) return TL_ERR_SHAPE;
+  constexpr int64_t far = int64_t(1) << 45;              // of a layer from the next
+  if (k_layer < 0 || v_layer < 0 || a_layer < 0 || b_layer < 0 || x_layer < 0 || k_layer > far || v_layer > far ||
+      a_layer > far || b_layer > far || x_layer > far)
+    return TL_ERR_SHAPE;
+  if (states > kMostState / (L * Hv * Dk * Dv) || (x && states > kMostState / (L * 3 * C))) return TL_ERR_SHAPE;
+  if (L * R * (Hv * ((Dv + 31) / 32) + (x ? (C + 2047) / 2048 : 0)) >= kMaxDim) return TL_ERR_SHAPE;
+  if (T == 0 || R == 0) return TL_OK;
+  if (any_null(accepted, path, q_start, kv_lens, state_slots, k, v, a, b) || (states && !state) || !a_log != !dt_bias ||
+      (x && states && !conv_state))
+    return TL_ERR_NULLPTR;
+  if (!aligned_to(16, k, v, state, x, conv_state) || ldk % 8 || ldv % 8 || k_layer % 8 || v_layer % 8 ||
+      (x && (ldx % 8 || x_layer % 8)) || !aligned_to(4, accepted, path, q_start, kv_lens, state_slots, a, b, a_log, dt_bias))
+    return TL_ERR_ALIGN;
+  const size_t r4 = size_t(R) * 4, h4 = size_t(Hv) * 4, last = size_t(T - 1), m = size_t(L - 1);
+  Span in[] = {{accepted, r4}, {path, r4 * path_width}, {q_start, r4 + 4}, {kv_lens, r4}, {state_slots, r4},
+               {k, (m * k_layer + last * ldk + Hk * Dk) * 2}, {v, (m * v_layer + last * ldv + Hv * Dv) * 2},
+               {a, (m * a_layer + last * lda) * 4 + h4}, {b, (m * b_layer + last * ldb) * 4 + h4},
+               {a_log, a_log ? L * h4 : 0}, {dt_bias, a_log ? L * h4 : 0},
+               {x, x ? (m * x_layer + last * ldx + C) * 2 : 0}};
+  Span o[] = {{state, size_t(L) * states * Hv * Dk * Dv * 4}, {x ? conv_state : nullptr, size_t(L) * states * (taps - 1) * C * 2}};
+  if (any_alias(in, 12, o, 2)) return TL_ERR_ALIAS;
+  tl::DeltaArgs d = {};
+  d.k = k, d.v = v, d.a = a, d.b = b, d.a_log = a_log, d.dt_bias = dt_bias;
+  d.q_start = q_start, d.kv_lens = kv_lens, d.slots = state_slots;
+  d.state = state;
+  d.ldk = ldk, d.ldv = ldv, d.lda = lda, d.ldb = ldb, d.state_count = states;
+  d.T = int(T), d.R = int(R), d.Hk = int(Hk), d.G = int(G), d.Hv = int(Hv), d.Dv = int(Dv);
+  d.accepted = accepted, d.path = path, d.x = x, d.conv_state = conv_state;
+  d.k_layer = k_layer, d.v_layer = v_layer, d.a_layer = a_layer, d.b_layer = b_layer, d.x_layer = x_layer, d.ldx = ldx;
+  d.path_width = int(path_width), d.L = int(L), d.C = int(C), d.taps = int(taps);
+  return from_hip(tl::launch_delta_commit(d, Dk, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

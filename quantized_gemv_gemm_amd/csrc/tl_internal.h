@@ -155,8 +155,14 @@ struct WriteArgs {
   float *k_scale, *v_scale;
   int64_t ldq, ldk, ldv, slot_count;
   int T, Hq, H, rot, max_pos, block_shift;
+  // with norms of the heads of q and k
+  const float *q_weight, *k_weight;  // f32 [D] or NULL
+  const int32_t *axis_of;     // [rot / 2] or NULL: positions [axes, T]
+  int64_t q_head;             // elements from a head of q to the next
+  int axes;
+  float eps;
 };
-hipError_t launch_kv_write(const WriteArgs &a, int64_t D, bool e4m3, hipStream_t stream);
+hipError_t launch_kv_write(const WriteArgs &a, int64_t D, bool e4m3, bool norm, hipStream_t stream);
 
 struct CommitArgs {
   const int32_t *accepted, *path, *ctx_lens, *kv_lens, *table;
@@ -179,6 +185,44 @@ struct VerifyArgs {
 };
 int verify_parts(int64_t T, int64_t V);
 hipError_t launch_tree_verify(const VerifyArgs &a, bool f32, hipStream_t stream);
+
+// ---------------------------------------------------------------------------
+// layers that keep a state per request
+struct ConvArgs {
+  const uint16_t *x;          // bf16 [T, C], rows ldx apart
+  const float *weight, *bias; // f32 [C, taps]; [C] or NULL
+  const int32_t *q_start, *kv_lens, *slots;
+  const uint64_t *tree_mask;
+  uint16_t *state;            // bf16 [state_count, taps - 1, C]
+  uint16_t *out;              // bf16 [T, C], rows ldo apart
+  int64_t ldx, ldo, state_count;
+  int T, R, C, norm_channels, norm_dim;
+  float eps;
+};
+hipError_t launch_short_conv(const ConvArgs &a, int64_t taps, hipStream_t stream);
+
+struct DeltaArgs {
+  const uint16_t *q, *k, *v;  // bf16 [T, heads, D], tokens ldq / ldk / ldv apart
+  const float *a, *b;         // f32 [T, Hv], rows lda / ldb apart
+  const float *a_log, *dt_bias;  // f32 [Hv], or both NULL
+  const int32_t *q_start, *kv_lens, *slots;
+  const uint64_t *tree_mask;
+  float *state;               // f32 [state_count, Hv, Dk, Dv]
+  uint16_t *out;              // bf16 [T, Hv, Dv]
+  char *heads, *keys;         // workspace: of each chunk and value head, and of each chunk and key head
+  int64_t ldq, ldk, ldv, lda, ldb, state_count;
+  int T, R, Hk, G, Hv, Dv;
+  float scale;
+  // the accepted branches of all layers (launch_delta_commit); *_layer: elements from a layer to the next
+  const int32_t *accepted, *path;
+  const uint16_t *x;          // bf16 [L, T, C] or NULL
+  uint16_t *conv_state;       // bf16 [L, state_count, taps - 1, C]
+  int64_t k_layer, v_layer, a_layer, b_layer, x_layer, ldx;
+  int path_width, L, C, taps;
+};
+size_t delta_workspace_bytes(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_t Dk, int64_t max_nodes, bool tree);
+hipError_t launch_delta_rule(DeltaArgs a, int64_t Dk, int64_t max_nodes, void *workspace, hipStream_t stream);
+hipError_t launch_delta_commit(const DeltaArgs &a, int64_t Dk, hipStream_t stream);
 
 // whole layer from the raw input (tl_api.cpp): the checks that need no workspace,
 // then the workspace checks and the launches on the path tl_linear_path names
