@@ -235,110 +235,144 @@ __device__ __forceinline__ void cut(const float (&x)[8], u32x4 (&o)[PARTS]) {
   }
 }
 
+// What one lane wrote to LDS is there for the wave's other lanes (which need no barrier: a
+// wave's LDS instructions are executed in order).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// One wave makes T and P of one chunk and value head, and for the first head of a key head K
+// transposed; four heads share a workgroup, and waves never wait for each other.  All of K
+// stays in registers as operands.  A lies in LDS; its diagonal blocks of 16 are solved column
+// by column, a lane each (T_ii = (I + A_ii)^-1), and the blocks below follow by
+// T_ij = -T_ii sum over k of A_ik T_kj on the f32 matrix instruction, whose steps take rows
+// 4 g + c in the order in which results lie, so T's blocks are operands as they stand.
 template <int DK>
-__global__ __launch_bounds__(kThreads) void delta_prep_kernel(const DeltaArgs a) {
-  constexpr int NS = DK / 32, PITCH = kChunk + 4;
-  __shared__ __attribute__((aligned(16))) float s_A[kChunk * PITCH], s_T[kChunk * PITCH];
-  __shared__ double s_total[kChunk];
-  __shared__ float s_g[kChunk], s_b[kChunk];
-  __shared__ uint64_t s_seen[kChunk];
-  __shared__ uint32_t s_bad[2];                          // tokens whose k, g or b is not finite
-  static_assert(sizeof(s_T) >= kChunk * (DK + 8) * 2, "K passes through s_T");
+__global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs a) {
+  constexpr int NS = DK / 32, PITCH = kChunk + 4, WAVES = kThreads / 64;
+  __shared__ __attribute__((aligned(16))) float s_A[WAVES][kChunk * PITCH];
+  __shared__ double s_total[WAVES][kChunk];
+  __shared__ float s_b[WAVES][kChunk];
+  __shared__ uint64_t s_seen[WAVES][kChunk];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
-  const int number = blockIdx.x, h = blockIdx.y, kh = h / a.G;
-  if (tid < 2) s_bad[tid] = 0;
+  const int number = blockIdx.x, h = int(blockIdx.y) * WAVES + wave, kh = h / a.G;
   const Piece piece = find_piece<kChunk>(a.q_start, a.R, a.T, number);
-  if (piece.r < 0 || state_row(a.kv_lens, a.slots, a.state_count, piece.r) < 0) return;
+  if (h >= a.Hv || piece.r < 0 || state_row(a.kv_lens, a.slots, a.state_count, piece.r) < 0) return;
   const int64_t t0 = int64_t(piece.first) + piece.part * kChunk;
   const int n = min(kChunk, piece.n - piece.part * kChunk);
   const bool tree = a.tree_mask && piece.n <= kTreeNodes;
   char *head = a.heads + (int64_t(number) * a.Hv + h) * kHeadBytes;
+  float *A = s_A[wave];
 
-  // K transposed, once for the value heads that share it
+  // K's rows as operands: tile t's row m is token dealt(t, m)
+  u32x4 k[4][NS];
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int c = 0; c < NS; ++c) {
+      const int i = dealt(t, m);
+      k[t][c] = u32x4{0, 0, 0, 0};
+      if (i < n) k[t][c] = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + 32 * c + 8 * g);
+    }
+  // a lane's token: gates, and what it sees
+  Gate gate = {0.0f, 0.0f};
+  if (lane < n) gate = gate_of(a, a.a, a.b, t0 + lane, h, 0);
+  const uint64_t own = uint64_t(1) << lane, upto = own | (own - 1);
+  const uint64_t seen = tree ? ((lane < n ? a.tree_mask[t0 + lane] : 0) | own) & upto : upto;
+  // exp of less is 0 either way, and sums of finite numbers can be subtracted
+  if (gate.g < -1.0e4f) gate.g = -1.0e4f;
+  const bool lost = !__builtin_isfinite(gate.g) || !__builtin_isfinite(gate.b);
+  if (lost) gate = {0.0f, 0.0f};
+  uint64_t bad = __ballot(lost);                         // tokens whose k, g or b is not finite
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    bool off = false;
+#pragma unroll
+    for (int c = 0; c < NS; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) off |= (k[t][c][e] & 0x7F80u) == 0x7F80u || (k[t][c][e] & 0x7F800000u) == 0x7F800000u;
+    uint64_t all = __ballot(off);
+    if (all == 0) continue;
+    all |= all >> 32;
+    all |= all >> 16;
+    for (int j = 0; j < 16; ++j) bad |= (all >> j & 1) << dealt(t, j);
+    if (all >> m & 1)
+#pragma unroll
+      for (int c = 0; c < NS; ++c) k[t][c] = u32x4{0, 0, 0, 0};
+  }
+  double total = double(gate.g) * 1.4426950408889634;    // powers of two from here on
+  if (!tree) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double before = __shfl_up(total, off, 64);
+      if (lane >= off) total += before;
+    }
+  } else {
+    const double mine = total;
+    total = 0.0;
+    for (int j = 0; j < n; ++j) {
+      const double x = __shfl(mine, j, 64);
+      if (seen >> j & 1) total += x;
+    }
+  }
+  s_total[wave][lane] = total;
+  s_b[wave][lane] = gate.b;
+  s_seen[wave][lane] = seen;
+  const double end = __shfl(total, n - 1, 64);
+  {
+    float *to = reinterpret_cast<float *>(head + kDecays);
+    to[lane] = lane < n ? __builtin_amdgcn_exp2f(float(total)) : 0.0f;
+    to[kChunk + lane] = lane < n ? __builtin_amdgcn_exp2f(float(end - total)) : 0.0f;
+    if (lane == 0) *reinterpret_cast<f32x4 *>(to + 2 * kChunk) =
+        f32x4{__builtin_amdgcn_exp2f(float(end)), 0.0f, __uint_as_float(uint32_t(bad)), __uint_as_float(uint32_t(bad >> 32))};
+  }
+  // K transposed: times one-hot columns, which picks element dealt(t, m) of every token
   if (h % a.G == 0 && !tree) {
-    uint16_t *rows = reinterpret_cast<uint16_t *>(s_T);
-    constexpr int ROW = DK + 8;
-    for (int u = tid; u < kChunk * DK / 8; u += kThreads) {
-      const int i = u / (DK / 8), d = u % (DK / 8) * 8;
-      u32x4 x = {0, 0, 0, 0};
-      if (i < n) x = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + d);
-      *reinterpret_cast<u32x4 *>(rows + i * ROW + d) = x;
-    }
-    __syncthreads();
     u32x4 *to = reinterpret_cast<u32x4 *>(a.keys + (int64_t(number) * a.Hk + kh) * key_bytes(DK));
-    for (int u = wave; u < DK / 16 * 2; u += 4) {        // tile of d's, 32 tokens
-      const int d = dealt(u >> 1, m), i0 = 32 * (u & 1) + 8 * g;
-      u32x4 x;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = rows[(i0 + 2 * e) * ROW + d] | uint32_t(rows[(i0 + 2 * e + 1) * ROW + d]) << 16;
-      to[u * 64 + lane] = x;
+    for (int t = 0; t < DK / 16; ++t) {
+      u32x4 pick;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = dealt(t & 1, m) - 8 * g - 2 * e;
+        pick[e] = d == 0 ? 0x3F80u : d == 1 ? 0x3F800000u : 0u;
+      }
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const f32x4 zero = {0, 0, 0, 0};
+        const f32x4 x = mfma(k[2 * s][t >> 1], pick, zero), y = mfma(k[2 * s + 1][t >> 1], pick, zero);
+        to[(t * 2 + s) * 64 + lane] = u32x4{upper(x[0], x[1]), upper(x[2], x[3]), upper(y[0], y[1]), upper(y[2], y[3])};
+      }
     }
-    __syncthreads();
   }
+  wave_sync();
 
-  // a lane holds token i = dealt(wave, m): its k and q, 8 elements of every 32
-  const int i = dealt(wave, m), last = wave >> 1;
-  u32x4 ki[NS], qi[NS];
+  // (K K^T)^T and (Q K^T)^T: a lane holds token i = dealt(t, m) against 8 consecutive j's
+  u32x4 *P = reinterpret_cast<u32x4 *>(head + kTParts * kTriangle * kTile);
 #pragma unroll
-  for (int c = 0; c < NS; ++c) {
-    ki[c] = qi[c] = u32x4{0, 0, 0, 0};
-    if (i < n) {
-      ki[c] = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + 32 * c + 8 * g);
-      qi[c] = *reinterpret_cast<const u32x4 *>(a.q + (t0 + i) * a.ldq + kh * DK + 32 * c + 8 * g);
+  for (int t = 0; t < 4; ++t) {
+    if (32 * (t >> 1) >= n) break;                       // uniform
+    const int i = dealt(t, m);
+    u32x4 q[NS];
+#pragma unroll
+    for (int c = 0; c < NS; ++c) {
+      q[c] = u32x4{0, 0, 0, 0};
+      if (i < n) q[c] = *reinterpret_cast<const u32x4 *>(a.q + (t0 + i) * a.ldq + kh * DK + 32 * c + 8 * g);
     }
-  }
-  if (tid < kChunk) {
-    Gate gate = {0.0f, 0.0f};
-    if (tid < n) gate = gate_of(a, a.a, a.b, t0 + tid, h, 0);
-    // exp of less is 0 either way, and sums of finite numbers can be subtracted
-    if (gate.g < -1.0e4f) gate.g = -1.0e4f;
-    if (!__builtin_isfinite(gate.g) || !__builtin_isfinite(gate.b)) {
-      atomicOr(&s_bad[tid >> 5], 1u << (tid & 31));
-      gate = {0.0f, 0.0f};
-    }
-    s_g[tid] = gate.g;
-    s_b[tid] = gate.b;
-    const uint64_t own = uint64_t(1) << tid, upto = own | (own - 1);
-    s_seen[tid] = tree ? ((tid < n ? a.tree_mask[t0 + tid] : 0) | own) & upto : upto;
-  }
-  bool off = false;
+    const double upto_i = s_total[wave][i];
+    const float step = s_b[wave][i];
+    const uint64_t sees = i < n ? s_seen[wave][i] : 0;
 #pragma unroll
-  for (int c = 0; c < NS; ++c)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) off |= (ki[c][e] & 0x7F80u) == 0x7F80u || (ki[c][e] & 0x7F800000u) == 0x7F800000u;
-  if (off) atomicOr(&s_bad[i >> 5], 1u << (i & 31));
-  __syncthreads();
-  const uint64_t bad = s_bad[0] | uint64_t(s_bad[1]) << 32;
-  if (tid < kChunk) {
-    const uint64_t seen = s_seen[tid];
-    double total = 0.0;
-    for (int j = 0; j < n; ++j)
-      if (seen >> j & 1) total += double(s_g[j]);
-    s_total[tid] = total;
-  }
-  __syncthreads();
-
-  // (K K^T)^T and (Q K^T)^T: token i against 8 consecutive j's
-  if (32 * last < n) {
-    if (bad >> i & 1) {
-#pragma unroll
-      for (int c = 0; c < NS; ++c) ki[c] = u32x4{0, 0, 0, 0};
-    }
-    const double total = s_total[i];
-    const float step = s_b[i];
-    const uint64_t seen = s_seen[i];
-    for (int s = 0; s <= last; ++s) {
+    for (int s = 0; s <= t >> 1; ++s) {
       float kk[8], qk[8];
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
-        const int j = dealt(2 * s + p, m);
         f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
 #pragma unroll
         for (int c = 0; c < NS; ++c) {
-          u32x4 kj = {0, 0, 0, 0};
-          if (j < n && !(bad >> j & 1)) kj = *reinterpret_cast<const u32x4 *>(a.k + (t0 + j) * a.ldk + kh * DK + 32 * c + 8 * g);
-          x = mfma(kj, ki[c], x);
-          y = mfma(kj, qi[c], y);
+          x = mfma(k[2 * s + p][c], k[t][c], x);
+          y = mfma(k[2 * s + p][c], q[c], y);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -349,82 +383,91 @@ __global__ __launch_bounds__(kThreads) void delta_prep_kernel(const DeltaArgs a)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int j = 32 * s + 8 * g + e;
-        const bool on = i < n && j <= i && (seen >> j & 1);
-        const float decay = expf(float(total - s_total[j]));
+        const float decay = __builtin_amdgcn_exp2f(float(upto_i - s_total[wave][j]));
+        const bool on = sees >> j & 1;
         kk[e] = on && j < i ? step * decay * kk[e] : 0.0f;
         qk[e] = on ? decay * qk[e] : 0.0f;
       }
-      f32x4 *to = reinterpret_cast<f32x4 *>(s_A + i * PITCH + 32 * s + 8 * g);
+      f32x4 *to = reinterpret_cast<f32x4 *>(A + i * PITCH + 32 * s + 8 * g);
       to[0] = f32x4{kk[0], kk[1], kk[2], kk[3]};
       to[1] = f32x4{kk[4], kk[5], kk[6], kk[7]};
       u32x4 part[kPParts];
       cut<kPParts>(qk, part);
-      u32x4 *P = reinterpret_cast<u32x4 *>(head + kTParts * kTriangle * kTile);
 #pragma unroll
-      for (int e = 0; e < kPParts; ++e) P[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = part[e];
+      for (int e = 0; e < kPParts; ++e) P[(e * kTriangle + tri_at(t, s)) * 64 + lane] = part[e];
     }
   }
-  __syncthreads();
+  wave_sync();
 
-  // T's diagonal blocks of 16: a lane solves one column, row by row
-  const int tiles = (n + 15) / 16;
-  if (wave < tiles) {
-    const float *A = s_A + (16 * wave) * PITCH + 16 * wave;
+  // T's diagonal blocks: lane 16 b + c solves column c of block b, row by row.  Tokens past the
+  // last one are rows of A that nobody wrote where 32 of them are missing: their blocks stay out.
+  const int tiles = n > 32 ? 4 : 2;
+  if (g < tiles) {
+    const float *D = A + 16 * g * PITCH + 16 * g;
     float t[16];
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
       float sum = x == m ? 1.0f : 0.0f;
 #pragma unroll
-      for (int y = 0; y < x; ++y) sum = fmaf(-A[x * PITCH + y], t[y], sum);
+      for (int y = 0; y < x; ++y) sum = fmaf(-D[x * PITCH + y], t[y], sum);
       t[x] = sum;
     }
+    float *to = A + 16 * g * PITCH + 16 * g + m;
 #pragma unroll
-    for (int x = 0; x < 16; ++x)
-      if (x >> 2 == g) s_T[(16 * wave + x) * PITCH + 16 * wave + m] = t[x];
+    for (int x = 0; x < 16; ++x) to[x * PITCH] = t[x];
   }
-  __syncthreads();
-  // the blocks below: T_ij = -T_ii sum over k of A_ik T_kj, a diagonal after the other
-  for (int off = 1; off < tiles; ++off) {
-    if (wave + off < tiles) {
-      const int bi = wave + off, bj = wave;
+  wave_sync();
+  f32x4 T[4][4];                                         // T[i][j][c]: row 16 i + 4 g + c, column 16 j + m
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) T[i][i][c] = i < tiles ? A[(16 * i + 4 * g + c) * PITCH + 16 * i + m] : 0.0f;
+#pragma unroll
+  for (int off = 1; off < 4; ++off) {
+    if (off == 2 && tiles == 2) break;                   // uniform
+#pragma unroll
+    for (int i = off; i < 4; ++i) {
+      if (i >= tiles) break;
+      const int j = i - off;
       f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-      for (int bk = bj; bk < bi; ++bk)
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          x = __builtin_amdgcn_mfma_f32_16x16x4f32(s_A[(16 * bi + m) * PITCH + 16 * bk + 4 * c + g],
-                                                   s_T[(16 * bk + 4 * c + g) * PITCH + 16 * bj + m], x, 0, 0, 0);
+      for (int b = j; b < i; ++b) {
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(A + (16 * i + m) * PITCH + 16 * b + 4 * g);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)                        // x's lane holds rows 4 g + c
-        y = __builtin_amdgcn_mfma_f32_16x16x4f32(s_T[(16 * bi + m) * PITCH + 16 * bi + 4 * g + c], x[c], y, 0, 0, 0);
+        for (int c = 0; c < 4; ++c) x = __builtin_amdgcn_mfma_f32_16x16x4f32(w[c], T[b][j][c], x, 0, 0, 0);
+      }
+      const f32x4 w = *reinterpret_cast<const f32x4 *>(A + (16 * i + m) * PITCH + 16 * i + 4 * g);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) s_T[(16 * bi + 4 * g + c) * PITCH + 16 * bj + m] = -y[c];
+      for (int c = 0; c < 4; ++c) y = __builtin_amdgcn_mfma_f32_16x16x4f32(w[c], x[c], y, 0, 0, 0);
+      T[i][j] = -y;
     }
-    __syncthreads();
   }
-  if (32 * last < n) {
-    u32x4 *T = reinterpret_cast<u32x4 *>(head);
-    for (int s = 0; s <= last; ++s) {
+  wave_sync();
+#pragma unroll
+  for (int i = 1; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < i; ++j)
+      if (i < tiles)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) A[(16 * i + 4 * g + c) * PITCH + 16 * j + m] = T[i][j][c];
+  wave_sync();
+  u32x4 *to = reinterpret_cast<u32x4 *>(head);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    if (32 * (t >> 1) >= n) break;
+    const int i = dealt(t, m);
+#pragma unroll
+    for (int s = 0; s <= t >> 1; ++s) {
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int j = 32 * s + 8 * g + e;
-        x[e] = i < n && j <= i ? s_T[i * PITCH + j] * s_b[j] : 0.0f;
+        x[e] = j <= i ? A[i * PITCH + j] * s_b[wave][j] : 0.0f;
       }
       u32x4 part[kTParts];
       cut<kTParts>(x, part);
 #pragma unroll
-      for (int e = 0; e < kTParts; ++e) T[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = part[e];
-    }
-  }
-  if (tid < kChunk) {
-    float *to = reinterpret_cast<float *>(head + kDecays);
-    const double end = s_total[n - 1];
-    to[tid] = tid < n ? expf(float(s_total[tid])) : 0.0f;
-    to[kChunk + tid] = tid < n ? expf(float(end - s_total[tid])) : 0.0f;
-    if (tid == 0) {
-      to[2 * kChunk] = expf(float(end));
-      reinterpret_cast<uint32_t *>(to)[2 * kChunk + 2] = s_bad[0];
-      reinterpret_cast<uint32_t *>(to)[2 * kChunk + 3] = s_bad[1];
+      for (int e = 0; e < kTParts; ++e) to[(e * kTriangle + tri_at(t, s)) * 64 + lane] = part[e];
     }
   }
 }
@@ -478,14 +521,61 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
 
   const int64_t number = int64_t(first) / kChunk + r;
   const int row0 = 32 * (wave >> 1) + 8 * g + 4 * (wave & 1), pairs = (wave >> 1) + 1;
+  // what a wave takes of a chunk, brought a chunk ahead
+  struct Ops {
+    u32x4 k[NS], q[NS], T[2][kTParts], P[2][kPParts], keys[2][2];
+    uint32_t v[4];                                       // CT columns of a row
+    f32x4 grown, left, end;                              // end: exp(D_last), nothing, a word of tokens
+  };
+  auto fetch = [&](int part, Ops &x) {
+    const int64_t t0 = int64_t(first) + part * kChunk;
+    const int here = min(kChunk, n - part * kChunk), i = dealt(wave, m);
+    const char *head = a.heads + ((number + part) * a.Hv + h) * kHeadBytes;
+    const float *decays = reinterpret_cast<const float *>(head + kDecays);
+    x.end = *reinterpret_cast<const f32x4 *>(decays + 2 * kChunk);
+    if (32 * (wave >> 1) < here) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        x.k[s] = x.q[s] = u32x4{0, 0, 0, 0};
+        if (i < here) {
+          x.k[s] = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + 32 * s + 8 * g);
+          x.q[s] = *reinterpret_cast<const u32x4 *>(a.q + (t0 + i) * a.ldq + kh * DK + 32 * s + 8 * g);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint16_t *from = a.v + (t0 + row0 + e) * a.ldv + int64_t(h) * a.Dv + col;
+        x.v[e] = 0;
+        if (live && row0 + e < here) x.v[e] = CT == 2 ? *reinterpret_cast<const uint32_t *>(from) : *from;
+      }
+      x.grown = *reinterpret_cast<const f32x4 *>(decays + row0);
+      const u32x4 *T = reinterpret_cast<const u32x4 *>(head) + tri_at(wave, 0) * 64 + lane, *P = T + kTParts * kTriangle * 64;
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s >= pairs) break;                           // uniform
+#pragma unroll
+        for (int e = 0; e < kTParts; ++e) x.T[s][e] = T[(e * kTriangle + s) * 64];
+#pragma unroll
+        for (int e = 0; e < kPParts; ++e) x.P[s][e] = P[(e * kTriangle + s) * 64];
+      }
+      x.left = *reinterpret_cast<const f32x4 *>(decays + kChunk + row0);
+    }
+    if (holds && !tree) {
+      const u32x4 *keys = reinterpret_cast<const u32x4 *>(a.keys + ((number + part) * a.Hk + kh) * key_bytes(DK)) + lane;
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) x.keys[p][s] = keys[((2 * wave + p) * 2 + s) * 64];
+    }
+  };
+  Ops now;
+  fetch(0, now);
   for (int part = 0; int64_t(part) * kChunk < n; ++part) {
     const int64_t t0 = int64_t(first) + part * kChunk;
     const int here = min(kChunk, n - part * kChunk);
     const bool rows = 32 * (wave >> 1) < here;           // this wave has tokens
-    const char *head = a.heads + ((number + part) * a.Hv + h) * kHeadBytes;
-    const u32x4 *T = reinterpret_cast<const u32x4 *>(head), *P = T + kTParts * kTriangle * 64;
-    const float *decays = reinterpret_cast<const float *>(head + kDecays);
-    const u32x4 *keys = reinterpret_cast<const u32x4 *>(a.keys + ((number + part) * a.Hk + kh) * key_bytes(DK));
+    Ops next;
+    if (int64_t(part + 1) * kChunk < n) fetch(part + 1, next);
     if (holds) {
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
@@ -500,39 +590,25 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
     f32x4 ks[CT], o[CT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) ks[c] = o[c] = f32x4{0, 0, 0, 0};
-    const uint64_t bad = *reinterpret_cast<const uint64_t *>(decays + 2 * kChunk + 2);
-    const f32x4 grown = *reinterpret_cast<const f32x4 *>(decays + row0);
+    const uint64_t bad = __float_as_uint(now.end[2]) | uint64_t(__float_as_uint(now.end[3])) << 32;
     if (rows) {
-      const int i = dealt(wave, m);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        u32x4 ki = {0, 0, 0, 0}, qi = {0, 0, 0, 0};
-        if (i < here) {
-          ki = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + 32 * s + 8 * g);
-          qi = *reinterpret_cast<const u32x4 *>(a.q + (t0 + i) * a.ldq + kh * DK + 32 * s + 8 * g);
-        }
+      for (int s = 0; s < NS; ++s)
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          ks[c] = mfma(ki, s_S[0][c][s][lane], ks[c]);
-          ks[c] = mfma(ki, s_S[1][c][s][lane], ks[c]);
-          ks[c] = mfma(ki, s_S[2][c][s][lane], ks[c]);
-          o[c] = mfma(qi, s_S[0][c][s][lane], o[c]);
-          o[c] = mfma(qi, s_S[1][c][s][lane], o[c]);
+          ks[c] = mfma(now.k[s], s_S[0][c][s][lane], ks[c]);
+          ks[c] = mfma(now.k[s], s_S[1][c][s][lane], ks[c]);
+          ks[c] = mfma(now.k[s], s_S[2][c][s][lane], ks[c]);
+          o[c] = mfma(now.q[s], s_S[0][c][s][lane], o[c]);
+          o[c] = mfma(now.q[s], s_S[1][c][s][lane], o[c]);
         }
-      }
       // R = V - exp(D) K S
-      float v[4][CT];
+      const f32x4 grown = now.grown;
+      float v[4][2];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool there = live && row0 + e < here;
-        const uint16_t *from = a.v + (t0 + row0 + e) * a.ldv + int64_t(h) * a.Dv + col;
-        if constexpr (CT == 2) {
-          const uint32_t w = there ? *reinterpret_cast<const uint32_t *>(from) : 0;
-          v[e][0] = lo_bf16(w);
-          v[e][1] = hi_bf16(w);
-        } else {
-          v[e][0] = there ? bf16_bits_to_float(*from) : 0.0f;
-        }
+        v[e][0] = lo_bf16(now.v[e]);
+        v[e][1] = hi_bf16(now.v[e]);
       }
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
@@ -567,9 +643,10 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
       f32x4 u[CT];
 #pragma unroll
       for (int c = 0; c < CT; ++c) u[c] = f32x4{0, 0, 0, 0};
-      for (int s = 0; s < pairs; ++s) {
-        const u32x4 *t = T + tri_at(wave, s) * 64 + lane;
-        const u32x4 hi = t[0], mid = t[kTriangle * 64], lo = t[2 * kTriangle * 64];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s >= pairs) break;
+        const u32x4 hi = now.T[s][0], mid = now.T[s][1], lo = now.T[s][2];
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
           const u32x4 x = s_R[0][c][s][lane], y = s_R[1][c][s][lane], z = s_R[2][c][s][lane];
@@ -581,7 +658,7 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
           u[c] = mfma(hi, x, u[c]);
         }
       }
-      const f32x4 left = *reinterpret_cast<const f32x4 *>(decays + kChunk + row0);
+      const f32x4 left = now.left;
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
         float x[4], y[4];
@@ -605,9 +682,10 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
     }
     __syncthreads();
     if (rows) {                                          // out = scale (exp(D) Q S + P U)
-      for (int s = 0; s < pairs; ++s) {
-        const u32x4 *t = P + tri_at(wave, s) * 64 + lane;
-        const u32x4 hi = t[0], lo = t[kTriangle * 64];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s >= pairs) break;
+        const u32x4 hi = now.P[s][0], lo = now.P[s][1];
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
           o[c] = mfma(lo, s_U[0][c][s][lane], o[c]);
@@ -632,16 +710,18 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
       }
     }
     if (holds && !tree) {                                // S = exp(D_last) S + K^T (exp(D_last - D) U)
-      const float end = decays[2 * kChunk];
+      const float end = now.end[0];
       const int half = here > 32 ? 2 : 1;
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int c = 0; c < CT; ++c) S[p][c] *= end;
-      for (int s = 0; s < half; ++s)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        if (s >= half) break;
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-          const u32x4 kt = keys[((2 * wave + p) * 2 + s) * 64 + lane];
+          const u32x4 kt = now.keys[p][s];
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
             S[p][c] = mfma(kt, s_W[2][c][s][lane], S[p][c]);
@@ -649,6 +729,7 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
             S[p][c] = mfma(kt, s_W[0][c][s][lane], S[p][c]);
           }
         }
+      }
       if (some) {
 #pragma unroll
         for (int p = 0; p < 2; ++p)
@@ -657,6 +738,7 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
             if (gone[c]) S[p][c] = S[p][c] + __builtin_nanf("");
       }
     }
+    now = next;
   }
   if (holds && live && !tree) {
 #pragma unroll
@@ -683,7 +765,7 @@ hipError_t run(DeltaArgs a, bool chunks, hipStream_t stream) {
     set_last_kernel("delta_step");
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(unsigned(chunks_of(a.T, a.R)), unsigned(a.Hv)), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(unsigned(chunks_of(a.T, a.R)), unsigned((a.Hv + 3) / 4)), dim3(kThreads), 0, stream, a);
   if (hipError_t e = hipGetLastError()) return e;
   const int64_t grid = int64_t(a.R) * a.Hv * ((a.Dv + 31) / 32);
   hipLaunchKernelGGL((delta_scan_kernel<DK, 2>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a);
