@@ -23,6 +23,8 @@
 // A product with a masked zero would still spread what is not finite to tokens that do not see
 // it.  So tokens with such a k, g or b, and elements of v, count as zeros in the products, and
 // the results of those that do see them, and the state, become NaN at the end.
+#include <type_traits>
+
 #include "kv_layout.h"
 #include "mixer_dev.h"
 
@@ -476,7 +478,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
 // w of the chunk's tokens and, of the state, the rows 32 w .. 32 w + 31 (a pair of tiles).
 // Column m of tile c is column CT m + c: a lane's columns are neighbours.
 template <int DK, int CT>
-__global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a) {
+__global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs a) {
   constexpr int NS = DK / 32;
   static_assert(NS <= 4, "a wave holds at most one pair of state tiles");
   __shared__ __attribute__((aligned(16))) u32x4 s_S[3][CT][NS][64], s_R[3][CT][2][64], s_U[2][CT][2][64], s_W[3][CT][2][64];
@@ -484,18 +486,19 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
   __shared__ int s_some;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
   const int blocks = (a.Dv + 16 * CT - 1) / (16 * CT);
-  int id = blockIdx.x;
-  const int cb = id % blocks;
-  id /= blocks;
-  const int h = id % a.Hv, r = id / a.Hv, kh = h / a.G;
+  // Workgroups go to the 8 L2s in turn: those of one key head, which read the same K, Q, T and P,
+  // are 8 numbers apart.
+  const int of_key = a.G * blocks, j = int(blockIdx.x) >> 3, key = j / of_key * 8 + (int(blockIdx.x) & 7);
+  if (key >= a.R * a.Hk) return;
+  const int r = key / a.Hk, kh = key - r * a.Hk, h = kh * a.G + j % of_key / blocks, cb = j % blocks;
   // a chain's state is NaN from such a token on, so the words need no clearing for later chunks
   if (tid < 32 * CT) s_bad[tid >> 1][tid & 1] = 0;
   if (tid == 0) s_some = 0;
   if (!starts_rise(a.q_start, a.R, a.T)) return;
   const int first = a.q_start[r], n = a.q_start[r + 1] - first;
   if (n <= 0) return;
-  const int col = 16 * CT * cb + CT * m;
-  const bool live = col < a.Dv;
+  // Past the last column a lane repeats the work of another one, value for value.
+  const int own_col = 16 * CT * cb + CT * m, col = own_col < a.Dv ? own_col : own_col - 16;
   const int srow = state_row(a.kv_lens, a.slots, a.state_count, r);
   auto store = [&](int64_t t, const float *o) {
     uint16_t *to = a.out + (t * a.Hv + h) * a.Dv + col;
@@ -504,8 +507,7 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
   };
   if (srow < 0) {
     const float zero[2] = {0.0f, 0.0f};
-    if (live)
-      for (int i = 4 * wave + g; i < n; i += 16) store(int64_t(first) + i, zero);
+    for (int i = 4 * wave + g; i < n; i += 16) store(int64_t(first) + i, zero);
     return;
   }
   const bool tree = a.tree_mask && n <= kTreeNodes, fresh = a.kv_lens[r] <= n;
@@ -517,148 +519,172 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int c = 0; c < CT; ++c) S[p][c][e] = holds && live && !fresh ? state[int64_t(4 * p + e) * a.Dv + c] : 0.0f;
+      for (int c = 0; c < CT; ++c) S[p][c][e] = holds && !fresh ? state[int64_t(4 * p + e) * a.Dv + c] : 0.0f;
 
   const int64_t number = int64_t(first) / kChunk + r;
-  const int row0 = 32 * (wave >> 1) + 8 * g + 4 * (wave & 1), pairs = (wave >> 1) + 1;
-  // what a wave takes of a chunk, brought a chunk ahead
-  struct Ops {
-    u32x4 k[NS], q[NS], T[2][kTParts], P[2][kPParts], keys[2][2];
-    uint32_t v[4];                                       // CT columns of a row
-    f32x4 grown, left, end;                              // end: exp(D_last), nothing, a word of tokens
-  };
-  auto fetch = [&](int part, Ops &x) {
-    const int64_t t0 = int64_t(first) + part * kChunk;
-    const int here = min(kChunk, n - part * kChunk), i = dealt(wave, m);
-    const char *head = a.heads + ((number + part) * a.Hv + h) * kHeadBytes;
-    const float *decays = reinterpret_cast<const float *>(head + kDecays);
-    x.end = *reinterpret_cast<const f32x4 *>(decays + 2 * kChunk);
-    if (32 * (wave >> 1) < here) {
+  const int row0 = 32 * (wave >> 1) + 8 * g + 4 * (wave & 1), pairs = (wave >> 1) + 1, i = dealt(wave, m);
+  // What a wave takes of a chunk.  Each piece is asked for as soon as the chunk before has used
+  // it.  Rows past the last token are the last one's: nothing of theirs is kept.
+  u32x4 K[NS], Q[NS], T[2][kTParts], P[2][kPParts], keys[2][2];
+  uint32_t V[4];                                         // CT columns of a row
+  f32x4 grown, left, end;                                // end: exp(D_last), nothing, a word of tokens
+  const int vcol = h * a.Dv + col;
+  auto head_of = [&](int part) { return a.heads + ((number + part) * a.Hv + h) * kHeadBytes; };
+  auto fetch_rows = [&](int part) {
+    const int here = min(kChunk, n - part * kChunk);     // in whole chunks: all
+    const int64_t t0 = int64_t(first) + part * kChunk, t = t0 + min(i, here - 1);
+    const uint16_t *k = a.k + t * a.ldk + kh * DK + 8 * g, *q = a.q + t * a.ldq + kh * DK + 8 * g;
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        x.k[s] = x.q[s] = u32x4{0, 0, 0, 0};
-        if (i < here) {
-          x.k[s] = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + 32 * s + 8 * g);
-          x.q[s] = *reinterpret_cast<const u32x4 *>(a.q + (t0 + i) * a.ldq + kh * DK + 32 * s + 8 * g);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint16_t *from = a.v + (t0 + row0 + e) * a.ldv + int64_t(h) * a.Dv + col;
-        x.v[e] = 0;
-        if (live && row0 + e < here) x.v[e] = CT == 2 ? *reinterpret_cast<const uint32_t *>(from) : *from;
-      }
-      x.grown = *reinterpret_cast<const f32x4 *>(decays + row0);
-      const u32x4 *T = reinterpret_cast<const u32x4 *>(head) + tri_at(wave, 0) * 64 + lane, *P = T + kTParts * kTriangle * 64;
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s >= pairs) break;                           // uniform
-#pragma unroll
-        for (int e = 0; e < kTParts; ++e) x.T[s][e] = T[(e * kTriangle + s) * 64];
-#pragma unroll
-        for (int e = 0; e < kPParts; ++e) x.P[s][e] = P[(e * kTriangle + s) * 64];
-      }
-      x.left = *reinterpret_cast<const f32x4 *>(decays + kChunk + row0);
+    for (int s = 0; s < NS; ++s) {
+      K[s] = *reinterpret_cast<const u32x4 *>(k + 32 * s);
+      Q[s] = *reinterpret_cast<const u32x4 *>(q + 32 * s);
     }
-    if (holds && !tree) {
-      const u32x4 *keys = reinterpret_cast<const u32x4 *>(a.keys + ((number + part) * a.Hk + kh) * key_bytes(DK)) + lane;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint16_t *v = a.v + (t0 + min(row0 + e, here - 1)) * a.ldv + vcol;
+      V[e] = CT == 2 ? *reinterpret_cast<const uint32_t *>(v) : *v;
+    }
+    grown = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + row0 * 4);
+    end = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + 2 * kChunk * 4);
+  };
+  // waves with one pair of columns bring it twice, so that all have asked for as much
+  auto fetch_solver = [&](int part) {
+    const u32x4 *from = reinterpret_cast<const u32x4 *>(head_of(part)) + tri_at(wave, 0) * 64 + lane;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int e = 0; e < kTParts; ++e) T[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
+    left = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + (kChunk + row0) * 4);
+  };
+  auto fetch_rest = [&](int part, bool chain) {
+    const u32x4 *from = reinterpret_cast<const u32x4 *>(head_of(part)) + (kTParts * kTriangle + tri_at(wave, 0)) * 64 + lane;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int e = 0; e < kPParts; ++e) P[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
+    if (chain) {
+      const u32x4 *kt = reinterpret_cast<const u32x4 *>(a.keys + ((number + part) * a.Hk + kh) * key_bytes(DK)) + lane;
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int s = 0; s < 2; ++s) x.keys[p][s] = keys[((2 * wave + p) * 2 + s) * 64];
+        for (int s = 0; s < 2; ++s) keys[p][s] = kt[((2 * (wave % NS) + p) * 2 + s) * 64];
     }
   };
-  Ops now;
-  fetch(0, now);
-  for (int part = 0; int64_t(part) * kChunk < n; ++part) {
-    const int64_t t0 = int64_t(first) + part * kChunk;
-    const int here = min(kChunk, n - part * kChunk);
-    const bool rows = 32 * (wave >> 1) < here;           // this wave has tokens
-    Ops next;
-    if (int64_t(part + 1) * kChunk < n) fetch(part + 1, next);
-    if (holds) {
+  auto share_state = [&] {                               // S in parts, as the second operand
+    if (!holds) return;
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        const float x[8] = {S[0][c][0], S[0][c][1], S[0][c][2], S[0][c][3], S[1][c][0], S[1][c][1], S[1][c][2], S[1][c][3]};
-        u32x4 o[3];
-        cut<3>(x, o);
+    for (int c = 0; c < CT; ++c) {
+      const float x[8] = {S[0][c][0], S[0][c][1], S[0][c][2], S[0][c][3], S[1][c][0], S[1][c][1], S[1][c][2], S[1][c][3]};
+      u32x4 o[3];
+      cut<3>(x, o);
 #pragma unroll
-        for (int e = 0; e < 3; ++e) s_S[e][c][wave][lane] = o[e];
-      }
+      for (int e = 0; e < 3; ++e) s_S[e][c][wave][lane] = o[e];
     }
+  };
+  fetch_rows(0);
+  fetch_solver(0);
+  share_state();
+  // One chunk.  Those before the last are whole and ask for the next one's operands, without
+  // branches around the loads: only then can each wait count what was asked for after it.
+  auto chunk = [&](int part, auto whole) {
+    constexpr bool more = decltype(whole)::value;
+    const int64_t t0 = int64_t(first) + part * kChunk;
+    const int here = more ? kChunk : n - part * kChunk;
+    const bool rows = more || 32 * (wave >> 1) < here;   // this wave has tokens
+    const float decay = end[0];
+    const uint64_t bad = __float_as_uint(end[2]) | uint64_t(__float_as_uint(end[3])) << 32;
     __syncthreads();
-    f32x4 ks[CT], o[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) ks[c] = o[c] = f32x4{0, 0, 0, 0};
-    const uint64_t bad = __float_as_uint(now.end[2]) | uint64_t(__float_as_uint(now.end[3])) << 32;
+    f32x4 o[CT];
     if (rows) {
+      f32x4 ks[CT];
+      u32x4 y[NS][CT][3];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) ks[c] = o[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          ks[c] = mfma(now.k[s], s_S[0][c][s][lane], ks[c]);
-          ks[c] = mfma(now.k[s], s_S[1][c][s][lane], ks[c]);
-          ks[c] = mfma(now.k[s], s_S[2][c][s][lane], ks[c]);
-          o[c] = mfma(now.q[s], s_S[0][c][s][lane], o[c]);
-          o[c] = mfma(now.q[s], s_S[1][c][s][lane], o[c]);
-        }
-      // R = V - exp(D) K S
-      const f32x4 grown = now.grown;
-      float v[4][2];
+        for (int e = 2; e >= 0; --e)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e][0] = lo_bf16(now.v[e]);
-        v[e][1] = hi_bf16(now.v[e]);
+          for (int c = 0; c < CT; ++c) y[s][c][e] = s_S[e][c][s][lane];
+      __builtin_amdgcn_sched_barrier(0);                 // every read on its way before the first product
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int e = 2; e >= 0; --e)
+#pragma unroll
+          for (int c = 0; c < CT; ++c) ks[c] = mfma(K[s], y[s][c][e], ks[c]);
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int e = 1; e >= 0; --e)
+#pragma unroll
+          for (int c = 0; c < CT; ++c) o[c] = mfma(Q[s], y[s][c][e], o[c]);
+      // R = V - exp(D) K S
+      float x[CT][4], sum = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          const float v = c ? hi_bf16(V[e]) : lo_bf16(V[e]);
+          sum += v;
+          x[c][e] = fmaf(-grown[e], ks[c][e], v);
+        }
+      const uint64_t none = bad | (here < kChunk ? ~uint64_t(0) << here : 0);
+      if (none || __any(!__builtin_isfinite(sum))) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            const bool off = none >> (row0 + e) & 1;
+            if (!off && !__builtin_isfinite(c ? hi_bf16(V[e]) : lo_bf16(V[e]))) {
+              atomicOr(&s_bad[CT * m + c][(row0 + e) >> 5], 1u << ((row0 + e) & 31));
+              s_some = 1;
+              x[c][e] = 0.0f;
+            }
+            if (off) x[c][e] = 0.0f;
+          }
       }
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[e] = fmaf(-grown[e], ks[c][e], v[e][c]);
-          if (!__builtin_isfinite(v[e][c])) {
-            atomicOr(&s_bad[CT * m + c][(row0 + e) >> 5], 1u << ((row0 + e) & 31));
-            s_some = 1;
-            x[e] = 0.0f;
-          }
-          if (bad >> (row0 + e) & 1) x[e] = 0.0f;
-          o[c][e] *= grown[e];
-        }
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
-          const u32x2 w = {upper(x[0], x[1]), upper(x[2], x[3])};
+          const u32x2 w = {upper(x[c][0], x[c][1]), upper(x[c][2], x[c][3])};
           reinterpret_cast<u32x2 *>(&s_R[e][c][wave >> 1][lane])[wave & 1] = w;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = below(x[j]);
+          for (int j = 0; j < 4; ++j) x[c][j] = below(x[c][j]);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[c][e] *= grown[e];
       }
     }
+    fetch_rest(part, more || !tree);
     __syncthreads();
-    uint64_t gone[CT];                                   // tokens that a column's results must not have seen
     const bool some = s_some || bad;
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-      gone[c] = some ? bad | s_bad[CT * m + c][0] | uint64_t(s_bad[CT * m + c][1]) << 32 : 0;
     if (rows) {                                          // U = T R
       f32x4 u[CT];
 #pragma unroll
       for (int c = 0; c < CT; ++c) u[c] = f32x4{0, 0, 0, 0};
+      auto solve = [&](auto two) {
+        constexpr int N = decltype(two)::value ? 2 : 1;
+        u32x4 x[N][CT][3];
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s >= pairs) break;
-        const u32x4 hi = now.T[s][0], mid = now.T[s][1], lo = now.T[s][2];
+        for (int s = 0; s < N; ++s)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          const u32x4 x = s_R[0][c][s][lane], y = s_R[1][c][s][lane], z = s_R[2][c][s][lane];
-          u[c] = mfma(lo, x, u[c]);
-          u[c] = mfma(mid, y, u[c]);
-          u[c] = mfma(hi, z, u[c]);
-          u[c] = mfma(mid, x, u[c]);
-          u[c] = mfma(hi, y, u[c]);
-          u[c] = mfma(hi, x, u[c]);
-        }
-      }
-      const f32x4 left = now.left;
+          for (int e = 0; e < 3; ++e)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) x[s][c][e] = s_R[e][c][s][lane];
+        __builtin_amdgcn_sched_barrier(0);
+        // what is below 2^-24 of the largest stays out: hi lo, mid mid, lo hi, hi mid, mid hi, hi hi
+        constexpr int of_T[6] = {2, 1, 0, 1, 0, 0}, of_R[6] = {0, 1, 2, 0, 1, 0};
+#pragma unroll
+        for (int j = 0; j < 6; ++j)
+#pragma unroll
+          for (int s = 0; s < N; ++s)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) u[c] = mfma(T[s][of_T[j]], x[s][c][of_R[j]], u[c]);
+      };
+      if (pairs == 2) solve(std::true_type());
+      else solve(std::false_type());
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
         float x[4], y[4];
@@ -669,67 +695,50 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
         }
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
-          const u32x2 w = {upper(x[0], x[1]), upper(x[2], x[3])}, z = {upper(y[0], y[1]), upper(y[2], y[3])};
-          if (e < 2) reinterpret_cast<u32x2 *>(&s_U[e][c][wave >> 1][lane])[wave & 1] = w;
+          const u32x2 z = {upper(y[0], y[1]), upper(y[2], y[3])};
           reinterpret_cast<u32x2 *>(&s_W[e][c][wave >> 1][lane])[wave & 1] = z;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            x[j] = below(x[j]);
-            y[j] = below(y[j]);
-          }
+          for (int j = 0; j < 4; ++j) y[j] = below(y[j]);
         }
+        const u32x2 hi = {upper(x[0], x[1]), upper(x[2], x[3])};
+        const u32x2 lo = {pack_bf16(below(x[0]), below(x[1])), pack_bf16(below(x[2]), below(x[3]))};
+        reinterpret_cast<u32x2 *>(&s_U[0][c][wave >> 1][lane])[wave & 1] = hi;
+        reinterpret_cast<u32x2 *>(&s_U[1][c][wave >> 1][lane])[wave & 1] = lo;
       }
     }
+    if constexpr (more) fetch_rows(part + 1);
     __syncthreads();
-    if (rows) {                                          // out = scale (exp(D) Q S + P U)
+    uint64_t gone[CT];                                   // tokens that a column's results must not have seen
+    if (some) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s >= pairs) break;
-        const u32x4 hi = now.P[s][0], lo = now.P[s][1];
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          o[c] = mfma(lo, s_U[0][c][s][lane], o[c]);
-          o[c] = mfma(hi, s_U[1][c][s][lane], o[c]);
-          o[c] = mfma(hi, s_U[0][c][s][lane], o[c]);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float x[CT];
-#pragma unroll
-        for (int c = 0; c < CT; ++c) x[c] = a.scale * o[c][e];
-        if (some) {
-          const int i = row0 + e;
-          const uint64_t own = uint64_t(1) << i, upto = own | (own - 1);
-          const uint64_t seen = tree ? ((i < here ? a.tree_mask[t0 + i] : 0) | own) & upto : upto;
-#pragma unroll
-          for (int c = 0; c < CT; ++c)
-            if (seen & gone[c]) x[c] = __builtin_nanf("");
-        }
-        if (live && row0 + e < here) store(t0 + row0 + e, x);
-      }
+      for (int c = 0; c < CT; ++c) gone[c] = bad | s_bad[CT * m + c][0] | uint64_t(s_bad[CT * m + c][1]) << 32;
     }
     if (holds && !tree) {                                // S = exp(D_last) S + K^T (exp(D_last - D) U)
-      const float end = now.end[0];
-      const int half = here > 32 ? 2 : 1;
+      auto advance = [&](auto two) {
+        constexpr int N = decltype(two)::value ? 2 : 1;
+        u32x4 x[N][CT][3];
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+        for (int s = 0; s < N; ++s)
 #pragma unroll
-        for (int c = 0; c < CT; ++c) S[p][c] *= end;
+          for (int e = 2; e >= 0; --e)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        if (s >= half) break;
+            for (int c = 0; c < CT; ++c) x[s][c][e] = s_W[e][c][s][lane];
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-          const u32x4 kt = now.keys[p][s];
+        for (int p = 0; p < 2; ++p)
 #pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            S[p][c] = mfma(kt, s_W[2][c][s][lane], S[p][c]);
-            S[p][c] = mfma(kt, s_W[1][c][s][lane], S[p][c]);
-            S[p][c] = mfma(kt, s_W[0][c][s][lane], S[p][c]);
-          }
-        }
-      }
+          for (int c = 0; c < CT; ++c) S[p][c] *= decay;
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < N; ++s)
+#pragma unroll
+          for (int e = 2; e >= 0; --e)
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+              for (int p = 0; p < 2; ++p) S[p][c] = mfma(keys[p][s], x[s][c][e], S[p][c]);
+      };
+      if (here > 32) advance(std::true_type());
+      else advance(std::false_type());
       if (some) {
 #pragma unroll
         for (int p = 0; p < 2; ++p)
@@ -738,9 +747,57 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(const DeltaArgs a)
             if (gone[c]) S[p][c] = S[p][c] + __builtin_nanf("");
       }
     }
-    now = next;
-  }
-  if (holds && live && !tree) {
+    if (rows) {                                          // out = scale (exp(D) Q S + P U)
+      auto add = [&](auto two) {
+        constexpr int N = decltype(two)::value ? 2 : 1;
+        u32x4 x[N][CT][2];
+#pragma unroll
+        for (int s = 0; s < N; ++s)
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[s][c][e] = s_U[e][c][s][lane];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < N; ++s) {
+#pragma unroll
+          for (int c = 0; c < CT; ++c) o[c] = mfma(P[s][1], x[s][c][0], o[c]);
+#pragma unroll
+          for (int c = 0; c < CT; ++c) o[c] = mfma(P[s][0], x[s][c][1], o[c]);
+#pragma unroll
+          for (int c = 0; c < CT; ++c) o[c] = mfma(P[s][0], x[s][c][0], o[c]);
+        }
+      };
+      if (pairs == 2) add(std::true_type());
+      else add(std::false_type());
+    }
+    if constexpr (more) share_state();
+    if (rows) {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) o[c] *= a.scale;
+      if (some) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = row0 + e;
+          const uint64_t own = uint64_t(1) << j, upto = own | (own - 1);
+          const uint64_t seen = tree ? ((j < here ? a.tree_mask[t0 + j] : 0) | own) & upto : upto;
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+            if (seen & gone[c]) o[c][e] = __builtin_nanf("");
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x[2] = {o[0][e], o[CT - 1][e]};
+        if (more || row0 + e < here) store(t0 + row0 + e, x);
+      }
+    }
+    if constexpr (more) fetch_solver(part + 1);
+  };
+  const int last = (n - 1) / kChunk;
+  for (int part = 0; part < last; ++part) chunk(part, std::true_type());
+  chunk(last, std::false_type());
+  if (holds && !tree) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -767,7 +824,7 @@ hipError_t run(DeltaArgs a, bool chunks, hipStream_t stream) {
   }
   hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(unsigned(chunks_of(a.T, a.R)), unsigned((a.Hv + 3) / 4)), dim3(kThreads), 0, stream, a);
   if (hipError_t e = hipGetLastError()) return e;
-  const int64_t grid = int64_t(a.R) * a.Hv * ((a.Dv + 31) / 32);
+  const int64_t grid = (int64_t(a.R) * a.Hk + 7) / 8 * 8 * a.G * ((a.Dv + 31) / 32);
   hipLaunchKernelGGL((delta_scan_kernel<DK, 2>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a);
   set_last_kernel("delta_scan");
   return hipGetLastError();
