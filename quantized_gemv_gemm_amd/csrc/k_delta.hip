@@ -474,17 +474,22 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
   }
 }
 
-// A workgroup walks the chunks of one request, head and 16 CT columns.  Wave w takes row tile
-// w of the chunk's tokens and, of the state, the rows 32 w .. 32 w + 31 (a pair of tiles).
-// Column m of tile c is column CT m + c: a lane's columns are neighbours.
+// A workgroup walks the chunks of one request, head and 16 CT columns.  Wave w of the first
+// four takes row tile w of the chunk's tokens and, of the state, the rows 32 w .. 32 w + 31 (a
+// pair of tiles), and goes the chain from one chunk's state to the next one's: K S, U, K^T U.
+// Wave 4 + w makes the results of row tile w beside it.  Column m of tile c is column CT m + c:
+// a lane's columns are neighbours.
+constexpr int kScanThreads = 512;
+
 template <int DK, int CT>
-__global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs a) {
+__global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const DeltaArgs a) {
   constexpr int NS = DK / 32;
   static_assert(NS <= 4, "a wave holds at most one pair of state tiles");
   __shared__ __attribute__((aligned(16))) u32x4 s_S[3][CT][NS][64], s_R[3][CT][2][64], s_U[2][CT][2][64], s_W[3][CT][2][64];
   __shared__ uint32_t s_bad[16 * CT][2];                 // of each column: tokens whose v is not finite
   __shared__ int s_some;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int all_waves = __builtin_amdgcn_readfirstlane(tid >> 6), wave = all_waves & 3;  // uniform: barriers follow
   const int blocks = (a.Dv + 16 * CT - 1) / (16 * CT);
   // Workgroups go to the 8 L2s in turn: those of one key head, which read the same K, Q, T and P,
   // are 8 numbers apart.
@@ -507,10 +512,124 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
   };
   if (srow < 0) {
     const float zero[2] = {0.0f, 0.0f};
-    for (int i = 4 * wave + g; i < n; i += 16) store(int64_t(first) + i, zero);
+    for (int i = 4 * all_waves + g; i < n; i += 32) store(int64_t(first) + i, zero);
     return;
   }
   const bool tree = a.tree_mask && n <= kTreeNodes, fresh = a.kv_lens[r] <= n;
+  const int64_t number = int64_t(first) / kChunk + r;
+  const int row0 = 32 * (wave >> 1) + 8 * g + 4 * (wave & 1), pairs = (wave >> 1) + 1, i = dealt(wave, m);
+  const int last = (n - 1) / kChunk;
+  auto head_of = [&](int part) { return a.heads + ((number + part) * a.Hv + h) * kHeadBytes; };
+  // tokens that a column's results, and the state after them, must not have seen
+  auto not_finite = [&](uint64_t bad, uint64_t (&gone)[CT]) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c) gone[c] = bad | s_bad[CT * m + c][0] | uint64_t(s_bad[CT * m + c][1]) << 32;
+  };
+  auto word_of = [](const f32x4 &end) { return __float_as_uint(end[2]) | uint64_t(__float_as_uint(end[3])) << 32; };
+
+  if (all_waves >= 4) {                                  // out = scale (exp(D) Q S + P U)
+    u32x4 Q[NS], P[2][kPParts];
+    f32x4 grown, end;
+    const uint16_t *to_q;
+    auto row_of = [&](int part) {
+      const int most = min(kChunk, n - part * kChunk) - 1;
+      to_q = a.q + (int64_t(first) + part * kChunk + min(i, most)) * a.ldq + kh * DK + 8 * g;
+    };
+    auto fetch_row = [&](int part) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) Q[s] = *reinterpret_cast<const u32x4 *>(to_q + 32 * s);
+      grown = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + row0 * 4);
+      end = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + 2 * kChunk * 4);
+    };
+    auto fetch_weights = [&](int part) {
+      const u32x4 *from = reinterpret_cast<const u32x4 *>(head_of(part)) + (kTParts * kTriangle + tri_at(wave, 0)) * 64 + lane;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int e = 0; e < kPParts; ++e) P[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
+    };
+    row_of(0);
+    fetch_row(0);
+    fetch_weights(0);
+    auto chunk = [&](int part, auto whole) {
+      constexpr bool more = decltype(whole)::value;
+      const int64_t t0 = int64_t(first) + part * kChunk;
+      const int here = more ? kChunk : n - part * kChunk;
+      const bool rows = more || 32 * (wave >> 1) < here;
+      const uint64_t bad = word_of(end);
+      f32x4 o[CT];
+      __syncthreads();
+      if (rows) {
+        u32x4 y[NS][CT][2];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) o[c] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int e = 1; e >= 0; --e)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) y[s][c][e] = s_S[e][c][s][lane];
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+          for (int e = 1; e >= 0; --e)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) o[c] = mfma(Q[s], y[s][c][e], o[c]);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[c][e] *= grown[e];
+      }
+      __syncthreads();
+      if constexpr (more) {
+        if (n - part * kChunk >= 2 * kChunk) to_q += kChunk * a.ldq;
+        else row_of(part + 1);
+        fetch_row(part + 1);
+      }
+      __syncthreads();
+      if (rows) {
+        auto add = [&](auto two) {
+          constexpr int N = decltype(two)::value ? 2 : 1;
+#pragma unroll
+          for (int s = 0; s < N; ++s)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+              const u32x4 x = s_U[0][c][s][lane], y = s_U[1][c][s][lane];
+              o[c] = mfma(P[s][1], x, o[c]);
+              o[c] = mfma(P[s][0], y, o[c]);
+              o[c] = mfma(P[s][0], x, o[c]);
+            }
+        };
+        if (pairs == 2) add(std::true_type());
+        else add(std::false_type());
+#pragma unroll
+        for (int c = 0; c < CT; ++c) o[c] *= a.scale;
+        if (s_some || bad) {
+          uint64_t gone[CT];
+          not_finite(bad, gone);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = row0 + e;
+            const uint64_t own = uint64_t(1) << j, upto = own | (own - 1);
+            const uint64_t seen = tree ? ((j < here ? a.tree_mask[t0 + j] : 0) | own) & upto : upto;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+              if (seen & gone[c]) o[c][e] = __builtin_nanf("");
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x[2] = {o[0][e], o[CT - 1][e]};
+          if (more || row0 + e < here) store(t0 + row0 + e, x);
+        }
+      }
+      if constexpr (more) fetch_weights(part + 1);
+    };
+    for (int part = 0; part < last; ++part) chunk(part, std::true_type());
+    chunk(last, std::false_type());
+    return;
+  }
+
   float *state = a.state + ((int64_t(srow) * a.Hv + h) * DK + 32 * wave + 8 * g) * a.Dv + col;
   const bool holds = wave < NS;
   f32x4 S[2][CT];                                        // [p][c][e]: row 32 w + 8 g + 4 p + e
@@ -521,29 +640,25 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
 #pragma unroll
       for (int c = 0; c < CT; ++c) S[p][c][e] = holds && !fresh ? state[int64_t(4 * p + e) * a.Dv + c] : 0.0f;
 
-  const int64_t number = int64_t(first) / kChunk + r;
-  const int row0 = 32 * (wave >> 1) + 8 * g + 4 * (wave & 1), pairs = (wave >> 1) + 1, i = dealt(wave, m);
   // What a wave takes of a chunk.  Each piece is asked for as soon as the chunk before has used
   // it.  Rows past the last token are the last one's: nothing of theirs is kept.
-  u32x4 K[NS], Q[NS], T[2][kTParts], P[2][kPParts], keys[2][2];
+  u32x4 K[NS], T[2][kTParts], keys[2][2];
   uint32_t V[4];                                         // CT columns of a row
   f32x4 grown, left, end;                                // end: exp(D_last), nothing, a word of tokens
   const int vcol = h * a.Dv + col;
-  auto head_of = [&](int part) { return a.heads + ((number + part) * a.Hv + h) * kHeadBytes; };
+  const uint16_t *to_k, *to_v[4];                 // this lane's rows of the chunk that is asked for next
+  auto rows_of = [&](int part) {
+    const int most = min(kChunk, n - part * kChunk) - 1;
+    const int64_t t0 = int64_t(first) + part * kChunk, t = t0 + min(i, most);
+    to_k = a.k + t * a.ldk + kh * DK + 8 * g;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) to_v[e] = a.v + (t0 + min(row0 + e, most)) * a.ldv + vcol;
+  };
   auto fetch_rows = [&](int part) {
-    const int here = min(kChunk, n - part * kChunk);     // in whole chunks: all
-    const int64_t t0 = int64_t(first) + part * kChunk, t = t0 + min(i, here - 1);
-    const uint16_t *k = a.k + t * a.ldk + kh * DK + 8 * g, *q = a.q + t * a.ldq + kh * DK + 8 * g;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      K[s] = *reinterpret_cast<const u32x4 *>(k + 32 * s);
-      Q[s] = *reinterpret_cast<const u32x4 *>(q + 32 * s);
-    }
+    for (int s = 0; s < NS; ++s) K[s] = *reinterpret_cast<const u32x4 *>(to_k + 32 * s);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint16_t *v = a.v + (t0 + min(row0 + e, here - 1)) * a.ldv + vcol;
-      V[e] = CT == 2 ? *reinterpret_cast<const uint32_t *>(v) : *v;
-    }
+    for (int e = 0; e < 4; ++e) V[e] = CT == 2 ? *reinterpret_cast<const uint32_t *>(to_v[e]) : *to_v[e];
     grown = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + row0 * 4);
     end = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + 2 * kChunk * 4);
   };
@@ -556,19 +671,12 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
       for (int e = 0; e < kTParts; ++e) T[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
     left = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + (kChunk + row0) * 4);
   };
-  auto fetch_rest = [&](int part, bool chain) {
-    const u32x4 *from = reinterpret_cast<const u32x4 *>(head_of(part)) + (kTParts * kTriangle + tri_at(wave, 0)) * 64 + lane;
+  auto fetch_keys = [&](int part) {
+    const u32x4 *kt = reinterpret_cast<const u32x4 *>(a.keys + ((number + part) * a.Hk + kh) * key_bytes(DK)) + lane;
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int e = 0; e < kPParts; ++e) P[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
-    if (chain) {
-      const u32x4 *kt = reinterpret_cast<const u32x4 *>(a.keys + ((number + part) * a.Hk + kh) * key_bytes(DK)) + lane;
-#pragma unroll
-      for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int s = 0; s < 2; ++s) keys[p][s] = kt[((2 * (wave % NS) + p) * 2 + s) * 64];
-    }
+      for (int s = 0; s < 2; ++s) keys[p][s] = kt[((2 * (wave % NS) + p) * 2 + s) * 64];
   };
   auto share_state = [&] {                               // S in parts, as the second operand
     if (!holds) return;
@@ -581,6 +689,7 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
       for (int e = 0; e < 3; ++e) s_S[e][c][wave][lane] = o[e];
     }
   };
+  rows_of(0);
   fetch_rows(0);
   fetch_solver(0);
   share_state();
@@ -588,18 +697,16 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
   // branches around the loads: only then can each wait count what was asked for after it.
   auto chunk = [&](int part, auto whole) {
     constexpr bool more = decltype(whole)::value;
-    const int64_t t0 = int64_t(first) + part * kChunk;
     const int here = more ? kChunk : n - part * kChunk;
     const bool rows = more || 32 * (wave >> 1) < here;   // this wave has tokens
     const float decay = end[0];
-    const uint64_t bad = __float_as_uint(end[2]) | uint64_t(__float_as_uint(end[3])) << 32;
+    const uint64_t bad = word_of(end);
     __syncthreads();
-    f32x4 o[CT];
     if (rows) {
       f32x4 ks[CT];
       u32x4 y[NS][CT][3];
 #pragma unroll
-      for (int c = 0; c < CT; ++c) ks[c] = o[c] = f32x4{0, 0, 0, 0};
+      for (int c = 0; c < CT; ++c) ks[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
       for (int s = 0; s < NS; ++s)
 #pragma unroll
@@ -613,12 +720,6 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
         for (int e = 2; e >= 0; --e)
 #pragma unroll
           for (int c = 0; c < CT; ++c) ks[c] = mfma(K[s], y[s][c][e], ks[c]);
-#pragma unroll
-      for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int e = 1; e >= 0; --e)
-#pragma unroll
-          for (int c = 0; c < CT; ++c) o[c] = mfma(Q[s], y[s][c][e], o[c]);
       // R = V - exp(D) K S
       float x[CT][4], sum = 0.0f;
 #pragma unroll
@@ -653,11 +754,9 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
 #pragma unroll
           for (int j = 0; j < 4; ++j) x[c][j] = below(x[c][j]);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[c][e] *= grown[e];
       }
     }
-    fetch_rest(part, more || !tree);
+    if (more || !tree) fetch_keys(part);
     __syncthreads();
     const bool some = s_some || bad;
     if (rows) {                                          // U = T R
@@ -706,13 +805,17 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
         reinterpret_cast<u32x2 *>(&s_U[1][c][wave >> 1][lane])[wave & 1] = lo;
       }
     }
-    if constexpr (more) fetch_rows(part + 1);
-    __syncthreads();
-    uint64_t gone[CT];                                   // tokens that a column's results must not have seen
-    if (some) {
+    if constexpr (more) {
+      if (n - part * kChunk >= 2 * kChunk) {             // the next chunk is whole
+        to_k += kChunk * a.ldk;
 #pragma unroll
-      for (int c = 0; c < CT; ++c) gone[c] = bad | s_bad[CT * m + c][0] | uint64_t(s_bad[CT * m + c][1]) << 32;
+        for (int e = 0; e < 4; ++e) to_v[e] += kChunk * a.ldv;
+      } else {
+        rows_of(part + 1);
+      }
+      fetch_rows(part + 1);
     }
+    __syncthreads();
     if (holds && !tree) {                                // S = exp(D_last) S + K^T (exp(D_last - D) U)
       auto advance = [&](auto two) {
         constexpr int N = decltype(two)::value ? 2 : 1;
@@ -740,6 +843,8 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
       if (here > 32) advance(std::true_type());
       else advance(std::false_type());
       if (some) {
+        uint64_t gone[CT];
+        not_finite(bad, gone);
 #pragma unroll
         for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -747,54 +852,9 @@ __global__ __launch_bounds__(kThreads, 1) void delta_scan_kernel(const DeltaArgs
             if (gone[c]) S[p][c] = S[p][c] + __builtin_nanf("");
       }
     }
-    if (rows) {                                          // out = scale (exp(D) Q S + P U)
-      auto add = [&](auto two) {
-        constexpr int N = decltype(two)::value ? 2 : 1;
-        u32x4 x[N][CT][2];
-#pragma unroll
-        for (int s = 0; s < N; ++s)
-#pragma unroll
-          for (int c = 0; c < CT; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) x[s][c][e] = s_U[e][c][s][lane];
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int s = 0; s < N; ++s) {
-#pragma unroll
-          for (int c = 0; c < CT; ++c) o[c] = mfma(P[s][1], x[s][c][0], o[c]);
-#pragma unroll
-          for (int c = 0; c < CT; ++c) o[c] = mfma(P[s][0], x[s][c][1], o[c]);
-#pragma unroll
-          for (int c = 0; c < CT; ++c) o[c] = mfma(P[s][0], x[s][c][0], o[c]);
-        }
-      };
-      if (pairs == 2) add(std::true_type());
-      else add(std::false_type());
-    }
     if constexpr (more) share_state();
-    if (rows) {
-#pragma unroll
-      for (int c = 0; c < CT; ++c) o[c] *= a.scale;
-      if (some) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = row0 + e;
-          const uint64_t own = uint64_t(1) << j, upto = own | (own - 1);
-          const uint64_t seen = tree ? ((j < here ? a.tree_mask[t0 + j] : 0) | own) & upto : upto;
-#pragma unroll
-          for (int c = 0; c < CT; ++c)
-            if (seen & gone[c]) o[c][e] = __builtin_nanf("");
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x[2] = {o[0][e], o[CT - 1][e]};
-        if (more || row0 + e < here) store(t0 + row0 + e, x);
-      }
-    }
     if constexpr (more) fetch_solver(part + 1);
   };
-  const int last = (n - 1) / kChunk;
   for (int part = 0; part < last; ++part) chunk(part, std::true_type());
   chunk(last, std::false_type());
   if (holds && !tree) {
@@ -825,7 +885,7 @@ hipError_t run(DeltaArgs a, bool chunks, hipStream_t stream) {
   hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(unsigned(chunks_of(a.T, a.R)), unsigned((a.Hv + 3) / 4)), dim3(kThreads), 0, stream, a);
   if (hipError_t e = hipGetLastError()) return e;
   const int64_t grid = (int64_t(a.R) * a.Hk + 7) / 8 * 8 * a.G * ((a.Dv + 31) / 32);
-  hipLaunchKernelGGL((delta_scan_kernel<DK, 2>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a);
+  hipLaunchKernelGGL((delta_scan_kernel<DK, 2>), dim3(unsigned(grid)), dim3(kScanThreads), 0, stream, a);
   set_last_kernel("delta_scan");
   return hipGetLastError();
 }
