@@ -29,19 +29,19 @@ __device__ __forceinline__ Row8 widen(u32x4 w) {
 
 template <int W>
 __global__ __launch_bounds__(kMixerThreads) void short_conv_kernel(const ConvArgs a) {
-  const Piece p = find_piece<kRun>(a.q_start, a.R, a.T, int(blockIdx.x));
+  int part;
+  const Request p = find_piece<kRun>(a.q_start, a.kv_lens, a.slots, a.R, a.T, a.state_count, int(blockIdx.x), part);
   if (p.r < 0) return;
   const int c0 = (int(blockIdx.y) * kMixerThreads + threadIdx.x) * 8;
   if (c0 >= a.C) return;                                 // heads are whole: their lanes agree
-  const int i0 = p.part * kRun, count = min(kRun, p.n - i0);
+  const int i0 = part * kRun, count = min(kRun, p.n - i0);
   uint16_t *out = a.out + int64_t(p.first + i0) * a.ldo + c0;
-  const int row = state_row(a.kv_lens, a.slots, a.state_count, p.r);
-  if (row < 0) {
+  if (p.row < 0) {
     for (int i = 0; i < count; ++i) *reinterpret_cast<u32x4 *>(out + int64_t(i) * a.ldo) = u32x4{0, 0, 0, 0};
     return;
   }
-  const bool tree = a.tree_mask && p.n <= kTreeNodes, fresh = a.kv_lens[p.r] <= p.n;
-  uint16_t *state = a.state + int64_t(row) * (W - 1) * a.C + c0;
+  const bool tree = a.tree_mask && p.n <= kTreeNodes, fresh = p.fresh;
+  uint16_t *state = a.state + int64_t(p.row) * (W - 1) * a.C + c0;
   const uint16_t *x = a.x + int64_t(p.first) * a.ldx + c0;
   auto load_row = [&](int at) -> u32x4 {                 // token `at`, or for at < 0 the state's row at + W - 1
     if (at < 0 && fresh) return u32x4{0, 0, 0, 0};

@@ -32,6 +32,7 @@ namespace tl {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kThreads = kMixerThreads;
 constexpr int kChunk = 64;          // tokens of a chunk: a tree's most
@@ -51,11 +52,14 @@ __device__ __forceinline__ float below(float x) { return x - __uint_as_float(__f
 struct Gate {
   float g, b;
 };
-__device__ __forceinline__ Gate gate_of(const DeltaArgs &a, const float *pa, const float *pb, int64_t t, int h, int layer) {
-  const float x = pa[t * a.lda + h], y = pb[t * a.ldb + h];
+__device__ __forceinline__ Gate make_gate(const DeltaArgs &a, float x, float y, float a_log, float dt_bias) {
   if (!a.a_log) return {x, y};
-  const float z = x + a.dt_bias[int64_t(layer) * a.Hv + h];
-  return {-expf(a.a_log[int64_t(layer) * a.Hv + h]) * (z > 20.0f ? z : log1pf(expf(z))), 1.0f / (1.0f + expf(-y))};
+  const float z = x + dt_bias;
+  return {-expf(a_log) * (z > 20.0f ? z : log1pf(expf(z))), 1.0f / (1.0f + expf(-y))};
+}
+__device__ __forceinline__ Gate gate_of(const DeltaArgs &a, const float *pa, const float *pb, int64_t t, int h, int layer) {
+  const int64_t at = int64_t(layer) * a.Hv + h;
+  return make_gate(a, pa[t * a.lda + h], pb[t * a.ldb + h], a.a_log ? a.a_log[at] : 0.0f, a.a_log ? a.dt_bias[at] : 0.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -86,11 +90,10 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a,
   }
   r = id % a.R;
   layer = id / a.R;
-  if (!starts_rise(a.q_start, a.R, a.T)) return;
-  const int first = a.q_start[r], n = a.q_start[r + 1] - first;
-  if (n <= 0) return;
-  const int srow = state_row(a.kv_lens, a.slots, a.state_count, r);
-  const bool fresh = a.kv_lens[r] <= n;
+  const Request rq = request_of(a.q_start, a.kv_lens, a.slots, a.R, a.T, a.state_count, r);
+  if (rq.r < 0 || rq.n <= 0) return;
+  const int first = rq.first, n = rq.n, srow = rq.row;
+  const bool fresh = rq.fresh;
   const int col = cb * 32 + 4 * (lane & 7);
   const bool live = col < a.Dv;
   int count = n;
@@ -255,54 +258,49 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
   constexpr int NS = DK / 32, PITCH = kChunk + 4, WAVES = kThreads / 64;
   __shared__ __attribute__((aligned(16))) float s_A[WAVES][kChunk * PITCH];
   __shared__ double s_total[WAVES][kChunk];
-  __shared__ float s_b[WAVES][kChunk];
+  __shared__ __attribute__((aligned(16))) float s_b[WAVES][kChunk];
   __shared__ uint64_t s_seen[WAVES][kChunk];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, m = lane & 15, g = lane >> 4;
   const int number = blockIdx.x, h = int(blockIdx.y) * WAVES + wave, kh = h / a.G;
-  const Piece piece = find_piece<kChunk>(a.q_start, a.R, a.T, number);
-  if (h >= a.Hv || piece.r < 0 || state_row(a.kv_lens, a.slots, a.state_count, piece.r) < 0) return;
-  const int64_t t0 = int64_t(piece.first) + piece.part * kChunk;
-  const int n = min(kChunk, piece.n - piece.part * kChunk);
-  const bool tree = a.tree_mask && piece.n <= kTreeNodes;
+  int part;
+  const Request rq = find_piece<kChunk>(a.q_start, a.kv_lens, a.slots, a.R, a.T, a.state_count, number, part);
+  if (h >= a.Hv || rq.r < 0 || rq.row < 0) return;
+  const int64_t t0 = int64_t(rq.first) + part * kChunk;
+  const int n = min(kChunk, rq.n - part * kChunk);
+  const bool tree = a.tree_mask && rq.n <= kTreeNodes;
   char *head = a.heads + (int64_t(number) * a.Hv + h) * kHeadBytes;
   float *A = s_A[wave];
 
-  // K's rows as operands: tile t's row m is token dealt(t, m)
-  u32x4 k[4][NS];
+  // Everything is asked for at once.  A lane's token: gates, and what it sees
+  const int64_t tl = t0 + min(lane, n - 1);
+  float ga = a.a[tl * a.lda + h], gb = a.b[tl * a.ldb + h], g_log = 0.0f, g_bias = 0.0f;
+  uint64_t seen = ~uint64_t(0);
+  if (tree) seen = a.tree_mask[tl];
+  if (a.a_log) {
+    g_log = a.a_log[h];
+    g_bias = a.dt_bias[h];
+  }
+  // rows of K and Q as operands: tile t's row m is token dealt(t, m); past the last one it is the last
+  u32x4 k[4][NS], q[4][NS];
 #pragma unroll
-  for (int t = 0; t < 4; ++t)
+  for (int t = 0; t < 4; ++t) {
+    const int64_t i = t0 + min(dealt(t, m), n - 1);
+    const uint16_t *pk = a.k + i * a.ldk + kh * DK + 8 * g, *pq = a.q + i * a.ldq + kh * DK + 8 * g;
 #pragma unroll
     for (int c = 0; c < NS; ++c) {
-      const int i = dealt(t, m);
-      k[t][c] = u32x4{0, 0, 0, 0};
-      if (i < n) k[t][c] = *reinterpret_cast<const u32x4 *>(a.k + (t0 + i) * a.ldk + kh * DK + 32 * c + 8 * g);
+      k[t][c] = *reinterpret_cast<const u32x4 *>(pk + 32 * c);
+      q[t][c] = *reinterpret_cast<const u32x4 *>(pq + 32 * c);
     }
-  // a lane's token: gates, and what it sees
-  Gate gate = {0.0f, 0.0f};
-  if (lane < n) gate = gate_of(a, a.a, a.b, t0 + lane, h, 0);
+  }
+  Gate gate = make_gate(a, ga, gb, g_log, g_bias);
+  if (lane >= n) gate = {0.0f, 0.0f};
   const uint64_t own = uint64_t(1) << lane, upto = own | (own - 1);
-  const uint64_t seen = tree ? ((lane < n ? a.tree_mask[t0 + lane] : 0) | own) & upto : upto;
+  seen = lane < n ? (seen | own) & upto : 0;
   // exp of less is 0 either way, and sums of finite numbers can be subtracted
   if (gate.g < -1.0e4f) gate.g = -1.0e4f;
   const bool lost = !__builtin_isfinite(gate.g) || !__builtin_isfinite(gate.b);
   if (lost) gate = {0.0f, 0.0f};
   uint64_t bad = __ballot(lost);                         // tokens whose k, g or b is not finite
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    bool off = false;
-#pragma unroll
-    for (int c = 0; c < NS; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) off |= (k[t][c][e] & 0x7F80u) == 0x7F80u || (k[t][c][e] & 0x7F800000u) == 0x7F800000u;
-    uint64_t all = __ballot(off);
-    if (all == 0) continue;
-    all |= all >> 32;
-    all |= all >> 16;
-    for (int j = 0; j < 16; ++j) bad |= (all >> j & 1) << dealt(t, j);
-    if (all >> m & 1)
-#pragma unroll
-      for (int c = 0; c < NS; ++c) k[t][c] = u32x4{0, 0, 0, 0};
-  }
   double total = double(gate.g) * 1.4426950408889634;    // powers of two from here on
   if (!tree) {
 #pragma unroll
@@ -311,17 +309,34 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
       if (lane >= off) total += before;
     }
   } else {
-    const double mine = total;
+    const uint64_t mine = __builtin_bit_cast(uint64_t, total);
     total = 0.0;
     for (int j = 0; j < n; ++j) {
-      const double x = __shfl(mine, j, 64);
-      if (seen >> j & 1) total += x;
+      const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(mine), j), hi = __builtin_amdgcn_readlane(uint32_t(mine >> 32), j);
+      if (seen >> j & 1) total += __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
     }
   }
   s_total[wave][lane] = total;
   s_b[wave][lane] = gate.b;
   s_seen[wave][lane] = seen;
   const double end = __shfl(total, n - 1, 64);
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {                          // an exponent of all ones is what is not finite
+    u16x2 top = {0, 0};
+#pragma unroll
+    for (int c = 0; c < NS; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, k[t][c][e] & 0x7FFF7FFFu));
+    uint64_t all = __ballot(top[0] >= 0x7F80u || top[1] >= 0x7F80u);
+    if (all == 0) continue;
+    all |= all >> 32;
+    all |= all >> 16;
+    for (int j = 0; j < 16; ++j) bad |= (all >> j & 1) << dealt(t, j);
+    if (all >> m & 1)
+#pragma unroll
+      for (int c = 0; c < NS; ++c) k[t][c] = u32x4{0, 0, 0, 0};
+  }
   {
     float *to = reinterpret_cast<float *>(head + kDecays);
     to[lane] = lane < n ? __builtin_amdgcn_exp2f(float(total)) : 0.0f;
@@ -356,15 +371,9 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
   for (int t = 0; t < 4; ++t) {
     if (32 * (t >> 1) >= n) break;                       // uniform
     const int i = dealt(t, m);
-    u32x4 q[NS];
-#pragma unroll
-    for (int c = 0; c < NS; ++c) {
-      q[c] = u32x4{0, 0, 0, 0};
-      if (i < n) q[c] = *reinterpret_cast<const u32x4 *>(a.q + (t0 + i) * a.ldq + kh * DK + 32 * c + 8 * g);
-    }
     const double upto_i = s_total[wave][i];
     const float step = s_b[wave][i];
-    const uint64_t sees = i < n ? s_seen[wave][i] : 0;
+    const uint64_t sees = s_seen[wave][i];
 #pragma unroll
     for (int s = 0; s <= t >> 1; ++s) {
       float kk[8], qk[8];
@@ -374,7 +383,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
 #pragma unroll
         for (int c = 0; c < NS; ++c) {
           x = mfma(k[2 * s + p][c], k[t][c], x);
-          y = mfma(k[2 * s + p][c], q[c], y);
+          y = mfma(k[2 * s + p][c], q[t][c], y);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -382,12 +391,13 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
           qk[4 * p + e] = y[e];
         }
       }
+      const int j0 = 32 * s + 8 * g;
+      const uint32_t bits = uint32_t(sees >> j0);        // i's own bit is its highest
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int j = 32 * s + 8 * g + e;
-        const float decay = __builtin_amdgcn_exp2f(float(upto_i - s_total[wave][j]));
-        const bool on = sees >> j & 1;
-        kk[e] = on && j < i ? step * decay * kk[e] : 0.0f;
+        const float decay = __builtin_amdgcn_exp2f(float(upto_i - s_total[wave][j0 + e]));
+        const bool on = bits >> e & 1;
+        kk[e] = on && j0 + e < i ? step * decay * kk[e] : 0.0f;
         qk[e] = on ? decay * qk[e] : 0.0f;
       }
       f32x4 *to = reinterpret_cast<f32x4 *>(A + i * PITCH + 32 * s + 8 * g);
@@ -461,11 +471,11 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
 #pragma unroll
     for (int s = 0; s <= t >> 1; ++s) {
       float x[8];
+      const int j0 = 32 * s + 8 * g;
+      const f32x4 *row = reinterpret_cast<const f32x4 *>(A + i * PITCH + j0), *b = reinterpret_cast<const f32x4 *>(s_b[wave] + j0);
+      const f32x4 u[2] = {row[0], row[1]}, v[2] = {b[0], b[1]};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int j = 32 * s + 8 * g + e;
-        x[e] = j <= i ? A[i * PITCH + j] * s_b[wave][j] : 0.0f;
-      }
+      for (int e = 0; e < 8; ++e) x[e] = j0 + e <= i ? u[e >> 2][e & 3] * v[e >> 2][e & 3] : 0.0f;
       u32x4 part[kTParts];
       cut<kTParts>(x, part);
 #pragma unroll
@@ -499,12 +509,12 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   // a chain's state is NaN from such a token on, so the words need no clearing for later chunks
   if (tid < 32 * CT) s_bad[tid >> 1][tid & 1] = 0;
   if (tid == 0) s_some = 0;
-  if (!starts_rise(a.q_start, a.R, a.T)) return;
-  const int first = a.q_start[r], n = a.q_start[r + 1] - first;
-  if (n <= 0) return;
+  __syncthreads();
+  const Request rq = request_of(a.q_start, a.kv_lens, a.slots, a.R, a.T, a.state_count, r);
+  if (rq.r < 0 || rq.n <= 0) return;
+  const int first = rq.first, n = rq.n, srow = rq.row;
   // Past the last column a lane repeats the work of another one, value for value.
   const int own_col = 16 * CT * cb + CT * m, col = own_col < a.Dv ? own_col : own_col - 16;
-  const int srow = state_row(a.kv_lens, a.slots, a.state_count, r);
   auto store = [&](int64_t t, const float *o) {
     uint16_t *to = a.out + (t * a.Hv + h) * a.Dv + col;
     if constexpr (CT == 2) *reinterpret_cast<uint32_t *>(to) = pack_bf16(o[0], o[1]);
@@ -515,7 +525,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
     for (int i = 4 * all_waves + g; i < n; i += 32) store(int64_t(first) + i, zero);
     return;
   }
-  const bool tree = a.tree_mask && n <= kTreeNodes, fresh = a.kv_lens[r] <= n;
+  const bool tree = a.tree_mask && n <= kTreeNodes, fresh = rq.fresh;
   const int64_t number = int64_t(first) / kChunk + r;
   const int row0 = 32 * (wave >> 1) + 8 * g + 4 * (wave & 1), pairs = (wave >> 1) + 1, i = dealt(wave, m);
   const int last = (n - 1) / kChunk;
