@@ -63,93 +63,36 @@ __device__ __forceinline__ Gate gate_of(const DeltaArgs &a, const float *pa, con
 }
 
 // ---------------------------------------------------------------------------
-// Token by token.  A workgroup takes one request, head and 32 columns; a thread holds 4
+// Token by token.  256 threads take one request, head and 32 columns; a thread holds 4
 // columns of Dk / 32 rows.  S^T k and S^T q of the old state are summed together: the new
 // state's S^T q is exp(g) S^T q + (q k) u.
+template <int DK>
+struct StepShared {
+  float k[DK], q[DK], sum[4][8][9];
+};
+
+// tokens: the numbers in the request of the `count` tokens, or NULL for the first ones.  Every
+// thread of the workgroup calls it; those that are not `on` only pass the barriers.
 template <int DK, bool COMMIT>
-__global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a, int conv_groups) {
+__device__ __forceinline__ void step_request(const DeltaArgs &a, const Request &rq, int h, int layer, int col0, int count,
+                                             const int *tokens, StepShared<DK> &lds, bool on) {
   constexpr int N = DK / 32;
-  __shared__ float s_k[DK], s_q[DK];
-  __shared__ float s_sum[4][8][9];
-  __shared__ int s_token[kTreeNodes];
-  __shared__ int s_count;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int blocks = (a.Dv + 31) / 32;
-  int id = blockIdx.x;
-  const bool conv = COMMIT && id >= a.L * a.R * a.Hv * blocks;
-  int cb, h = 0, r, layer;
-  if (conv) {
-    id -= a.L * a.R * a.Hv * blocks;
-    cb = id % conv_groups;
-    id /= conv_groups;
-  } else {
-    cb = id % blocks;
-    id /= blocks;
-    h = id % a.Hv;
-    id /= a.Hv;
-  }
-  r = id % a.R;
-  layer = id / a.R;
-  const Request rq = request_of(a.q_start, a.kv_lens, a.slots, a.R, a.T, a.state_count, r);
-  if (rq.r < 0 || rq.n <= 0) return;
-  const int first = rq.first, n = rq.n, srow = rq.row;
-  const bool fresh = rq.fresh;
-  const int col = cb * 32 + 4 * (lane & 7);
-  const bool live = col < a.Dv;
-  int count = n;
-  if constexpr (COMMIT) {
-    if (srow < 0 || n > kTreeNodes) return;
-    if (wave == 0) {
-      const int most = min(min(max(a.accepted[r], 0), a.path_width), n);
-      const int at = lane < most ? a.path[int64_t(r) * a.path_width + lane] : -1;
-      const bool on = at >= 0 && at < n;
-      const uint64_t all = __ballot(on);
-      if (on) s_token[__popcll(all & ((uint64_t(1) << lane) - 1))] = at;
-      if (lane == 0) s_count = __popcll(all);
-    }
-    __syncthreads();
-    count = s_count;
-    if (count == 0) return;
-    if (conv) {                                          // the last rows of x along the branch
-      const int c = (cb * kThreads + tid) * 8, W = a.taps;
-      if (c >= a.C) return;
-      uint16_t *st = a.conv_state + (int64_t(layer) * a.state_count + srow) * (W - 1) * a.C + c;
-      const uint16_t *x = a.x + int64_t(layer) * a.x_layer + int64_t(first) * a.ldx + c;
-      u32x4 next[3];
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        next[j] = u32x4{0, 0, 0, 0};
-        const int back = count - (W - 1) + j;
-        if (j < W - 1) {
-          if (back >= 0) next[j] = *reinterpret_cast<const u32x4 *>(x + int64_t(s_token[back]) * a.ldx);
-          else if (!fresh) next[j] = *reinterpret_cast<const u32x4 *>(st + int64_t(back + W - 1) * a.C);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < 3; ++j)
-        if (j < W - 1) *reinterpret_cast<u32x4 *>(st + int64_t(j) * a.C) = next[j];
-      return;
-    }
-  } else if (srow < 0) {
-    if (live)
-      for (int i = wave * 8 + (lane >> 3); i < n; i += 32)
-        *reinterpret_cast<u32x2 *>(a.out + (int64_t(first + i) * a.Hv + h) * a.Dv + col) = u32x2{0, 0};
-    return;
-  }
-  const int kh = h / a.G;
-  float *state = a.state + ((int64_t(layer) * a.state_count + srow) * a.Hv + h) * DK * a.Dv + col;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6 & 3;
+  const int col = col0 + 4 * (lane & 7), kh = h / a.G;
+  const bool live = on && col < a.Dv;
+  float *state = a.state + ((int64_t(layer) * a.state_count + rq.row) * a.Hv + h) * DK * a.Dv + col;
   f32x4 S[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     S[i] = f32x4{0, 0, 0, 0};
-    if (!fresh && live) S[i] = *reinterpret_cast<const f32x4 *>(state + int64_t(32 * i + 8 * wave + (lane >> 3)) * a.Dv);
+    if (!rq.fresh && live) S[i] = *reinterpret_cast<const f32x4 *>(state + int64_t(32 * i + 8 * wave + (lane >> 3)) * a.Dv);
   }
   const uint16_t *pq = a.q, *pk = a.k + int64_t(layer) * a.k_layer, *pv = a.v + int64_t(layer) * a.v_layer;
   const float *pa = a.a + int64_t(layer) * a.a_layer, *pb = a.b + int64_t(layer) * a.b_layer;
   for (int i = 0; i < count; ++i) {
-    const int64_t t = first + (COMMIT ? s_token[i] : i);
-    if (tid < DK) s_k[tid] = bf16_bits_to_float(pk[t * a.ldk + kh * DK + tid]);
-    if (!COMMIT && tid >= 128 && tid < 128 + DK) s_q[tid - 128] = bf16_bits_to_float(pq[t * a.ldq + kh * DK + tid - 128]);
+    const int64_t t = rq.first + (tokens ? tokens[i] : i);
+    if (on && tid < DK) lds.k[tid] = bf16_bits_to_float(pk[t * a.ldk + kh * DK + tid]);
+    if (!COMMIT && on && tid >= 128 && tid < 128 + DK) lds.q[tid - 128] = bf16_bits_to_float(pq[t * a.ldq + kh * DK + tid - 128]);
     const Gate gate = gate_of(a, pa, pb, t, h, layer);
     u32x2 vw = {0, 0};
     if (live) vw = *reinterpret_cast<const u32x2 *>(pv + t * a.ldv + int64_t(h) * a.Dv + col);
@@ -162,11 +105,11 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a,
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const int row = 32 * j + 8 * wave + (lane >> 3);
-      kk[j] = s_k[row];
+      kk[j] = lds.k[row];
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[e] = fmaf(S[j][e], kk[j], sum[e]);
       if constexpr (!COMMIT) {
-        const float qq = s_q[row];
+        const float qq = lds.q[row];
 #pragma unroll
         for (int e = 0; e < 4; ++e) sum[4 + e] = fmaf(S[j][e], qq, sum[4 + e]);
         sum[8] = fmaf(kk[j], qq, sum[8]);
@@ -176,13 +119,13 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a,
     for (int e = 0; e < (COMMIT ? 4 : 9); ++e) {
 #pragma unroll
       for (int off = 8; off < 64; off <<= 1) sum[e] += __shfl_xor(sum[e], off, 64);
-      if (lane < 8) s_sum[wave][lane][e] = sum[e];
+      if (on && lane < 8) lds.sum[wave][lane][e] = sum[e];
     }
     __syncthreads();
     float u[4];
 #pragma unroll
     for (int e = 0; e < (COMMIT ? 4 : 9); ++e)
-      sum[e] = s_sum[0][lane & 7][e] + s_sum[1][lane & 7][e] + (s_sum[2][lane & 7][e] + s_sum[3][lane & 7][e]);
+      sum[e] = lds.sum[0][lane & 7][e] + lds.sum[1][lane & 7][e] + (lds.sum[2][lane & 7][e] + lds.sum[3][lane & 7][e]);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       u[e] = gate.b * (v[e] - decay * sum[e]);
@@ -202,6 +145,76 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a,
 #pragma unroll
     for (int i = 0; i < N; ++i)
       *reinterpret_cast<f32x4 *>(state + int64_t(32 * i + 8 * wave + (lane >> 3)) * a.Dv) = S[i];
+  }
+}
+
+template <int DK, bool COMMIT>
+__global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a, int conv_groups) {
+  __shared__ StepShared<DK> lds;
+  __shared__ int s_token[kTreeNodes];
+  __shared__ int s_count;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int blocks = (a.Dv + 31) / 32;
+  int id = blockIdx.x;
+  const bool conv = COMMIT && id >= a.L * a.R * a.Hv * blocks;
+  int cb, h = 0;
+  if (conv) {
+    id -= a.L * a.R * a.Hv * blocks;
+    cb = id % conv_groups;
+    id /= conv_groups;
+  } else {
+    cb = id % blocks;
+    id /= blocks;
+    h = id % a.Hv;
+    id /= a.Hv;
+  }
+  const int r = id % a.R, layer = id / a.R;
+  const Request rq = request_of(a.q_start, a.kv_lens, a.slots, a.R, a.T, a.state_count, r);
+  if (rq.r < 0 || rq.n <= 0) return;
+  const int first = rq.first, n = rq.n;
+  if constexpr (COMMIT) {
+    if (rq.row < 0 || n > kTreeNodes) return;
+    if (wave == 0) {
+      const int most = min(min(max(a.accepted[r], 0), a.path_width), n);
+      const int at = lane < most ? a.path[int64_t(r) * a.path_width + lane] : -1;
+      const bool on = at >= 0 && at < n;
+      const uint64_t all = __ballot(on);
+      if (on) s_token[__popcll(all & ((uint64_t(1) << lane) - 1))] = at;
+      if (lane == 0) s_count = __popcll(all);
+    }
+    __syncthreads();
+    const int count = s_count;
+    if (count == 0) return;
+    if (conv) {                                          // the last rows of x along the branch
+      const int c = (cb * kThreads + tid) * 8, W = a.taps;
+      if (c >= a.C) return;
+      uint16_t *st = a.conv_state + (int64_t(layer) * a.state_count + rq.row) * (W - 1) * a.C + c;
+      const uint16_t *x = a.x + int64_t(layer) * a.x_layer + int64_t(first) * a.ldx + c;
+      u32x4 next[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        next[j] = u32x4{0, 0, 0, 0};
+        const int back = count - (W - 1) + j;
+        if (j < W - 1) {
+          if (back >= 0) next[j] = *reinterpret_cast<const u32x4 *>(x + int64_t(s_token[back]) * a.ldx);
+          else if (!rq.fresh) next[j] = *reinterpret_cast<const u32x4 *>(st + int64_t(back + W - 1) * a.C);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 3; ++j)
+        if (j < W - 1) *reinterpret_cast<u32x4 *>(st + int64_t(j) * a.C) = next[j];
+      return;
+    }
+    step_request<DK, true>(a, rq, h, layer, cb * 32, count, s_token, lds, true);
+  } else {
+    if (rq.row < 0) {
+      const int col = cb * 32 + 4 * (lane & 7);
+      if (col < a.Dv)
+        for (int i = wave * 8 + (lane >> 3); i < n; i += 32)
+          *reinterpret_cast<u32x2 *>(a.out + (int64_t(first + i) * a.Hv + h) * a.Dv + col) = u32x2{0, 0};
+      return;
+    }
+    step_request<DK, false>(a, rq, h, 0, cb * 32, n, nullptr, lds, true);
   }
 }
 
@@ -240,11 +253,131 @@ __device__ __forceinline__ void cut(const float (&x)[8], u32x4 (&o)[PARTS]) {
   }
 }
 
+struct Eight {
+  float v[8];
+};
+__device__ __forceinline__ Eight both(f32x4 x, f32x4 y) { return {{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}}; }
+template <int PARTS>
+__device__ __forceinline__ void cut(const Eight &x, u32x4 (&o)[PARTS]) {
+  cut<PARTS>(x.v, o);
+}
+
 // What one lane wrote to LDS is there for the wave's other lanes (which need no barrier: a
 // wave's LDS instructions are executed in order).
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
+}
+
+// A token's part of a chunk: what it sees, its gate, and D (a power of two's exponent) up to it
+// and up to the last token.  Tokens whose gates are not finite are named in `lost` and count
+// as ones that do nothing; of tokens past the n there is nothing.
+struct Chunk64 {
+  double total, end;
+  float b;
+  uint64_t seen, lost;
+};
+struct GateRow {
+  float a, b, a_log, dt_bias;
+  uint64_t seen;
+};
+__device__ __forceinline__ GateRow ask_gates(const DeltaArgs &a, int64_t t0, int n, int h, int lane, bool tree) {
+  const int64_t t = t0 + min(lane, n - 1);
+  GateRow x = {a.a[t * a.lda + h], a.b[t * a.ldb + h], 0.0f, 0.0f, ~uint64_t(0)};
+  if (tree) x.seen = a.tree_mask[t];
+  if (a.a_log) {
+    x.a_log = a.a_log[h];
+    x.dt_bias = a.dt_bias[h];
+  }
+  return x;
+}
+__device__ __forceinline__ Chunk64 sum_gates(const DeltaArgs &a, const GateRow &x, int n, int lane, bool tree) {
+  Chunk64 c;
+  Gate gate = make_gate(a, x.a, x.b, x.a_log, x.dt_bias);
+  if (lane >= n) gate = {0.0f, 0.0f};
+  const uint64_t own = uint64_t(1) << lane, upto = own | (own - 1);
+  c.seen = lane < n ? (x.seen | own) & upto : 0;
+  // exp of less is 0 either way, and sums of finite numbers can be subtracted
+  if (gate.g < -1.0e4f) gate.g = -1.0e4f;
+  const bool lost = !__builtin_isfinite(gate.g) || !__builtin_isfinite(gate.b);
+  if (lost) gate = {0.0f, 0.0f};
+  c.lost = __ballot(lost);
+  c.b = gate.b;
+  c.total = double(gate.g) * 1.4426950408889634;
+  if (!tree) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double before = __shfl_up(c.total, off, 64);
+      if (lane >= off) c.total += before;
+    }
+  } else {
+    const uint64_t mine = __builtin_bit_cast(uint64_t, c.total);
+    c.total = 0.0;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(mine), j), hi = __builtin_amdgcn_readlane(uint32_t(mine >> 32), j);
+      if (c.seen >> j & 1) c.total += __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+    }
+  }
+  c.end = __shfl(c.total, n - 1, 64);
+  return c;
+}
+
+__device__ __forceinline__ Chunk64 tokens_of(const DeltaArgs &a, int64_t t0, int n, int h, int lane, bool tree) {
+  return sum_gates(a, ask_gates(a, t0, n, h, lane, tree), n, lane, tree);
+}
+
+// 8 values of k_i k_j and q_i k_j, j = j0 .., become those of A and P
+__device__ __forceinline__ void weigh(float (&kk)[8], float (&qk)[8], int i, int j0, uint64_t seen, float step, double total,
+                                      const double *totals) {
+  const uint32_t bits = uint32_t(seen >> j0);            // i's own bit is its highest
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float decay = __builtin_amdgcn_exp2f(float(total - totals[j0 + e]));
+    const bool on = bits >> e & 1;
+    kk[e] = on && j0 + e < i ? step * decay * kk[e] : 0.0f;
+    qk[e] = on ? decay * qk[e] : 0.0f;
+  }
+}
+
+// Column m of (I + D)^-1 for a strictly lower block D of 16 rows
+template <int PITCH>
+__device__ __forceinline__ void solve_block(const float *D, int m, float (&t)[16]) {
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    f32x4 d[4];
+#pragma unroll
+    for (int y = 0; y < x; y += 4) d[y / 4] = *reinterpret_cast<const f32x4 *>(D + x * PITCH + y);
+    float sum = x == m ? 1.0f : 0.0f;
+#pragma unroll
+    for (int y = 0; y < x; ++y) sum = fmaf(-d[y / 4][y & 3], t[y], sum);
+    t[x] = sum;
+    if (x % 4 == 3) __builtin_amdgcn_sched_barrier(0);   // four rows' reads at a time: registers
+  }
+}
+
+// 8 values of T's row i, columns j0 .., with the steps, in parts
+template <int PITCH>
+__device__ __forceinline__ void solver_row(const float *A, const float *steps, int i, int j0, u32x4 (&o)[kTParts]) {
+  const f32x4 *row = reinterpret_cast<const f32x4 *>(A + i * PITCH + j0), *b = reinterpret_cast<const f32x4 *>(steps + j0);
+  const f32x4 u[2] = {row[0], row[1]}, v[2] = {b[0], b[1]};
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = j0 + e <= i ? u[e >> 2][e & 3] * v[e >> 2][e & 3] : 0.0f;
+  cut<kTParts>(x, o);
+}
+
+// An operand of K transposed, 32 tokens of elements dealt(p, m) of 32, from the tokens' two row
+// tiles: times one-hot columns, which pick that element of every token.
+__device__ __forceinline__ u32x4 transposed(u32x4 lower, u32x4 higher, int p, int m, int g) {
+  u32x4 pick;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int d = dealt(p, m) - 8 * g - 2 * e;
+    pick[e] = d == 0 ? 0x3F80u : d == 1 ? 0x3F800000u : 0u;
+  }
+  const f32x4 zero = {0, 0, 0, 0};
+  const f32x4 x = mfma(lower, pick, zero), y = mfma(higher, pick, zero);
+  return u32x4{upper(x[0], x[1]), upper(x[2], x[3]), upper(y[0], y[1]), upper(y[2], y[3])};
 }
 
 // One wave makes T and P of one chunk and value head, and for the first head of a key head K
@@ -271,15 +404,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
   char *head = a.heads + (int64_t(number) * a.Hv + h) * kHeadBytes;
   float *A = s_A[wave];
 
-  // Everything is asked for at once.  A lane's token: gates, and what it sees
-  const int64_t tl = t0 + min(lane, n - 1);
-  float ga = a.a[tl * a.lda + h], gb = a.b[tl * a.ldb + h], g_log = 0.0f, g_bias = 0.0f;
-  uint64_t seen = ~uint64_t(0);
-  if (tree) seen = a.tree_mask[tl];
-  if (a.a_log) {
-    g_log = a.a_log[h];
-    g_bias = a.dt_bias[h];
-  }
+  // Everything is asked for at once, the gates first.
+  const GateRow row = ask_gates(a, t0, n, h, lane, tree);
   // rows of K and Q as operands: tile t's row m is token dealt(t, m); past the last one it is the last
   u32x4 k[4][NS], q[4][NS];
 #pragma unroll
@@ -292,34 +418,11 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
       q[t][c] = *reinterpret_cast<const u32x4 *>(pq + 32 * c);
     }
   }
-  Gate gate = make_gate(a, ga, gb, g_log, g_bias);
-  if (lane >= n) gate = {0.0f, 0.0f};
-  const uint64_t own = uint64_t(1) << lane, upto = own | (own - 1);
-  seen = lane < n ? (seen | own) & upto : 0;
-  // exp of less is 0 either way, and sums of finite numbers can be subtracted
-  if (gate.g < -1.0e4f) gate.g = -1.0e4f;
-  const bool lost = !__builtin_isfinite(gate.g) || !__builtin_isfinite(gate.b);
-  if (lost) gate = {0.0f, 0.0f};
-  uint64_t bad = __ballot(lost);                         // tokens whose k, g or b is not finite
-  double total = double(gate.g) * 1.4426950408889634;    // powers of two from here on
-  if (!tree) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double before = __shfl_up(total, off, 64);
-      if (lane >= off) total += before;
-    }
-  } else {
-    const uint64_t mine = __builtin_bit_cast(uint64_t, total);
-    total = 0.0;
-    for (int j = 0; j < n; ++j) {
-      const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(mine), j), hi = __builtin_amdgcn_readlane(uint32_t(mine >> 32), j);
-      if (seen >> j & 1) total += __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
-    }
-  }
-  s_total[wave][lane] = total;
-  s_b[wave][lane] = gate.b;
-  s_seen[wave][lane] = seen;
-  const double end = __shfl(total, n - 1, 64);
+  const Chunk64 mine = sum_gates(a, row, n, lane, tree);
+  uint64_t bad = mine.lost;                              // tokens whose k, g or b is not finite
+  s_total[wave][lane] = mine.total;
+  s_b[wave][lane] = mine.b;
+  s_seen[wave][lane] = mine.seen;
 #pragma unroll
   for (int t = 0; t < 4; ++t) {                          // an exponent of all ones is what is not finite
     u16x2 top = {0, 0};
@@ -339,29 +442,18 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
   }
   {
     float *to = reinterpret_cast<float *>(head + kDecays);
-    to[lane] = lane < n ? __builtin_amdgcn_exp2f(float(total)) : 0.0f;
-    to[kChunk + lane] = lane < n ? __builtin_amdgcn_exp2f(float(end - total)) : 0.0f;
+    to[lane] = lane < n ? __builtin_amdgcn_exp2f(float(mine.total)) : 0.0f;
+    to[kChunk + lane] = lane < n ? __builtin_amdgcn_exp2f(float(mine.end - mine.total)) : 0.0f;
     if (lane == 0) *reinterpret_cast<f32x4 *>(to + 2 * kChunk) =
-        f32x4{__builtin_amdgcn_exp2f(float(end)), 0.0f, __uint_as_float(uint32_t(bad)), __uint_as_float(uint32_t(bad >> 32))};
+        f32x4{__builtin_amdgcn_exp2f(float(mine.end)), 0.0f, __uint_as_float(uint32_t(bad)), __uint_as_float(uint32_t(bad >> 32))};
   }
-  // K transposed: times one-hot columns, which picks element dealt(t, m) of every token
   if (h % a.G == 0 && !tree) {
     u32x4 *to = reinterpret_cast<u32x4 *>(a.keys + (int64_t(number) * a.Hk + kh) * key_bytes(DK));
 #pragma unroll
-    for (int t = 0; t < DK / 16; ++t) {
-      u32x4 pick;
+    for (int t = 0; t < DK / 16; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int d = dealt(t & 1, m) - 8 * g - 2 * e;
-        pick[e] = d == 0 ? 0x3F80u : d == 1 ? 0x3F800000u : 0u;
-      }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const f32x4 zero = {0, 0, 0, 0};
-        const f32x4 x = mfma(k[2 * s][t >> 1], pick, zero), y = mfma(k[2 * s + 1][t >> 1], pick, zero);
-        to[(t * 2 + s) * 64 + lane] = u32x4{upper(x[0], x[1]), upper(x[2], x[3]), upper(y[0], y[1]), upper(y[2], y[3])};
-      }
-    }
+      for (int s = 0; s < 2; ++s)
+        to[(t * 2 + s) * 64 + lane] = transposed(k[2 * s][t >> 1], k[2 * s + 1][t >> 1], t & 1, m, g);
   }
   wave_sync();
 
@@ -391,15 +483,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
           qk[4 * p + e] = y[e];
         }
       }
-      const int j0 = 32 * s + 8 * g;
-      const uint32_t bits = uint32_t(sees >> j0);        // i's own bit is its highest
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float decay = __builtin_amdgcn_exp2f(float(upto_i - s_total[wave][j0 + e]));
-        const bool on = bits >> e & 1;
-        kk[e] = on && j0 + e < i ? step * decay * kk[e] : 0.0f;
-        qk[e] = on ? decay * qk[e] : 0.0f;
-      }
+      weigh(kk, qk, i, 32 * s + 8 * g, sees, step, upto_i, s_total[wave]);
       f32x4 *to = reinterpret_cast<f32x4 *>(A + i * PITCH + 32 * s + 8 * g);
       to[0] = f32x4{kk[0], kk[1], kk[2], kk[3]};
       to[1] = f32x4{kk[4], kk[5], kk[6], kk[7]};
@@ -417,13 +501,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
   if (g < tiles) {
     const float *D = A + 16 * g * PITCH + 16 * g;
     float t[16];
-#pragma unroll
-    for (int x = 0; x < 16; ++x) {
-      float sum = x == m ? 1.0f : 0.0f;
-#pragma unroll
-      for (int y = 0; y < x; ++y) sum = fmaf(-D[x * PITCH + y], t[y], sum);
-      t[x] = sum;
-    }
+    solve_block<PITCH>(D, m, t);
     float *to = A + 16 * g * PITCH + 16 * g + m;
 #pragma unroll
     for (int x = 0; x < 16; ++x) to[x * PITCH] = t[x];
@@ -470,14 +548,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
     const int i = dealt(t, m);
 #pragma unroll
     for (int s = 0; s <= t >> 1; ++s) {
-      float x[8];
-      const int j0 = 32 * s + 8 * g;
-      const f32x4 *row = reinterpret_cast<const f32x4 *>(A + i * PITCH + j0), *b = reinterpret_cast<const f32x4 *>(s_b[wave] + j0);
-      const f32x4 u[2] = {row[0], row[1]}, v[2] = {b[0], b[1]};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = j0 + e <= i ? u[e >> 2][e & 3] * v[e >> 2][e & 3] : 0.0f;
       u32x4 part[kTParts];
-      cut<kTParts>(x, part);
+      solver_row<PITCH>(A, s_b[wave], i, 32 * s + 8 * g, part);
 #pragma unroll
       for (int e = 0; e < kTParts; ++e) to[(e * kTriangle + tri_at(t, s)) * 64 + lane] = part[e];
     }
@@ -643,12 +715,19 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   float *state = a.state + ((int64_t(srow) * a.Hv + h) * DK + 32 * wave + 8 * g) * a.Dv + col;
   const bool holds = wave < NS;
   f32x4 S[2][CT];                                        // [p][c][e]: row 32 w + 8 g + 4 p + e
+  if (holds && !fresh) {
 #pragma unroll
-  for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < 2; ++p)
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int c = 0; c < CT; ++c) S[p][c][e] = holds && !fresh ? state[int64_t(4 * p + e) * a.Dv + c] : 0.0f;
+        for (int c = 0; c < CT; ++c) S[p][c][e] = state[int64_t(4 * p + e) * a.Dv + c];
+  } else {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) S[p][c] = f32x4{0, 0, 0, 0};
+  }
 
   // What a wave takes of a chunk.  Each piece is asked for as soon as the chunk before has used
   // it.  Rows past the last token are the last one's: nothing of theirs is kept.
@@ -877,19 +956,332 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   }
 }
 
-// Few tokens a request: token by token.
+// Drafted trees: a workgroup takes one request, value head and 128 columns, makes T and P in LDS
+// and uses them there, in one launch; a wave has 16 columns for all tokens, so K S, R and U
+// stay in its registers from product to product.  A longer request of the call, a chain, goes
+// token by token.
+constexpr int kFusedThreads = 512;
+
+template <int DK>
+__global__ __launch_bounds__(kFusedThreads, 4) void delta_tree_kernel(const DeltaArgs a) {
+  constexpr int NS = DK / 32, PITCH = kChunk + 4;
+  __shared__ u32x4 s_K[4][NS][64];
+  __shared__ u32x4 s_QT[kTParts * kTriangle * 64];       // Q's operands, then T's
+  __shared__ __attribute__((aligned(16))) float s_A[kChunk * PITCH];  // A, then T
+  __shared__ u32x4 s_P[kPParts * kTriangle * 64];
+  __shared__ f32x4 s_T[kTriangle][64];                   // T's blocks below the diagonal, as results lie
+  __shared__ double s_total[kChunk];
+  __shared__ __attribute__((aligned(16))) float s_b[kChunk], s_grown[kChunk];
+  __shared__ uint64_t s_seen[kChunk], s_bad[5];
+  static_assert(sizeof(s_QT) >= sizeof(s_K) && sizeof(s_K) >= sizeof(StepShared<DK>), "Q fits where T is");
+  const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int blocks = (a.Dv + 127) / 128;
+  int id = blockIdx.x;
+  const int cb = id % blocks;
+  id /= blocks;
+  const int h = id % a.Hv, kh = h / a.G;
+  const Request rq = request_of(a.q_start, a.kv_lens, a.slots, a.R, a.T, a.state_count, id / a.Hv);
+  if (rq.r < 0 || rq.n <= 0) return;
+  const int col0 = 128 * cb + 16 * wave, col = col0 < a.Dv ? col0 + m : m;
+  const bool cols = col0 < a.Dv;                         // uniform
+  uint16_t *out = a.out + (int64_t(rq.first) * a.Hv + h) * a.Dv + col;
+  if (rq.row < 0) {
+    if (cols)
+      for (int i = g; i < rq.n; i += 4) out[i * int64_t(a.Hv) * a.Dv] = 0;
+    return;
+  }
+  if (rq.n > kTreeNodes) {
+    StepShared<DK> *const lds = reinterpret_cast<StepShared<DK> *>(s_K);
+    for (int c = 0; c < 128 && 128 * cb + c < a.Dv; c += 32)
+      step_request<DK, false>(a, rq, h, 0, 128 * cb + c, rq.n, nullptr, *lds, tid < kThreads);
+    return;
+  }
+  const float *state = a.state + ((int64_t(rq.row) * a.Hv + h) * DK + 8 * g) * a.Dv + col;
+  const int64_t t0 = rq.first;
+  const int n = rq.n;
+  const bool wide = n > 32;                              // else the tokens of tiles 2 and 3 are not there
+  f32x4 S[2 * NS];                                       // tile t, e: row 32 (t / 2) + 8 g + 4 (t % 2) + e
+  if (cols && !rq.fresh) {
+#pragma unroll
+    for (int t = 0; t < 2 * NS; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] = state[int64_t(32 * (t >> 1) + 4 * (t & 1) + e) * a.Dv];
+  } else {
+#pragma unroll
+    for (int t = 0; t < 2 * NS; ++t) S[t] = f32x4{0, 0, 0, 0};
+  }
+  // K (four waves) and Q (the others) of row tile `rt`; past the last token it is the last one
+  const int rt = wave & 3;
+  if (wave == 7) {                                     // and the gates
+    const Chunk64 x = tokens_of(a, t0, n, h, lane, true);
+    s_total[lane] = x.total;
+    s_b[lane] = x.b;
+    s_seen[lane] = x.seen;
+    s_grown[lane] = lane < n ? __builtin_amdgcn_exp2f(float(x.total)) : 0.0f;
+    if (lane == 0) s_bad[4] = x.lost;
+  }
+  if (32 * (rt >> 1) < n) {
+    const int64_t i = t0 + min(dealt(rt, m), n - 1);
+    const uint16_t *from = (wave < 4 ? a.k + i * a.ldk : a.q + i * a.ldq) + kh * DK + 8 * g;
+    u32x4 k[NS];
+#pragma unroll
+    for (int c = 0; c < NS; ++c) k[c] = *reinterpret_cast<const u32x4 *>(from + 32 * c);
+    if (wave < 4) {
+      u16x2 top = {0, 0};                              // an exponent of all ones is what is not finite
+#pragma unroll
+      for (int c = 0; c < NS; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, k[c][e] & 0x7FFF7FFFu));
+      uint64_t all = __ballot(top[0] >= 0x7F80u || top[1] >= 0x7F80u), bad = 0;
+      if (all) {
+        all |= all >> 32;
+        all |= all >> 16;
+        for (int j = 0; j < 16; ++j) bad |= (all >> j & 1) << dealt(rt, j);
+        if (all >> m & 1)
+#pragma unroll
+          for (int c = 0; c < NS; ++c) k[c] = u32x4{0, 0, 0, 0};
+      }
+      if (lane == 0) s_bad[wave] = bad;
+    }
+    u32x4 *to = wave < 4 ? &s_K[rt][0][lane] : &s_QT[rt * NS * 64 + lane];
+#pragma unroll
+    for (int c = 0; c < NS; ++c) to[c * 64] = k[c];
+  } else if (wave < 4 && lane == 0) {
+    s_bad[wave] = 0;
+  }
+  __syncthreads();
+  const uint64_t bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3] | s_bad[4];
+
+  // A and P of row tile `wave`
+  if (wave < 4 && 32 * (wave >> 1) < n) {
+    u32x4 k[NS], q[NS];
+#pragma unroll
+    for (int c = 0; c < NS; ++c) {
+      k[c] = s_K[wave][c][lane];
+      q[c] = s_QT[(wave * NS + c) * 64 + lane];
+    }
+    const int i = dealt(wave, m);
+    for (int s = 0; s <= wave >> 1; ++s) {
+      float kk[8], qk[8];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < NS; ++c) {
+          const u32x4 kj = s_K[2 * s + p][c][lane];
+          x = mfma(kj, k[c], x);
+          y = mfma(kj, q[c], y);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          kk[4 * p + e] = x[e];
+          qk[4 * p + e] = y[e];
+        }
+      }
+      weigh(kk, qk, i, 32 * s + 8 * g, s_seen[i], s_b[i], s_total[i], s_total);
+      f32x4 *to = reinterpret_cast<f32x4 *>(s_A + i * PITCH + 32 * s + 8 * g);
+      to[0] = f32x4{kk[0], kk[1], kk[2], kk[3]};
+      to[1] = f32x4{kk[4], kk[5], kk[6], kk[7]};
+      u32x4 x[kPParts];
+      cut<kPParts>(qk, x);
+#pragma unroll
+      for (int e = 0; e < kPParts; ++e) s_P[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = x[e];
+    }
+  }
+  // K S and Q S of the wave's columns
+  f32x4 R[4], o[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) R[t] = o[t] = f32x4{0, 0, 0, 0};
+  if (cols) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      u32x4 y[3];
+      cut<3>(both(S[2 * s], S[2 * s + 1]), y);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (t >= 2 && !wide) break;                    // uniform
+        const u32x4 k = s_K[t][s][lane], q = s_QT[(t * NS + s) * 64 + lane];
+#pragma unroll
+        for (int e = 2; e >= 0; --e) {
+          R[t] = mfma(k, y[e], R[t]);
+          if (e < 2) o[t] = mfma(q, y[e], o[t]);
+        }
+      }
+    }
+  }
+  uint16_t V[4][4];                                    // rows of the four tiles
+  const int64_t ldv = a.ldv;
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + e;
+      V[t][e] = a.v[(t0 + min(i, n - 1)) * ldv + int64_t(h) * a.Dv + col];
+    }
+  __syncthreads();
+
+  // T: the diagonal blocks, a wave each, then those below, a diagonal after the other
+  const int tiles = wide ? 4 : 2;
+  if (wave < tiles) {
+    float t[16];
+    const float *D = s_A + 16 * wave * PITCH + 16 * wave;
+    solve_block<PITCH>(D, m, t);
+    wave_sync();
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+      if (x >> 2 == g) s_A[(16 * wave + x) * PITCH + 16 * wave + m] = t[x];
+  }
+  __syncthreads();
+  f32x4 own[3];
+#pragma unroll
+  for (int off = 1; off < 4; ++off) {
+    if (off >= tiles) break;                           // uniform
+    own[off - 1] = f32x4{0, 0, 0, 0};
+    if (wave + off < tiles) {
+      const int bi = wave + off, bj = wave;
+      f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0}, first;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) first[c] = s_A[(16 * bj + 4 * g + c) * PITCH + 16 * bj + m];
+      for (int b = bj; b < bi; ++b) {
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(s_A + (16 * bi + m) * PITCH + 16 * b + 4 * g);
+        const f32x4 u = b == bj ? first : s_T[b * (b - 1) / 2 + bj][lane];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x = __builtin_amdgcn_mfma_f32_16x16x4f32(w[c], u[c], x, 0, 0, 0);
+      }
+      const f32x4 w = *reinterpret_cast<const f32x4 *>(s_A + (16 * bi + m) * PITCH + 16 * bi + 4 * g);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) y = __builtin_amdgcn_mfma_f32_16x16x4f32(w[c], x[c], y, 0, 0, 0);
+      own[off - 1] = -y;
+      s_T[bi * (bi - 1) / 2 + bj][lane] = -y;
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int off = 1; off < 4; ++off)
+    if (off < tiles && wave + off < tiles)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) s_A[(16 * (wave + off) + 4 * g + c) * PITCH + 16 * wave + m] = own[off - 1][c];
+  __syncthreads();
+  if (wave < 4 && 32 * (wave >> 1) < n) {
+    const int i = dealt(wave, m);
+    for (int s = 0; s <= wave >> 1; ++s) {
+      u32x4 x[kTParts];
+      solver_row<PITCH>(s_A, s_b, i, 32 * s + 8 * g, x);
+#pragma unroll
+      for (int e = 0; e < kTParts; ++e) s_QT[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = x[e];
+    }
+  }
+  // R = V - exp(D) K S, in parts; what must not be seen counts as zero
+  uint64_t gone = bad;
+  u32x4 x[2][3];
+  if (cols) {
+    const uint64_t none = bad | (n < kChunk ? ~uint64_t(0) << n : 0);
+    float sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t >= 2 && !wide) break;
+      const f32x4 grown = *reinterpret_cast<const f32x4 *>(s_grown + 32 * (t >> 1) + 8 * g + 4 * (t & 1));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = bf16_bits_to_float(V[t][e]);
+        sum += v;
+        R[t][e] = fmaf(-grown[e], R[t][e], v);
+        o[t][e] *= grown[e];
+      }
+    }
+    if (none || __any(!__builtin_isfinite(sum))) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int i = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + e;
+          const bool off = none >> i & 1, lost = !__builtin_isfinite(bf16_bits_to_float(V[t][e]));
+          if (!off && lost) gone |= uint64_t(1) << i;
+          if (off || lost) R[t][e] = 0.0f;
+        }
+      gone |= __shfl_xor(gone, 16, 64);                // a column's four lanes
+      gone |= __shfl_xor(gone, 32, 64);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (s == 0 || wide) cut<3>(both(R[2 * s], R[2 * s + 1]), x[s]);
+  }
+  __syncthreads();
+  if (cols) {
+    f32x4 U[4];
+    constexpr int of_T[6] = {2, 1, 0, 1, 0, 0}, of_R[6] = {0, 1, 2, 0, 1, 0};
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      U[t] = f32x4{0, 0, 0, 0};
+      if (t >= 2 && !wide) continue;
+#pragma unroll
+      for (int s = 0; s <= t >> 1; ++s) {
+        u32x4 w[kTParts];
+#pragma unroll
+        for (int e = 0; e < kTParts; ++e) w[e] = s_QT[(e * kTriangle + tri_at(t, s)) * 64 + lane];
+#pragma unroll
+        for (int j = 0; j < 6; ++j) U[t] = mfma(w[of_T[j]], x[s][of_R[j]], U[t]);
+      }
+    }
+    // out = scale (exp(D) Q S + P U)
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+      if (s == 0 || wide) {
+        u32x4 u[2];
+        cut<2>(both(U[2 * s], U[2 * s + 1]), u);
+#pragma unroll
+        for (int t = 2 * s; t < 4; ++t) {
+          if (t >= 2 && !wide) break;
+          const u32x4 hi = s_P[tri_at(t, s) * 64 + lane], lo = s_P[(kTriangle + tri_at(t, s)) * 64 + lane];
+          o[t] = mfma(lo, u[0], o[t]);
+          o[t] = mfma(hi, u[1], o[t]);
+          o[t] = mfma(hi, u[0], o[t]);
+        }
+      }
+    if (__any(gone != 0)) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (gone & s_seen[32 * (t >> 1) + 8 * g + 4 * (t & 1) + e]) o[t][e] = __builtin_nanf("");
+    }
+    const int64_t out_row = int64_t(a.Hv) * a.Dv;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      if (t >= 2 && !wide) break;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + e;
+        if (i < n) out[i * out_row] = uint16_t(pack_bf16(a.scale * o[t][e], 0.0f));
+      }
+    }
+  }
+}
+
+// Which kernels take a call: one launch for trees, unless prompts' chunks come with them; token
+// by token for few tokens; chunks prepared beforehand for the rest.
 constexpr int64_t kStepTokens = 8;
-bool by_chunks(int64_t max_nodes, bool tree) { return tree || max_nodes > kStepTokens; }
+enum class Form { kStep, kTree, kScan };
+Form form_of(int64_t max_nodes, bool tree) {
+  if (tree && max_nodes <= kTreeNodes) return Form::kTree;
+  return max_nodes <= kStepTokens ? Form::kStep : Form::kScan;
+}
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 int64_t chunks_of(int64_t T, int64_t R) { return T / kChunk + R; }
 
 template <int DK>
-hipError_t run(DeltaArgs a, bool chunks, hipStream_t stream) {
+hipError_t run(DeltaArgs a, Form form, hipStream_t stream) {
   (void)hipGetLastError();
-  if (!chunks) {
-    const int64_t grid = int64_t(a.R) * a.Hv * ((a.Dv + 31) / 32);
-    hipLaunchKernelGGL((delta_step_kernel<DK, false>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a, 1);
+  const int64_t heads = int64_t(a.R) * a.Hv;
+  if (form == Form::kStep) {
+    hipLaunchKernelGGL((delta_step_kernel<DK, false>), dim3(unsigned(heads * ((a.Dv + 31) / 32))), dim3(kThreads), 0, stream, a, 1);
     set_last_kernel("delta_step");
+    return hipGetLastError();
+  }
+  if (form == Form::kTree) {
+    hipLaunchKernelGGL((delta_tree_kernel<DK>), dim3(unsigned(heads * ((a.Dv + 127) / 128))), dim3(kFusedThreads), 0, stream, a);
+    set_last_kernel("delta_tree");
     return hipGetLastError();
   }
   hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(unsigned(chunks_of(a.T, a.R)), unsigned((a.Hv + 3) / 4)), dim3(kThreads), 0, stream, a);
@@ -903,16 +1295,16 @@ hipError_t run(DeltaArgs a, bool chunks, hipStream_t stream) {
 }  // namespace
 
 size_t delta_workspace_bytes(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_t Dk, int64_t max_nodes, bool tree) {
-  if (!by_chunks(max_nodes, tree)) return 0;
+  if (form_of(max_nodes, tree) != Form::kScan) return 0;
   const size_t n = size_t(chunks_of(T, R));
   return up(n * size_t(Hk * G) * kHeadBytes) + n * size_t(Hk) * key_bytes(int(Dk));
 }
 
 hipError_t launch_delta_rule(DeltaArgs a, int64_t Dk, int64_t max_nodes, void *workspace, hipStream_t stream) {
-  const bool chunks = by_chunks(max_nodes, a.tree_mask != nullptr);
+  const Form form = form_of(max_nodes, a.tree_mask != nullptr);
   a.heads = static_cast<char *>(workspace);
   a.keys = a.heads + up(size_t(chunks_of(a.T, a.R)) * size_t(a.Hv) * kHeadBytes);
-  return Dk == 64 ? run<64>(a, chunks, stream) : run<128>(a, chunks, stream);
+  return Dk == 64 ? run<64>(a, form, stream) : run<128>(a, form, stream);
 }
 
 hipError_t launch_delta_commit(const DeltaArgs &a, int64_t Dk, hipStream_t stream) {

@@ -278,13 +278,13 @@ def _check_delta(got, got_state, want, want_state, size, before, tokens):
             assert miss <= STATE_TOL * np.linalg.norm(want_state[row]), (row, miss / np.linalg.norm(want_state[row]))
 
 
-@pytest.mark.parametrize("form", ["step", "chunks", "trees"])
+@pytest.mark.parametrize("form", ["step", "chunks", "trees", "trees and chunks"])
 @pytest.mark.parametrize("lens", LENGTHS, ids=str)
 @pytest.mark.parametrize("Hk,G,Dk,Dv,raw", [(1, 1, 64, 16, False), (2, 3, 128, 128, True), (3, 1, 64, 80, True), (1, 4, 128, 48, False)])
 def test_delta_rule(tl, torch, Hk, G, Dk, Dv, raw, lens, form):
     announce(f"delta_rule {form} Hk={Hk} G={G} Dk={Dk} Dv={Dv} raw={raw} lens={lens}")
     d, rng = dev(), np.random.default_rng(sum(lens) + Dk + Dv + G)
-    s = Step(np.array(lens), rng, trees=form == "trees")
+    s = Step(np.array(lens), rng, trees="trees" in form)
     plain, given, gates, state = _delta_inputs(s, Hk, G, Dk, Dv, rng, raw, d)
     free = np.setdiff1d(np.arange(s.states), s.slots)
     state[free[0]] = np.nan                               # a row that nobody reads
@@ -293,23 +293,23 @@ def test_delta_rule(tl, torch, Hk, G, Dk, Dv, raw, lens, form):
             state[s.slots[r]] = np.inf
     stated = to_dev(state, d)
     out = torch.full((s.T, Hk * G, Dv), -7.0, dtype=torch.bfloat16, device=d)
-    tl.delta_rule(*given, *s.dev(d), stated, **gates, tree_mask=s.mask_dev(d), max_nodes=1 if form == "step" else 1000, out=out)
+    tl.delta_rule(*given, *s.dev(d), stated, **gates, tree_mask=s.mask_dev(d), max_nodes={"step": 1, "chunks": 1000, "trees": 64, "trees and chunks": 130}[form], out=out)
     torch.cuda.synchronize()
-    assert tl.last_kernel_name() == ("delta_step" if form == "step" else "delta_scan")
+    assert tl.last_kernel_name() == {"step": "delta_step", "trees": "delta_tree"}.get(form, "delta_scan")
     want, after, size = ref.delta_rule(*plain, s.q_start, s.kv_lens, s.slots, state.astype(np.float64), s.mask, Dk ** -0.5,
                                        np.full((s.T, Hk * G, Dv), -7.0))
     _check_delta(f64(out), stated.cpu().numpy(), want, after, size, state, s.q_start[-1])
 
 
-@pytest.mark.parametrize("form", ["step", "chunks", "trees"])
+@pytest.mark.parametrize("form", ["step", "chunks", "trees", "trees and chunks"])
 @pytest.mark.parametrize("kind", ["resets", "far", "same keys", "no steps", "kept"])
 def test_delta_rule_extremes(tl, torch, kind, form):
     """Decays of exp(-inf) and far below any exponent between ordinary ones, the same key again and again with a step
     of one (the solved system at its worst), steps of zero, and no decay at all."""
     announce(f"delta_rule extremes {kind} {form}")
     d, rng = dev(), np.random.default_rng(11)
-    lens = [64, 40, 1] if form == "trees" else [150, 64, 1]
-    s = Step(np.array(lens), rng, trees=form == "trees")
+    lens = [64, 40, 1] if "trees" in form else [150, 64, 1]
+    s = Step(np.array(lens), rng, trees="trees" in form)
     (q, k, v, g, b), (qd, kd, vd, ad, bd), _, state = _delta_inputs(s, 2, 2, 64, 32, rng, False, d)
     if kind == "resets":
         g[::7] = -np.inf
@@ -326,7 +326,7 @@ def test_delta_rule_extremes(tl, torch, kind, form):
     stated = to_dev(state, d)
     out = torch.full((s.T, 4, 32), -7.0, dtype=torch.bfloat16, device=d)
     tl.delta_rule(qd, bf16_dev(k, d), vd, to_dev(g, d), to_dev(b, d), *s.dev(d), stated, tree_mask=s.mask_dev(d),
-                  max_nodes=1 if form == "step" else 64, out=out)
+                  max_nodes={"step": 1, "trees and chunks": 100}.get(form, 64), out=out)
     torch.cuda.synchronize()
     want, after, size = ref.delta_rule(q, k, v, g.astype(np.float64), b.astype(np.float64), s.q_start, s.kv_lens, s.slots,
                                        state.astype(np.float64), s.mask, 0.125, np.full((s.T, 4, 32), -7.0))
@@ -339,15 +339,15 @@ def test_delta_rule_not_finite_stays_where_it_is(tl, torch):
     announce("delta_rule with NaN and infinities beside")
     d, rng = dev(), np.random.default_rng(5)
     for form in ("step", "chunks", "trees"):
-        s = Step(np.array([20, 40, 33]), rng, behind=64, trees=form == "trees")
-        if form == "trees":                               # request 1: two chains from the root, 1..19 and 20..39
+        s = Step(np.array([20, 40, 33]), rng, behind=64, trees="trees" in form)
+        if "trees" in form:                               # request 1: two chains from the root, 1..19 and 20..39
             first = int(s.q_start[1])
             for i in range(40):
                 s.mask[first + i] = (1 << i + 1) - 1 if i < 20 else 1 | ((1 << i + 1) - 1 >> 20 << 20)
         plain, given, _, state = _delta_inputs(s, 1, 2, 128, 32, rng, False, d)
         bad = np.zeros(s.T, dtype=bool)
         bad[:20] = bad[93:] = True
-        if form == "trees":
+        if "trees" in form:
             bad[20 + 20:20 + 40] = True
         rows = torch.from_numpy(bad).to(d)
         q, k, v, a, b = (x.clone() for x in given)
@@ -355,11 +355,11 @@ def test_delta_rule_not_finite_stays_where_it_is(tl, torch):
             x[rows] = fill
         stated = to_dev(state, d)
         out = torch.full((s.T, 2, 32), -7.0, dtype=torch.bfloat16, device=d)
-        tl.delta_rule(q, k, v, a, b, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes=1 if form == "step" else 64, out=out)
+        tl.delta_rule(q, k, v, a, b, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes={"step": 1, "trees and chunks": 100}.get(form, 64), out=out)
         torch.cuda.synchronize()
         want, after, size = ref.delta_rule(*plain, s.q_start, s.kv_lens, s.slots, state.astype(np.float64), s.mask, 128 ** -0.5,
                                            np.full((s.T, 2, 32), -7.0))
-        if form == "trees":                               # no state is touched, whatever the tokens held
+        if "trees" in form:                               # no state is touched, whatever the tokens held
             np.testing.assert_array_equal(stated.cpu().numpy(), state)
         else:
             assert np.isnan(stated.cpu().numpy()[s.slots[0]]).all() == (s.kv_lens[0] > 0 and s.slots[0] >= 0)
@@ -400,21 +400,21 @@ def test_starts_that_fall_write_nothing(tl, torch, starts, op):
 
 
 @pytest.mark.parametrize("what", ["q", "k", "v", "a", "b"])
-@pytest.mark.parametrize("form", ["step", "chunks", "trees"])
+@pytest.mark.parametrize("form", ["step", "chunks", "trees", "trees and chunks"])
 def test_delta_rule_not_finite_later_tokens_only(tl, torch, form, what):
     """A token whose rows are not finite spoils its own result and those of the tokens that see it, and no other's."""
     announce(f"delta_rule with a {what} that is not finite, {form}")
     d, rng = dev(), np.random.default_rng(6)
-    s = Step(np.array([50 if form == "trees" else 150]), rng, trees=form == "trees")
+    s = Step(np.array([50 if "trees" in form else 150]), rng, trees="trees" in form)
     plain, given, _, state = _delta_inputs(s, 1, 2, 64, 32, rng, False, d)
-    at = 21 if form == "trees" else 90
+    at = 21 if "trees" in form else 90
     given = [x.clone() for x in given]
     j = "qkvab".index(what)
     given[j][at, 0] = float("nan") if what in "qa" else float("inf")
     if what == "v":
         given[j][at, 0, 3:] = given[j][at + 1, 0, 3:]      # columns 0 to 2 of head 0 only
     stated = to_dev(state, d)
-    out = tl.delta_rule(*given, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes=1 if form == "step" else 64)
+    out = tl.delta_rule(*given, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes={"step": 1, "trees and chunks": 100}.get(form, 64))
     torch.cuda.synchronize()
     v = plain[2].copy()
     if what == "v":
@@ -422,7 +422,7 @@ def test_delta_rule_not_finite_later_tokens_only(tl, torch, form, what):
     want, after, size = ref.delta_rule(plain[0], plain[1], v, *plain[3:], s.q_start, s.kv_lens, s.slots, state.astype(np.float64),
                                        s.mask, 0.125, np.zeros((s.T, 2, 32)))
     n = int(s.lens[0])
-    sees = np.array([at in line for line in ref.lines(n, form == "trees", s.mask)])
+    sees = np.array([at in line for line in ref.lines(n, "trees" in form, s.mask)])
     spoilt = np.zeros((n, 2, 32), dtype=bool)
     heads, cols = (slice(None), slice(None)) if what in "qk" else (0, slice(3)) if what == "v" else (0, slice(None))
     spoilt[(at if what == "q" else sees), heads, cols] = True
@@ -431,7 +431,7 @@ def test_delta_rule_not_finite_later_tokens_only(tl, torch, form, what):
     tol = BF16_HALF * np.abs(want[:n]) + (PARTS + STATE_TOL) * size[:n]
     assert (np.abs(got - want[:n])[~spoilt] <= tol[~spoilt]).all()
     row, S = s.slots[0], stated.cpu().numpy()
-    if form == "trees":
+    if "trees" in form:
         np.testing.assert_array_equal(S, state)
     elif what == "q":
         assert np.linalg.norm(S[row] - after[row]) <= STATE_TOL * np.linalg.norm(after[row])
