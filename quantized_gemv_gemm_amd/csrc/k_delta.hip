@@ -65,79 +65,124 @@ __device__ __forceinline__ Gate gate_of(const DeltaArgs &a, const float *pa, con
 // ---------------------------------------------------------------------------
 // Token by token.  256 threads take one request, head and 32 columns; a thread holds 4
 // columns of Dk / 32 rows.  S^T k and S^T q of the old state are summed together: the new
-// state's S^T q is exp(g) S^T q + (q k) u.
+// state's S^T q is exp(g) S^T q + (q k) u.  What 16 tokens bring is asked for at once, beside
+// the state, and passes through LDS; a token then costs one barrier.
+constexpr int kStepBatch = 16;
+
 template <int DK>
 struct StepShared {
-  float k[DK], q[DK], sum[4][8][9];
+  float k[kStepBatch][DK], q[kStepBatch][DK], v[kStepBatch][32], decay[kStepBatch], step[kStepBatch];
+  float sum[2][4][8][12];
 };
+
+// the sum over the lanes that differ in bits 3 to 5
+__device__ __forceinline__ float sum_rows(float x) {
+  x += __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x128, 0xF, 0xF, true));  // row_ror:8
+  const auto h = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(h[0]) + __uint_as_float(h[1]);
+  const auto w = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(w[0]) + __uint_as_float(w[1]);
+}
 
 // tokens: the numbers in the request of the `count` tokens, or NULL for the first ones.  Every
 // thread of the workgroup calls it; those that are not `on` only pass the barriers.
 template <int DK, bool COMMIT>
 __device__ __forceinline__ void step_request(const DeltaArgs &a, const Request &rq, int h, int layer, int col0, int count,
                                              const int *tokens, StepShared<DK> &lds, bool on) {
-  constexpr int N = DK / 32;
+  constexpr int N = DK / 32, P = DK / 8;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6 & 3;
   const int col = col0 + 4 * (lane & 7), kh = h / a.G;
   const bool live = on && col < a.Dv;
   float *state = a.state + ((int64_t(layer) * a.state_count + rq.row) * a.Hv + h) * DK * a.Dv + col;
   f32x4 S[N];
+  if (!rq.fresh && live) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    S[i] = f32x4{0, 0, 0, 0};
-    if (!rq.fresh && live) S[i] = *reinterpret_cast<const f32x4 *>(state + int64_t(32 * i + 8 * wave + (lane >> 3)) * a.Dv);
+    for (int i = 0; i < N; ++i) S[i] = *reinterpret_cast<const f32x4 *>(state + int64_t(32 * i + 8 * wave + (lane >> 3)) * a.Dv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) S[i] = f32x4{0, 0, 0, 0};
   }
-  const uint16_t *pq = a.q, *pk = a.k + int64_t(layer) * a.k_layer, *pv = a.v + int64_t(layer) * a.v_layer;
+  const uint16_t *pk = a.k + int64_t(layer) * a.k_layer + kh * DK, *pq = a.q + kh * DK;
+  const uint16_t *pv = a.v + int64_t(layer) * a.v_layer + int64_t(h) * a.Dv + col0;
   const float *pa = a.a + int64_t(layer) * a.a_layer, *pb = a.b + int64_t(layer) * a.b_layer;
-  for (int i = 0; i < count; ++i) {
-    const int64_t t = rq.first + (tokens ? tokens[i] : i);
-    if (on && tid < DK) lds.k[tid] = bf16_bits_to_float(pk[t * a.ldk + kh * DK + tid]);
-    if (!COMMIT && on && tid >= 128 && tid < 128 + DK) lds.q[tid - 128] = bf16_bits_to_float(pq[t * a.ldq + kh * DK + tid - 128]);
-    const Gate gate = gate_of(a, pa, pb, t, h, layer);
-    u32x2 vw = {0, 0};
-    if (live) vw = *reinterpret_cast<const u32x2 *>(pv + t * a.ldv + int64_t(h) * a.Dv + col);
-    const float v[4] = {lo_bf16(vw[0]), hi_bf16(vw[0]), lo_bf16(vw[1]), hi_bf16(vw[1])};
-    const float decay = expf(gate.g);
-    __syncthreads();
-    float kk[N], sum[9];
-#pragma unroll
-    for (int e = 0; e < 9; ++e) sum[e] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int row = 32 * j + 8 * wave + (lane >> 3);
-      kk[j] = lds.k[row];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[e] = fmaf(S[j][e], kk[j], sum[e]);
-      if constexpr (!COMMIT) {
-        const float qq = lds.q[row];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sum[4 + e] = fmaf(S[j][e], qq, sum[4 + e]);
-        sum[8] = fmaf(kk[j], qq, sum[8]);
+  for (int i0 = 0; i0 < count; i0 += kStepBatch) {
+    const int here = min(kStepBatch, count - i0);
+    auto token = [&](int j) { return int64_t(rq.first) + (tokens ? tokens[i0 + j] : i0 + j); };
+    if (on) {
+      Gate gate = {0.0f, 0.0f};
+      if (tid < here) gate = gate_of(a, pa, pb, token(tid), h, layer);
+      for (int u = tid; u < here * P * (COMMIT ? 1 : 2); u += kThreads) {
+        const int w = u < here * P ? u : u - here * P, j = w / P, d = w % P * 8;
+        const int64_t t = token(j);
+        const u32x4 x = *reinterpret_cast<const u32x4 *>((u < here * P ? pk + t * a.ldk : pq + t * a.ldq) + d);
+        f32x4 *to = reinterpret_cast<f32x4 *>((u < here * P ? lds.k[j] : lds.q[j]) + d);
+        to[0] = f32x4{lo_bf16(x[0]), hi_bf16(x[0]), lo_bf16(x[1]), hi_bf16(x[1])};
+        to[1] = f32x4{lo_bf16(x[2]), hi_bf16(x[2]), lo_bf16(x[3]), hi_bf16(x[3])};
+      }
+      const int j = tid >> 2 & (kStepBatch - 1), d = (tid & 3) * 8;
+      if (tid >= kThreads - 4 * kStepBatch && j < here && col0 + d < a.Dv) {   // the last wave: the others have the gates and k
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(pv + token(j) * a.ldv + d);
+        f32x4 *to = reinterpret_cast<f32x4 *>(lds.v[j] + d);
+        to[0] = f32x4{lo_bf16(x[0]), hi_bf16(x[0]), lo_bf16(x[1]), hi_bf16(x[1])};
+        to[1] = f32x4{lo_bf16(x[2]), hi_bf16(x[2]), lo_bf16(x[3]), hi_bf16(x[3])};
+      }
+      if (tid < here) {
+        lds.decay[tid] = expf(gate.g);
+        lds.step[tid] = gate.b;
       }
     }
-#pragma unroll
-    for (int e = 0; e < (COMMIT ? 4 : 9); ++e) {
-#pragma unroll
-      for (int off = 8; off < 64; off <<= 1) sum[e] += __shfl_xor(sum[e], off, 64);
-      if (on && lane < 8) lds.sum[wave][lane][e] = sum[e];
-    }
     __syncthreads();
-    float u[4];
+    for (int i = 0; i < here; ++i) {
+      const float decay = lds.decay[i], step = lds.step[i];
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(lds.v[i] + 4 * (lane & 7));
+      constexpr int SUMS = COMMIT ? 4 : 9;
+      float kk[N], sum[12];
 #pragma unroll
-    for (int e = 0; e < (COMMIT ? 4 : 9); ++e)
-      sum[e] = lds.sum[0][lane & 7][e] + lds.sum[1][lane & 7][e] + (lds.sum[2][lane & 7][e] + lds.sum[3][lane & 7][e]);
+      for (int e = 0; e < 12; ++e) sum[e] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      u[e] = gate.b * (v[e] - decay * sum[e]);
+      for (int j = 0; j < N; ++j) {
+        const int row = 32 * j + 8 * wave + (lane >> 3);
+        kk[j] = lds.k[i][row];
 #pragma unroll
-      for (int j = 0; j < N; ++j) S[j][e] = fmaf(kk[j], u[e], decay * S[j][e]);
-    }
-    if constexpr (!COMMIT) {
-      if (tid < 8 && live) {
-        float o[4];
+        for (int e = 0; e < 4; ++e) sum[e] = fmaf(S[j][e], kk[j], sum[e]);
+        if constexpr (!COMMIT) {
+          const float qq = lds.q[i][row];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = a.scale * fmaf(sum[8], u[e], decay * sum[4 + e]);
-        *reinterpret_cast<u32x2 *>(a.out + (t * a.Hv + h) * a.Dv + col) = u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+          for (int e = 0; e < 4; ++e) sum[4 + e] = fmaf(S[j][e], qq, sum[4 + e]);
+          sum[8] = fmaf(kk[j], qq, sum[8]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < SUMS; ++e) sum[e] = sum_rows(sum[e]);
+      auto &sums = lds.sum[i & 1];                       // the token before may still be read
+      if (on && lane < 8)
+#pragma unroll
+        for (int e = 0; e < SUMS; e += 4)
+          *reinterpret_cast<f32x4 *>(sums[wave][lane] + e) = f32x4{sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < SUMS; e += 4) {
+        f32x4 x[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) x[w] = *reinterpret_cast<const f32x4 *>(sums[w][lane & 7] + e);
+        x[0] = x[0] + x[1] + (x[2] + x[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[e + j] = x[0][j];
+      }
+      float u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        u[e] = step * (v[e] - decay * sum[e]);
+#pragma unroll
+        for (int j = 0; j < N; ++j) S[j][e] = fmaf(kk[j], u[e], decay * S[j][e]);
+      }
+      if constexpr (!COMMIT) {
+        if (tid < 8 && live) {
+          float o[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = a.scale * fmaf(sum[8], u[e], decay * sum[4 + e]);
+          *reinterpret_cast<u32x2 *>(a.out + (token(i) * a.Hv + h) * a.Dv + col) = u32x2{pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3])};
+        }
       }
     }
   }
@@ -819,7 +864,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
           sum += v;
           x[c][e] = fmaf(-grown[e], ks[c][e], v);
         }
-      const uint64_t none = bad | (here < kChunk ? ~uint64_t(0) << here : 0);
+      const uint64_t none = bad | (here < kChunk ? ~uint64_t(0) << (here & 63) : 0);
       if (none || __any(!__builtin_isfinite(sum))) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -965,15 +1010,19 @@ constexpr int kFusedThreads = 512;
 template <int DK>
 __global__ __launch_bounds__(kFusedThreads, 4) void delta_tree_kernel(const DeltaArgs a) {
   constexpr int NS = DK / 32, PITCH = kChunk + 4;
-  __shared__ u32x4 s_K[4][NS][64];
-  __shared__ u32x4 s_QT[kTParts * kTriangle * 64];       // Q's operands, then T's
+  struct Operands {
+    u32x4 K[4][NS][64], QT[kTParts * kTriangle * 64];    // K's; Q's, then T's
+  };
+  __shared__ Operands lds;
+  auto &s_K = lds.K;
+  auto &s_QT = lds.QT;
   __shared__ __attribute__((aligned(16))) float s_A[kChunk * PITCH];  // A, then T
   __shared__ u32x4 s_P[kPParts * kTriangle * 64];
   __shared__ f32x4 s_T[kTriangle][64];                   // T's blocks below the diagonal, as results lie
   __shared__ double s_total[kChunk];
   __shared__ __attribute__((aligned(16))) float s_b[kChunk], s_grown[kChunk];
   __shared__ uint64_t s_seen[kChunk], s_bad[5];
-  static_assert(sizeof(s_QT) >= sizeof(s_K) && sizeof(s_K) >= sizeof(StepShared<DK>), "Q fits where T is");
+  static_assert(sizeof(lds.QT) >= sizeof(lds.K) && sizeof(lds) >= sizeof(StepShared<DK>), "Q fits where T is");
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int blocks = (a.Dv + 127) / 128;
@@ -992,9 +1041,9 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_tree_kernel(const Delt
     return;
   }
   if (rq.n > kTreeNodes) {
-    StepShared<DK> *const lds = reinterpret_cast<StepShared<DK> *>(s_K);
+    StepShared<DK> &step = reinterpret_cast<StepShared<DK> &>(lds);
     for (int c = 0; c < 128 && 128 * cb + c < a.Dv; c += 32)
-      step_request<DK, false>(a, rq, h, 0, 128 * cb + c, rq.n, nullptr, *lds, tid < kThreads);
+      step_request<DK, false>(a, rq, h, 0, 128 * cb + c, rq.n, nullptr, step, tid < kThreads);
     return;
   }
   const float *state = a.state + ((int64_t(rq.row) * a.Hv + h) * DK + 8 * g) * a.Dv + col;
