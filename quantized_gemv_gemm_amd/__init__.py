@@ -601,10 +601,14 @@ def _raw_stream(index):
 def _call(name, index, *args):
     """Calls the library on GPU ``index`` and its current stream (appended), whichever GPU is current."""
     import torch
-    if torch._C._cuda_getDevice() != index:
+    c = torch._C
+    if c._cuda_getDevice() != index:
         with torch.cuda.device(index):
-            return _check(name, getattr(lib(), name)(*args, _raw_stream(index)))
-    return _check(name, getattr(lib(), name)(*args, _raw_stream(index)))
+            status = getattr(lib(), name)(*args, c._cuda_getCurrentRawStream(index))
+    else:
+        status = getattr(lib(), name)(*args, c._cuda_getCurrentRawStream(index))
+    if status:
+        _check(name, status)
 
 
 def _given(t, name, dtype, shape, index):
@@ -945,26 +949,33 @@ def _columns(t, name, dtype, shape, index):
         if t.get_device() != index:
             raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    *lead, ld, one = t.stride()
-    rows, cols = shape[-2:]
-    if one != 1 and cols > 1:
-        raise ValueError(f"{name}'s columns must lie next to each other (strides {t.stride()})")
-    ld = ld if rows > 1 else cols
+    strides, cols = t.stride(), shape[-1]
+    ld = strides[-2] if shape[-2] > 1 else cols
+    if strides[-1] != 1 and cols > 1:
+        raise ValueError(f"{name}'s columns must lie next to each other (strides {strides})")
     if ld < cols:
-        raise ValueError(f"{name}'s rows must not overlap (strides {t.stride()}): copy a broadcast tensor first")
-    return (t.data_ptr(), ld) if len(shape) == 2 else (t.data_ptr(), ld, lead[0] if shape[0] > 1 else 0)
+        raise ValueError(f"{name}'s rows must not overlap (strides {strides}): copy a broadcast tensor first")
+    if len(shape) == 2:
+        return t.data_ptr(), ld
+    return t.data_ptr(), ld, strides[0] if shape[0] > 1 else 0
 
 
-def _heads(t, name, index, layers):
-    """A bf16 [tokens, heads, D] tensor, or [layers, tokens, heads, D], as _columns of its heads' elements."""
-    import torch
-    if t.dim() != (4 if layers else 3):
-        raise ValueError(f"{name} must be [{'layers, ' if layers else ''}tokens, heads, D], got {list(t.shape)}")
-    H, D = t.shape[-2:]
-    if t.stride(-1) != 1 and D > 1 or t.stride(-2) != D and H > 1:
-        raise ValueError(f"{name}'s heads must lie next to each other (strides {t.stride()})")
-    flat = t.as_strided((*t.shape[:-2], H * D), (*t.stride()[:-2], 1))
-    return _columns(flat, name, torch.bfloat16, flat.shape, index)
+def _heads(t, name, dtype, index, layers):
+    """A [tokens, heads, D] tensor, or [layers, tokens, heads, D], of this dtype: its address and the distances of
+    tokens and, with layers, of those."""
+    shape, strides = t.shape, t.stride()
+    if t.dtype is not dtype or len(shape) != 3 + layers or t.get_device() != index:
+        _need(t.contiguous(), name, dtype, 3 + layers)
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
+    T, H, D = shape[-3:]
+    if strides[-1] != 1 and D > 1 or strides[-2] != D and H > 1:
+        raise ValueError(f"{name}'s heads must lie next to each other (strides {strides})")
+    ld = strides[-3] if T > 1 else H * D
+    if ld < H * D:
+        raise ValueError(f"{name}'s tokens must not overlap (strides {strides}): copy a broadcast tensor first")
+    if not layers:
+        return t.data_ptr(), ld
+    return t.data_ptr(), ld, strides[0] if shape[0] > 1 else 0
 
 
 def _step_args(q_start, kv_lens, state_slots, tree_mask, T, index):
@@ -1008,7 +1019,7 @@ def _gates(a, b, a_log, dt_bias, shape, index):
     f32 = torch.float32
     if (a_log is None) != (dt_bias is None):
         raise ValueError("a_log and dt_bias come together")
-    lead = shape[:-2] + shape[-1:]
+    lead = shape[:-2] + shape[-1:]                       # of each layer and head
     return (_columns(a, "a", f32, shape, index), _columns(b, "b", f32, shape, index),
             None if a_log is None else _given(a_log, "a_log", f32, lead, index),
             None if a_log is None else _given(dt_bias, "dt_bias", f32, lead, index))
@@ -1025,17 +1036,18 @@ def delta_rule(q, k, v, a, b, q_start, kv_lens, state_slots, state, a_log=None, 
     i = _index_of(q, "q")
     if state.dim() != 4:
         raise ValueError("state must be [states, value heads, Dk, Dv]")
-    qp, ldq = _heads(q, "q", i, False)
-    kp, ldk = _heads(k, "k", i, False)
-    vp, ldv = _heads(v, "v", i, False)
+    bf16, f32 = torch.bfloat16, torch.float32
+    qp, ldq = _heads(q, "q", bf16, i, False)
+    kp, ldk = _heads(k, "k", bf16, i, False)
+    vp, ldv = _heads(v, "v", bf16, i, False)
     (T, Hk, Dk), (states, Hv, _, Dv) = q.shape, state.shape
     if k.shape != q.shape or v.shape != (T, Hv, Dv) or Hk == 0 or Hv % Hk or Hv == 0:
         raise ValueError(f"k must be {list(q.shape)} and v [T, a multiple of {Hk}, Dv] as the state has them")
     R, sp, lp, np_, mp = _step_args(q_start, kv_lens, state_slots, tree_mask, T, i)
     (ap, lda), (bp, ldb), gp, dp = _gates(a, b, a_log, dt_bias, (T, Hv), i)
-    tp = _given(state, "state", torch.float32, (states, Hv, Dk, Dv), i)
-    out = torch.empty((T, Hv, Dv), dtype=torch.bfloat16, device=q.device) if out is None else out
-    op = _given(out, "out", torch.bfloat16, (T, Hv, Dv), i)
+    tp = _given(state, "state", f32, (states, Hv, Dk, Dv), i)
+    out = torch.empty((T, Hv, Dv), dtype=bf16, device=q.device) if out is None else out
+    op = _given(out, "out", bf16, (T, Hv, Dv), i)
     if max_nodes is None:
         max_nodes = max(1, -(-T // max(R, 1)))
     wp, size = None, 0
@@ -1060,32 +1072,32 @@ def delta_commit(accepted, path, q_start, kv_lens, state_slots, k, v, a, b, stat
     without the leading dimension."""
     import torch
     i = _index_of(accepted, "accepted")
+    layers = state.dim() == 5
     if state.dim() not in (4, 5):
         raise ValueError("state must be [states, value heads, Dk, Dv], with or without layers before")
-    if state.dim() == 4:
-        one = lambda t: None if t is None else t.unsqueeze(0)
-        k, v, a, b, state, a_log, dt_bias, x, conv_state = map(one, (k, v, a, b, state, a_log, dt_bias, x, conv_state))
-    L, states, Hv, Dk, Dv = state.shape
-    kp = _heads(k, "k", i, True)
-    vp = _heads(v, "v", i, True)
-    _, T, Hk, _ = k.shape
-    if k.shape != (L, T, Hk, Dk) or v.shape != (L, T, Hv, Dv) or Hk == 0 or Hv % Hk or Hv == 0:
-        raise ValueError(f"k must be [{L}, T, heads, {Dk}] and v [{L}, T, {Hv}, {Dv}]")
+    f32, bf16, i32 = torch.float32, torch.bfloat16, torch.int32
+    lead = tuple(state.shape[:-4])
+    L, (states, Hv, Dk, Dv) = lead[0] if layers else 1, state.shape[-4:]
+    one = (lambda t: t) if layers else (lambda t: (*t, 0))
+    kp, vp = one(_heads(k, "k", bf16, i, layers)), one(_heads(v, "v", bf16, i, layers))
+    T, Hk, _ = k.shape[-3:]
+    if k.shape != (*lead, T, Hk, Dk) or v.shape != (*lead, T, Hv, Dv) or Hk == 0 or Hv % Hk or Hv == 0:
+        raise ValueError(f"k must be {[*lead, 'T', 'heads', Dk]} and v {[*lead, 'T', Hv, Dv]}")
     R, sp, lp, np_, _ = _step_args(q_start, kv_lens, state_slots, None, T, i)
-    ap, bp, gp, dp = _gates(a, b, a_log, dt_bias, (L, T, Hv), i)
+    ap, bp, gp, dp = _gates(a, b, a_log, dt_bias, (*lead, T, Hv), i)
+    ap, bp = one(ap), one(bp)
     if path.dim() != 2:
         raise ValueError("path must be [R, width]")
     xp, C, taps, cp = (None, 0, 0), 0, 0, None
     if x is not None:
-        if conv_state is None or x.dim() != 3 or conv_state.dim() != 4:
+        if conv_state is None or x.dim() != 2 + layers or conv_state.dim() != 3 + layers:
             raise ValueError("x [T, C] and conv_state [states, taps - 1, C] come together")
-        C, taps = x.shape[2], conv_state.shape[2] + 1
-        xp = _columns(x, "x", torch.bfloat16, (L, T, C), i)
-        cp = _given(conv_state, "conv_state", torch.bfloat16, (L, states, taps - 1, C), i)
+        C, taps = x.shape[-1], conv_state.shape[-2] + 1
+        xp = one(_columns(x, "x", bf16, (*lead, T, C), i))
+        cp = _given(conv_state, "conv_state", bf16, (*lead, states, taps - 1, C), i)
     elif conv_state is not None:
         raise ValueError("x [T, C] and conv_state [states, taps - 1, C] come together")
     _call("tl_delta_commit", i,
-        _given(accepted, "accepted", torch.int32, (R,), i), _given(path, "path", torch.int32, (R, path.shape[1]), i),
-        path.shape[1], sp, lp, np_, R, T, L, *kp, *vp, *ap, *bp, gp, dp, Hk, Hv // Hk, Dk, Dv,
-        _given(state, "state", torch.float32, (L, states, Hv, Dk, Dv), i), states, *xp, C, taps, cp)
+        _given(accepted, "accepted", i32, (R,), i), _given(path, "path", i32, (R, path.shape[1]), i), path.shape[1], sp, lp, np_, R, T, L, *kp, *vp, *ap, *bp, gp, dp, Hk, Hv // Hk, Dk, Dv,
+        _given(state, "state", f32, state.shape, i), states, *xp, C, taps, cp)
     return state

@@ -114,14 +114,15 @@ def test_conv_rejections():
 def test_delta_rejections():
     L = tl.lib()
     size = L.tl_delta_rule_workspace_size
-    assert size(64, 64, 16, 3, 128, 1, 0) == 0 and size(64, 64, 16, 3, 128, 1, 1) > 0 and size(100, 2, 16, 3, 128, 50, 0) > 0
+    assert size(64, 64, 16, 3, 128, 1, 0) == 0 and size(64, 64, 16, 3, 128, 64, 1) == 0      # one launch each
+    assert size(64, 64, 16, 3, 128, 65, 1) > 0 and size(100, 2, 16, 3, 128, 50, 0) > 0
     for bad in ((-1, 2, 1, 1, 64, 50, 0), (9, -1, 1, 1, 64, 50, 0), (9, 4097, 1, 1, 64, 50, 0), (9, 2, 0, 1, 64, 50, 0),
                 (9, 2, 1, 1, 32, 50, 0), (9, 2, 1, 1, 64, 0, 0), (9, 2, 65536, 1, 64, 50, 0)):
         assert size(*bad) == 0, bad
-    need = size(90, 2, 2, 3, 64, 50, 1)
+    need = size(90, 2, 2, 3, 64, 80, 1)
 
     def call(q=P(0), ldq=128, k=P(1), ldk=128, v=P(2), ldv=192, a=P(3), lda=6, b=P(4), ldb=6, log=P(5), bias=P(6), T=90, Hk=2, G=3,
-             Dk=64, Dv=32, qs=P(7), kv=P(8), slots=P(9), R=2, mask=P(10), scale=0.1, state=P(11), states=5, nodes=50, out=P(12),
+             Dk=64, Dv=32, qs=P(7), kv=P(8), slots=P(9), R=2, mask=P(10), scale=0.1, state=P(11), states=5, nodes=80, out=P(12),
              ws=P(13), wb=need):
         return L.tl_delta_rule(q, ldq, k, ldk, v, ldv, a, lda, b, ldb, log, bias, T, Hk, G, Dk, Dv, qs, kv, slots, R, mask, scale,
                                state, states, nodes, out, ws, wb, None)
