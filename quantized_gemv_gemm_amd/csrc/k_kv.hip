@@ -102,10 +102,41 @@ __device__ __forceinline__ void load8(const float *from, float (&to)[8]) {
   to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w, to[4] = y.x, to[5] = y.y, to[6] = y.z, to[7] = y.w;
 }
 
-// Piece p of token t's row, normalised and turned.  The P lanes of a row call it together.
+// Cosines and sines of `count` tokens from t0 on, [count][rot], to LDS: each pair's angle goes by
+// its own axis of positions.  The workgroup passes a barrier before it reads them.
+__device__ __forceinline__ void stage_angles(const WriteArgs &a, int t0, int count, float *to) {
+  const int h = a.rot / 2;
+  for (int u = threadIdx.x; u < count * h; u += kThreads) {
+    const int i = u / h, d = u - i * h;
+    const int axis = a.axis_of ? min(max(a.axis_of[d], 0), a.axes - 1) : 0;
+    const int pos = min(max(a.positions[int64_t(axis) * a.T + min(t0 + i, a.T - 1)], 0), a.max_pos - 1);
+    const float *at = a.cos_sin + int64_t(pos) * a.rot + d;
+    to[i * a.rot + d] = at[0];
+    to[i * a.rot + h + d] = at[h];
+  }
+}
+
+// Piece p's elements of the weights, or ones.
+struct Weight16 {
+  float a[8], b[8];
+};
+__device__ __forceinline__ Weight16 weights(const float *weight, int lo, int hi) {
+  Weight16 w;
+  if (weight) {
+    load8(weight + lo, w.a);
+    load8(weight + hi, w.b);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w.a[e] = w.b[e] = 1.0f;
+  }
+  return w;
+}
+
+// Piece p of a row, normalised and turned by its token's staged angles.  The P lanes of a row
+// call it together.
 template <int P>
-__device__ __forceinline__ Piece16 normed(const Row16 &x, const WriteArgs &a, const float *weight, int t, int p, int lo,
-                                          int hi) {
+__device__ __forceinline__ Piece16 normed(const Row16 &x, const WriteArgs &a, const Weight16 &w, const float *angle, int p,
+                                          int lo) {
   Piece16 y;
   float sum = 0.0f;
 #pragma unroll
@@ -118,32 +149,15 @@ __device__ __forceinline__ Piece16 normed(const Row16 &x, const WriteArgs &a, co
 #pragma unroll
   for (int off = P / 2; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
   const float by = 1.0f / sqrtf(sum / float(16 * P) + a.eps);
-  float wa[8], wb[8];
-  if (weight) {
-    load8(weight + lo, wa);
-    load8(weight + hi, wb);
-  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    y.a[e] = y.a[e] * by * (weight ? wa[e] : 1.0f);
-    y.b[e] = y.b[e] * by * (weight ? wb[e] : 1.0f);
+    y.a[e] = y.a[e] * by * w.a[e];
+    y.b[e] = y.b[e] * by * w.b[e];
   }
   if (16 * p < a.rot) {                                  // pairs lo .. lo + 7
     float c[8], s[8];
-    if (a.axis_of) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int axis = min(max(a.axis_of[lo + e], 0), a.axes - 1);
-        const int pos = min(max(a.positions[int64_t(axis) * a.T + t], 0), a.max_pos - 1);
-        const float *at = a.cos_sin + int64_t(pos) * a.rot + lo + e;
-        c[e] = at[0];
-        s[e] = at[a.rot / 2];
-      }
-    } else {
-      const float *at = angles(a, t) + lo;
-      load8(at, c);
-      load8(at + a.rot / 2, s);
-    }
+    load8(angle + lo, c);
+    load8(angle + a.rot / 2 + lo, s);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float u = y.a[e], v = y.b[e];
@@ -173,28 +187,57 @@ __device__ __forceinline__ u32x2 codes8(const float (&x)[8], float scale) {
   return o;
 }
 
-template <int D, bool E4M3, bool NORM>
+// PASSES: 0 without norms, else how many rows of q a thread takes a piece of; its weights stay in
+// registers, and the rows' angles, staged once, serve all heads of a token.
+template <int D, bool E4M3, int PASSES>
 __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, int cache_groups) {
+  constexpr bool NORM = PASSES > 0;
+  constexpr int kAngles = kThreads / (D / 16);           // tokens whose angles have a place
+  __shared__ __attribute__((aligned(16))) float s_angle[NORM ? kAngles * D : 4];
   constexpr int P = D / 16;                              // pieces (lanes) of a row
   constexpr int ES = E4M3 ? 1 : 2;
   const int tid = threadIdx.x, h = a.rot / 2;
   if (int(blockIdx.x) >= cache_groups) {                 // q
-    const int64_t row = int64_t(blockIdx.x - cache_groups) * (kThreads / P) + tid / P;
-    if (row >= int64_t(a.T) * a.Hq) return;
-    const int t = int(row / a.Hq), head = int(row - int64_t(t) * a.Hq), p = tid % P;
-    int lo, hi;
-    piece(p, a.rot, lo, hi);
-    const uint16_t *src = a.q + t * a.ldq + int64_t(head) * (NORM ? a.q_head : D);
-    Row16 x = {*reinterpret_cast<const u32x4 *>(src + lo), *reinterpret_cast<const u32x4 *>(src + hi)};
     if constexpr (NORM) {
-      const Piece16 y = normed<P>(x, a, a.q_weight, t, p, lo, hi);
-      x = {pack8(y.a), pack8(y.b)};
-    } else if (16 * p < a.rot) {
-      rotate(x, angles(a, t), h, lo);
+      const int64_t rows = int64_t(a.T) * a.Hq, row0 = int64_t(blockIdx.x - cache_groups) * (PASSES * kAngles);
+      const int p = tid % P, t0 = int(row0 / a.Hq);
+      const int t1 = int((min(row0 + PASSES * kAngles, rows) - 1) / a.Hq);
+      int lo, hi;
+      piece(p, a.rot, lo, hi);
+      Row16 x[PASSES];
+      int token[PASSES];
+#pragma unroll
+      for (int j = 0; j < PASSES; ++j) {                 // past the last row it is the last one again
+        const int64_t row = min(row0 + j * kAngles + tid / P, rows - 1);
+        token[j] = int(row / a.Hq);
+        const uint16_t *src = a.q + token[j] * a.ldq + (row - int64_t(token[j]) * a.Hq) * a.q_head;
+        x[j] = {*reinterpret_cast<const u32x4 *>(src + lo), *reinterpret_cast<const u32x4 *>(src + hi)};
+      }
+      const Weight16 w = weights(a.q_weight, lo, hi);
+      if (a.rot) stage_angles(a, t0, t1 - t0 + 1, s_angle);
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < PASSES; ++j) {
+        const Piece16 y = normed<P>(x[j], a, w, s_angle + (token[j] - t0) * a.rot, p, lo);
+        const int64_t row = row0 + j * kAngles + tid / P;
+        if (row < rows) {
+          *reinterpret_cast<u32x4 *>(a.q_out + row * D + lo) = pack8(y.a);
+          *reinterpret_cast<u32x4 *>(a.q_out + row * D + hi) = pack8(y.b);
+        }
+      }
+    } else {
+      const int64_t row = int64_t(blockIdx.x - cache_groups) * (kThreads / P) + tid / P;
+      if (row >= int64_t(a.T) * a.Hq) return;
+      const int t = int(row / a.Hq), head = int(row - int64_t(t) * a.Hq), p = tid % P;
+      int lo, hi;
+      piece(p, a.rot, lo, hi);
+      const uint16_t *src = a.q + t * a.ldq + int64_t(head) * D;
+      Row16 x = {*reinterpret_cast<const u32x4 *>(src + lo), *reinterpret_cast<const u32x4 *>(src + hi)};
+      if (16 * p < a.rot) rotate(x, angles(a, t), h, lo);
+      uint16_t *dst = a.q_out + row * D;
+      *reinterpret_cast<u32x4 *>(dst + lo) = x.a;
+      *reinterpret_cast<u32x4 *>(dst + hi) = x.b;
     }
-    uint16_t *dst = a.q_out + row * D;
-    *reinterpret_cast<u32x4 *>(dst + lo) = x.a;
-    *reinterpret_cast<u32x4 *>(dst + hi) = x.b;
     return;
   }
 
@@ -206,6 +249,9 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
     const int t = t0 + tid - 1;
     int64_t s = t >= 0 && t < a.T ? a.slots[t] : -1;
     s_slot[tid] = s >= 0 && s < a.slot_count ? s : -1;
+  }
+  if constexpr (NORM) {
+    if (a.rot) stage_angles(a, t0, min(kTokens, a.T - t0), s_angle);
   }
   __syncthreads();
   const int mask = (1 << a.block_shift) - 1;
@@ -256,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
     const int in_tile = int(slot & 15);
     Piece16 y;
     if constexpr (NORM) {                                // rows that are not there are zeros, of an existing token
-      y = normed<P>(k, a, a.k_weight, min(t, a.T - 1), p, lo, hi);
+      y = normed<P>(k, a, weights(a.k_weight, lo, hi), s_angle + min(i, a.T - 1 - t0) * a.rot, p, lo);
       if constexpr (!E4M3) k = {pack8(y.a), pack8(y.b)};
     }
     if constexpr (E4M3 && NORM) {
@@ -450,15 +496,23 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(const CommitArgs a)
   }
 }
 
-template <int D, bool E4M3, bool NORM>
+template <int D, bool E4M3, int PASSES>
 hipError_t write_rows(const WriteArgs &a, hipStream_t stream) {
-  const int64_t cache = (int64_t(a.T) + kTokens - 1) / kTokens * a.H;
-  const int64_t q = a.q ? (int64_t(a.T) * a.Hq + kThreads / (D / 16) - 1) / (kThreads / (D / 16)) : 0;
+  const int64_t cache = (int64_t(a.T) + kTokens - 1) / kTokens * a.H, rows = a.q ? int64_t(a.T) * a.Hq : 0;
+  const int64_t of_group = kThreads / (D / 16) * (PASSES ? PASSES : 1), q = (rows + of_group - 1) / of_group;
   if (cache + q > 0x7FFFFFFF) return hipErrorInvalidValue;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((kv_write_kernel<D, E4M3, NORM>), dim3(unsigned(cache + q)), dim3(kThreads), 0, stream, a, int(cache));
-  set_last_kernel(NORM ? E4M3 ? "kv_write_norm_e4m3" : "kv_write_norm_bf16" : E4M3 ? "kv_write_e4m3" : "kv_write_bf16");
+  hipLaunchKernelGGL((kv_write_kernel<D, E4M3, PASSES>), dim3(unsigned(cache + q)), dim3(kThreads), 0, stream, a, int(cache));
+  set_last_kernel(PASSES ? E4M3 ? "kv_write_norm_e4m3" : "kv_write_norm_bf16" : E4M3 ? "kv_write_e4m3" : "kv_write_bf16");
   return hipGetLastError();
+}
+
+// Four rows of q a thread once they make a thousand workgroups; with heads enough that the
+// tokens of such a group are no more than the angles have places for.
+template <int D, bool E4M3>
+hipError_t write_normed(const WriteArgs &a, hipStream_t stream) {
+  if (a.Hq >= 8 && int64_t(a.T) * a.Hq >= int64_t(1024) * 4 * (kThreads / (D / 16))) return write_rows<D, E4M3, 4>(a, stream);
+  return write_rows<D, E4M3, 1>(a, stream);
 }
 
 template <int D, bool E4M3>
@@ -473,16 +527,20 @@ hipError_t commit_rows(const CommitArgs &a, hipStream_t stream) {
 
 }  // namespace
 
-template <bool E4M3, bool NORM>
-static hipError_t write_of(const WriteArgs &a, int64_t D, hipStream_t stream) {
-  return D == 64    ? write_rows<64, E4M3, NORM>(a, stream)
-         : D == 128 ? write_rows<128, E4M3, NORM>(a, stream)
-                    : write_rows<256, E4M3, NORM>(a, stream);
+template <bool E4M3>
+static hipError_t write_of(const WriteArgs &a, int64_t D, bool norm, hipStream_t stream) {
+  if (norm) {
+    return D == 64    ? write_normed<64, E4M3>(a, stream)
+           : D == 128 ? write_normed<128, E4M3>(a, stream)
+                      : write_normed<256, E4M3>(a, stream);
+  }
+  return D == 64    ? write_rows<64, E4M3, 0>(a, stream)
+         : D == 128 ? write_rows<128, E4M3, 0>(a, stream)
+                    : write_rows<256, E4M3, 0>(a, stream);
 }
 
 hipError_t launch_kv_write(const WriteArgs &a, int64_t D, bool e4m3, bool norm, hipStream_t stream) {
-  if (norm) return e4m3 ? write_of<true, true>(a, D, stream) : write_of<false, true>(a, D, stream);
-  return e4m3 ? write_of<true, false>(a, D, stream) : write_of<false, false>(a, D, stream);
+  return e4m3 ? write_of<true>(a, D, norm, stream) : write_of<false>(a, D, norm, stream);
 }
 
 hipError_t launch_kv_commit(const CommitArgs &a, int64_t D, bool e4m3, hipStream_t stream) {
