@@ -108,8 +108,15 @@ __device__ __forceinline__ void stage_angles(const WriteArgs &a, int t0, int cou
   const int h = a.rot / 2;
   for (int u = threadIdx.x; u < count * h; u += kThreads) {
     const int i = u / h, d = u - i * h;
-    const int axis = a.axis_of ? min(max(a.axis_of[d], 0), a.axes - 1) : 0;
-    const int pos = min(max(a.positions[int64_t(axis) * a.T + min(t0 + i, a.T - 1)], 0), a.max_pos - 1);
+    const int32_t *at_t = a.positions + min(t0 + i, a.T - 1);
+    int pos = at_t[0];
+    if (a.axis_of && a.axes <= 3) {                      // asked for beside the axis, not after it
+      const int axis = a.axis_of[d], second = at_t[a.axes > 1 ? a.T : 0], third = at_t[a.axes > 2 ? 2 * int64_t(a.T) : 0];
+      pos = axis <= 0 || a.axes == 1 ? pos : axis == 1 || a.axes == 2 ? second : third;
+    } else if (a.axis_of) {
+      pos = at_t[int64_t(min(max(a.axis_of[d], 0), a.axes - 1)) * a.T];
+    }
+    pos = min(max(pos, 0), a.max_pos - 1);
     const float *at = a.cos_sin + int64_t(pos) * a.rot + d;
     to[i * a.rot + d] = at[0];
     to[i * a.rot + h + d] = at[h];
@@ -200,25 +207,27 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
   if (int(blockIdx.x) >= cache_groups) {                 // q
     if constexpr (NORM) {
       const int64_t rows = int64_t(a.T) * a.Hq, row0 = int64_t(blockIdx.x - cache_groups) * (PASSES * kAngles);
-      const int p = tid % P, t0 = int(row0 / a.Hq);
-      const int t1 = int((min(row0 + PASSES * kAngles, rows) - 1) / a.Hq);
+      const uint32_t heads = uint32_t(a.Hq), here = uint32_t(min(rows - row0, int64_t(PASSES * kAngles)));
+      const int p = tid % P, t0 = rows <= 0xFFFFFFFF ? int(uint32_t(row0) / heads) : int(row0 / a.Hq);
+      const uint32_t first = uint32_t(row0 - int64_t(t0) * a.Hq);  // head of the group's first row
+      const int tokens = int((first + here - 1) / heads) + 1;
       int lo, hi;
       piece(p, a.rot, lo, hi);
       Row16 x[PASSES];
       int token[PASSES];
 #pragma unroll
       for (int j = 0; j < PASSES; ++j) {                 // past the last row it is the last one again
-        const int64_t row = min(row0 + j * kAngles + tid / P, rows - 1);
-        token[j] = int(row / a.Hq);
-        const uint16_t *src = a.q + token[j] * a.ldq + (row - int64_t(token[j]) * a.Hq) * a.q_head;
+        const uint32_t at = first + min(uint32_t(j * kAngles + tid / P), here - 1);
+        token[j] = int(at / heads);
+        const uint16_t *src = a.q + int64_t(t0 + token[j]) * a.ldq + int64_t(at - token[j] * heads) * a.q_head;
         x[j] = {*reinterpret_cast<const u32x4 *>(src + lo), *reinterpret_cast<const u32x4 *>(src + hi)};
       }
       const Weight16 w = weights(a.q_weight, lo, hi);
-      if (a.rot) stage_angles(a, t0, t1 - t0 + 1, s_angle);
+      if (a.rot) stage_angles(a, t0, tokens, s_angle);
       __syncthreads();
 #pragma unroll
       for (int j = 0; j < PASSES; ++j) {
-        const Piece16 y = normed<P>(x[j], a, w, s_angle + (token[j] - t0) * a.rot, p, lo);
+        const Piece16 y = normed<P>(x[j], a, w, s_angle + token[j] * a.rot, p, lo);
         const int64_t row = row0 + j * kAngles + tid / P;
         if (row < rows) {
           *reinterpret_cast<u32x4 *>(a.q_out + row * D + lo) = pack8(y.a);
@@ -250,7 +259,18 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
     int64_t s = t >= 0 && t < a.T ? a.slots[t] : -1;
     s_slot[tid] = s >= 0 && s < a.slot_count ? s : -1;
   }
+  // with norms, rows are asked for beside their slots, and for the first round of the loop below
+  // before the barrier
+  auto ask = [&](const uint16_t *rows, int64_t ld, int u, int lo, int hi) {
+    const uint16_t *src = rows + int64_t(min(t0 + u / P, a.T - 1)) * ld + int64_t(head) * D;
+    return Row16{*reinterpret_cast<const u32x4 *>(src + lo), *reinterpret_cast<const u32x4 *>(src + hi)};
+  };
+  Row16 first_v, first_k;
   if constexpr (NORM) {
+    int lo, hi;
+    piece(tid % P, a.rot, lo, hi);
+    first_v = ask(a.v, a.ldv, tid, 16 * (tid % P), 16 * (tid % P) + 8);
+    first_k = ask(a.k, a.ldk, tid, lo, hi);
     if (a.rot) stage_angles(a, t0, min(kTokens, a.T - t0), s_angle);
   }
   __syncthreads();
@@ -268,7 +288,10 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
     const bool live = t < a.T && slot >= 0;              // the lanes of a row agree
     // V: also the tokens that a run begun here goes on to
     Row16 x = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    if (live) {
+    if constexpr (NORM) {
+      x = u == tid ? first_v : ask(a.v, a.ldv, u, 16 * p, 16 * p + 8);
+      if (!live) x = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    } else if (live) {
       const uint16_t *src = a.v + t * a.ldv + int64_t(head) * D + 16 * p;
       x = {*reinterpret_cast<const u32x4 *>(src), *reinterpret_cast<const u32x4 *>(src + 8)};
     }
@@ -294,14 +317,16 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
     Row16 k = {{0, 0, 0, 0}, {0, 0, 0, 0}};
     int lo, hi;
     piece(p, a.rot, lo, hi);
-    if (live) {
+    if constexpr (NORM) {
+      k = u == tid ? first_k : ask(a.k, a.ldk, u, lo, hi);
+    } else if (live) {
       const uint16_t *src = a.k + t * a.ldk + int64_t(head) * D;
       k = {*reinterpret_cast<const u32x4 *>(src + lo), *reinterpret_cast<const u32x4 *>(src + hi)};
-      if (!NORM && 16 * p < a.rot) rotate(k, angles(a, t), h, lo);
+      if (16 * p < a.rot) rotate(k, angles(a, t), h, lo);
     }
     const int in_tile = int(slot & 15);
     Piece16 y;
-    if constexpr (NORM) {                                // rows that are not there are zeros, of an existing token
+    if constexpr (NORM) {                                // rows past the last token are an existing token's
       y = normed<P>(k, a, weights(a.k_weight, lo, hi), s_angle + min(i, a.T - 1 - t0) * a.rot, p, lo);
       if constexpr (!E4M3) k = {pack8(y.a), pack8(y.b)};
     }
