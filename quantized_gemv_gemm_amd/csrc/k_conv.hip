@@ -5,14 +5,18 @@
 // step's first token into the request's state: its last W - 1 rows of x, the oldest first.
 //
 // A thread holds 8 neighbouring channels of a run of tokens; D / 8 neighbouring lanes hold a head.
+// A run keeps the last W - 1 rows in registers, so that each row of x is read once, but for the
+// W - 1 before a run; a tree's tokens gather theirs along the branch. Memory bounds it: 8191
+// tokens of 10240 channels and 4 taps move 336 MB in 76 us, 4.4 TB/s; without any arithmetic
+// between the loads and the stores the same kernel took 75. A prompt's results are stored past
+// the L2, which is worth 3 of 82 us.
 #include "kv_layout.h"
 #include "mixer_dev.h"
 
 namespace tl {
 namespace {
 
-constexpr int kRun = 16;   // tokens of a run
-constexpr int kAhead = 4;  // rows of a run on their way together
+constexpr int kThreads = 256;
 
 struct Row8 {
   float v[8];
@@ -27,14 +31,15 @@ __device__ __forceinline__ Row8 widen(u32x4 w) {
   return x;
 }
 
-template <int W>
-__global__ __launch_bounds__(kMixerThreads) void short_conv_kernel(const ConvArgs a) {
+// RUN tokens of a run, AHEAD of its rows on their way together
+template <int W, int RUN, int AHEAD>
+__global__ __launch_bounds__(kThreads) void short_conv_kernel(const ConvArgs a) {
   int part;
-  const Request p = find_piece<kRun>(a.q_start, a.kv_lens, a.slots, a.R, a.T, a.state_count, int(blockIdx.x), part);
+  const Request p = find_piece<RUN>(a.q_start, a.kv_lens, a.slots, a.R, a.T, a.state_count, int(blockIdx.x), part);
   if (p.r < 0) return;
-  const int c0 = (int(blockIdx.y) * kMixerThreads + threadIdx.x) * 8;
+  const int c0 = (int(blockIdx.y) * kThreads + threadIdx.x) * 8;
   if (c0 >= a.C) return;                                 // heads are whole: their lanes agree
-  const int i0 = part * kRun, count = min(kRun, p.n - i0);
+  const int i0 = part * RUN, count = min(RUN, p.n - i0);
   uint16_t *out = a.out + int64_t(p.first + i0) * a.ldo + c0;
   if (p.row < 0) {
     for (int i = 0; i < count; ++i) *reinterpret_cast<u32x4 *>(out + int64_t(i) * a.ldo) = u32x4{0, 0, 0, 0};
@@ -70,7 +75,9 @@ __global__ __launch_bounds__(kMixerThreads) void short_conv_kernel(const ConvArg
     u32x4 o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = pack_bf16(y[2 * e], y[2 * e + 1]);
-    *reinterpret_cast<u32x4 *>(out + int64_t(i) * a.ldo) = o;
+    u32x4 *to = reinterpret_cast<u32x4 *>(out + int64_t(i) * a.ldo);
+    if (RUN > 16) __builtin_nontemporal_store(o, to);    // a prompt's rows do not stay in the L2 until they are read
+    else *to = o;
   };
   if (tree) {
     for (int i = 0; i < count; ++i) {
@@ -100,14 +107,14 @@ __global__ __launch_bounds__(kMixerThreads) void short_conv_kernel(const ConvArg
     }
     return;
   }
-  Row8 rows[W - 1 + kAhead];                             // the last W - 1 rows, and the next ones
+  Row8 rows[W - 1 + AHEAD];                             // the last W - 1 rows, and the next ones
 #pragma unroll
   for (int j = 0; j < W - 1; ++j) rows[j] = widen(load_row(i0 - (W - 1) + j));
-  for (int i = 0; i < count; i += kAhead) {
+  for (int i = 0; i < count; i += AHEAD) {
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) rows[W - 1 + u] = widen(load_row(min(i0 + i + u, p.n - 1)));
+    for (int u = 0; u < AHEAD; ++u) rows[W - 1 + u] = widen(load_row(min(i0 + i + u, p.n - 1)));
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
+    for (int u = 0; u < AHEAD; ++u) {
       if (i + u >= count) break;                         // uniform
       float y[8];
 #pragma unroll
@@ -119,7 +126,7 @@ __global__ __launch_bounds__(kMixerThreads) void short_conv_kernel(const ConvArg
       finish(y, i + u);
     }
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) rows[j] = rows[kAhead + j];
+    for (int j = 0; j < W - 1; ++j) rows[j] = rows[AHEAD + j];
   }
   if (i0 == 0) {                                         // the thread that has read the old rows
     u32x4 next[W - 1];
@@ -130,14 +137,22 @@ __global__ __launch_bounds__(kMixerThreads) void short_conv_kernel(const ConvArg
   }
 }
 
-template <int W>
-hipError_t run(const ConvArgs &a, hipStream_t stream) {
-  const int64_t pieces = int64_t(a.T) / kRun + a.R;
+template <int W, int RUN, int AHEAD>
+hipError_t launch(const ConvArgs &a, hipStream_t stream) {
+  const int64_t pieces = int64_t(a.T) / RUN + a.R;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((short_conv_kernel<W>), dim3(unsigned(pieces), unsigned((a.C + 2047) / 2048)), dim3(kMixerThreads), 0,
-                     stream, a);
+  hipLaunchKernelGGL((short_conv_kernel<W, RUN, AHEAD>), dim3(unsigned(pieces), unsigned((a.C + 8 * kThreads - 1) / (8 * kThreads))),
+                     dim3(kThreads), 0, stream, a);
   set_last_kernel("short_conv");
   return hipGetLastError();
+}
+
+// Long runs read fewer rows twice and the weights less often, once they fill the card twice
+// over (8191 tokens of 10240 channels: 76 us, with runs of 16 tokens 86); short ones else, whose
+// kernel needs fewer registers (one token of each of 64 requests: 6.9 us, with the long ones 7.4).
+template <int W>
+hipError_t run(const ConvArgs &a, hipStream_t stream) {
+  return int64_t(a.T) / 64 * ((a.C + 8 * kThreads - 1) / (8 * kThreads)) >= 512 ? launch<W, 64, 8>(a, stream) : launch<W, 16, 4>(a, stream);
 }
 
 }  // namespace

@@ -69,7 +69,7 @@ __device__ __forceinline__ Request find_piece(const int32_t *q_start, const int3
   } else {
     int before = 0;
     bool bad = false;
-    for (int r0 = 0; r0 < R; r0 += kMixerThreads) {
+    for (int r0 = 0; r0 < R; r0 += int(blockDim.x)) {
       const int r = r0 + threadIdx.x;
       bool counts = false;
       if (r < R) {

@@ -237,6 +237,34 @@ def test_short_conv(tl, torch, taps, C, heads, dim, bias, lens, trees):
     np.testing.assert_array_equal(f64(stated), after)
 
 
+@pytest.mark.parametrize("taps", [2, 3, 4])
+def test_short_conv_long_runs(tl, torch, taps):
+    """Enough tokens and channels for runs of 64 tokens, with requests that end inside a run, and trees among them."""
+    announce(f"short_conv long runs taps={taps}")
+    d, rng = dev(), np.random.default_rng(taps)
+    s = Step(np.array([1500, 1, 0, 63, 64, 65, 700, 3] + [20] * 70), rng, trees=taps == 3)
+    C = 32768
+    assert s.T // 64 * (C // 2048) >= 512
+    x = spec.bf16(rng.standard_normal((s.T, 64)))
+    w = rng.standard_normal((64, taps)).astype(np.float32)
+    state = spec.bf16(rng.standard_normal((s.states, taps - 1, 64)))
+    wide = lambda a: a.repeat(*([1] * (a.dim() - 1)), C // 64)         # the same 64 channels again and again
+    stated = wide(bf16_dev(state, d))
+    out = torch.full((s.T, C), -7.0, dtype=torch.bfloat16, device=d)
+    tl.short_conv(wide(bf16_dev(x, d)), to_dev(w, d).repeat(C // 64, 1), *s.dev(d), stated, tree_mask=s.mask_dev(d), norm_heads=256,
+                  norm_dim=64, out=out)
+    torch.cuda.synchronize()
+    want, after, err = ref.short_conv(x, w.astype(np.float64), None, s.q_start, s.kv_lens, s.slots, state, s.mask, 1, 64, 1e-6,
+                                      np.full((s.T, 64), -7.0))
+    plain, _, e0 = ref.short_conv(x, w.astype(np.float64), None, s.q_start, s.kv_lens, s.slots, state, s.mask, 0, 64, 1e-6,
+                                  np.full((s.T, 64), -7.0))
+    got = f64(out).reshape(s.T, C // 64, 64)
+    tol = lambda v, e: BF16_HALF * np.abs(v) + 1.01 * F32_HALF * e
+    assert (np.abs(got[:, :256] - want[:, None]) <= tol(want, err)[:, None]).all()
+    assert (np.abs(got[:, 256:] - plain[:, None]) <= tol(plain, e0)[:, None]).all()
+    np.testing.assert_array_equal(f64(stated).reshape(s.states, taps - 1, C // 64, 64), np.repeat(after[:, :, None], C // 64, 2))
+
+
 def _delta_inputs(s, Hk, G, Dk, Dv, rng, raw, d, decay=0.3):
     T, Hv = s.T, Hk * G
     unit = lambda n: (lambda y: y / np.sqrt((y * y).sum(-1, keepdims=True)))(rng.standard_normal((T, n, Dk)) + 0.4)
