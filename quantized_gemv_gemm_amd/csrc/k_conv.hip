@@ -149,7 +149,7 @@ hipError_t launch(const ConvArgs &a, hipStream_t stream) {
 
 // Long runs read fewer rows twice and the weights less often, once they fill the card twice
 // over (8191 tokens of 10240 channels: 76 us, with runs of 16 tokens 86); short ones else, whose
-// kernel needs fewer registers (one token of each of 64 requests: 6.9 us, with the long ones 7.4).
+// kernel needs fewer registers (a call for one token of each of 64 requests: 8.9 us, with the long ones 9.1).
 template <int W>
 hipError_t run(const ConvArgs &a, hipStream_t stream) {
   return int64_t(a.T) / 64 * ((a.C + 8 * kThreads - 1) / (8 * kThreads)) >= 512 ? launch<W, 64, 8>(a, stream) : launch<W, 16, 4>(a, stream);
