@@ -34,7 +34,7 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kThreads = kMixerThreads;
+constexpr int kThreads = 256;
 constexpr int kChunk = 64;          // tokens of a chunk: a tree's most
 static_assert(kChunk == kTreeNodes, "a tree is one chunk");
 
@@ -601,16 +601,16 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
   }
 }
 
-// A workgroup walks the chunks of one request, head and 16 CT columns.  Wave w of the first
+// A workgroup walks the chunks of one request, head and 32 columns.  Wave w of the first
 // four takes row tile w of the chunk's tokens and, of the state, the rows 32 w .. 32 w + 31 (a
 // pair of tiles), and goes the chain from one chunk's state to the next one's: K S, U, K^T U.
-// Wave 4 + w makes the results of row tile w beside it.  Column m of tile c is column CT m + c:
+// Wave 4 + w makes the results of row tile w beside it.  Column m of tile c is column 2 m + c:
 // a lane's columns are neighbours.
 constexpr int kScanThreads = 512;
 
-template <int DK, int CT>
+template <int DK>
 __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const DeltaArgs a) {
-  constexpr int NS = DK / 32;
+  constexpr int NS = DK / 32, CT = 2;                    // column tiles of the workgroup
   static_assert(NS <= 4, "a wave holds at most one pair of state tiles");
   __shared__ __attribute__((aligned(16))) u32x4 s_S[3][CT][NS][64], s_R[3][CT][2][64], s_U[2][CT][2][64], s_W[3][CT][2][64];
   __shared__ uint32_t s_bad[16 * CT][2];                 // of each column: tokens whose v is not finite
@@ -634,8 +634,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   const int own_col = 16 * CT * cb + CT * m, col = own_col < a.Dv ? own_col : own_col - 16;
   auto store = [&](int64_t t, const float *o) {
     uint16_t *to = a.out + (t * a.Hv + h) * a.Dv + col;
-    if constexpr (CT == 2) *reinterpret_cast<uint32_t *>(to) = pack_bf16(o[0], o[1]);
-    else *to = uint16_t(pack_bf16(o[0], 0.0f));
+    *reinterpret_cast<uint32_t *>(to) = pack_bf16(o[0], o[1]);
   };
   if (srow < 0) {
     const float zero[2] = {0.0f, 0.0f};
@@ -746,7 +745,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float x[2] = {o[0][e], o[CT - 1][e]};
+          const float x[2] = {o[0][e], o[1][e]};
           if (more || row0 + e < here) store(t0 + row0 + e, x);
         }
       }
@@ -777,7 +776,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   // What a wave takes of a chunk.  Each piece is asked for as soon as the chunk before has used
   // it.  Rows past the last token are the last one's: nothing of theirs is kept.
   u32x4 K[NS], T[2][kTParts], keys[2][2];
-  uint32_t V[4];                                         // CT columns of a row
+  uint32_t V[4];                                         // two columns of a row
   f32x4 grown, left, end;                                // end: exp(D_last), nothing, a word of tokens
   const int vcol = h * a.Dv + col;
   const uint16_t *to_k, *to_v[4];                 // this lane's rows of the chunk that is asked for next
@@ -792,7 +791,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
 #pragma unroll
     for (int s = 0; s < NS; ++s) K[s] = *reinterpret_cast<const u32x4 *>(to_k + 32 * s);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) V[e] = CT == 2 ? *reinterpret_cast<const uint32_t *>(to_v[e]) : *to_v[e];
+    for (int e = 0; e < 4; ++e) V[e] = *reinterpret_cast<const uint32_t *>(to_v[e]);
     grown = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + row0 * 4);
     end = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + 2 * kChunk * 4);
   };
@@ -1336,7 +1335,7 @@ hipError_t run(DeltaArgs a, Form form, hipStream_t stream) {
   hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(unsigned(chunks_of(a.T, a.R)), unsigned((a.Hv + 3) / 4)), dim3(kThreads), 0, stream, a);
   if (hipError_t e = hipGetLastError()) return e;
   const int64_t grid = (int64_t(a.R) * a.Hk + 7) / 8 * 8 * a.G * ((a.Dv + 31) / 32);
-  hipLaunchKernelGGL((delta_scan_kernel<DK, 2>), dim3(unsigned(grid)), dim3(kScanThreads), 0, stream, a);
+  hipLaunchKernelGGL((delta_scan_kernel<DK>), dim3(unsigned(grid)), dim3(kScanThreads), 0, stream, a);
   set_last_kernel("delta_scan");
   return hipGetLastError();
 }

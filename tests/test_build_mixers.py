@@ -12,7 +12,11 @@ def test_no_register_saved_early(src):
     check_lanes(src)
 
 
-def test_scan_holds_two_workgroups_per_cu(resources):  # noqa: F811
-    """Two workgroups of a compute unit hide each other's barriers: two waves a SIMD, two shares of LDS."""
-    figs = [v for k, v in resources.items() if "delta_scan_kernel" in k]
-    assert figs and all(f["occupancy"] >= 2 and 2 * f["lds"] <= 160 * 1024 for f in figs)
+@pytest.mark.parametrize("kernel,waves,groups", [("delta_scan_kernel", 2, 1), ("delta_tree_kernel", 4, 2), ("delta_prep_kernel", 2, 2),
+                                                 ("delta_step_kernel", 5, 5)])
+def test_nothing_spills(resources, kernel, waves, groups):  # noqa: F811
+    """Waves on a SIMD, workgroups whose LDS a compute unit holds, and no scratch memory."""
+    figs = [v for k, v in resources.items() if kernel in k]
+    assert len(figs) >= 2
+    for f in figs:
+        assert f["occupancy"] >= waves and groups * f["lds"] <= 160 * 1024 and f["scratch"] == 0, f

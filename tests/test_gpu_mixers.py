@@ -169,6 +169,49 @@ def test_kv_write_norm_without_norm_effect_is_kv_write(tl, torch):
         np.testing.assert_array_equal(bits(x), bits(y))
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("H,Hq,D,rot,axes,gated,T", [(1, 8, 256, 64, 5, True, 8200), (2, 9, 64, 64, 1, False, 29300), (3, 33, 128, 32, 3, True, 4097)])
+def test_kv_write_norm_of_a_prompt(tl, torch, H, Hq, D, rot, axes, gated, T, e4m3):
+    """Enough rows for workgroups that take several: the same bits as the call cut into short ones, whose values the
+    other tests check."""
+    announce(f"kv_write_norm of a prompt T={T} H={H} Hq={Hq} D={D} e4m3={e4m3}")
+    d, rng = dev(), np.random.default_rng(D)
+    assert T * Hq >= 4096 * (256 // (D // 16)) > 1000 * Hq
+    wide = 2 * D if gated else D
+    x = torch.empty((T, Hq * wide + 2 * H * D + 8), dtype=torch.bfloat16, device=d).normal_(generator=torch.Generator(d).manual_seed(7))
+    q = x[:, :Hq * wide].unflatten(1, (Hq, wide))[..., :D]
+    k, v = (x[:, Hq * wide + i * H * D:][:, :H * D].unflatten(1, (H, D)) for i in (0, 1))
+    wq, wk = (f32_dev(rng.standard_normal(D), d) for _ in "qk")
+    pages = T // 64 + 2
+    slots = rng.permutation(pages * 64)[:T].astype(np.int64)
+    slots[rng.random(T) < 0.05] = -1
+    slots = to_dev(slots, d)
+    positions = to_dev(rng.integers(0, 4096, (axes, T)).astype(np.int32), d)
+    axis_of = to_dev(rng.integers(0, axes, rot // 2).astype(np.int32), d) if axes > 1 else None
+    cs = f32_dev(rng.uniform(-1, 1, (4096, rot)), d)
+    caches, queries = [], []
+    for cut in (T, 1000):
+        kc, vc, ks, vs = tl.kv_cache(pages, H, 64, D, dtype=torch.float8_e4m3fn if e4m3 else torch.bfloat16, device=d)
+        for c in (kc, vc):
+            c.view(torch.uint8).fill_(0x5A)
+        if e4m3:
+            ks.fill_(-3.0)
+            vs.fill_(-3.0)
+        qs = []
+        for lo in range(0, T, cut):
+            at = slice(lo, min(lo + cut, T))
+            pos = positions[:, at].contiguous() if axes > 1 else positions[0, at]
+            qs.append(tl.kv_write_norm(k[at], v[at], slots[at], kc, vc, k_scale=ks, v_scale=vs, q=q[at], q_weight=wq, k_weight=wk,
+                                       positions=pos, cos_sin=cs, axis_of=axis_of))
+        queries.append(torch.cat(qs))
+        caches.append([c for c in (kc, vc, ks, vs) if c is not None])
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(*(bits(y) for y in queries))
+    assert torch.isfinite(queries[0].float()).all()
+    for a, b in zip(*caches):
+        np.testing.assert_array_equal(bits(a), bits(b))
+
+
 # --------------------------------------------------------------------------- steps of requests with states
 class Step:
     """Requests of these lengths: starts, lengths after the step, rows of states; tokens behind the last one."""
@@ -324,6 +367,49 @@ def test_delta_rule(tl, torch, Hk, G, Dk, Dv, raw, lens, form):
     tl.delta_rule(*given, *s.dev(d), stated, **gates, tree_mask=s.mask_dev(d), max_nodes={"step": 1, "chunks": 1000, "trees": 64, "trees and chunks": 130}[form], out=out)
     torch.cuda.synchronize()
     assert tl.last_kernel_name() == {"step": "delta_step", "trees": "delta_tree"}.get(form, "delta_scan")
+    want, after, size = ref.delta_rule(*plain, s.q_start, s.kv_lens, s.slots, state.astype(np.float64), s.mask, Dk ** -0.5,
+                                       np.full((s.T, Hk * G, Dv), -7.0))
+    _check_delta(f64(out), stated.cpu().numpy(), want, after, size, state, s.q_start[-1])
+
+
+@pytest.mark.parametrize("op", ["conv", "step", "chunks", "trees", "trees and chunks", "commit"])
+@pytest.mark.parametrize("R", [64, 65, 300, 513])
+def test_many_requests(tl, torch, R, op):
+    """More requests than a wave's lanes, than a workgroup's, than twice that; and more columns than a tree's workgroup has."""
+    announce(f"{op} of {R} requests")
+    d, rng = dev(), np.random.default_rng(R)
+    lens = rng.integers(0, 4, R)
+    lens[[0, R // 2, R - 1]] = 66, 20, 9
+    s = Step(lens, rng, trees="trees" in op or op == "commit")
+    Hk, G, Dk, Dv = 1, 2, 64, 144
+    plain, given, _, state = _delta_inputs(s, Hk, G, Dk, Dv, rng, False, d)
+    stated = to_dev(state, d)
+    if op == "conv":
+        x, w = spec.bf16(rng.standard_normal((s.T, 64))), rng.standard_normal((64, 4)).astype(np.float32)
+        conv = spec.bf16(rng.standard_normal((s.states, 3, 64)))
+        convd = bf16_dev(conv, d)
+        got = f64(tl.short_conv(bf16_dev(x, d), to_dev(w, d), *s.dev(d), convd))
+        want, after, err = ref.short_conv(x, w.astype(np.float64), None, s.q_start, s.kv_lens, s.slots, conv, None, 0, 64, 1e-6,
+                                          np.zeros((s.T, 64)))
+        n = s.q_start[-1]
+        assert (np.abs(got - want)[:n] <= (BF16_HALF * np.abs(want) + 1.01 * F32_HALF * err)[:n]).all()
+        np.testing.assert_array_equal(f64(convd), after)
+        return
+    if op == "commit":
+        path = np.sort(rng.random((R, 70)).argsort(1)[:, :4] % np.maximum(lens, 1)[:, None], 1).astype(np.int32)
+        accepted = rng.integers(0, 5, R).astype(np.int32)
+        tl.delta_commit(to_dev(accepted, d), to_dev(path, d), *s.dev(d), *given[1:], stated)
+        torch.cuda.synchronize()
+        want, _ = ref.delta_commit(accepted, path, s.q_start, s.kv_lens, s.slots, *plain[1:], state.astype(np.float64),
+                                   np.zeros((s.T, 8)), np.zeros((s.states, 3, 8)))
+        got = stated.cpu().numpy()
+        for row in range(s.states):
+            assert np.linalg.norm(got[row] - want[row]) <= STATE_TOL * np.linalg.norm(want[row]), row
+        return
+    out = torch.full((s.T, Hk * G, Dv), -7.0, dtype=torch.bfloat16, device=d)
+    tl.delta_rule(*given, *s.dev(d), stated, tree_mask=s.mask_dev(d),
+                  max_nodes={"step": 1, "chunks": 1000, "trees": 64, "trees and chunks": 130}[op], out=out)
+    torch.cuda.synchronize()
     want, after, size = ref.delta_rule(*plain, s.q_start, s.kv_lens, s.slots, state.astype(np.float64), s.mask, Dk ** -0.5,
                                        np.full((s.T, Hk * G, Dv), -7.0))
     _check_delta(f64(out), stated.cpu().numpy(), want, after, size, state, s.q_start[-1])
