@@ -12,6 +12,7 @@
 //   S <- exp(D_last) S + sum_j k_j (exp(D_last - D_j) u_j)^T.
 // T and P need no state: delta_prep_kernel makes them for all chunks at once, and
 // delta_scan_kernel walks a request's chunks with 32 columns of a head's state in registers.
+// Where a call's requests have one chunk each, delta_chunk_kernel does both in one launch.
 //
 // Products run on the bf16 matrix instructions.  q and k are bf16; an f32 operand is the sum
 // of three bf16 parts of 8 bits each, cut off exactly (x = hi + mid + lo), and its products
@@ -1000,14 +1001,14 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   }
 }
 
-// Drafted trees: a workgroup takes one request, value head and 128 columns, makes T and P in LDS
-// and uses them there, in one launch; a wave has 16 columns for all tokens, so K S, R and U
-// stay in its registers from product to product.  A longer request of the call, a chain, goes
-// token by token.
+// Drafted trees, and chains of one chunk: a workgroup takes one request, value head and 128
+// columns, makes T and P in LDS and uses them there, in one launch; a wave has 16 columns for
+// all tokens, so K S, R and U stay in its registers from product to product.  A longer request
+// of the call, a chain, goes token by token.
 constexpr int kFusedThreads = 512;
 
-template <int DK>
-__global__ __launch_bounds__(kFusedThreads, 4) void delta_tree_kernel(const DeltaArgs a) {
+template <int DK, bool TREE>
+__global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const DeltaArgs a) {
   constexpr int NS = DK / 32, PITCH = kChunk + 4;
   struct Operands {
     u32x4 K[4][NS][64], QT[kTParts * kTriangle * 64];    // K's; Q's, then T's
@@ -1019,7 +1020,7 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_tree_kernel(const Delt
   __shared__ u32x4 s_P[kPParts * kTriangle * 64];
   __shared__ f32x4 s_T[kTriangle][64];                   // T's blocks below the diagonal, as results lie
   __shared__ double s_total[kChunk];
-  __shared__ __attribute__((aligned(16))) float s_b[kChunk], s_grown[kChunk];
+  __shared__ __attribute__((aligned(16))) float s_b[kChunk], s_grown[kChunk], s_left[kChunk];
   __shared__ uint64_t s_seen[kChunk], s_bad[5];
   static_assert(sizeof(lds.QT) >= sizeof(lds.K) && sizeof(lds) >= sizeof(StepShared<DK>), "Q fits where T is");
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
@@ -1045,7 +1046,7 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_tree_kernel(const Delt
       step_request<DK, false>(a, rq, h, 0, 128 * cb + c, rq.n, nullptr, step, tid < kThreads);
     return;
   }
-  const float *state = a.state + ((int64_t(rq.row) * a.Hv + h) * DK + 8 * g) * a.Dv + col;
+  float *state = a.state + ((int64_t(rq.row) * a.Hv + h) * DK + 8 * g) * a.Dv + col;
   const int64_t t0 = rq.first;
   const int n = rq.n;
   const bool wide = n > 32;                              // else the tokens of tiles 2 and 3 are not there
@@ -1062,11 +1063,12 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_tree_kernel(const Delt
   // K (four waves) and Q (the others) of row tile `rt`; past the last token it is the last one
   const int rt = wave & 3;
   if (wave == 7) {                                     // and the gates
-    const Chunk64 x = tokens_of(a, t0, n, h, lane, true);
+    const Chunk64 x = tokens_of(a, t0, n, h, lane, TREE);
     s_total[lane] = x.total;
     s_b[lane] = x.b;
     s_seen[lane] = x.seen;
     s_grown[lane] = lane < n ? __builtin_amdgcn_exp2f(float(x.total)) : 0.0f;
+    if (!TREE) s_left[lane] = lane < n ? __builtin_amdgcn_exp2f(float(x.end - x.total)) : 0.0f;
     if (lane == 0) s_bad[4] = x.lost;
   }
   if (32 * (rt >> 1) < n) {
@@ -1304,16 +1306,51 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_tree_kernel(const Delt
         if (i < n) out[i * out_row] = uint16_t(pack_bf16(a.scale * o[t][e], 0.0f));
       }
     }
+    if constexpr (!TREE) {                             // S = exp(D_last) S + K^T (exp(D_last - D) U)
+      const float decay = s_grown[n - 1];
+      u32x4 w[2][3];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        if (s == 0 || wide) {
+          const f32x4 *left = reinterpret_cast<const f32x4 *>(s_left + 32 * s + 8 * g);
+          cut<3>(both(left[0] * U[2 * s], left[1] * U[2 * s + 1]), w[s]);
+        }
+#pragma unroll
+      for (int t = 0; t < 2 * NS; ++t) {
+        float *to = state + int64_t(32 * (t >> 1) + 4 * (t & 1)) * a.Dv;
+        f32x4 next = {0, 0, 0, 0};
+        if (!rq.fresh)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) next[e] = decay * to[int64_t(e) * a.Dv];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          if (s == 0 || wide) {
+            const u32x4 key = transposed(s_K[2 * s][t >> 1][lane], s_K[2 * s + 1][t >> 1][lane], t & 1, m, g);
+#pragma unroll
+            for (int e = 2; e >= 0; --e) next = mfma(key, w[s][e], next);
+          }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to[int64_t(e) * a.Dv] = gone ? __builtin_nanf("") : next[e];
+      }
+    }
   }
 }
 
-// Which kernels take a call: one launch for trees, unless prompts' chunks come with them; token
-// by token for few tokens; chunks prepared beforehand for the rest.
-constexpr int64_t kStepTokens = 8;
-enum class Form { kStep, kTree, kScan };
+// Which kernels take a call: token by token for few tokens, one launch for trees and chains
+// of one chunk, chunks prepared beforehand for the rest.  With 48 heads of 128 x 128, us:
+//   chains of tokens       1     4     6     8    16    32    64
+//   1 request:   step    4.9   7.2   8.8  10.4  17.0  30.4  56.7
+//                chunk  11.7  11.7  11.8  11.9  11.8  11.9  15.9
+//                scan   13.1  13.4  13.4  13.6  13.8  14.5  19.3
+//   64 requests: step   62.7  88.9   114   133   233   438   860
+//                chunk   103   107   108   107   110   118   166
+//                scan    244   253   256   260   266   275   332
+// Trees of 64 take 15 us for one request, 122 for 64; in the scan's chunks 21 and 293.
+constexpr int64_t kStepTokens = 6;
+enum class Form { kStep, kChunk, kScan };
 Form form_of(int64_t max_nodes, bool tree) {
-  if (tree && max_nodes <= kTreeNodes) return Form::kTree;
-  return max_nodes <= kStepTokens ? Form::kStep : Form::kScan;
+  if (!tree && max_nodes <= kStepTokens) return Form::kStep;
+  return max_nodes <= kChunk ? Form::kChunk : Form::kScan;
 }
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 int64_t chunks_of(int64_t T, int64_t R) { return T / kChunk + R; }
@@ -1327,9 +1364,11 @@ hipError_t run(DeltaArgs a, Form form, hipStream_t stream) {
     set_last_kernel("delta_step");
     return hipGetLastError();
   }
-  if (form == Form::kTree) {
-    hipLaunchKernelGGL((delta_tree_kernel<DK>), dim3(unsigned(heads * ((a.Dv + 127) / 128))), dim3(kFusedThreads), 0, stream, a);
-    set_last_kernel("delta_tree");
+  if (form == Form::kChunk) {
+    const dim3 grid(unsigned(heads * ((a.Dv + 127) / 128)));
+    if (a.tree_mask) hipLaunchKernelGGL((delta_chunk_kernel<DK, true>), grid, dim3(kFusedThreads), 0, stream, a);
+    else hipLaunchKernelGGL((delta_chunk_kernel<DK, false>), grid, dim3(kFusedThreads), 0, stream, a);
+    set_last_kernel(a.tree_mask ? "delta_tree" : "delta_chunk");
     return hipGetLastError();
   }
   hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(unsigned(chunks_of(a.T, a.R)), unsigned((a.Hv + 3) / 4)), dim3(kThreads), 0, stream, a);

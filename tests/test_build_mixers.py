@@ -12,7 +12,7 @@ def test_no_register_saved_early(src):
     check_lanes(src)
 
 
-@pytest.mark.parametrize("kernel,waves,groups", [("delta_scan_kernel", 2, 1), ("delta_tree_kernel", 4, 2), ("delta_prep_kernel", 2, 2),
+@pytest.mark.parametrize("kernel,waves,groups", [("delta_scan_kernel", 2, 1), ("delta_chunk_kernel", 4, 2), ("delta_prep_kernel", 2, 2),
                                                  ("delta_step_kernel", 5, 5)])
 def test_nothing_spills(resources, kernel, waves, groups):  # noqa: F811
     """Waves on a SIMD, workgroups whose LDS a compute unit holds, and no scratch memory."""

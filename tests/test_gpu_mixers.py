@@ -18,6 +18,9 @@ F32_HALF = 2.0 ** -24
 # with independent signs: 14 half steps for each sum and the few roundings around it, over the chunks that the state
 # remembers.  With decays and steps of these tests that is at most 16 of them, 4 in the root: 56.
 STATE_TOL = 64 * F32_HALF
+# of each form of the delta rule a max_nodes that takes it
+FORMS = {"step": 1, "one chunk": 64, "chunks": 1000, "trees": 64, "trees and chunks": 130}
+KERNEL = {"step": "delta_step", "one chunk": "delta_chunk", "trees": "delta_tree"}
 # P and S^T q reach the output as two parts of 8 bits each, the first cut off: 2^-16 of each term, in both operands
 PARTS = 2.0 ** -14
 
@@ -349,7 +352,7 @@ def _check_delta(got, got_state, want, want_state, size, before, tokens):
             assert miss <= STATE_TOL * np.linalg.norm(want_state[row]), (row, miss / np.linalg.norm(want_state[row]))
 
 
-@pytest.mark.parametrize("form", ["step", "chunks", "trees", "trees and chunks"])
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("lens", LENGTHS, ids=str)
 @pytest.mark.parametrize("Hk,G,Dk,Dv,raw", [(1, 1, 64, 16, False), (2, 3, 128, 128, True), (3, 1, 64, 80, True), (1, 4, 128, 48, False)])
 def test_delta_rule(tl, torch, Hk, G, Dk, Dv, raw, lens, form):
@@ -364,15 +367,15 @@ def test_delta_rule(tl, torch, Hk, G, Dk, Dv, raw, lens, form):
             state[s.slots[r]] = np.inf
     stated = to_dev(state, d)
     out = torch.full((s.T, Hk * G, Dv), -7.0, dtype=torch.bfloat16, device=d)
-    tl.delta_rule(*given, *s.dev(d), stated, **gates, tree_mask=s.mask_dev(d), max_nodes={"step": 1, "chunks": 1000, "trees": 64, "trees and chunks": 130}[form], out=out)
+    tl.delta_rule(*given, *s.dev(d), stated, **gates, tree_mask=s.mask_dev(d), max_nodes=FORMS[form], out=out)
     torch.cuda.synchronize()
-    assert tl.last_kernel_name() == {"step": "delta_step", "trees": "delta_tree"}.get(form, "delta_scan")
+    assert tl.last_kernel_name() == KERNEL.get(form, "delta_scan")
     want, after, size = ref.delta_rule(*plain, s.q_start, s.kv_lens, s.slots, state.astype(np.float64), s.mask, Dk ** -0.5,
                                        np.full((s.T, Hk * G, Dv), -7.0))
     _check_delta(f64(out), stated.cpu().numpy(), want, after, size, state, s.q_start[-1])
 
 
-@pytest.mark.parametrize("op", ["conv", "step", "chunks", "trees", "trees and chunks", "commit"])
+@pytest.mark.parametrize("op", ["conv", *FORMS, "commit"])
 @pytest.mark.parametrize("R", [64, 65, 300, 513])
 def test_many_requests(tl, torch, R, op):
     """More requests than a wave's lanes, than a workgroup's, than twice that; and more columns than a tree's workgroup has."""
@@ -408,21 +411,21 @@ def test_many_requests(tl, torch, R, op):
         return
     out = torch.full((s.T, Hk * G, Dv), -7.0, dtype=torch.bfloat16, device=d)
     tl.delta_rule(*given, *s.dev(d), stated, tree_mask=s.mask_dev(d),
-                  max_nodes={"step": 1, "chunks": 1000, "trees": 64, "trees and chunks": 130}[op], out=out)
+                  max_nodes=FORMS[op], out=out)
     torch.cuda.synchronize()
     want, after, size = ref.delta_rule(*plain, s.q_start, s.kv_lens, s.slots, state.astype(np.float64), s.mask, Dk ** -0.5,
                                        np.full((s.T, Hk * G, Dv), -7.0))
     _check_delta(f64(out), stated.cpu().numpy(), want, after, size, state, s.q_start[-1])
 
 
-@pytest.mark.parametrize("form", ["step", "chunks", "trees", "trees and chunks"])
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("kind", ["resets", "far", "same keys", "no steps", "kept"])
 def test_delta_rule_extremes(tl, torch, kind, form):
     """Decays of exp(-inf) and far below any exponent between ordinary ones, the same key again and again with a step
     of one (the solved system at its worst), steps of zero, and no decay at all."""
     announce(f"delta_rule extremes {kind} {form}")
     d, rng = dev(), np.random.default_rng(11)
-    lens = [64, 40, 1] if "trees" in form else [150, 64, 1]
+    lens = [64, 40, 1] if "trees" in form or form == "one chunk" else [150, 64, 1]
     s = Step(np.array(lens), rng, trees="trees" in form)
     (q, k, v, g, b), (qd, kd, vd, ad, bd), _, state = _delta_inputs(s, 2, 2, 64, 32, rng, False, d)
     if kind == "resets":
@@ -440,7 +443,7 @@ def test_delta_rule_extremes(tl, torch, kind, form):
     stated = to_dev(state, d)
     out = torch.full((s.T, 4, 32), -7.0, dtype=torch.bfloat16, device=d)
     tl.delta_rule(qd, bf16_dev(k, d), vd, to_dev(g, d), to_dev(b, d), *s.dev(d), stated, tree_mask=s.mask_dev(d),
-                  max_nodes={"step": 1, "trees and chunks": 100}.get(form, 64), out=out)
+                  max_nodes=FORMS[form], out=out)
     torch.cuda.synchronize()
     want, after, size = ref.delta_rule(q, k, v, g.astype(np.float64), b.astype(np.float64), s.q_start, s.kv_lens, s.slots,
                                        state.astype(np.float64), s.mask, 0.125, np.full((s.T, 4, 32), -7.0))
@@ -452,7 +455,7 @@ def test_delta_rule_not_finite_stays_where_it_is(tl, torch):
     other requests or other branches."""
     announce("delta_rule with NaN and infinities beside")
     d, rng = dev(), np.random.default_rng(5)
-    for form in ("step", "chunks", "trees"):
+    for form in FORMS:
         s = Step(np.array([20, 40, 33]), rng, behind=64, trees="trees" in form)
         if "trees" in form:                               # request 1: two chains from the root, 1..19 and 20..39
             first = int(s.q_start[1])
@@ -469,7 +472,7 @@ def test_delta_rule_not_finite_stays_where_it_is(tl, torch):
             x[rows] = fill
         stated = to_dev(state, d)
         out = torch.full((s.T, 2, 32), -7.0, dtype=torch.bfloat16, device=d)
-        tl.delta_rule(q, k, v, a, b, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes={"step": 1, "trees and chunks": 100}.get(form, 64), out=out)
+        tl.delta_rule(q, k, v, a, b, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes=FORMS[form], out=out)
         torch.cuda.synchronize()
         want, after, size = ref.delta_rule(*plain, s.q_start, s.kv_lens, s.slots, state.astype(np.float64), s.mask, 128 ** -0.5,
                                            np.full((s.T, 2, 32), -7.0))
@@ -486,12 +489,12 @@ def test_delta_rule_not_finite_stays_where_it_is(tl, torch):
             assert np.linalg.norm(stated.cpu().numpy()[row] - after[row]) <= STATE_TOL * np.linalg.norm(after[row]), (form, r)
 
 
-@pytest.mark.parametrize("op", ["conv", "step", "chunks", "trees", "commit"])
+@pytest.mark.parametrize("op", ["conv", *FORMS, "commit"])
 @pytest.mark.parametrize("starts", [[0, 5, 3, 9], [-1, 2, 3, 9], [0, 2, 3, 10], [9, 0, 0, 0], [0, 0, 12, 9]], ids=str)
 def test_starts_that_fall_write_nothing(tl, torch, starts, op):
     announce(f"starts {starts} {op}")
     d, rng = dev(), np.random.default_rng(2)
-    s = Step(np.array([3, 3, 3]), rng, behind=0, trees=op in ("trees", "commit"))
+    s = Step(np.array([3, 3, 3]), rng, behind=0, trees="trees" in op or op == "commit")
     s.q_start = np.array(starts, dtype=np.int32)
     _, (q, k, v, a, b), _, state = _delta_inputs(s, 1, 1, 64, 16, rng, False, d)
     stated = to_dev(state, d)
@@ -507,28 +510,29 @@ def test_starts_that_fall_write_nothing(tl, torch, starts, op):
                         a, b, stated, x=x, conv_state=conv)
     else:
         out = torch.full((9, 1, 16), -7.0, dtype=torch.bfloat16, device=d)
-        tl.delta_rule(q, k, v, a, b, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes=1 if op == "step" else 64, out=out)
+        tl.delta_rule(q, k, v, a, b, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes=FORMS[op], out=out)
     torch.cuda.synchronize()
     assert (out == -7.0).all()
     assert torch.equal(stated, before[0]) and torch.equal(conv, before[1])
 
 
 @pytest.mark.parametrize("what", ["q", "k", "v", "a", "b"])
-@pytest.mark.parametrize("form", ["step", "chunks", "trees", "trees and chunks"])
+@pytest.mark.parametrize("form", FORMS)
 def test_delta_rule_not_finite_later_tokens_only(tl, torch, form, what):
     """A token whose rows are not finite spoils its own result and those of the tokens that see it, and no other's."""
     announce(f"delta_rule with a {what} that is not finite, {form}")
     d, rng = dev(), np.random.default_rng(6)
-    s = Step(np.array([50 if "trees" in form else 150]), rng, trees="trees" in form)
+    short = "trees" in form or form == "one chunk"
+    s = Step(np.array([50 if short else 150]), rng, trees="trees" in form)
     plain, given, _, state = _delta_inputs(s, 1, 2, 64, 32, rng, False, d)
-    at = 21 if "trees" in form else 90
+    at = 21 if short else 90
     given = [x.clone() for x in given]
     j = "qkvab".index(what)
     given[j][at, 0] = float("nan") if what in "qa" else float("inf")
     if what == "v":
         given[j][at, 0, 3:] = given[j][at + 1, 0, 3:]      # columns 0 to 2 of head 0 only
     stated = to_dev(state, d)
-    out = tl.delta_rule(*given, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes={"step": 1, "trees and chunks": 100}.get(form, 64))
+    out = tl.delta_rule(*given, *s.dev(d), stated, tree_mask=s.mask_dev(d), max_nodes=FORMS[form])
     torch.cuda.synchronize()
     v = plain[2].copy()
     if what == "v":
@@ -615,7 +619,7 @@ def test_states_past_32_bits(tl, torch):
     s.kv_lens = (np.array([70, 3]) + 5).astype(np.int32)
     small = np.array([1, 0], np.int32)
     s.slots = np.array([states - 1, states - 2], np.int32)
-    for form in (1, 64):
+    for form in (1, 64, 1000):
         pool[states - 2:] = to_dev(state[:2], d)
         out = torch.full((s.T, Hk * G, Dv), -7.0, dtype=torch.bfloat16, device=d)
         tl.delta_rule(*given, *s.dev(d), pool, max_nodes=form, out=out)
@@ -698,6 +702,11 @@ def test_a_step_captured_and_replayed(tl, torch):
     as_tree = to_dev(np.array([(1 << i + 1) - 1 for n in s.lens for i in range(n)], dtype=np.uint64).view(np.int64), d)
     a = tl.delta_rule(*given, *s.dev(d), chain_state, max_nodes=64)
     b = tl.delta_rule(*given, *s.dev(d), tree_state, tree_mask=as_tree, max_nodes=64)
+    parts_state = state0[:s.states].clone()
+    c = tl.delta_rule(*given, *s.dev(d), parts_state, max_nodes=65)
+    torch.cuda.synchronize()
+    assert (parts_state - chain_state).norm() <= 2 * STATE_TOL * chain_state.norm()
+    assert (c.double() - a.double()).norm() <= 2 * BF16_HALF * a.double().norm()
     assert torch.equal(a, b) and torch.equal(tree_state, state0[:s.states])
     tl.delta_commit(to_dev(s.lens.astype(np.int32), d), to_dev(np.tile(np.arange(64, dtype=np.int32), (3, 1)), d), *s.dev(d), *given[1:], tree_state)
     torch.cuda.synchronize()

@@ -115,7 +115,8 @@ def test_delta_rejections():
     L = tl.lib()
     size = L.tl_delta_rule_workspace_size
     assert size(64, 64, 16, 3, 128, 1, 0) == 0 and size(64, 64, 16, 3, 128, 64, 1) == 0      # one launch each
-    assert size(64, 64, 16, 3, 128, 65, 1) > 0 and size(100, 2, 16, 3, 128, 50, 0) > 0
+    assert size(100, 2, 16, 3, 128, 64, 0) == 0
+    assert size(64, 64, 16, 3, 128, 65, 1) > 0 and size(100, 2, 16, 3, 128, 65, 0) > 0
     for bad in ((-1, 2, 1, 1, 64, 50, 0), (9, -1, 1, 1, 64, 50, 0), (9, 4097, 1, 1, 64, 50, 0), (9, 2, 0, 1, 64, 50, 0),
                 (9, 2, 1, 1, 32, 50, 0), (9, 2, 1, 1, 64, 0, 0), (9, 2, 65536, 1, 64, 50, 0)):
         assert size(*bad) == 0, bad
