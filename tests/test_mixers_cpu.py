@@ -183,3 +183,27 @@ def test_binding_refuses():
         tl.delta_commit(i32(1), i32(1, 4), i32(2), i32(1), i32(1), x, x, torch.zeros(2, 2), torch.zeros(2, 2), torch.zeros(1, 2, 64, 64))
     with pytest.raises(TypeError):
         tl.short_conv([1], torch.zeros(64, 4), i32(2), i32(1), i32(1), None)
+
+
+def test_the_plain_hybrid_decoder_goes_on_where_it_stopped():
+    """Its states and rows carry everything: a history in parts is the history; a token lost from the states shows in
+    every later logit and in none before."""
+    from oracle.hybrid import Decoder
+    rng = np.random.default_rng(0)
+    Hk, Hv, Dk, Dv, taps = 2, 4, 32, 256, 3
+    C = 2 * Hk * Dk + Hv * Dv
+    linear = lambda K, N: (rng.integers(-1, 2, (N, K)).astype(np.int8), np.full((N, K // 128), (1.5 / K) ** 0.5, np.float16))
+    layer = lambda N, K: [linear(1024, N), linear(K, 1024), linear(1024, 2048), linear(1024, 1024)]
+    angle = rng.uniform(0, 6, (64, 16))
+    w = dict(embed=rng.standard_normal((32, 1024)), taps=rng.standard_normal((2, C, taps)), gates=rng.standard_normal((2, 1024, 2 * Hv)) / 32,
+             a_log=rng.standard_normal((2, Hv)) - 2, dt_bias=rng.standard_normal((2, Hv)), q_weight=rng.standard_normal((1, 128)),
+             k_weight=rng.standard_normal((1, 128)), cos_sin=np.concatenate([np.cos(angle), np.sin(angle)], 1))
+    d = Decoder(w, [layer(C, Hv * Dv) for _ in range(2)], [layer(10 * 128, 1024)], linear(1024, 32), (8, 1, 128, Hk, Hv, Dk, Dv), True)
+    tokens = rng.integers(0, 32, 20).tolist()
+    y, _ = d.rows(tokens, None)
+    a, state = d.rows(tokens[:7], None)
+    b, _ = d.rows(tokens[7:], state)
+    np.testing.assert_allclose(np.concatenate([a, b]), y, atol=1e-9)
+    assert d.greedy(tokens, 2)[0] == np.argmax(y[-1])
+    far = np.sqrt(((d.rows(tokens, None, {9})[0] - y) ** 2).mean(-1))
+    assert (far[:10] == 0).all() and (far[10:] > 0.1).all()
