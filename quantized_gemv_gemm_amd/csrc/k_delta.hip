@@ -266,8 +266,10 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a,
 
 // ---------------------------------------------------------------------------
 // Chunks.  The workspace holds, for each chunk and value head, T and P as the matrix
-// instructions take their first operand, and the decays; for each chunk and key head, K
-// transposed.  A 16x16x32 operand is 64 lanes of 16 bytes: lane 16 g + m holds row m, columns
+// instructions take their first operand, and the decays; for each chunk and key head, K, Q
+// and K transposed in the same order.  (The scan's workgroups would else ask for rows that
+// lie a token of all heads apart, in halves of lines and mostly in the same few channels of
+// an L2: a call for 8191 tokens of 48 heads of 128 x 128 took 395 us, this way 370.)  A 16x16x32 operand is 64 lanes of 16 bytes: lane 16 g + m holds row m, columns
 // 8 g .. 8 g + 7 of 32.  Its result's lane 16 g + m holds column m, rows 4 g .. 4 g + 3.  Rows
 // are dealt to pairs of tiles so that a pair's results are the next product's second operand
 // as they stand: row m of tile 2 s + p is token (or element of k)
@@ -282,7 +284,7 @@ constexpr int kTriangle = 6;
 constexpr int kTParts = 3, kPParts = 2;
 constexpr int kDecays = (kTParts + kPParts) * kTriangle * kTile;  // behind T and P: three lists of 64
 constexpr int kHeadBytes = kDecays + 3 * kChunk * 4;      // the third: exp(D_last) and a word of tokens
-__host__ __device__ constexpr int key_bytes(int DK) { return kChunk * DK * 2; }
+__host__ __device__ constexpr int key_bytes(int DK) { return 3 * kChunk * DK * 2; }
 
 // three (PARTS = 3) or two bf16 parts of 8 floats, as an operand's lane holds them
 template <int PARTS>
@@ -426,8 +428,8 @@ __device__ __forceinline__ u32x4 transposed(u32x4 lower, u32x4 higher, int p, in
   return u32x4{upper(x[0], x[1]), upper(x[2], x[3]), upper(y[0], y[1]), upper(y[2], y[3])};
 }
 
-// One wave makes T and P of one chunk and value head, and for the first head of a key head K
-// transposed; four heads share a workgroup, and waves never wait for each other.  All of K
+// One wave makes T and P of one chunk and value head, and for the first and last head of a key
+// head K's and Q's operands; four heads share a workgroup, and waves never wait for each other.  All of K
 // stays in registers as operands.  A lies in LDS; its diagonal blocks of 16 are solved column
 // by column, a lane each (T_ii = (I + A_ii)^-1), and the blocks below follow by
 // T_ij = -T_ii sum over k of A_ik T_kj on the f32 matrix instruction, whose steps take rows
@@ -493,14 +495,25 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
     if (lane == 0) *reinterpret_cast<f32x4 *>(to + 2 * kChunk) =
         f32x4{__builtin_amdgcn_exp2f(float(mine.end)), 0.0f, __uint_as_float(uint32_t(bad)), __uint_as_float(uint32_t(bad >> 32))};
   }
-  if (h % a.G == 0 && !tree) {
-    u32x4 *to = reinterpret_cast<u32x4 *>(a.keys + (int64_t(number) * a.Hk + kh) * key_bytes(DK));
+  const int share = h % a.G;                             // the key head's operands, by its first and last value head
+  u32x4 *keys = reinterpret_cast<u32x4 *>(a.keys + (int64_t(number) * a.Hk + kh) * key_bytes(DK)) + lane;
+  if (share == 0) {
 #pragma unroll
-    for (int t = 0; t < DK / 16; ++t)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
-        to[(t * 2 + s) * 64 + lane] = transposed(k[2 * s][t >> 1], k[2 * s + 1][t >> 1], t & 1, m, g);
+      for (int c = 0; c < NS; ++c) keys[(t * NS + c) * 64] = k[t][c];
+    if (!tree)
+#pragma unroll
+      for (int t = 0; t < DK / 16; ++t)
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          keys[(8 * NS + t * 2 + s) * 64] = transposed(k[2 * s][t >> 1], k[2 * s + 1][t >> 1], t & 1, m, g);
   }
+  if (share == a.G - 1)
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int c = 0; c < NS; ++c) keys[((4 + t) * NS + c) * 64] = q[t][c];
   wave_sync();
 
   // (K K^T)^T and (Q K^T)^T: a lane holds token i = dealt(t, m) against 8 consecutive j's
@@ -644,9 +657,10 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   }
   const bool tree = a.tree_mask && n <= kTreeNodes, fresh = rq.fresh;
   const int64_t number = int64_t(first) / kChunk + r;
-  const int row0 = 32 * (wave >> 1) + 8 * g + 4 * (wave & 1), pairs = (wave >> 1) + 1, i = dealt(wave, m);
+  const int row0 = 32 * (wave >> 1) + 8 * g + 4 * (wave & 1), pairs = (wave >> 1) + 1;
   const int last = (n - 1) / kChunk;
   auto head_of = [&](int part) { return a.heads + ((number + part) * a.Hv + h) * kHeadBytes; };
+  auto key_of = [&](int part) { return reinterpret_cast<const u32x4 *>(a.keys + ((number + part) * a.Hk + kh) * key_bytes(DK)) + lane; };
   // tokens that a column's results, and the state after them, must not have seen
   auto not_finite = [&](uint64_t bad, uint64_t (&gone)[CT]) {
 #pragma unroll
@@ -657,14 +671,10 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   if (all_waves >= 4) {                                  // out = scale (exp(D) Q S + P U)
     u32x4 Q[NS], P[2][kPParts];
     f32x4 grown, end;
-    const uint16_t *to_q;
-    auto row_of = [&](int part) {
-      const int most = min(kChunk, n - part * kChunk) - 1;
-      to_q = a.q + (int64_t(first) + part * kChunk + min(i, most)) * a.ldq + kh * DK + 8 * g;
-    };
     auto fetch_row = [&](int part) {
+      const u32x4 *from = key_of(part) + (4 + wave) * NS * 64;
 #pragma unroll
-      for (int s = 0; s < NS; ++s) Q[s] = *reinterpret_cast<const u32x4 *>(to_q + 32 * s);
+      for (int s = 0; s < NS; ++s) Q[s] = from[s * 64];
       grown = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + row0 * 4);
       end = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + 2 * kChunk * 4);
     };
@@ -675,7 +685,6 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
 #pragma unroll
         for (int e = 0; e < kPParts; ++e) P[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
     };
-    row_of(0);
     fetch_row(0);
     fetch_weights(0);
     auto chunk = [&](int part, auto whole) {
@@ -708,11 +717,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
           for (int e = 0; e < 4; ++e) o[c][e] *= grown[e];
       }
       __syncthreads();
-      if constexpr (more) {
-        if (n - part * kChunk >= 2 * kChunk) to_q += kChunk * a.ldq;
-        else row_of(part + 1);
-        fetch_row(part + 1);
-      }
+      if constexpr (more) fetch_row(part + 1);
       __syncthreads();
       if (rows) {
         auto add = [&](auto two) {
@@ -780,17 +785,17 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   uint32_t V[4];                                         // two columns of a row
   f32x4 grown, left, end;                                // end: exp(D_last), nothing, a word of tokens
   const int vcol = h * a.Dv + col;
-  const uint16_t *to_k, *to_v[4];                 // this lane's rows of the chunk that is asked for next
+  const uint16_t *to_v[4];                               // this lane's rows of the chunk that is asked for next
   auto rows_of = [&](int part) {
     const int most = min(kChunk, n - part * kChunk) - 1;
-    const int64_t t0 = int64_t(first) + part * kChunk, t = t0 + min(i, most);
-    to_k = a.k + t * a.ldk + kh * DK + 8 * g;
+    const int64_t t0 = int64_t(first) + part * kChunk;
 #pragma unroll
     for (int e = 0; e < 4; ++e) to_v[e] = a.v + (t0 + min(row0 + e, most)) * a.ldv + vcol;
   };
   auto fetch_rows = [&](int part) {
+    const u32x4 *from = key_of(part) + wave * NS * 64;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) K[s] = *reinterpret_cast<const u32x4 *>(to_k + 32 * s);
+    for (int s = 0; s < NS; ++s) K[s] = from[s * 64];
 #pragma unroll
     for (int e = 0; e < 4; ++e) V[e] = *reinterpret_cast<const uint32_t *>(to_v[e]);
     grown = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + row0 * 4);
@@ -806,7 +811,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
     left = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + (kChunk + row0) * 4);
   };
   auto fetch_keys = [&](int part) {
-    const u32x4 *kt = reinterpret_cast<const u32x4 *>(a.keys + ((number + part) * a.Hk + kh) * key_bytes(DK)) + lane;
+    const u32x4 *kt = key_of(part) + 8 * NS * 64;
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -891,6 +896,15 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
       }
     }
     if (more || !tree) fetch_keys(part);
+    if constexpr (more) {
+      if (n - part * kChunk >= 2 * kChunk) {             // the next chunk is whole
+#pragma unroll
+        for (int e = 0; e < 4; ++e) to_v[e] += kChunk * a.ldv;
+      } else {
+        rows_of(part + 1);
+      }
+      fetch_rows(part + 1);
+    }
     __syncthreads();
     const bool some = s_some || bad;
     if (rows) {                                          // U = T R
@@ -938,16 +952,6 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
         reinterpret_cast<u32x2 *>(&s_U[0][c][wave >> 1][lane])[wave & 1] = hi;
         reinterpret_cast<u32x2 *>(&s_U[1][c][wave >> 1][lane])[wave & 1] = lo;
       }
-    }
-    if constexpr (more) {
-      if (n - part * kChunk >= 2 * kChunk) {             // the next chunk is whole
-        to_k += kChunk * a.ldk;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) to_v[e] += kChunk * a.ldv;
-      } else {
-        rows_of(part + 1);
-      }
-      fetch_rows(part + 1);
     }
     __syncthreads();
     if (holds && !tree) {                                // S = exp(D_last) S + K^T (exp(D_last - D) U)
