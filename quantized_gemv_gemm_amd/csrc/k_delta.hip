@@ -360,18 +360,21 @@ __device__ __forceinline__ Chunk64 sum_gates(const DeltaArgs &a, const GateRow &
     }
   } else {
     const uint64_t mine = __builtin_bit_cast(uint64_t, c.total);
-    c.total = 0.0;
-    for (int j = 0; j < n; ++j) {
-      const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(mine), j), hi = __builtin_amdgcn_readlane(uint32_t(mine >> 32), j);
-      if (c.seen >> j & 1) c.total += __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+    double sum[4] = {0.0, 0.0, 0.0, 0.0};
+    for (int j0 = 0; j0 < n; j0 += 16) {                 // without branches, so that tokens overlap
+      const int bits = int(uint32_t(c.seen >> j0));
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int on = bits << (31 - j) >> 31;
+        const uint32_t lo = __builtin_amdgcn_readlane(uint32_t(mine), j0 + j) & on;
+        const uint32_t hi = __builtin_amdgcn_readlane(uint32_t(mine >> 32), j0 + j) & on;
+        sum[j & 3] += __builtin_bit_cast(double, uint64_t(hi) << 32 | lo);
+      }
     }
+    c.total = sum[0] + sum[1] + (sum[2] + sum[3]);
   }
   c.end = __shfl(c.total, n - 1, 64);
   return c;
-}
-
-__device__ __forceinline__ Chunk64 tokens_of(const DeltaArgs &a, int64_t t0, int n, int h, int lane, bool tree) {
-  return sum_gates(a, ask_gates(a, t0, n, h, lane, tree), n, lane, tree);
 }
 
 // 8 values of k_i k_j and q_i k_j, j = j0 .., become those of A and P
@@ -1054,20 +1057,20 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
   const int64_t t0 = rq.first;
   const int n = rq.n;
   const bool wide = n > 32;                              // else the tokens of tiles 2 and 3 are not there
-  f32x4 S[2 * NS];                                       // tile t, e: row 32 (t / 2) + 8 g + 4 (t % 2) + e
-  if (cols && !rq.fresh) {
-#pragma unroll
-    for (int t = 0; t < 2 * NS; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) S[t][e] = state[int64_t(32 * (t >> 1) + 4 * (t & 1) + e) * a.Dv];
-  } else {
-#pragma unroll
-    for (int t = 0; t < 2 * NS; ++t) S[t] = f32x4{0, 0, 0, 0};
-  }
-  // K (four waves) and Q (the others) of row tile `rt`; past the last token it is the last one
+  // K (four waves) and Q (the others) of row tile `rt`; past the last token it is the last one.
   const int rt = wave & 3;
-  if (wave == 7) {                                     // and the gates
-    const Chunk64 x = tokens_of(a, t0, n, h, lane, TREE);
+  const bool stage = 32 * (rt >> 1) < n;
+  GateRow gates;
+  if (wave == 7) gates = ask_gates(a, t0, n, h, lane, TREE);
+  u32x4 k[NS];
+  if (stage) {
+    const int64_t i = t0 + min(dealt(rt, m), n - 1);
+    const uint16_t *from = (wave < 4 ? a.k + i * a.ldk : a.q + i * a.ldq) + kh * DK + 8 * g;
+#pragma unroll
+    for (int c = 0; c < NS; ++c) k[c] = *reinterpret_cast<const u32x4 *>(from + 32 * c);
+  }
+  if (wave == 7) {
+    const Chunk64 x = sum_gates(a, gates, n, lane, TREE);
     s_total[lane] = x.total;
     s_b[lane] = x.b;
     s_seen[lane] = x.seen;
@@ -1075,12 +1078,7 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
     if (!TREE) s_left[lane] = lane < n ? __builtin_amdgcn_exp2f(float(x.end - x.total)) : 0.0f;
     if (lane == 0) s_bad[4] = x.lost;
   }
-  if (32 * (rt >> 1) < n) {
-    const int64_t i = t0 + min(dealt(rt, m), n - 1);
-    const uint16_t *from = (wave < 4 ? a.k + i * a.ldk : a.q + i * a.ldq) + kh * DK + 8 * g;
-    u32x4 k[NS];
-#pragma unroll
-    for (int c = 0; c < NS; ++c) k[c] = *reinterpret_cast<const u32x4 *>(from + 32 * c);
+  if (stage) {
     if (wave < 4) {
       u16x2 top = {0, 0};                              // an exponent of all ones is what is not finite
 #pragma unroll
@@ -1105,6 +1103,18 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
     s_bad[wave] = 0;
   }
   __syncthreads();
+  // The state comes while T is made: asked for beside K and Q it held them up (16 trees of up
+  // to 64, 48 heads of 128 x 128: 36.9 us, this way 35.2).
+  f32x4 S[2 * NS];                                       // tile t, e: row 32 (t / 2) + 8 g + 4 (t % 2) + e
+  if (cols && !rq.fresh) {
+#pragma unroll
+    for (int t = 0; t < 2 * NS; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) S[t][e] = state[int64_t(32 * (t >> 1) + 4 * (t & 1) + e) * a.Dv];
+  } else {
+#pragma unroll
+    for (int t = 0; t < 2 * NS; ++t) S[t] = f32x4{0, 0, 0, 0};
+  }
   const uint64_t bad = s_bad[0] | s_bad[1] | s_bad[2] | s_bad[3] | s_bad[4];
 
   // A and P of row tile `wave`
@@ -1143,36 +1153,6 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
       for (int e = 0; e < kPParts; ++e) s_P[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = x[e];
     }
   }
-  // K S and Q S of the wave's columns
-  f32x4 R[4], o[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) R[t] = o[t] = f32x4{0, 0, 0, 0};
-  if (cols) {
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      u32x4 y[3];
-      cut<3>(both(S[2 * s], S[2 * s + 1]), y);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (t >= 2 && !wide) break;                    // uniform
-        const u32x4 k = s_K[t][s][lane], q = s_QT[(t * NS + s) * 64 + lane];
-#pragma unroll
-        for (int e = 2; e >= 0; --e) {
-          R[t] = mfma(k, y[e], R[t]);
-          if (e < 2) o[t] = mfma(q, y[e], o[t]);
-        }
-      }
-    }
-  }
-  uint16_t V[4][4];                                    // rows of the four tiles
-  const int64_t ldv = a.ldv;
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + e;
-      V[t][e] = a.v[(t0 + min(i, n - 1)) * ldv + int64_t(h) * a.Dv + col];
-    }
   __syncthreads();
 
   // T: the diagonal blocks, a wave each, then those below, a diagonal after the other
@@ -1216,6 +1196,36 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
     if (off < tiles && wave + off < tiles)
 #pragma unroll
       for (int c = 0; c < 4; ++c) s_A[(16 * (wave + off) + 4 * g + c) * PITCH + 16 * wave + m] = own[off - 1][c];
+  // K S and Q S of the wave's columns
+  f32x4 R[4], o[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) R[t] = o[t] = f32x4{0, 0, 0, 0};
+  if (cols) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      u32x4 y[3];
+      cut<3>(both(S[2 * s], S[2 * s + 1]), y);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (t >= 2 && !wide) break;                    // uniform
+        const u32x4 k = s_K[t][s][lane], q = s_QT[(t * NS + s) * 64 + lane];
+#pragma unroll
+        for (int e = 2; e >= 0; --e) {
+          R[t] = mfma(k, y[e], R[t]);
+          if (e < 2) o[t] = mfma(q, y[e], o[t]);
+        }
+      }
+    }
+  }
+  uint16_t V[4][4];                                    // rows of the four tiles
+  const int64_t ldv = a.ldv;
+#pragma unroll
+  for (int t = 0; t < 4; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = 32 * (t >> 1) + 8 * g + 4 * (t & 1) + e;
+      V[t][e] = a.v[(t0 + min(i, n - 1)) * ldv + int64_t(h) * a.Dv + col];
+    }
   __syncthreads();
   if (wave < 4 && 32 * (wave >> 1) < n) {
     const int i = dealt(wave, m);
@@ -1343,13 +1353,13 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
 // Which kernels take a call: token by token for few tokens, one launch for trees and chains
 // of one chunk, chunks prepared beforehand for the rest.  With 48 heads of 128 x 128, us:
 //   chains of tokens       1     4     6     8    16    32    64
-//   1 request:   step    4.9   7.2   8.8  10.4  17.0  30.4  56.7
-//                chunk  11.7  11.7  11.8  11.9  11.8  11.9  15.9
-//                scan   13.1  13.4  13.4  13.6  13.8  14.5  19.3
-//   64 requests: step   62.7  88.9   114   133   233   438   860
-//                chunk   103   107   108   107   110   118   166
-//                scan    244   253   256   260   266   275   332
-// Trees of 64 take 15 us for one request, 122 for 64; in the scan's chunks 21 and 293.
+//   1 request:   step    5.4   7.2   8.8  10.3  17.1  30.2  56.7
+//                chunk  12.0  12.1  12.1  12.1  12.1  12.1  16.3
+//                scan   13.6  13.8  13.8  13.9  14.2  14.9  19.4
+//   64 requests: step   62.6  88.6   113   142   241   436   860
+//                chunk   106   109   109   110   110   114   165
+//                scan    252   262   265   271   273   282   332
+// Trees of 64 take 13.7 us for one request, 125 for 64; in the scan's chunks 19 and 286.
 constexpr int64_t kStepTokens = 6;
 enum class Form { kStep, kChunk, kScan };
 Form form_of(int64_t max_nodes, bool tree) {
