@@ -147,12 +147,18 @@ hipError_t launch(const ConvArgs &a, hipStream_t stream) {
   return hipGetLastError();
 }
 
-// Long runs read fewer rows twice and the weights less often, once they fill the card twice
-// over (8191 tokens of 10240 channels: 76 us, with runs of 16 tokens 86); short ones else, whose
-// kernel needs fewer registers (a call for one token of each of 64 requests: 8.9 us, with the long ones 9.1).
+// The longest run that leaves two workgroups for each compute unit: long ones read fewer rows
+// twice and the weights less often, short ones have fewer rows to wait for.  One request of
+// 10240 channels, us, with runs of 4, 16, 32 and 64 tokens: 64 tokens 6.3, 14.3, 23.9, 43; 1024
+// 16.6, 18.2, 26, 46; 2048 25.8, 22.2, 27.8, 47; 4096 68, 52, 36, 49; 8191 131, 84, 81, 77.
 template <int W>
 hipError_t run(const ConvArgs &a, hipStream_t stream) {
-  return int64_t(a.T) / 64 * ((a.C + 8 * kThreads - 1) / (8 * kThreads)) >= 512 ? launch<W, 64, 8>(a, stream) : launch<W, 16, 4>(a, stream);
+  const int64_t groups = (a.C + 8 * kThreads - 1) / (8 * kThreads);
+  auto fills = [&](int run) { return a.T / run * groups >= 512; };
+  return fills(64)   ? launch<W, 64, 8>(a, stream)
+         : fills(32) ? launch<W, 32, 8>(a, stream)
+         : fills(16) ? launch<W, 16, 4>(a, stream)
+                     : launch<W, 4, 4>(a, stream);
 }
 
 }  // namespace

@@ -175,8 +175,8 @@ def test_kv_write_norm_without_norm_effect_is_kv_write(tl, torch):
 @pytest.mark.parametrize("e4m3", [False, True])
 @pytest.mark.parametrize("H,Hq,D,rot,axes,gated,T", [(1, 8, 256, 64, 5, True, 8200), (2, 9, 64, 64, 1, False, 29300), (3, 33, 128, 32, 3, True, 4097)])
 def test_kv_write_norm_of_a_prompt(tl, torch, H, Hq, D, rot, axes, gated, T, e4m3):
-    """Enough rows for workgroups that take several: the same bits as the call cut into short ones, whose values the
-    other tests check."""
+    """Thousands of tokens in one call: the same bits as the call cut into short ones, whose values the other tests
+    check."""
     announce(f"kv_write_norm of a prompt T={T} H={H} Hq={Hq} D={D} e4m3={e4m3}")
     d, rng = dev(), np.random.default_rng(D)
     assert T * Hq >= 4096 * (256 // (D // 16)) > 1000 * Hq
@@ -283,21 +283,22 @@ def test_short_conv(tl, torch, taps, C, heads, dim, bias, lens, trees):
     np.testing.assert_array_equal(f64(stated), after)
 
 
+@pytest.mark.parametrize("run,C", [(16, 8192), (32, 12288), (64, 32768)])
 @pytest.mark.parametrize("taps", [2, 3, 4])
-def test_short_conv_long_runs(tl, torch, taps):
-    """Enough tokens and channels for runs of 64 tokens, with requests that end inside a run, and trees among them."""
-    announce(f"short_conv long runs taps={taps}")
+def test_short_conv_long_runs(tl, torch, taps, run, C):
+    """Enough tokens and channels for runs of this many tokens, with requests that end inside a run, and trees among them."""
+    announce(f"short_conv runs of {run} taps={taps}")
     d, rng = dev(), np.random.default_rng(taps)
     s = Step(np.array([1500, 1, 0, 63, 64, 65, 700, 3] + [20] * 70), rng, trees=taps == 3)
-    C = 32768
-    assert s.T // 64 * (C // 2048) >= 512
+    assert s.T // run * (C // 2048) >= 512 and (run == 64 or s.T // (2 * run) * (C // 2048) < 512)
+    heads = C // 128                                                   # half of the channels
     x = spec.bf16(rng.standard_normal((s.T, 64)))
     w = rng.standard_normal((64, taps)).astype(np.float32)
     state = spec.bf16(rng.standard_normal((s.states, taps - 1, 64)))
     wide = lambda a: a.repeat(*([1] * (a.dim() - 1)), C // 64)         # the same 64 channels again and again
     stated = wide(bf16_dev(state, d))
     out = torch.full((s.T, C), -7.0, dtype=torch.bfloat16, device=d)
-    tl.short_conv(wide(bf16_dev(x, d)), to_dev(w, d).repeat(C // 64, 1), *s.dev(d), stated, tree_mask=s.mask_dev(d), norm_heads=256,
+    tl.short_conv(wide(bf16_dev(x, d)), to_dev(w, d).repeat(C // 64, 1), *s.dev(d), stated, tree_mask=s.mask_dev(d), norm_heads=heads,
                   norm_dim=64, out=out)
     torch.cuda.synchronize()
     want, after, err = ref.short_conv(x, w.astype(np.float64), None, s.q_start, s.kv_lens, s.slots, state, s.mask, 1, 64, 1e-6,
@@ -306,8 +307,8 @@ def test_short_conv_long_runs(tl, torch, taps):
                                   np.full((s.T, 64), -7.0))
     got = f64(out).reshape(s.T, C // 64, 64)
     tol = lambda v, e: BF16_HALF * np.abs(v) + 1.01 * F32_HALF * e
-    assert (np.abs(got[:, :256] - want[:, None]) <= tol(want, err)[:, None]).all()
-    assert (np.abs(got[:, 256:] - plain[:, None]) <= tol(plain, e0)[:, None]).all()
+    assert (np.abs(got[:, :heads] - want[:, None]) <= tol(want, err)[:, None]).all()
+    assert (np.abs(got[:, heads:] - plain[:, None]) <= tol(plain, e0)[:, None]).all()
     np.testing.assert_array_equal(f64(stated).reshape(s.states, taps - 1, C // 64, 64), np.repeat(after[:, :, None], C // 64, 2))
 
 
