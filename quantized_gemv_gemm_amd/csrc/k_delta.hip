@@ -272,8 +272,9 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a,
 // instructions take their first operand, and the decays; for each chunk and key head, K, Q
 // and K transposed in the same order.  (The scan's workgroups would else ask for rows that
 // lie a token of all heads apart, in halves of lines and mostly in the same few channels of
-// an L2: a call for 8191 tokens of 48 heads of 128 x 128 took 395 us, this way 370.)  A 16x16x32 operand is 64 lanes of 16 bytes: lane 16 g + m holds row m, columns
-// 8 g .. 8 g + 7 of 32.  Its result's lane 16 g + m holds column m, rows 4 g .. 4 g + 3.  Rows
+// an L2: a call for 8191 tokens of 48 heads of 128 x 128 took 395 us, this way 370.)  A
+// 16x16x32 operand is 64 lanes of 16 bytes: lane 16 g + m holds row m, columns 8 g .. 8 g + 7
+// of 32.  Its result's lane 16 g + m holds column m, rows 4 g .. 4 g + 3.  Rows
 // are dealt to pairs of tiles so that a pair's results are the next product's second operand
 // as they stand: row m of tile 2 s + p is token (or element of k)
 //   32 s + 8 (m / 4) + 4 p + m % 4,
