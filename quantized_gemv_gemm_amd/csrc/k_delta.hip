@@ -624,8 +624,8 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
 }
 
 // A workgroup walks the chunks of one request, head and 32 columns.  Wave w of the first
-// four takes row tile w of the chunk's tokens and, of the state, the rows 32 w .. 32 w + 31 (a
-// pair of tiles), and goes the chain from one chunk's state to the next one's: K S, U, K^T U.
+// four takes row tile w of the chunk's tokens and of the state the tiles TP w .. (a pair for Dk
+// 128, one for Dk 64), and goes the chain from one chunk's state to the next one's: K S, U, K^T U.
 // Wave 4 + w makes the results of row tile w beside it.  The chain's latency bounds it: 8191
 // tokens of 48 heads of 128 x 128 take 285 us, about 4800 cycles a chunk, of which matrix
 // instructions take 1456, LDS reads 1530 at full rate and global loads some 700.  Column m of tile c is column 2 m + c:
@@ -634,8 +634,8 @@ constexpr int kScanThreads = 512;
 
 template <int DK>
 __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const DeltaArgs a) {
-  constexpr int NS = DK / 32, CT = 2;                    // column tiles of the workgroup
-  static_assert(NS <= 4, "a wave holds at most one pair of state tiles");
+  constexpr int NS = DK / 32, CT = 2, TP = DK / 64;      // column tiles of the workgroup, state tiles of a wave
+  static_assert(TP == 1 || TP == 2, "a wave holds a pair of state tiles, or one of a pair");
   __shared__ __attribute__((aligned(16))) u32x4 s_S[3][CT][NS][64], s_R[3][CT][2][64], s_U[2][CT][2][64], s_W[3][CT][2][64];
   __shared__ uint32_t s_bad[16 * CT][2];                 // of each column: tokens whose v is not finite
   __shared__ int s_some;
@@ -772,26 +772,26 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
     return;
   }
 
-  float *state = a.state + ((int64_t(srow) * a.Hv + h) * DK + 32 * wave + 8 * g) * a.Dv + col;
-  const bool holds = wave < NS;
-  f32x4 S[2][CT];                                        // [p][c][e]: row 32 w + 8 g + 4 p + e
-  if (holds && !fresh) {
+  const int state_row = TP == 2 ? 32 * wave + 8 * g : 32 * (wave >> 1) + 8 * g + 4 * (wave & 1);
+  float *state = a.state + ((int64_t(srow) * a.Hv + h) * DK + state_row) * a.Dv + col;
+  f32x4 S[TP][CT];                                       // [p][c][e]: row state_row + 4 p + e
+  if (!fresh) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < TP; ++p)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
         for (int c = 0; c < CT; ++c) S[p][c][e] = state[int64_t(4 * p + e) * a.Dv + c];
   } else {
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < TP; ++p)
 #pragma unroll
       for (int c = 0; c < CT; ++c) S[p][c] = f32x4{0, 0, 0, 0};
   }
 
   // What a wave takes of a chunk.  Each piece is asked for as soon as the chunk before has used
   // it.  Rows past the last token are the last one's: nothing of theirs is kept.
-  u32x4 K[NS], T[2][kTParts], keys[2][2];
+  u32x4 K[NS], T[2][kTParts], keys[TP][2];
   uint32_t V[4];                                         // two columns of a row
   f32x4 grown, left, end;                                // end: exp(D_last), nothing, a word of tokens
   const int vcol = h * a.Dv + col;
@@ -823,19 +823,28 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   auto fetch_keys = [&](int part) {
     const u32x4 *kt = key_of(part) + 8 * NS * 64;
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < TP; ++p)
 #pragma unroll
-      for (int s = 0; s < 2; ++s) keys[p][s] = kt[((2 * (wave % NS) + p) * 2 + s) * 64];
+      for (int s = 0; s < 2; ++s) keys[p][s] = kt[((TP * wave + p) * 2 + s) * 64];
   };
   auto share_state = [&] {                               // S in parts, as the second operand
-    if (!holds) return;
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-      const float x[8] = {S[0][c][0], S[0][c][1], S[0][c][2], S[0][c][3], S[1][c][0], S[1][c][1], S[1][c][2], S[1][c][3]};
-      u32x4 o[3];
-      cut<3>(x, o);
+      if constexpr (TP == 2) {
+        u32x4 o[3];
+        cut<3>(both(S[0][c], S[TP - 1][c]), o);
 #pragma unroll
-      for (int e = 0; e < 3; ++e) s_S[e][c][wave][lane] = o[e];
+        for (int e = 0; e < 3; ++e) s_S[e][c][wave][lane] = o[e];
+      } else {
+        float x[4] = {S[0][c][0], S[0][c][1], S[0][c][2], S[0][c][3]};
+#pragma unroll
+        for (int e = 0; e < 3; ++e) {
+          const u32x2 w = {upper(x[0], x[1]), upper(x[2], x[3])};
+          reinterpret_cast<u32x2 *>(&s_S[e][c][wave >> 1][lane])[wave & 1] = w;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = below(x[j]);
+        }
+      }
     }
   };
   rows_of(0);
@@ -964,7 +973,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
       }
     }
     __syncthreads();
-    if (holds && !tree) {                                // S = exp(D_last) S + K^T (exp(D_last - D) U)
+    if (!tree) {                                         // S = exp(D_last) S + K^T (exp(D_last - D) U)
       auto advance = [&](auto two) {
         constexpr int N = decltype(two)::value ? 2 : 1;
         u32x4 x[N][CT][3];
@@ -975,7 +984,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
 #pragma unroll
             for (int c = 0; c < CT; ++c) x[s][c][e] = s_W[e][c][s][lane];
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < TP; ++p)
 #pragma unroll
           for (int c = 0; c < CT; ++c) S[p][c] *= decay;
         __builtin_amdgcn_sched_barrier(0);
@@ -986,7 +995,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
 #pragma unroll
             for (int c = 0; c < CT; ++c)
 #pragma unroll
-              for (int p = 0; p < 2; ++p) S[p][c] = mfma(keys[p][s], x[s][c][e], S[p][c]);
+              for (int p = 0; p < TP; ++p) S[p][c] = mfma(keys[p][s], x[s][c][e], S[p][c]);
       };
       if (here > 32) advance(std::true_type());
       else advance(std::false_type());
@@ -994,7 +1003,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
         uint64_t gone[CT];
         not_finite(bad, gone);
 #pragma unroll
-        for (int p = 0; p < 2; ++p)
+        for (int p = 0; p < TP; ++p)
 #pragma unroll
           for (int c = 0; c < CT; ++c)
             if (gone[c]) S[p][c] = S[p][c] + __builtin_nanf("");
@@ -1005,9 +1014,9 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   };
   for (int part = 0; part < last; ++part) chunk(part, std::true_type());
   chunk(last, std::false_type());
-  if (holds && !tree) {
+  if (!tree) {
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
+    for (int p = 0; p < TP; ++p)
 #pragma unroll
       for (int e = 0; e < 4; ++e)
 #pragma unroll
