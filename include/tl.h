@@ -637,8 +637,8 @@ int tl_short_conv(const uint16_t *x, int64_t ldx, int64_t T, int64_t C, const fl
  * in  a, b       f32 [T, Hk * G], rows lda, ldb apart; with a_log and dt_bias f32 [Hk * G]:
  *                g = -exp(a_log) log(1 + exp(a + dt_bias)), b = 1 / (1 + exp(-b));
  *                with both NULL a is the log decay g and b the step b
- * out out        bf16 [T, Hk * G, Dv]
- * io  state      f32 [states, Hk * G, Dk, Dv]; computed as exactly as f32 products and sums are
+ * out out        bf16 [T, Hk * G, Dv]: computed as exactly as f32 products and sums are, rounded once
+ * io  state      f32 [states, Hk * G, Dk, Dv]: the same, not rounded
  * max_nodes      the most tokens a request has, as far as the caller knows: it chooses the
  *                kernel and sizes the workspace; lengths above it are still right
  * workspace      tl_delta_rule_workspace_size(T, R, Hk, G, Dk, max_nodes, tree) bytes (tree: not 0

@@ -16,10 +16,11 @@
 //
 // Products run on the bf16 matrix instructions.  q and k are bf16; an f32 operand is the sum
 // of three bf16 parts of 8 bits each, cut off exactly (x = hi + mid + lo), and its products
-// are added part by part in f32: S and u are as exact as f32 products would make them, at
-// three instructions (six for T times an f32 operand, without the terms below 2^-24) where
-// f32 matrix instructions would take eight times the cycles.  What only reaches the bf16
-// output, P and S^T q, takes two parts: 16 bits.
+// are added part by part in f32: S, u and the outputs are as exact as f32 products would make
+// them, at three instructions (six for T or P times an f32 operand, without the terms below
+// 2^-24) where f32 matrix instructions would take eight times the cycles.  (P, U and S^T q in
+// two parts, 16 bits, spared 3 to 6 % of a call and left nothing of outputs whose terms
+// cancel to 2^-17.)
 //
 // A product with a masked zero would still spread what is not finite to tokens that do not see
 // it.  So tokens with such a k, g or b, and elements of v, count as zeros in the products, and
@@ -285,20 +286,21 @@ constexpr int kTile = 1024;                              // bytes of an operand
 // tile i of T or P has its columns of 32 up to s = i / 2: 6 operands for each part
 __host__ __device__ constexpr int tri_at(int i, int s) { return (i < 2 ? i : 2 * (i - 1)) + s; }
 constexpr int kTriangle = 6;
-constexpr int kTParts = 3, kPParts = 2;
-constexpr int kDecays = (kTParts + kPParts) * kTriangle * kTile;  // behind T and P: three lists of 64
+constexpr int kParts = 3;
+// T lies in parts; P in f32, as two halves of a lane's 8 values: what a wave cuts for itself is
+// a third less to write and to read
+constexpr int kDecays = (kParts + 2) * kTriangle * kTile;  // behind T and P: three lists of 64
 constexpr int kHeadBytes = kDecays + 3 * kChunk * 4;      // the third: exp(D_last) and a word of tokens
 __host__ __device__ constexpr int key_bytes(int DK) { return 3 * kChunk * DK * 2; }
 
-// three (PARTS = 3) or two bf16 parts of 8 floats, as an operand's lane holds them
-template <int PARTS>
-__device__ __forceinline__ void cut(const float (&x)[8], u32x4 (&o)[PARTS]) {
+// the three bf16 parts of 8 floats, as an operand's lane holds them
+__device__ __forceinline__ void cut(const float (&x)[8], u32x4 (&o)[kParts]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     float p = x[2 * e], q = x[2 * e + 1];
 #pragma unroll
-    for (int part = 0; part < PARTS; ++part) {
-      o[part][e] = PARTS == 2 && part == 1 ? pack_bf16(p, q) : upper(p, q);
+    for (int part = 0; part < kParts; ++part) {
+      o[part][e] = upper(p, q);
       p = below(p);
       q = below(q);
     }
@@ -309,10 +311,11 @@ struct Eight {
   float v[8];
 };
 __device__ __forceinline__ Eight both(f32x4 x, f32x4 y) { return {{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]}}; }
-template <int PARTS>
-__device__ __forceinline__ void cut(const Eight &x, u32x4 (&o)[PARTS]) {
-  cut<PARTS>(x.v, o);
-}
+__device__ __forceinline__ void cut(const Eight &x, u32x4 (&o)[kParts]) { cut(x.v, o); }
+
+// The part products of two f32 operands, smallest first: hi lo, mid mid, lo hi, hi mid, mid hi,
+// hi hi.  What is below 2^-24 of the largest stays out.
+constexpr int kPartProducts = 6, kOfFirst[kPartProducts] = {2, 1, 0, 1, 0, 0}, kOfSecond[kPartProducts] = {0, 1, 2, 0, 1, 0};
 
 // What one lane wrote to LDS is there for the wave's other lanes (which need no barrier: a
 // wave's LDS instructions are executed in order).
@@ -412,13 +415,13 @@ __device__ __forceinline__ void solve_block(const float *D, int m, float (&t)[16
 
 // 8 values of T's row i, columns j0 .., with the steps, in parts
 template <int PITCH>
-__device__ __forceinline__ void solver_row(const float *A, const float *steps, int i, int j0, u32x4 (&o)[kTParts]) {
+__device__ __forceinline__ void solver_row(const float *A, const float *steps, int i, int j0, u32x4 (&o)[kParts]) {
   const f32x4 *row = reinterpret_cast<const f32x4 *>(A + i * PITCH + j0), *b = reinterpret_cast<const f32x4 *>(steps + j0);
   const f32x4 u[2] = {row[0], row[1]}, v[2] = {b[0], b[1]};
   float x[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = j0 + e <= i ? u[e >> 2][e & 3] * v[e >> 2][e & 3] : 0.0f;
-  cut<kTParts>(x, o);
+  cut(x, o);
 }
 
 // An operand of K transposed, 32 tokens of elements dealt(p, m) of 32, from the tokens' two row
@@ -525,7 +528,7 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
   wave_sync();
 
   // (K K^T)^T and (Q K^T)^T: a lane holds token i = dealt(t, m) against 8 consecutive j's
-  u32x4 *P = reinterpret_cast<u32x4 *>(head + kTParts * kTriangle * kTile);
+  f32x4 *P = reinterpret_cast<f32x4 *>(head + kParts * kTriangle * kTile);
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
     if (32 * (t >> 1) >= n) break;                       // uniform
@@ -554,10 +557,9 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
       f32x4 *to = reinterpret_cast<f32x4 *>(A + i * PITCH + 32 * s + 8 * g);
       to[0] = f32x4{kk[0], kk[1], kk[2], kk[3]};
       to[1] = f32x4{kk[4], kk[5], kk[6], kk[7]};
-      u32x4 part[kPParts];
-      cut<kPParts>(qk, part);
 #pragma unroll
-      for (int e = 0; e < kPParts; ++e) P[(e * kTriangle + tri_at(t, s)) * 64 + lane] = part[e];
+      for (int e = 0; e < 2; ++e)
+        P[(e * kTriangle + tri_at(t, s)) * 64 + lane] = f32x4{qk[4 * e], qk[4 * e + 1], qk[4 * e + 2], qk[4 * e + 3]};
     }
   }
   wave_sync();
@@ -615,10 +617,10 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
     const int i = dealt(t, m);
 #pragma unroll
     for (int s = 0; s <= t >> 1; ++s) {
-      u32x4 part[kTParts];
+      u32x4 part[kParts];
       solver_row<PITCH>(A, s_b[wave], i, 32 * s + 8 * g, part);
 #pragma unroll
-      for (int e = 0; e < kTParts; ++e) to[(e * kTriangle + tri_at(t, s)) * 64 + lane] = part[e];
+      for (int e = 0; e < kParts; ++e) to[(e * kTriangle + tri_at(t, s)) * 64 + lane] = part[e];
     }
   }
 }
@@ -636,7 +638,7 @@ template <int DK>
 __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const DeltaArgs a) {
   constexpr int NS = DK / 32, CT = 2, TP = DK / 64;      // column tiles of the workgroup, state tiles of a wave
   static_assert(TP == 1 || TP == 2, "a wave holds a pair of state tiles, or one of a pair");
-  __shared__ __attribute__((aligned(16))) u32x4 s_S[3][CT][NS][64], s_R[3][CT][2][64], s_U[2][CT][2][64], s_W[3][CT][2][64];
+  __shared__ __attribute__((aligned(16))) u32x4 s_S[3][CT][NS][64], s_R[3][CT][2][64], s_U[3][CT][2][64], s_W[3][CT][2][64];
   __shared__ uint32_t s_bad[16 * CT][2];                 // of each column: tokens whose v is not finite
   __shared__ int s_some;
   const int tid = threadIdx.x, lane = tid & 63, m = lane & 15, g = lane >> 4;
@@ -679,7 +681,8 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
   auto word_of = [](const f32x4 &end) { return __float_as_uint(end[2]) | uint64_t(__float_as_uint(end[3])) << 32; };
 
   if (all_waves >= 4) {                                  // out = scale (exp(D) Q S + P U)
-    u32x4 Q[NS], P[2][kPParts];
+    u32x4 Q[NS];
+    f32x4 P[2][2];
     f32x4 grown, end;
     auto fetch_row = [&](int part) {
       const u32x4 *from = key_of(part) + (4 + wave) * NS * 64;
@@ -689,11 +692,11 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
       end = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + 2 * kChunk * 4);
     };
     auto fetch_weights = [&](int part) {
-      const u32x4 *from = reinterpret_cast<const u32x4 *>(head_of(part)) + (kTParts * kTriangle + tri_at(wave, 0)) * 64 + lane;
+      const f32x4 *from = reinterpret_cast<const f32x4 *>(head_of(part)) + (kParts * kTriangle + tri_at(wave, 0)) * 64 + lane;
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int e = 0; e < kPParts; ++e) P[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
+        for (int e = 0; e < 2; ++e) P[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
     };
     fetch_row(0);
     fetch_weights(0);
@@ -706,19 +709,19 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
       f32x4 o[CT];
       __syncthreads();
       if (rows) {
-        u32x4 y[NS][CT][2];
+        u32x4 y[NS][CT][kParts];
 #pragma unroll
         for (int c = 0; c < CT; ++c) o[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < NS; ++s)
 #pragma unroll
-          for (int e = 1; e >= 0; --e)
+          for (int e = kParts - 1; e >= 0; --e)
 #pragma unroll
             for (int c = 0; c < CT; ++c) y[s][c][e] = s_S[e][c][s][lane];
 #pragma unroll
         for (int s = 0; s < NS; ++s)
 #pragma unroll
-          for (int e = 1; e >= 0; --e)
+          for (int e = kParts - 1; e >= 0; --e)
 #pragma unroll
             for (int c = 0; c < CT; ++c) o[c] = mfma(Q[s], y[s][c][e], o[c]);
 #pragma unroll
@@ -733,14 +736,18 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
         auto add = [&](auto two) {
           constexpr int N = decltype(two)::value ? 2 : 1;
 #pragma unroll
-          for (int s = 0; s < N; ++s)
+          for (int s = 0; s < N; ++s) {
+            u32x4 w[kParts], x[CT][kParts];
+            cut(both(P[s][0], P[s][1]), w);
 #pragma unroll
-            for (int c = 0; c < CT; ++c) {
-              const u32x4 x = s_U[0][c][s][lane], y = s_U[1][c][s][lane];
-              o[c] = mfma(P[s][1], x, o[c]);
-              o[c] = mfma(P[s][0], y, o[c]);
-              o[c] = mfma(P[s][0], x, o[c]);
-            }
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+              for (int e = 0; e < kParts; ++e) x[c][e] = s_U[e][c][s][lane];
+#pragma unroll
+            for (int j = 0; j < kPartProducts; ++j)
+#pragma unroll
+              for (int c = 0; c < CT; ++c) o[c] = mfma(w[kOfFirst[j]], x[c][kOfSecond[j]], o[c]);
+          }
         };
         if (pairs == 2) add(std::true_type());
         else add(std::false_type());
@@ -791,7 +798,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
 
   // What a wave takes of a chunk.  Each piece is asked for as soon as the chunk before has used
   // it.  Rows past the last token are the last one's: nothing of theirs is kept.
-  u32x4 K[NS], T[2][kTParts], keys[TP][2];
+  u32x4 K[NS], T[2][kParts], keys[TP][2];
   uint32_t V[4];                                         // two columns of a row
   f32x4 grown, left, end;                                // end: exp(D_last), nothing, a word of tokens
   const int vcol = h * a.Dv + col;
@@ -817,7 +824,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int e = 0; e < kTParts; ++e) T[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
+      for (int e = 0; e < kParts; ++e) T[s][e] = from[(e * kTriangle + (s < pairs ? s : 0)) * 64];
     left = *reinterpret_cast<const f32x4 *>(head_of(part) + kDecays + (kChunk + row0) * 4);
   };
   auto fetch_keys = [&](int part) {
@@ -832,7 +839,7 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
     for (int c = 0; c < CT; ++c) {
       if constexpr (TP == 2) {
         u32x4 o[3];
-        cut<3>(both(S[0][c], S[TP - 1][c]), o);
+        cut(both(S[0][c], S[TP - 1][c]), o);
 #pragma unroll
         for (int e = 0; e < 3; ++e) s_S[e][c][wave][lane] = o[e];
       } else {
@@ -940,14 +947,12 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
 #pragma unroll
             for (int c = 0; c < CT; ++c) x[s][c][e] = s_R[e][c][s][lane];
         __builtin_amdgcn_sched_barrier(0);
-        // what is below 2^-24 of the largest stays out: hi lo, mid mid, lo hi, hi mid, mid hi, hi hi
-        constexpr int of_T[6] = {2, 1, 0, 1, 0, 0}, of_R[6] = {0, 1, 2, 0, 1, 0};
 #pragma unroll
-        for (int j = 0; j < 6; ++j)
+        for (int j = 0; j < kPartProducts; ++j)
 #pragma unroll
           for (int s = 0; s < N; ++s)
 #pragma unroll
-            for (int c = 0; c < CT; ++c) u[c] = mfma(T[s][of_T[j]], x[s][c][of_R[j]], u[c]);
+            for (int c = 0; c < CT; ++c) u[c] = mfma(T[s][kOfFirst[j]], x[s][c][kOfSecond[j]], u[c]);
       };
       if (pairs == 2) solve(std::true_type());
       else solve(std::false_type());
@@ -963,13 +968,14 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
         for (int e = 0; e < 3; ++e) {
           const u32x2 z = {upper(y[0], y[1]), upper(y[2], y[3])};
           reinterpret_cast<u32x2 *>(&s_W[e][c][wave >> 1][lane])[wave & 1] = z;
+          const u32x2 w = {upper(x[0], x[1]), upper(x[2], x[3])};
+          reinterpret_cast<u32x2 *>(&s_U[e][c][wave >> 1][lane])[wave & 1] = w;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) y[j] = below(y[j]);
+          for (int j = 0; j < 4; ++j) {
+            x[j] = below(x[j]);
+            y[j] = below(y[j]);
+          }
         }
-        const u32x2 hi = {upper(x[0], x[1]), upper(x[2], x[3])};
-        const u32x2 lo = {pack_bf16(below(x[0]), below(x[1])), pack_bf16(below(x[2]), below(x[3]))};
-        reinterpret_cast<u32x2 *>(&s_U[0][c][wave >> 1][lane])[wave & 1] = hi;
-        reinterpret_cast<u32x2 *>(&s_U[1][c][wave >> 1][lane])[wave & 1] = lo;
       }
     }
     __syncthreads();
@@ -1036,13 +1042,13 @@ template <int DK, bool TREE>
 __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const DeltaArgs a) {
   constexpr int NS = DK / 32, PITCH = kChunk + 4;
   struct Operands {
-    u32x4 K[4][NS][64], QT[kTParts * kTriangle * 64];    // K's; Q's, then T's
+    u32x4 K[4][NS][64], QT[kParts * kTriangle * 64];    // K's; Q's, then T's
   };
   __shared__ Operands lds;
   auto &s_K = lds.K;
   auto &s_QT = lds.QT;
   __shared__ __attribute__((aligned(16))) float s_A[kChunk * PITCH];  // A, then T
-  __shared__ u32x4 s_P[kPParts * kTriangle * 64];
+  __shared__ u32x4 s_P[kParts * kTriangle * 64];
   __shared__ f32x4 s_T[kTriangle][64];                   // T's blocks below the diagonal, as results lie
   __shared__ double s_total[kChunk];
   __shared__ __attribute__((aligned(16))) float s_b[kChunk], s_grown[kChunk], s_left[kChunk];
@@ -1165,10 +1171,10 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
       f32x4 *to = reinterpret_cast<f32x4 *>(s_A + i * PITCH + 32 * s + 8 * g);
       to[0] = f32x4{kk[0], kk[1], kk[2], kk[3]};
       to[1] = f32x4{kk[4], kk[5], kk[6], kk[7]};
-      u32x4 x[kPParts];
-      cut<kPParts>(qk, x);
+      u32x4 x[kParts];
+      cut(qk, x);
 #pragma unroll
-      for (int e = 0; e < kPParts; ++e) s_P[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = x[e];
+      for (int e = 0; e < kParts; ++e) s_P[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = x[e];
     }
   }
   __syncthreads();
@@ -1222,7 +1228,7 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       u32x4 y[3];
-      cut<3>(both(S[2 * s], S[2 * s + 1]), y);
+      cut(both(S[2 * s], S[2 * s + 1]), y);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         if (t >= 2 && !wide) break;                    // uniform
@@ -1230,7 +1236,7 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
 #pragma unroll
         for (int e = 2; e >= 0; --e) {
           R[t] = mfma(k, y[e], R[t]);
-          if (e < 2) o[t] = mfma(q, y[e], o[t]);
+          o[t] = mfma(q, y[e], o[t]);
         }
       }
     }
@@ -1248,10 +1254,10 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
   if (wave < 4 && 32 * (wave >> 1) < n) {
     const int i = dealt(wave, m);
     for (int s = 0; s <= wave >> 1; ++s) {
-      u32x4 x[kTParts];
+      u32x4 x[kParts];
       solver_row<PITCH>(s_A, s_b, i, 32 * s + 8 * g, x);
 #pragma unroll
-      for (int e = 0; e < kTParts; ++e) s_QT[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = x[e];
+      for (int e = 0; e < kParts; ++e) s_QT[(e * kTriangle + tri_at(wave, s)) * 64 + lane] = x[e];
     }
   }
   // R = V - exp(D) K S, in parts; what must not be seen counts as zero
@@ -1287,38 +1293,38 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
     }
 #pragma unroll
     for (int s = 0; s < 2; ++s)
-      if (s == 0 || wide) cut<3>(both(R[2 * s], R[2 * s + 1]), x[s]);
+      if (s == 0 || wide) cut(both(R[2 * s], R[2 * s + 1]), x[s]);
   }
   __syncthreads();
   if (cols) {
     f32x4 U[4];
-    constexpr int of_T[6] = {2, 1, 0, 1, 0, 0}, of_R[6] = {0, 1, 2, 0, 1, 0};
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       U[t] = f32x4{0, 0, 0, 0};
       if (t >= 2 && !wide) continue;
 #pragma unroll
       for (int s = 0; s <= t >> 1; ++s) {
-        u32x4 w[kTParts];
+        u32x4 w[kParts];
 #pragma unroll
-        for (int e = 0; e < kTParts; ++e) w[e] = s_QT[(e * kTriangle + tri_at(t, s)) * 64 + lane];
+        for (int e = 0; e < kParts; ++e) w[e] = s_QT[(e * kTriangle + tri_at(t, s)) * 64 + lane];
 #pragma unroll
-        for (int j = 0; j < 6; ++j) U[t] = mfma(w[of_T[j]], x[s][of_R[j]], U[t]);
+        for (int j = 0; j < kPartProducts; ++j) U[t] = mfma(w[kOfFirst[j]], x[s][kOfSecond[j]], U[t]);
       }
     }
     // out = scale (exp(D) Q S + P U)
 #pragma unroll
     for (int s = 0; s < 2; ++s)
       if (s == 0 || wide) {
-        u32x4 u[2];
-        cut<2>(both(U[2 * s], U[2 * s + 1]), u);
+        u32x4 u[kParts];
+        cut(both(U[2 * s], U[2 * s + 1]), u);
 #pragma unroll
         for (int t = 2 * s; t < 4; ++t) {
           if (t >= 2 && !wide) break;
-          const u32x4 hi = s_P[tri_at(t, s) * 64 + lane], lo = s_P[(kTriangle + tri_at(t, s)) * 64 + lane];
-          o[t] = mfma(lo, u[0], o[t]);
-          o[t] = mfma(hi, u[1], o[t]);
-          o[t] = mfma(hi, u[0], o[t]);
+          u32x4 w[kParts];
+#pragma unroll
+          for (int e = 0; e < kParts; ++e) w[e] = s_P[(e * kTriangle + tri_at(t, s)) * 64 + lane];
+#pragma unroll
+          for (int j = 0; j < kPartProducts; ++j) o[t] = mfma(w[kOfFirst[j]], u[kOfSecond[j]], o[t]);
         }
       }
     if (__any(gone != 0)) {
@@ -1345,7 +1351,7 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
       for (int s = 0; s < 2; ++s)
         if (s == 0 || wide) {
           const f32x4 *left = reinterpret_cast<const f32x4 *>(s_left + 32 * s + 8 * g);
-          cut<3>(both(left[0] * U[2 * s], left[1] * U[2 * s + 1]), w[s]);
+          cut(both(left[0] * U[2 * s], left[1] * U[2 * s + 1]), w[s]);
         }
 #pragma unroll
       for (int t = 0; t < 2 * NS; ++t) {
