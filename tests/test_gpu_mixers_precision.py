@@ -5,6 +5,8 @@ from __future__ import annotations
 import numpy as np
 import pytest
 
+import oracle.mixers as ref
+import oracle.speculative as spec
 from gpu_common import announce, to_dev
 from test_gpu_mixers import BF16_HALF, F32_HALF, FORMS, KERNEL, bf16_dev, dev, f64, tl, torch  # noqa: F401  (fixtures)
 
@@ -70,3 +72,50 @@ def test_what_cancellation_leaves(tl, torch, form, Dk, at, what):  # noqa: F811
     got = f64(out)
     tol = 8 * F32_HALF * 2.02 * cols + BF16_HALF * left * cols
     assert (np.abs(got[i2, 0] - want[i2, 0]) <= tol).all(), (got[i2, 0] / cols, left)
+
+
+# A state that forgets slowly (0.997 a token: a chunk of 64 leaves 0.83 of it), against f32 sums.  A chunk rounds it 7 times
+# (the decay, three parts of each of two products), root 2.6 for independent signs; over the chunks it remembers 1.8 times as
+# much: 4.8 half steps.  An update u is off by K S (12 sums), R, T R (12) and its weight: root 5.1.  Together 7.0.
+# tests/test_mixers_precision_cpu.py shows that a last part missing anywhere takes a state past this bound.
+SLOW_TOL = 8 * F32_HALF
+
+
+def slow_step(rng, T, Hk, G, Dk, Dv):
+    """q, k, v, g, b and a state in f64, as the operator gets them."""
+    unit = lambda y: y / np.sqrt((y * y).sum(-1, keepdims=True))
+    q, k = (spec.bf16(unit(rng.standard_normal((T, Hk, Dk)) + 0.4)) for _ in "qk")
+    v = spec.bf16(rng.standard_normal((T, Hk * G, Dv)))
+    g = (-0.003 * np.exp(0.5 * rng.standard_normal((T, Hk * G)))).astype(np.float32)
+    b = (1 / (1 + np.exp(-rng.standard_normal((T, Hk * G))))).astype(np.float32)
+    return q, k, v, g, b, (0.3 * rng.standard_normal((1, Hk * G, Dk, Dv))).astype(np.float32)
+
+
+@pytest.mark.parametrize("form,T,step", [("chunks", 2085, 2085), ("trees and chunks", 1100, 1100), ("chunks", 64, 64), ("one chunk", 640, 64),
+                                         ("one chunk", 33, 33)])
+@pytest.mark.parametrize("Hk,G,Dk,Dv", [(1, 2, 64, 48), (1, 2, 128, 48)])
+def test_a_state_that_forgets_slowly(tl, torch, Hk, G, Dk, Dv, form, T, step):  # noqa: F811
+    """Thousands of tokens through the chunks, in one call or in several: states within f32's roundings of the recurrence in
+    64 bits; outputs within bfloat16's and, for what the sums leave (Q S 12 sums, the weights 4, the updates 7, P U 12), 35
+    half steps of f32 of the magnitudes that were added."""
+    announce(f"slow decays, {form}, {T} tokens by {step}, Dk={Dk}")
+    d, rng = dev(), np.random.default_rng(T + Dk)
+    q, k, v, g, b, state = slow_step(rng, T, Hk, G, Dk, Dv)
+    stated = to_dev(state, d)
+    outs = []
+    for lo in range(0, T, step):
+        at = slice(lo, lo + step)
+        n = len(q[at])
+        meta = [to_dev(np.array(x, np.int32), d) for x in ([0, n], [n + 9], [0])]
+        mask = torch.zeros(n, dtype=torch.int64, device=d) if "trees" in form else None
+        outs.append(tl.delta_rule(*(bf16_dev(x[at], d) for x in (q, k, v)), to_dev(g[at], d), to_dev(b[at], d), *meta, stated,
+                                  tree_mask=mask, max_nodes=FORMS[form]))
+        assert tl.last_kernel_name() == KERNEL.get(form, "delta_scan")
+    torch.cuda.synchronize()
+    want, after, size = ref.delta_rule(q, k, v, g.astype(np.float64), b.astype(np.float64), [0, T], [T + 9], [0],
+                                       state.astype(np.float64), None, Dk ** -0.5, np.zeros((T, Hk * G, Dv)))
+    for h in range(Hk * G):
+        miss = np.linalg.norm(stated.cpu().numpy()[0, h] - after[0, h]) / np.linalg.norm(after[0, h])
+        assert miss <= SLOW_TOL, (h, miss / F32_HALF)
+    got = np.concatenate([f64(o) for o in outs])
+    assert (np.abs(got - want) <= BF16_HALF * np.abs(want) + 35 * F32_HALF * size).all()
