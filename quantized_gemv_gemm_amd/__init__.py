@@ -1031,7 +1031,10 @@ def delta_rule(q, k, v, a, b, q_start, kv_lens, state_slots, state, a_log=None, 
     tree_mask int64 [T], each tree's branches).  q, k bf16 [T, Hk, Dk] and v bf16 [T, Hv, Dv] (tokens a row or more apart);
     a, b f32 [T, Hv]: with a_log and dt_bias f32 [Hv], g = -exp(a_log) softplus(a + dt_bias) and b = sigmoid(b), else g = a.
     state f32 [states, Hv, Dk, Dv], request r's at state_slots[r], is brought up to date for chains.  Returns out bf16
-    [T, Hv, Dv].  ``max_nodes``: the most tokens of a request, as far as known (chooses the kernel)."""
+    [T, Hv, Dv].  ``max_nodes``: the most tokens of a request, as far as known: it chooses the kernel (up to 6 token by token,
+    up to 64 and trees one launch, else chunks), and one that is too low costs time, 1 to 4 us a token of a longer
+    request.  Without it, it is the most that a request can have where each has a token, T - R + 1: right for single tokens,
+    for one request and for prompts; 64 for a step of short requests or trees alone is faster."""
     import torch
     i = _index_of(q, "q")
     if state.dim() != 4:
@@ -1049,7 +1052,7 @@ def delta_rule(q, k, v, a, b, q_start, kv_lens, state_slots, state, a_log=None, 
     out = torch.empty((T, Hv, Dv), dtype=bf16, device=q.device) if out is None else out
     op = _given(out, "out", bf16, (T, Hv, Dv), i)
     if max_nodes is None:
-        max_nodes = max(1, -(-T // max(R, 1)))
+        max_nodes = max(1, T - R + 1)                    # a mean would send one long prompt among many tokens token by token
     wp, size = None, 0
     if workspace is None:
         size = lib().tl_delta_rule_workspace_size(T, R, Hk, Hv // Hk, Dk, max_nodes, mp is not None)
