@@ -571,7 +571,8 @@ int tl_kv_commit(const int32_t *accepted, const int32_t *path, int64_t path_widt
  * in  q_weight, k_weight  f32 [D] or NULL (ones).  Every row x of q and k becomes
  *                x w / sqrt(mean of x^2 + eps), then is rotated as in tl_kv_write, all in f32;
  *                q and a bf16 cache get it rounded once, an e4m3 cache takes scale and codes
- *                from the f32 values.  v is written as in tl_kv_write.
+ *                from the f32 values, all NaN where a row of k is not finite (or its length is
+ *                0: a row of zeros with eps 0).  v is written as in tl_kv_write.
  * in  positions  int32 [axes, T], axis_of int32 [rot/2]: the axis whose positions turn the
  *                pair (d, d + rot/2); clamped to the axes.  axis_of may be NULL with one axis.
  * Requires 1 <= axes <= 16, eps >= 0 and finite; otherwise as tl_kv_write.

@@ -179,8 +179,12 @@ __device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
   return u32x4{pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7])};
 }
 
+// A magnitude's bits rise with it, and a NaN's are above infinity's: their maximum is NaN where an
+// element is, and a row that is not finite does not pass for a row of zeros.
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
 __device__ __forceinline__ u32x2 codes8(const float (&x)[8], float scale) {
-  const bool some = scale > 0.0f;
+  const bool some = scale != 0.0f;                       // NaN too: its codes are NaN
   u32x2 o;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -324,12 +328,12 @@ __global__ __launch_bounds__(kThreads) void kv_write_kernel(const WriteArgs a, i
       if constexpr (!E4M3) k = {pack8(y.a), pack8(y.b)};
     }
     if constexpr (E4M3 && NORM) {
-      float m = 0.0f;
+      uint32_t m = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(fmaxf(m, fabsf(y.a[e])), fabsf(y.b[e]));
+      for (int e = 0; e < 8; ++e) m = max(max(m, magnitude(y.a[e])), magnitude(y.b[e]));
 #pragma unroll
-      for (int off = P / 2; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-      const float scale = m / 448.0f;
+      for (int off = P / 2; off > 0; off >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), off, 64)));
+      const float scale = __uint_as_float(m) / 448.0f;
       if (live) {
         if (p == 0) a.k_scale[scale_of(slot)] = scale;
         char *dst = static_cast<char *>(a.k_cache) + tile_of(slot);
