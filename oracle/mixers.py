@@ -144,8 +144,6 @@ def delta_commit(accepted, path, q_start, kv_lens, slots, k, v, g, b, state, x, 
     after, conv = state.copy(), conv_state.copy()
     for r, first, n, row, fresh in requests(q_start, kv_lens, slots, len(state), len(k)):
         nodes = [int(p) for p in path[r][:max(int(accepted[r]), 0)] if 0 <= p < n] if n <= NODES and row >= 0 else []
-        if accepted[r] > n:
-            nodes = [int(p) for p in path[r][:n] if 0 <= p < n] if n <= NODES and row >= 0 else []
         if not nodes:
             continue
         at = [first + p for p in nodes]

@@ -225,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a,
   if constexpr (COMMIT) {
     if (rq.row < 0 || n > kTreeNodes) return;
     if (wave == 0) {
-      const int most = min(min(max(a.accepted[r], 0), a.path_width), n);
+      const int most = min(a.accepted[r], a.path_width);   // entries, of which those that name a token count
       const int at = lane < most ? a.path[int64_t(r) * a.path_width + lane] : -1;
       const bool on = at >= 0 && at < n;
       const uint64_t all = __ballot(on);

@@ -1,5 +1,5 @@
-"""Corners of the token mixers' contracts on the GPU: keys that are not finite in an 8-bit cache and the
-longest request when it is not named."""
+"""Corners of the token mixers' contracts on the GPU: keys that are not finite in an 8-bit cache, the longest request when it
+is not named, accepted counts past a tree's tokens."""
 from __future__ import annotations
 
 import numpy as np
@@ -8,7 +8,7 @@ import pytest
 import oracle.mixers as ref
 import oracle.speculative as spec
 from gpu_common import announce, to_dev
-from test_gpu_mixers import Step, _check_delta, _delta_inputs, bf16_dev, bits, dev, f64, tl, torch  # noqa: F401
+from test_gpu_mixers import STATE_TOL, _check_delta, _delta_inputs, Step, bf16_dev, bits, dev, f64, tl, torch  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,30 @@ def test_delta_rule_without_max_nodes(tl, torch, lens, kernel):  # noqa: F811
     want, after, size = ref.delta_rule(*plain, s.q_start, s.kv_lens, s.slots, state.astype(np.float64), None, 0.125,
                                        np.zeros((s.T, 2, 32)))
     _check_delta(f64(got), stated.cpu().numpy(), want, after, size, state, s.T)
+
+
+def test_commit_of_a_path_longer_than_the_tree(tl, torch):  # noqa: F811
+    """accepted counts entries of the path up to its width; those that name no token are skipped, and the others are taken,
+    also where there are more entries than the tree has tokens."""
+    announce("commit of a path longer than the tree")
+    d, rng = dev(), np.random.default_rng(3)
+    s = Step(np.array([2, 3, 1]), rng, trees=True, unserved=False)
+    plain, given, _, state = _delta_inputs(s, 1, 2, 64, 32, rng, False, d)
+    accepted = np.array([3, 9, 2], np.int32)
+    path = np.array([[-1, 0, 1, -1, -1, 0], [0, 7, -3, 1, 1 << 30, 2], [5, 0, -1, -1, -1, -1]], np.int32)
+    x, conv = spec.bf16(rng.standard_normal((s.T, 64))), spec.bf16(rng.standard_normal((s.states, 3, 64)))
+    stated, convd = to_dev(state, d), bf16_dev(conv, d)
+    tl.delta_commit(to_dev(accepted, d), to_dev(path, d), *s.dev(d), *given[1:], stated, x=bf16_dev(x, d), conv_state=convd)
+    torch.cuda.synchronize()
+    # by hand: the chains of tokens 0, 1 of request 0, of 0, 1, 2 of request 1, and of token 0 of request 2
+    lens = [2, 3, 1]
+    _, want, _ = ref.delta_rule(*plain, s.q_start, s.kv_lens, s.slots, state.astype(np.float64), None, 1.0,
+                                np.zeros((s.T, 2, 32)))
+    got = stated.cpu().numpy()
+    for r in range(3):
+        row, first, n = s.slots[r], s.q_start[r], lens[r]
+        assert np.linalg.norm(got[row] - want[row]) <= STATE_TOL * np.linalg.norm(want[row]), r
+        old = np.zeros((3, 64)) if s.kv_lens[r] <= n else conv[row]
+        np.testing.assert_array_equal(f64(convd[row]), np.concatenate([old, x[first:first + n]])[-3:])
+    by_oracle, _ = ref.delta_commit(accepted, path, s.q_start, s.kv_lens, s.slots, *plain[1:], state.astype(np.float64), x, conv)
+    np.testing.assert_allclose(by_oracle, want, rtol=1e-12)
