@@ -25,6 +25,7 @@
 // A product with a masked zero would still spread what is not finite to tokens that do not see
 // it.  So tokens with such a k, g or b, and elements of v, count as zeros in the products, and
 // the results of those that do see them, and the state, become NaN at the end.
+#include <cstddef>
 #include <type_traits>
 
 #include "kv_layout.h"
@@ -75,10 +76,13 @@ __device__ __forceinline__ Gate gate_of(const DeltaArgs &a, const float *pa, con
 constexpr int kStepBatch = 16;
 
 template <int DK>
-struct StepShared {
+struct alignas(16) StepShared {
   float k[kStepBatch][DK], q[kStepBatch][DK], v[kStepBatch][32], decay[kStepBatch], step[kStepBatch];
   float sum[2][4][8][12];
 };
+static_assert(alignof(StepShared<64>) >= 16 && offsetof(StepShared<64>, v) % 16 == 0 && offsetof(StepShared<64>, sum) % 16 == 0 &&
+                  alignof(StepShared<128>) >= 16 && offsetof(StepShared<128>, v) % 16 == 0 && offsetof(StepShared<128>, sum) % 16 == 0,
+              "read and written 16 bytes at a time");
 
 // the sum over the lanes that differ in bits 3 to 5
 __device__ __forceinline__ float sum_rows(float x) {
