@@ -472,7 +472,8 @@ int tl_step_plan(const int32_t *ctx_lens, const int32_t *new_lens, const int32_t
  * io  k_cache, v_cache and, for e4m3, k_scale, v_scale: the tokens' rows.  e4m3: scale =
  *                fl32(amax / 448) of the (rotated, rounded) row, code = RNE(fl32(x / scale)),
  *                both 0 for a row of zeros.
- * Requires rot a multiple of 16, at most D; max_pos < 2^31; Hq <= 65536; finite inputs.
+ * Requires rot a multiple of 16, at most D; max_pos < 2^31; Hq <= 65536; (T / 16) * H +
+ * T * Hq * D / 4096 < 2^24 (quotients rounded up); finite inputs.
  */
 int tl_kv_write(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t ldv, const int64_t *slots, int64_t T,
                 int64_t H, int64_t D, const uint16_t *q, int64_t ldq, int64_t Hq, const int32_t *positions,
@@ -621,7 +622,8 @@ int tl_kv_write_norm(const uint16_t *k, int64_t ldk, const uint16_t *v, int64_t 
  * out out        bf16 [T, C], rows ldo elements apart (a multiple of 8); sums and norms in f32,
  *                rounded once
  * io  state      bf16 [states, taps - 1, C]: the last taps - 1 rows of x, the oldest first
- * Requires taps 2, 3 or 4, C a multiple of 8 up to 2^20, norm_dim 64, 128 or 256, finite inputs.
+ * Requires taps 2, 3 or 4, C a multiple of 8 up to 2^20, norm_dim 64, 128 or 256, T / 64 + R < 2^24,
+ * finite inputs.
  */
 int tl_short_conv(const uint16_t *x, int64_t ldx, int64_t T, int64_t C, const float *weight, int64_t taps,
                   const float *bias, const int32_t *q_start, const int32_t *kv_lens, const int32_t *state_slots,
@@ -649,8 +651,11 @@ int tl_short_conv(const uint16_t *x, int64_t ldx, int64_t T, int64_t C, const fl
  * result is that of u_i = b_i (v_i - exp(D_i) S^T k_i - sum over i's other bits j of
  * exp(D_i - D_j) (k_i k_j) u_j), out_i = scale (exp(D_i) S^T q_i + sum over i's bits of
  * exp(D_i - D_j) (q_i k_j) u_j).
- * Requires Dk 64 or 128, Dv a multiple of 16 up to 65536, Hk * G <= 65535,
- * R * Hk * G * Dv / 16 < 2^31, max_nodes < 2^31, finite scale.  What is not finite in a token's k, v,
+ * Requires Dk 64 or 128, Dv a multiple of 16 up to 65536, Hk * G <= 65535, max_nodes < 2^31,
+ * finite scale, and what a launch can count (quotients rounded up, but for T / 64):
+ *   max_nodes up to 6 without a tree_mask: R * Hk * G * (Dv / 32) < 2^24
+ *   else up to 64:                         R * Hk * G * (Dv / 128) < 2^23
+ *   else:        (R * Hk / 8) * 8 * G * (Dv / 32) < 2^23 and T / 64 + R < 2^24.  What is not finite in a token's k, v,
  * g or b leaves nothing finite in the results of the tokens that see it and in the state after it,
  * and changes nothing else; -inf is a log decay like any other: one below -10^4 counts as
  * -10^4, whose exp is 0.
@@ -677,8 +682,8 @@ int tl_delta_rule(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk
  *                apart, or NULL; io conv_state bf16 [L, states, taps - 1, C] (with x)
  * Requests of more than 64 tokens, that are not served or of which nothing is accepted are
  * left alone.
- * Requires 1 <= path_width <= 64, 1 <= L <= 4096, L * R * (Hk * G * Dv / 32 + C / 2048) < 2^31;
- * otherwise as tl_delta_rule and tl_short_conv.
+ * Requires 1 <= path_width <= 64, 1 <= L <= 4096, L * R * (Hk * G * (Dv / 32) + C / 2048) < 2^24 with
+ * quotients rounded up; otherwise as tl_delta_rule and tl_short_conv.
  */
 int tl_delta_commit(const int32_t *accepted, const int32_t *path, int64_t path_width, const int32_t *q_start,
                     const int32_t *kv_lens, const int32_t *state_slots, int64_t R, int64_t T, int64_t L,

@@ -163,6 +163,9 @@ hipError_t run(const ConvArgs &a, hipStream_t stream) {
 
 }  // namespace
 
+// Shorter runs than 64 are taken only for tokens that 2^15 bounds.
+bool conv_fits_grid(int64_t T, int64_t R) { return fits_grid(T / 64 + R, kThreads); }
+
 hipError_t launch_short_conv(const ConvArgs &a, int64_t taps, hipStream_t stream) {
   return taps == 2 ? run<2>(a, stream) : taps == 3 ? run<3>(a, stream) : run<4>(a, stream);
 }

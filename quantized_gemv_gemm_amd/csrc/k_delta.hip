@@ -1397,26 +1397,32 @@ Form form_of(int64_t max_nodes, bool tree) {
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 int64_t chunks_of(int64_t T, int64_t R) { return T / kChunk + R; }
 
+// Workgroups of a form's launch over all requests, heads and columns; of threads_of threads.
+int64_t groups_of(Form form, int64_t R, int64_t Hk, int64_t G, int64_t Dv) {
+  return form == Form::kStep    ? R * Hk * G * ((Dv + 31) / 32)
+         : form == Form::kChunk ? R * Hk * G * ((Dv + 127) / 128)
+                                : (R * Hk + 7) / 8 * 8 * G * ((Dv + 31) / 32);
+}
+int threads_of(Form form) { return form == Form::kStep ? kThreads : form == Form::kChunk ? kFusedThreads : kScanThreads; }
+
 template <int DK>
 hipError_t run(DeltaArgs a, Form form, hipStream_t stream) {
   (void)hipGetLastError();
-  const int64_t heads = int64_t(a.R) * a.Hv;
+  const dim3 grid(unsigned(groups_of(form, a.R, a.Hk, a.G, a.Dv))), threads(threads_of(form));
   if (form == Form::kStep) {
-    hipLaunchKernelGGL((delta_step_kernel<DK, false>), dim3(unsigned(heads * ((a.Dv + 31) / 32))), dim3(kThreads), 0, stream, a, 1);
+    hipLaunchKernelGGL((delta_step_kernel<DK, false>), grid, threads, 0, stream, a, 1);
     set_last_kernel("delta_step");
     return hipGetLastError();
   }
   if (form == Form::kChunk) {
-    const dim3 grid(unsigned(heads * ((a.Dv + 127) / 128)));
-    if (a.tree_mask) hipLaunchKernelGGL((delta_chunk_kernel<DK, true>), grid, dim3(kFusedThreads), 0, stream, a);
-    else hipLaunchKernelGGL((delta_chunk_kernel<DK, false>), grid, dim3(kFusedThreads), 0, stream, a);
+    if (a.tree_mask) hipLaunchKernelGGL((delta_chunk_kernel<DK, true>), grid, threads, 0, stream, a);
+    else hipLaunchKernelGGL((delta_chunk_kernel<DK, false>), grid, threads, 0, stream, a);
     set_last_kernel(a.tree_mask ? "delta_tree" : "delta_chunk");
     return hipGetLastError();
   }
   hipLaunchKernelGGL((delta_prep_kernel<DK>), dim3(unsigned(chunks_of(a.T, a.R)), unsigned((a.Hv + 3) / 4)), dim3(kThreads), 0, stream, a);
   if (hipError_t e = hipGetLastError()) return e;
-  const int64_t grid = (int64_t(a.R) * a.Hk + 7) / 8 * 8 * a.G * ((a.Dv + 31) / 32);
-  hipLaunchKernelGGL((delta_scan_kernel<DK>), dim3(unsigned(grid)), dim3(kScanThreads), 0, stream, a);
+  hipLaunchKernelGGL((delta_scan_kernel<DK>), grid, threads, 0, stream, a);
   set_last_kernel("delta_scan");
   return hipGetLastError();
 }
@@ -1429,6 +1435,11 @@ size_t delta_workspace_bytes(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_
   return up(n * size_t(Hk * G) * kHeadBytes) + n * size_t(Hk) * key_bytes(int(Dk));
 }
 
+bool delta_fits_grid(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_t Dv, int64_t max_nodes, bool tree) {
+  const Form form = form_of(max_nodes, tree);
+  return fits_grid(groups_of(form, R, Hk, G, Dv), threads_of(form)) && (form != Form::kScan || fits_grid(chunks_of(T, R), kThreads));
+}
+
 hipError_t launch_delta_rule(DeltaArgs a, int64_t Dk, int64_t max_nodes, void *workspace, hipStream_t stream) {
   const Form form = form_of(max_nodes, a.tree_mask != nullptr);
   a.heads = static_cast<char *>(workspace);
@@ -1436,9 +1447,14 @@ hipError_t launch_delta_rule(DeltaArgs a, int64_t Dk, int64_t max_nodes, void *w
   return Dk == 64 ? run<64>(a, form, stream) : run<128>(a, form, stream);
 }
 
+static int64_t conv_groups_of(int64_t C) { return (C + 8 * kThreads - 1) / (8 * kThreads); }
+
+int64_t delta_commit_groups(int64_t L, int64_t R, int64_t Hv, int64_t Dv, int64_t C) {
+  return L * R * (Hv * ((Dv + 31) / 32) + conv_groups_of(C));
+}
+
 hipError_t launch_delta_commit(const DeltaArgs &a, int64_t Dk, hipStream_t stream) {
-  const int64_t items = int64_t(a.L) * a.R, conv = a.x ? (a.C + 2047) / 2048 : 0;
-  const int64_t grid = items * a.Hv * ((a.Dv + 31) / 32) + items * conv;
+  const int64_t conv = a.x ? conv_groups_of(a.C) : 0, grid = delta_commit_groups(a.L, a.R, a.Hv, a.Dv, a.x ? a.C : 0);
   (void)hipGetLastError();
   if (Dk == 64) hipLaunchKernelGGL((delta_step_kernel<64, true>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a, int(conv));
   else hipLaunchKernelGGL((delta_step_kernel<128, true>), dim3(unsigned(grid)), dim3(kThreads), 0, stream, a, int(conv));

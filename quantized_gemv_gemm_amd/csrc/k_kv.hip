@@ -518,13 +518,14 @@ __global__ __launch_bounds__(kThreads) void kv_commit_kernel(const CommitArgs a)
   }
 }
 
+int64_t cache_groups(int64_t T, int64_t H) { return (T + kTokens - 1) / kTokens * H; }
+
 template <int D, bool E4M3, bool NORM>
 hipError_t write_rows(const WriteArgs &a, hipStream_t stream) {
-  const int64_t cache = (int64_t(a.T) + kTokens - 1) / kTokens * a.H, rows = a.q ? int64_t(a.T) * a.Hq : 0;
-  const int64_t of_group = kThreads / (D / 16), q = (rows + of_group - 1) / of_group;
-  if (cache + q > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int64_t cache = cache_groups(a.T, a.H), all = kv_write_groups(a.T, a.H, a.q ? a.Hq : 0, D);
+  if (!fits_grid(all, kThreads)) return hipErrorInvalidValue;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((kv_write_kernel<D, E4M3, NORM>), dim3(unsigned(cache + q)), dim3(kThreads), 0, stream, a, int(cache));
+  hipLaunchKernelGGL((kv_write_kernel<D, E4M3, NORM>), dim3(unsigned(all)), dim3(kThreads), 0, stream, a, int(cache));
   set_last_kernel(NORM ? E4M3 ? "kv_write_norm_e4m3" : "kv_write_norm_bf16" : E4M3 ? "kv_write_e4m3" : "kv_write_bf16");
   return hipGetLastError();
 }
@@ -551,6 +552,11 @@ static hipError_t write_of(const WriteArgs &a, int64_t D, bool norm, hipStream_t
   return D == 64    ? write_rows<64, E4M3, false>(a, stream)
          : D == 128 ? write_rows<128, E4M3, false>(a, stream)
                     : write_rows<256, E4M3, false>(a, stream);
+}
+
+int64_t kv_write_groups(int64_t T, int64_t H, int64_t Hq, int64_t D) {
+  const int64_t of_group = kThreads / (D / 16);          // rows of q
+  return cache_groups(T, H) + (T * Hq + of_group - 1) / of_group;
 }
 
 hipError_t launch_kv_write(const WriteArgs &a, int64_t D, bool e4m3, bool norm, hipStream_t stream) {

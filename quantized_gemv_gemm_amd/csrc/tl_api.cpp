@@ -539,6 +539,7 @@ int kv_write(tl::WriteArgs a, int64_t T, int64_t H, int64_t D, int64_t Hq, int64
   if (a.cos_sin && (rot < 16 || rot % 16 || rot > D || max_pos < 1 || max_pos >= kMaxDim)) return TL_ERR_SHAPE;
   if (a.cos_sin && (axes < 1 || axes > 16)) return TL_ERR_SHAPE;
   if (norm && !(a.eps >= 0.0f && a.eps < __builtin_inff())) return TL_ERR_SHAPE;
+  if (!tl::fits_grid(tl::kv_write_groups(T, H, a.q ? Hq : 0, D), 256)) return TL_ERR_SHAPE;
   if (T == 0) return TL_OK;
   const bool e4m3 = cache_dtype == TL_E4M3;
   if (any_null(a.k, a.v, a.slots, a.k_cache, a.v_cache) || (a.q && !a.q_out) || (a.cos_sin && !a.positions))
@@ -737,7 +738,7 @@ int tl_short_conv(const uint16_t *x, int64_t ldx, int64_t T, int64_t C, const fl
   if (!distance_ok(ldx, C) || !distance_ok(ldo, C)) return TL_ERR_SHAPE;
   if (norm_heads < 0 || (norm_heads && (!width_ok(norm_dim) || norm_heads > C / norm_dim))) return TL_ERR_SHAPE;
   if (norm_heads && !(eps >= 0.0f && eps < __builtin_inff())) return TL_ERR_SHAPE;
-  if (states > kMostState / (3 * C)) return TL_ERR_SHAPE;
+  if (states > kMostState / (3 * C) || !tl::conv_fits_grid(T, R)) return TL_ERR_SHAPE;
   if (T == 0 || R == 0) return TL_OK;
   if (any_null(x, weight, q_start, kv_lens, state_slots, out) || (states && !state)) return TL_ERR_NULLPTR;
   if (!aligned_to(16, x, state, out, weight, bias) || ldx % 8 || ldo % 8 || !aligned_to(8, tree_mask) ||
@@ -771,7 +772,8 @@ int tl_delta_rule(const uint16_t *q, int64_t ldq, const uint16_t *k, int64_t ldk
   if (!distance_ok(ldq, Hk * Dk) || !distance_ok(ldk, Hk * Dk) || !distance_ok(ldv, Hv * Dv) || !distance_ok(lda, Hv) ||
       !distance_ok(ldb, Hv))
     return TL_ERR_SHAPE;
-  if (states > kMostState / (Hv * Dk * Dv) || R * Hv * ((Dv + 15) / 16) >= kMaxDim) return TL_ERR_SHAPE;
+  if (states > kMostState / (Hv * Dk * Dv) || !tl::delta_fits_grid(T, R, Hk, G, Dv, max_nodes, tree_mask != nullptr))
+    return TL_ERR_SHAPE;
   if (!(scale > -__builtin_inff() && scale < __builtin_inff())) return TL_ERR_SHAPE;
   if (T == 0 || R == 0) return TL_OK;
   if (any_null(q, k, v, a, b, q_start, kv_lens, state_slots, out) || (states && !state) || !a_log != !dt_bias)
@@ -816,7 +818,7 @@ int tl_delta_commit(const int32_t *accepted, const int32_t *path, int64_t path_w
       a_layer > far || b_layer > far || x_layer > far)
     return TL_ERR_SHAPE;
   if (states > kMostState / (L * Hv * Dk * Dv) || (x && states > kMostState / (L * 3 * C))) return TL_ERR_SHAPE;
-  if (L * R * (Hv * ((Dv + 31) / 32) + (x ? (C + 2047) / 2048 : 0)) >= kMaxDim) return TL_ERR_SHAPE;
+  if (!tl::fits_grid(tl::delta_commit_groups(L, R, Hv, Dv, x ? C : 0), 256)) return TL_ERR_SHAPE;
   if (T == 0 || R == 0) return TL_OK;
   if (any_null(accepted, path, q_start, kv_lens, state_slots, k, v, a, b) || (states && !state) || !a_log != !dt_bias ||
       (x && states && !conv_state))

@@ -162,6 +162,9 @@ struct WriteArgs {
   int axes;
   float eps;
 };
+// workgroups of a launch, and whether it can be made: a grid counts its threads in 32 bits
+inline bool fits_grid(int64_t groups, int64_t threads) { return groups <= int64_t(0xFFFFFFFF) / threads; }
+int64_t kv_write_groups(int64_t T, int64_t H, int64_t Hq, int64_t D);  // of 256 threads; Hq 0: no q
 hipError_t launch_kv_write(const WriteArgs &a, int64_t D, bool e4m3, bool norm, hipStream_t stream);
 
 struct CommitArgs {
@@ -199,6 +202,7 @@ struct ConvArgs {
   int T, R, C, norm_channels, norm_dim;
   float eps;
 };
+bool conv_fits_grid(int64_t T, int64_t R);
 hipError_t launch_short_conv(const ConvArgs &a, int64_t taps, hipStream_t stream);
 
 struct DeltaArgs {
@@ -221,6 +225,8 @@ struct DeltaArgs {
   int path_width, L, C, taps;
 };
 size_t delta_workspace_bytes(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_t Dk, int64_t max_nodes, bool tree);
+bool delta_fits_grid(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_t Dv, int64_t max_nodes, bool tree);
+int64_t delta_commit_groups(int64_t L, int64_t R, int64_t Hv, int64_t Dv, int64_t C);  // of 256 threads; C 0: no x
 hipError_t launch_delta_rule(DeltaArgs a, int64_t Dk, int64_t max_nodes, void *workspace, hipStream_t stream);
 hipError_t launch_delta_commit(const DeltaArgs &a, int64_t Dk, hipStream_t stream);
 
