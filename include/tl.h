@@ -658,7 +658,9 @@ int tl_short_conv(const uint16_t *x, int64_t ldx, int64_t T, int64_t C, const fl
  *   else:        (R * Hk / 8) * 8 * G * (Dv / 32) < 2^23 and T / 64 + R < 2^24.  What is not finite in a token's k, v,
  * g or b leaves nothing finite in the results of the tokens that see it and in the state after it,
  * and changes nothing else; -inf is a log decay like any other: one below -10^4 counts as
- * -10^4, whose exp is 0.
+ * -10^4, whose exp is 0.  Finite values whose products overflow f32 (keys of 10^19, log decays far
+ * above 0) are not looked for: the tokens of their chunk, other branches of a tree among them, may
+ * become NaN.
  */
 size_t tl_delta_rule_workspace_size(int64_t T, int64_t R, int64_t Hk, int64_t G, int64_t Dk, int64_t max_nodes,
                                     int tree);

@@ -277,7 +277,7 @@ __global__ __launch_bounds__(kThreads) void delta_step_kernel(const DeltaArgs a,
 // instructions take their first operand, and the decays; for each chunk and key head, K, Q
 // and K transposed in the same order.  (The scan's workgroups would else ask for rows that
 // lie a token of all heads apart, in halves of lines and mostly in the same few channels of
-// an L2: a call for 8191 tokens of 48 heads of 128 x 128 took 395 us, this way 370.)  A
+// an L2: a call for 8191 tokens of 48 heads of 128 x 128 took 25 us longer, of 390.)  A
 // 16x16x32 operand is 64 lanes of 16 bytes: lane 16 g + m holds row m, columns 8 g .. 8 g + 7
 // of 32.  Its result's lane 16 g + m holds column m, rows 4 g .. 4 g + 3.  Rows
 // are dealt to pairs of tiles so that a pair's results are the next product's second operand
@@ -444,7 +444,7 @@ __device__ __forceinline__ u32x4 transposed(u32x4 lower, u32x4 higher, int p, in
 
 // One wave makes T and P of one chunk and value head, and for the first and last head of a key
 // head K's and Q's operands; four heads share a workgroup, and waves never wait for each other.
-// What it writes bounds it: 297 MB for 8191 tokens of 48 heads of 128 x 128 in 82 us.  All of K
+// What it writes bounds it: 294 MB for 8191 tokens of 48 heads of 128 x 128 in 77 us.  All of K
 // stays in registers as operands.  A lies in LDS; its diagonal blocks of 16 are solved column
 // by column, a lane each (T_ii = (I + A_ii)^-1), and the blocks below follow by
 // T_ij = -T_ii sum over k of A_ik T_kj on the f32 matrix instruction, whose steps take rows
@@ -633,9 +633,11 @@ __global__ __launch_bounds__(kThreads, 2) void delta_prep_kernel(const DeltaArgs
 // four takes row tile w of the chunk's tokens and of the state the tiles TP w .. (a pair for Dk
 // 128, one for Dk 64), and goes the chain from one chunk's state to the next one's: K S, U, K^T U.
 // Wave 4 + w makes the results of row tile w beside it.  The chain's latency bounds it: 8191
-// tokens of 48 heads of 128 x 128 take 285 us, about 4800 cycles a chunk, of which matrix
-// instructions take 1456, LDS reads 1530 at full rate and global loads some 700.  Column m of tile c is column 2 m + c:
-// a lane's columns are neighbours.
+// tokens of 48 heads of 128 x 128 take 305 us, about 5100 cycles a chunk; its matrix
+// instructions take 1728 of them a SIMD, its 312 LDS reads of 1 KB 2500 at 128 bytes a cycle, and
+// its global loads some 700.  Requests of very different lengths wait for a place instead: a
+// workgroup needs 8 waves of 182 registers or more, and a compute unit holds one.  Column m of
+// tile c is column 2 m + c: a lane's columns are neighbours.
 constexpr int kScanThreads = 512;
 
 template <int DK>
@@ -1037,9 +1039,10 @@ __global__ __launch_bounds__(kScanThreads, 1) void delta_scan_kernel(const Delta
 // Drafted trees, and chains of one chunk: a workgroup takes one request, value head and 128
 // columns, makes T and P in LDS and uses them there, in one launch; a wave has 16 columns for
 // all tokens, so K S, R and U stay in its registers from product to product.  A longer request
-// of the call, a chain, goes token by token.  Latency bounds it: a tree of 64 takes 13.7 us, ten
-// steps behind barriers of 1000 to 3000 cycles each and the gates' sums; 16 of up to 64, with 48
-// heads, 32 us in one and a half rounds of two workgroups a compute unit, 69 MB.
+// of the call, a chain, goes token by token, its four blocks of 32 columns one after another
+// (3.6 us a token).  Latency bounds it: a tree of 64 takes 15.8 us, ten steps behind barriers of
+// 1000 to 3000 cycles each and the gates' sums, which one wave makes while seven wait; 16 of up to
+// 64, with 48 heads, 35 us in one and a half rounds of two workgroups a compute unit, 69 MB.
 constexpr int kFusedThreads = 512;
 
 template <int DK, bool TREE>
@@ -1132,7 +1135,7 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
   }
   __syncthreads();
   // The state comes while T is made: asked for beside K and Q it held them up (16 trees of up
-  // to 64, 48 heads of 128 x 128: 36.9 us, this way 35.2).
+  // to 64, 48 heads of 128 x 128: 1.7 us longer, of 35).
   f32x4 S[2 * NS];                                       // tile t, e: row 32 (t / 2) + 8 g + 4 (t % 2) + e
   if (cols && !rq.fresh) {
 #pragma unroll
@@ -1379,15 +1382,24 @@ __global__ __launch_bounds__(kFusedThreads, 4) void delta_chunk_kernel(const Del
 }
 
 // Which kernels take a call: token by token for few tokens, one launch for trees and chains
-// of one chunk, chunks prepared beforehand for the rest.  With 48 heads of 128 x 128, us:
+// of one chunk, chunks prepared beforehand for the rest.  Kernels, us, with states that come from
+// memory (the calls go through 800 MB of them in turn):
+//   48 heads of 128 x 128
 //   chains of tokens       1     4     6     8    16    32    64
-//   1 request:   step    5.4   7.2   8.8  10.3  17.1  30.2  56.7
-//                chunk  12.0  12.1  12.1  12.1  12.1  12.1  16.3
-//                scan   13.6  13.8  13.8  13.9  14.2  14.9  19.4
-//   64 requests: step   62.6  88.6   113   142   241   436   860
-//                chunk   106   109   109   110   110   114   165
-//                scan    252   262   265   271   273   282   332
-// Trees of 64 take 13.7 us for one request, 125 for 64; in the scan's chunks 19 and 286.
+//   1 request:   step    6.0   8.2   9.8  11.2  17.5  30.7  57.4
+//                chunk  12.9  13.0  13.1  13.1  13.2  13.4  17.9
+//                scan   14.9  15.2  15.3  15.4  15.1  16.0  20.6
+//   64 requests: step   79.4  93.6   118   155   260   464   874
+//                chunk   125   129   128   129   133   138   180
+//                scan    257   271   273   276   279   285   342
+//   16 heads of 64 x 64
+//   1 request:   step    5.2   7.1   8.5   9.9  15.1  26.5  49.4
+//                chunk   9.6   9.6   9.7   9.8   9.8   9.7  12.4
+//   64 requests: step   13.4  19.4  24.0  28.6  44.5  80.5   154
+//                chunk  24.3  24.4  24.8  24.8  24.8  25.3  33.9
+// Trees of 64 with 48 heads of 128 x 128 take 15.8 us for one request, 38 for 16, 152 for 64; in
+// the scan's chunks 20, 86 and 313.  One form serves the whole call: 63 single tokens beside a
+// chain of 512 take 285 us in the scan, where each alone takes 78 (step) and 44.
 constexpr int64_t kStepTokens = 6;
 enum class Form { kStep, kChunk, kScan };
 Form form_of(int64_t max_nodes, bool tree) {
